@@ -210,6 +210,106 @@ int moments_rot_fwd(const moments_desc* desc, const void* inc, void* rot, void* 
 int moments_rot_bwd(const moments_desc* desc, const void* inc, const void* d_rot, void* d_inc,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* Linear attention with a decay for each head: reads the states of the scan.
+ *   h~[t] = exp(da_t) h~[t-1] + sum_c xhat[t,c] (outer) bhat[t,c],  h~[-1] = h0
+ *   y[t,c,:] = sum_r h~[t][:,r] qhat[t,c,r]            (all channels of token t written first)
+ * over the same xhat[b,s,c,h,p] and da[b,s,h] as moments_fwd, with keys bhat and
+ * queries qhat [b,s,c,g,r] of g groups: head hi uses group hi / (h/g) (g = h: the
+ * layout of moments_fwd). Keys and queries that carry the position rotation are
+ * what moments_qk_fwd makes: with M_t the de-rotation of moments_fwd,
+ * y[t] = c_t q[t] for qhat[t] = M_t^T q[t] (c_t the de-rotated state).
+ *
+ * States are float32 whatever desc->dtype is, [b,h,p,r]: h0 (NULL: zeros), h_last
+ * (the state after the last valid token; NULL: not wanted). They are kept to fp32
+ * accuracy (the scores, and the copy of the state that y reads, are rounded to bf16
+ * for bf16 inputs), so a sequence may be cut into calls that hand them on.
+ * desc->valid_len and valid_lens are those of moments_desc: rows of y, and of every
+ * gradient, past a sequence's length are zero, whatever the inputs hold there; a
+ * sequence of length 0 leaves h_last = h0. da below -110 (-inf among it) is a decay
+ * of exactly zero: a token with da = -inf starts its sequence anew.
+ *
+ * moments_attn_bwd is the vector-Jacobian product: d_y[b,s,c,h,p] (desc->dtype) and
+ * d_h_last[b,h,p,r] (float32, NULL: zeros) to d_xhat, d_bhat, d_qhat (summed over
+ * the heads of a group), d_da, in desc->dtype, and d_h0 (float32); any of them may be
+ * NULL (not wanted). moments_attn_fwd_save also leaves, in the caller's buffer
+ * `saved` of moments_attn_saved_size() bytes, the state that enters each chunk of
+ * the kernels, as moments_attn_bwd_saved reads it (opaque; same descriptor and
+ * inputs); moments_attn_bwd makes these itself from one more pass over xhat and bhat.
+ *
+ * Supported: 1 <= c <= 4, r <= 128, p <= 4096, s <= 2^28; h a multiple of g; b, s or h
+ * may be 0 (nothing to do, but with s = 0 h_last is h0 and d_h0 is d_h_last). Rows of
+ * r and p elements that are whole 16-byte pieces are read as such, others one element
+ * at a time. Layout, alignment, ownership, errors and MOMENTS_CHECK_FINITE are those
+ * stated above; the workspace is never optional. */
+typedef struct {
+  int64_t b, s, c, h, g, p, r; /* batch, sequence, channels, heads, key groups, rows, state rank */
+  int64_t valid_len;           /* positions >= valid_len are padding; >= s acts as s */
+  int32_t dtype;               /* moments_dtype */
+  int32_t reserved;            /* 0 */
+  const int32_t* valid_lens;   /* per-sequence lengths [b] on the device, or NULL (see moments_desc) */
+} moments_attn_desc;
+
+int moments_attn_validate(const moments_attn_desc* desc);
+int64_t moments_attn_workspace_size(const moments_attn_desc* desc, int is_bwd);
+int64_t moments_attn_saved_size(const moments_attn_desc* desc);
+int moments_attn_fwd(const moments_attn_desc* desc, const void* xhat, const void* bhat, const void* qhat,
+                     const void* da, const float* h0, void* y, float* h_last, void* workspace,
+                     size_t workspace_bytes, void* stream);
+int moments_attn_fwd_save(const moments_attn_desc* desc, const void* xhat, const void* bhat, const void* qhat,
+                          const void* da, const float* h0, void* y, float* h_last, void* saved, size_t saved_bytes,
+                          void* workspace, size_t workspace_bytes, void* stream);
+int moments_attn_bwd(const moments_attn_desc* desc, const void* xhat, const void* bhat, const void* qhat,
+                     const void* da, const float* h0, const void* d_y, const float* d_h_last, void* d_xhat,
+                     void* d_bhat, void* d_qhat, void* d_da, float* d_h0, void* workspace, size_t workspace_bytes,
+                     void* stream);
+int moments_attn_bwd_saved(const moments_attn_desc* desc, const void* xhat, const void* bhat, const void* qhat,
+                           const void* da, const float* h0, const void* saved, size_t saved_bytes, const void* d_y,
+                           const float* d_h_last, void* d_xhat, void* d_bhat, void* d_qhat, void* d_da, float* d_h0,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same for one token of each sequence (desc->s = 1), on a pool of states
+ * state[nslots,h,p,r] (float32, updated in place): sequence bi uses slot slots[bi]
+ * (device int32 [b]; NULL: slot bi, nslots >= b). A slot below 0 or not below nslots, or
+ * a sequence of length 0, is a row without a sequence: its y is zero and no state
+ * is touched. No two sequences of a call may name the same slot. No workspace. */
+int moments_attn_step(const moments_attn_desc* desc, const void* xhat, const void* bhat, const void* qhat,
+                      const void* da, const int32_t* slots, int64_t nslots, float* state, void* y, void* stream);
+
+/* Norms of queries and keys for each head, with the position rotation in the same
+ * pass: makes qhat and bhat from a projection's q and k.
+ *   n = x / sqrt(mean_r x^2 + eps),  u = n * w + bias[head],  hat[t] = M_t^T u[t]
+ * with M_t the de-rotation of moments_fwd at rot[t] (so pairs turn by +angle and
+ * quaternion blocks by the conjugate), for x = q and x = k alike. q and k are
+ * [b,s,c,g,r] in desc->dtype, each token's c*g*r values together and tokens q_stride
+ * and k_stride elements apart (0: c*g*r), so they may be columns of a wider
+ * projection. w[r] and bias[h,r] (NULL: none) are float32. rot is [b,s,rot_h,a] or
+ * [b,s,rot_h,J,4] in desc->dtype with rot_h = h, or 1 (all heads turn alike). qhat and
+ * khat are [b,s,c,h,r]: head hi takes group hi / (h/g), with its own bias and rotation.
+ *
+ * moments_qk_bwd is the vector-Jacobian product at d_qhat, d_khat: d_q, d_k
+ * [b,s,c,g,r] and d_rot in desc->dtype (dense), d_wq, d_wk[r] and d_bq, d_bk[h,r] in
+ * float32 (summed over tokens in a fixed order). d_rot must be NULL without a
+ * rotation, d_bq (d_bk) without that bias; any gradient may be NULL. Every position is
+ * computed (there is no valid_len here). Supported: r <= 128, c <= 4, s, b, h as above. */
+typedef struct {
+  int64_t b, s, c, h, g, r;
+  int64_t q_stride, k_stride;    /* elements between tokens of q and of k, or 0: c*g*r */
+  int64_t rope_dim, quat_blocks; /* as in moments_desc */
+  int64_t rot_h;                 /* heads of rot: h or 1 */
+  int32_t dtype;                 /* moments_dtype */
+  int32_t rot_kind;              /* moments_rot_kind */
+  float eps;                     /* >= 0 */
+  int32_t reserved;              /* 0 */
+} moments_qk_desc;
+
+int64_t moments_qk_workspace_size(const moments_qk_desc* desc);
+int moments_qk_fwd(const moments_qk_desc* desc, const void* q, const void* k, const float* wq, const float* wk,
+                   const float* bq, const float* bk, const void* rot, void* qhat, void* khat, void* stream);
+int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, const float* wq, const float* wk,
+                   const float* bq, const float* bk, const void* rot, const void* d_qhat, const void* d_khat,
+                   void* d_q, void* d_k, float* d_wq, float* d_wk, float* d_bq, float* d_bk, void* d_rot,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
 const char* moments_strerror(int code);
 int moments_last_hip_error(void);
 

@@ -11,12 +11,16 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import (BF16, F32, ROT_HALF, ROT_NONE, ROT_PAIRWISE, ROT_QUAT, Desc,  # noqa: F401
-                   MomentsError)
+from ._lib import (BF16, F32, ROT_HALF, ROT_NONE, ROT_PAIRWISE, ROT_QUAT, AttnDesc, Desc,  # noqa: F401
+                   MomentsError, QkDesc)
 
 __all__ = ["make_desc", "set_valid_lens", "moments_validate", "moments_workspace_size", "moments_fwd", "moments_fwd_static",
            "moments_bwd", "moments_saved_size", "moments_fwd_save", "moments_bwd_saved", "rot_desc", "moments_rot_workspace_size", "moments_rot_fwd", "moments_rot_bwd",
            "kernel_chunk_len",
+           "attn_desc", "moments_attn_validate", "moments_attn_workspace_size", "moments_attn_saved_size",
+           "moments_attn_fwd", "moments_attn_fwd_save", "moments_attn_bwd", "moments_attn_bwd_saved",
+           "moments_attn_step", "qk_desc", "moments_qk_workspace_size", "moments_qk_fwd", "moments_qk_bwd",
+           "AttnDesc", "QkDesc",
            "Desc", "MomentsError", "ROT_NONE", "ROT_PAIRWISE", "ROT_HALF", "ROT_QUAT"]
 
 
@@ -31,7 +35,7 @@ def make_desc(xhat, bhat, chunk_len, valid_len, rot_kind, rope_dim=0, quat_block
     return set_valid_lens(d, valid_lens)
 
 
-def set_valid_lens(desc: Desc, valid_lens):
+def set_valid_lens(desc, valid_lens):
     """Per-sequence valid lengths: ``valid_lens`` is an int32 GPU tensor of shape
     [b] (or None for one length, desc.valid_len, for the whole batch). Sequence
     bi then uses min(max(valid_lens[bi], 0), desc.valid_len, s). The descriptor
@@ -324,6 +328,286 @@ def moments_rot_fwd(desc: Desc, inc, rot=None):
 def moments_rot_bwd(desc: Desc, inc, d_rot, d_inc=None):
     """Cotangent of the increments from the cotangent of the cumulative rotation."""
     return _rot_call(desc, True, inc, d_rot, d_inc)
+
+
+# ---------------------------------------------------------------- linear attention
+def _dt(desc):
+    return torch.bfloat16 if desc.dtype == BF16 else torch.float32
+
+
+def attn_desc(xhat, bhat, valid_len=None, valid_lens=None, dtype=None) -> AttnDesc:
+    """Descriptor of linear attention for xhat [b,s,c,h,p] and keys bhat
+    [b,s,c,g,r] of g groups of heads. ``valid_len`` defaults to s; ``valid_lens``
+    as in make_desc."""
+    for name, t in (("xhat", xhat), ("bhat", bhat)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 5:
+            raise ValueError(f"{name} must be a torch.Tensor of five dimensions")
+    b, s, c, h, p = xhat.shape
+    if dtype is None:
+        dtype = BF16 if xhat.dtype == torch.bfloat16 else F32
+    d = AttnDesc(b, s, c, h, bhat.shape[3], p, bhat.shape[4], s if valid_len is None else int(valid_len), int(dtype))
+    return set_valid_lens(d, valid_lens) if valid_lens is not None else d
+
+
+def moments_attn_validate(desc: AttnDesc) -> int:
+    return _lib.load().moments_attn_validate(ctypes.byref(desc))
+
+
+def _size(n):
+    if n < 0:
+        _lib.check(int(n))
+    return int(n)
+
+
+def moments_attn_workspace_size(desc: AttnDesc, is_bwd: bool) -> int:
+    return _size(_lib.load().moments_attn_workspace_size(ctypes.byref(desc), int(bool(is_bwd))))
+
+
+def moments_attn_saved_size(desc: AttnDesc) -> int:
+    """Bytes of the buffer of moments_attn_fwd_save / moments_attn_bwd_saved."""
+    return _size(_lib.load().moments_attn_saved_size(ctypes.byref(desc)))
+
+
+def _attn_inputs(desc: AttnDesc, xhat, bhat, qhat, da, h0):
+    """Checks the inputs against the descriptor (all on xhat's device, a GPU)."""
+    if not isinstance(xhat, torch.Tensor):
+        raise ValueError("xhat must be a torch.Tensor")
+    dev, dt = xhat.device, _dt(desc)
+    if desc.valid_lens:
+        ref = getattr(desc, "_valid_lens_ref", None)
+        if ref is None or ref.data_ptr() != desc.valid_lens:
+            raise ValueError("set per-sequence lengths with set_valid_lens (the descriptor keeps the tensor)")
+        if ref.device != dev:
+            raise ValueError(f"valid_lens is on {ref.device}, the inputs on {dev}")
+    b, s, c, h, g, p, r = desc.b, desc.s, desc.c, desc.h, desc.g, desc.p, desc.r
+    _expect("xhat", xhat, (b, s, c, h, p), dt, dev)
+    _expect("bhat", bhat, (b, s, c, g, r), dt, dev)
+    _expect("qhat", qhat, (b, s, c, g, r), dt, dev)
+    _expect("da", da, (b, s, h), dt, dev)
+    _expect("h0", h0, (b, h, p, r), torch.float32, dev, optional=True)
+    return dev
+
+
+def _buffer(name, n, device, t):
+    """The caller's scratch tensor, checked, or a new one of n bytes."""
+    if t is None:
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    if t.numel() * t.element_size() < n:
+        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, the descriptor needs {n}")
+    return t
+
+
+def _bytes(t):
+    return t.numel() * t.element_size()
+
+
+def _attn_forward(desc, xhat, bhat, qhat, da, h0, y, h_last, saved, want_saved, workspace):
+    dev = _attn_inputs(desc, xhat, bhat, qhat, da, h0)
+    _expect("y", y, xhat.shape, xhat.dtype, dev, optional=True)
+    _expect("h_last", h_last, (desc.b, desc.h, desc.p, desc.r), torch.float32, dev, optional=True)
+    _require_gpu(dev)
+    lib = _lib.load()
+    ws = _buffer("workspace", moments_attn_workspace_size(desc, False), dev, workspace)
+    if want_saved:
+        saved = _buffer("saved", moments_attn_saved_size(desc), dev, saved)
+    if y is None:
+        y = torch.empty_like(xhat)
+    if h_last is None:
+        h_last = torch.empty(desc.b, desc.h, desc.p, desc.r, dtype=torch.float32, device=dev)
+    head = (ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(qhat), _ptr(da), _ptr(h0), _ptr(y), _ptr(h_last))
+    tail = (_ptr(ws), _bytes(ws), _stream(dev))
+    if want_saved:
+        _lib.check(lib.moments_attn_fwd_save(*head, _ptr(saved), _bytes(saved), *tail))
+        return y, h_last, saved
+    _lib.check(lib.moments_attn_fwd(*head, *tail))
+    return y, h_last
+
+
+def moments_attn_fwd(desc: AttnDesc, xhat, bhat, qhat, da, h0=None, y=None, h_last=None, workspace=None):
+    """Linear attention over a whole sequence: returns (y [b,s,c,h,p] in the input
+    dtype, h_last [b,h,p,r] float32)."""
+    return _attn_forward(desc, xhat, bhat, qhat, da, h0, y, h_last, None, False, workspace)
+
+
+def moments_attn_fwd_save(desc: AttnDesc, xhat, bhat, qhat, da, h0=None, y=None, h_last=None, saved=None,
+                          workspace=None):
+    """moments_attn_fwd that also keeps the states entering the kernels' chunks.
+    Returns (y, h_last, saved); saved is opaque, for moments_attn_bwd_saved."""
+    return _attn_forward(desc, xhat, bhat, qhat, da, h0, y, h_last, saved, True, workspace)
+
+
+def moments_attn_bwd(desc: AttnDesc, xhat, bhat, qhat, da, h0, d_y, d_h_last=None,
+                     want=("xhat", "bhat", "qhat", "da", "h0"), out=None, workspace=None, _saved=None):
+    """Returns dict d_xhat, d_bhat, d_qhat, d_da (input dtype), d_h0 (float32); None
+    when not wanted (d_h0: or when there is no h0)."""
+    dev = _attn_inputs(desc, xhat, bhat, qhat, da, h0)
+    _expect("d_y", d_y, xhat.shape, xhat.dtype, dev)
+    state = (desc.b, desc.h, desc.p, desc.r)
+    _expect("d_h_last", d_h_last, state, torch.float32, dev, optional=True)
+    out = dict(out or {})
+    like = {"xhat": xhat, "bhat": bhat, "qhat": qhat, "da": da, "h0": h0}
+    for k, t in like.items():
+        if k in want and t is not None:
+            _expect("d_" + k, out.get("d_" + k), t.shape, t.dtype, dev, optional=True)
+        else:
+            out["d_" + k] = None
+    _require_gpu(dev)
+    for k, t in like.items():
+        if k in want and t is not None and out.get("d_" + k) is None:
+            out["d_" + k] = torch.empty_like(t)
+    lib = _lib.load()
+    ws = _buffer("workspace", moments_attn_workspace_size(desc, True), dev, workspace)
+    head = (ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(qhat), _ptr(da), _ptr(h0))
+    grads = (_ptr(d_y), _ptr(d_h_last), _ptr(out["d_xhat"]), _ptr(out["d_bhat"]), _ptr(out["d_qhat"]),
+             _ptr(out["d_da"]), _ptr(out["d_h0"]), _ptr(ws), _bytes(ws), _stream(dev))
+    if _saved is None:
+        _lib.check(lib.moments_attn_bwd(*head, *grads))
+    else:
+        sv = _buffer("saved", moments_attn_saved_size(desc), dev, _saved)
+        _lib.check(lib.moments_attn_bwd_saved(*head, _ptr(sv), _bytes(sv), *grads))
+    return out
+
+
+def moments_attn_bwd_saved(desc: AttnDesc, xhat, bhat, qhat, da, h0, saved, d_y, d_h_last=None,
+                           want=("xhat", "bhat", "qhat", "da", "h0"), out=None, workspace=None):
+    """moments_attn_bwd reading what moments_attn_fwd_save kept. Same returns."""
+    if saved is None:
+        raise ValueError("saved is required")
+    return moments_attn_bwd(desc, xhat, bhat, qhat, da, h0, d_y, d_h_last, want=want, out=out,
+                            workspace=workspace, _saved=saved)
+
+
+def moments_attn_step(desc: AttnDesc, xhat, bhat, qhat, da, state, slots=None, y=None):
+    """One token of each sequence (s = 1) on a pool of states, state [nslots,h,p,r]
+    float32, updated in place; ``slots`` int32 [b] (None: slot i for sequence i; a
+    slot outside the pool marks an unused row, whose y is zero). Returns y."""
+    dev = _attn_inputs(desc, xhat, bhat, qhat, da, None)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be a torch.Tensor [nslots,h,p,r]")
+    n = state.shape[0]
+    _expect("state", state, (n, desc.h, desc.p, desc.r), torch.float32, dev)
+    _expect("slots", slots, (desc.b,), torch.int32, dev, optional=True)
+    _expect("y", y, xhat.shape, xhat.dtype, dev, optional=True)
+    _require_gpu(dev)
+    if y is None:
+        y = torch.empty_like(xhat)
+    _lib.check(_lib.load().moments_attn_step(ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(qhat), _ptr(da),
+                                             _ptr(slots), n, _ptr(state), _ptr(y), _stream(dev)))
+    return y
+
+
+# ---------------------------------------------------------------- norms of queries and keys
+def qk_desc(q, k, h, rot_kind, rot=None, eps=1e-5, rope_dim=None, quat_blocks=None) -> QkDesc:
+    """Descriptor of the norms with rotation for q and k [b,s,c,g,r] and h heads.
+    q and k may be columns of a wider projection: each token's values together,
+    tokens a fixed stride apart. The rotated width and the heads of the rotation
+    are taken from ``rot`` ([b,s,h or 1,a] angles or [b,s,h or 1,J,4])."""
+    strides = []
+    for name, t in (("q", q), ("k", k)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 5:
+            raise ValueError(f"{name} must be a torch.Tensor of five dimensions")
+        strides.append(_token_stride(name, t))
+    b, s, c, g, r = q.shape
+    rot_h = h
+    if rot_kind != ROT_NONE:
+        if not isinstance(rot, torch.Tensor) or rot.dim() != (5 if rot_kind == ROT_QUAT else 4):
+            raise ValueError("rot must be a torch.Tensor [b,s,heads,a] of angles or [b,s,heads,J,4] of quaternions")
+        rot_h = rot.shape[2]
+        if rot_kind == ROT_QUAT:
+            quat_blocks = rot.shape[3] if quat_blocks is None else quat_blocks
+        else:
+            rope_dim = 2 * rot.shape[3] if rope_dim is None else rope_dim
+    return QkDesc(b, s, c, h, g, r, strides[0], strides[1], rope_dim or 0, quat_blocks or 0, rot_h,
+                  BF16 if q.dtype == torch.bfloat16 else F32, int(rot_kind), float(eps))
+
+
+def _token_stride(name, t):
+    """Elements between tokens of t [b,s,c,g,r] (0 where any would do)."""
+    b, s, c, g, r = t.shape
+    if t.numel() == 0:
+        return 0
+    inner = t[0, 0]
+    step = t.stride(1) if s > 1 else (t.stride(0) if b > 1 else c * g * r)
+    if not inner.is_contiguous() or step < c * g * r or (b > 1 and s > 1 and t.stride(0) != s * step):
+        raise ValueError(f"{name} must hold each token's values together, tokens a fixed stride apart")
+    return step
+
+
+def _qk_inputs(desc: QkDesc, q, k, wq, wk, bq, bk, rot):
+    if not isinstance(q, torch.Tensor):
+        raise ValueError("q must be a torch.Tensor")
+    dev, dt = q.device, _dt(desc)
+    b, s, c, h, g, r = desc.b, desc.s, desc.c, desc.h, desc.g, desc.r
+    for name, t, stride in (("q", q, desc.q_stride), ("k", k, desc.k_stride)):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a torch.Tensor")
+        if tuple(t.shape) != (b, s, c, g, r) or t.dtype != dt or t.device != dev:
+            raise ValueError(f"{name} must be {dt} of shape {(b, s, c, g, r)} on {dev}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        if t.numel() and _token_stride(name, t) != (stride or c * g * r):
+            raise ValueError(f"{name} has another token stride than the descriptor ({stride or c * g * r})")
+    for name, t in (("wq", wq), ("wk", wk)):
+        _expect(name, t, (r,), torch.float32, dev)
+    for name, t in (("bq", bq), ("bk", bk)):
+        _expect(name, t, (h, r), torch.float32, dev, optional=True)
+    if desc.rot_kind == ROT_NONE:
+        if rot is not None:
+            raise ValueError("rot must be None when the descriptor has no rotation")
+    else:
+        _expect("rot", rot, (b, s, desc.rot_h, desc.quat_blocks, 4) if desc.rot_kind == ROT_QUAT
+                else (b, s, desc.rot_h, desc.rope_dim // 2), dt, dev)
+    return dev, dt
+
+
+def moments_qk_workspace_size(desc: QkDesc) -> int:
+    """Bytes of the backward's workspace (the forward needs none)."""
+    return _size(_lib.load().moments_qk_workspace_size(ctypes.byref(desc)))
+
+
+def moments_qk_fwd(desc: QkDesc, q, k, wq, wk, bq=None, bk=None, rot=None, qhat=None, khat=None):
+    """Returns (qhat, khat) [b,s,c,h,r]: normed, weighted, biased and turned into the
+    frame of the cached states (khat is what the moments path takes as bhat)."""
+    dev, dt = _qk_inputs(desc, q, k, wq, wk, bq, bk, rot)
+    shape = (desc.b, desc.s, desc.c, desc.h, desc.r)
+    _expect("qhat", qhat, shape, dt, dev, optional=True)
+    _expect("khat", khat, shape, dt, dev, optional=True)
+    _require_gpu(dev)
+    if qhat is None:
+        qhat = torch.empty(shape, dtype=dt, device=dev)
+    if khat is None:
+        khat = torch.empty(shape, dtype=dt, device=dev)
+    _lib.check(_lib.load().moments_qk_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(bq),
+                                          _ptr(bk), _ptr(rot), _ptr(qhat), _ptr(khat), _stream(dev)))
+    return qhat, khat
+
+
+def moments_qk_bwd(desc: QkDesc, q, k, wq, wk, bq, bk, rot, d_qhat, d_khat,
+                   want=("q", "k", "wq", "wk", "bq", "bk", "rot"), out=None, workspace=None):
+    """Returns dict d_q, d_k, d_rot (input dtype, dense), d_wq, d_wk, d_bq, d_bk
+    (float32); None when not wanted or not defined."""
+    dev, dt = _qk_inputs(desc, q, k, wq, wk, bq, bk, rot)
+    shape = (desc.b, desc.s, desc.c, desc.h, desc.r)
+    _expect("d_qhat", d_qhat, shape, dt, dev)
+    _expect("d_khat", d_khat, shape, dt, dev)
+    out = dict(out or {})
+    like = {"q": q, "k": k, "wq": wq, "wk": wk, "bq": bq, "bk": bk, "rot": rot}
+    for n, t in like.items():
+        if n in want and t is not None:
+            _expect("d_" + n, out.get("d_" + n), t.shape, t.dtype, dev, optional=True)
+        else:
+            out["d_" + n] = None
+    _require_gpu(dev)
+    for n, t in like.items():
+        if n in want and t is not None and out.get("d_" + n) is None:
+            out["d_" + n] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+    ws = _buffer("workspace", moments_qk_workspace_size(desc), dev, workspace)
+    _lib.check(_lib.load().moments_qk_bwd(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(bq), _ptr(bk), _ptr(rot), _ptr(d_qhat),
+        _ptr(d_khat), _ptr(out["d_q"]), _ptr(out["d_k"]), _ptr(out["d_wq"]), _ptr(out["d_wk"]), _ptr(out["d_bq"]),
+        _ptr(out["d_bk"]), _ptr(out["d_rot"]), _ptr(ws), _bytes(ws), _stream(dev)))
+    return out
 
 
 def kernel_chunk_len() -> int:

@@ -21,7 +21,10 @@ EXPORTS = ("moments_validate", "moments_workspace_size", "moments_fwd", "moments
            "moments_strerror", "moments_last_hip_error", "moments_kernel_chunk_len",
            "moments_profile_enable", "moments_profile_read", "moments_profile_reset",
            "moments_rot_workspace_size", "moments_rot_fwd", "moments_rot_bwd",
-           "moments_saved_size", "moments_fwd_save", "moments_bwd_saved")
+           "moments_saved_size", "moments_fwd_save", "moments_bwd_saved",
+           "moments_attn_validate", "moments_attn_workspace_size", "moments_attn_saved_size", "moments_attn_fwd",
+           "moments_attn_fwd_save", "moments_attn_bwd", "moments_attn_bwd_saved", "moments_attn_step",
+           "moments_qk_workspace_size", "moments_qk_fwd", "moments_qk_bwd")
 
 
 class Desc(ctypes.Structure):
@@ -31,6 +34,22 @@ class Desc(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("rot_kind", ctypes.c_int32),
                 ("rope_dim", ctypes.c_int64), ("quat_blocks", ctypes.c_int64),
                 ("valid_lens", ctypes.c_void_p)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("s", ctypes.c_int64), ("c", ctypes.c_int64),
+                ("h", ctypes.c_int64), ("g", ctypes.c_int64), ("p", ctypes.c_int64), ("r", ctypes.c_int64),
+                ("valid_len", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("valid_lens", ctypes.c_void_p)]
+
+
+class QkDesc(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("s", ctypes.c_int64), ("c", ctypes.c_int64),
+                ("h", ctypes.c_int64), ("g", ctypes.c_int64), ("r", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("rope_dim", ctypes.c_int64), ("quat_blocks", ctypes.c_int64), ("rot_h", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("rot_kind", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
 
 
 class MomentsError(RuntimeError):
@@ -74,6 +93,21 @@ def load():
         lib.moments_rot_fwd.restype = ctypes.c_int
         lib.moments_rot_bwd.argtypes = [dp, vp, vp, vp, vp, ctypes.c_size_t, vp]
         lib.moments_rot_bwd.restype = ctypes.c_int
+        ap, qp, sz, i64 = ctypes.POINTER(AttnDesc), ctypes.POINTER(QkDesc), ctypes.c_size_t, ctypes.c_int64
+        for name, args, res in (
+                ("moments_attn_validate", [ap], ctypes.c_int),
+                ("moments_attn_workspace_size", [ap, ctypes.c_int], i64),
+                ("moments_attn_saved_size", [ap], i64),
+                ("moments_attn_fwd", [ap] + [vp] * 7 + [vp, sz, vp], ctypes.c_int),
+                ("moments_attn_fwd_save", [ap] + [vp] * 7 + [vp, sz, vp, sz, vp], ctypes.c_int),
+                ("moments_attn_bwd", [ap] + [vp] * 12 + [vp, sz, vp], ctypes.c_int),
+                ("moments_attn_bwd_saved", [ap] + [vp] * 5 + [vp, sz] + [vp] * 7 + [vp, sz, vp], ctypes.c_int),
+                ("moments_attn_step", [ap] + [vp] * 5 + [i64, vp, vp, vp], ctypes.c_int),
+                ("moments_qk_workspace_size", [qp], i64),
+                ("moments_qk_fwd", [qp] + [vp] * 9 + [vp], ctypes.c_int),
+                ("moments_qk_bwd", [qp] + [vp] * 16 + [vp, sz, vp], ctypes.c_int)):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = res
         lib.moments_strerror.argtypes = [ctypes.c_int]
         lib.moments_strerror.restype = ctypes.c_char_p
         lib.moments_last_hip_error.argtypes = []

@@ -1,10 +1,12 @@
 """Build the HIP library libmoments.so for gfx950 (in-tree, under _build/).
 
-Three translation units: moments.hip (the C ABI, the dispatcher and every
-kernel but the lane-pair forward), and fwd4.hip twice, for the lane-pair
-forward's instances that do not save carries (with the ILP machine-scheduling
-strategy) and for those that do (default strategy). They are compiled in
-parallel and linked with no undefined symbols allowed."""
+Five translation units: moments.hip (the moments' C ABI, the dispatcher and
+every kernel of theirs but the lane-pair forward), fwd4.hip twice, for the
+lane-pair forward's instances that do not save carries (with the ILP
+machine-scheduling strategy) and for those that do (default strategy), attn.hip
+(linear attention with a decay for each head) and qk.hip (norms of queries and
+keys with the rotation). They are compiled in parallel and linked with no
+undefined symbols allowed."""
 from __future__ import annotations
 
 import os
@@ -28,6 +30,8 @@ UNITS = {
     "moments.o": ("moments.hip", []),
     "fwd4.o": ("fwd4.hip", ["-DMOM_FWD4_SAVE=0", "-mllvm", "-amdgpu-sched-strategy=max-ilp"]),
     "fwd4_save.o": ("fwd4.hip", ["-DMOM_FWD4_SAVE=1"]),
+    "attn.o": ("attn.hip", []),
+    "qk.o": ("qk.hip", []),
 }
 
 

@@ -1,0 +1,381 @@
+// Linear attention with a decay for each head: gradients.
+//
+// With G the cotangent of the state after a chunk, over the chunk's rows u, j
+// (s = (q.k) e^{a_u - a_j} and t = (dy.x) e^{a_u - a_j}, both for j <= u):
+//   d_q[u] = sum_j t[u][j] k[j] + e^{a_u} H^T dy[u]
+//   d_k[j] = sum_u t[u][j] q[u] + e^{a_end - a_j} G^T x[j]
+//   d_x[j] = sum_u s[u][j] dy[u] + e^{a_end - a_j} G k[j]
+//   G'     = e^{a_end} G + sum_u e^{a_u} dy[u] (outer) q[u]
+// with H the state entering the chunk. The log-decay of token t scales all that
+// crosses it, and is summed from just that, so no large terms cancel over a long
+// sequence: pairs j < t <= u inside the chunk (row sums of (q.k) t minus its column
+// sums, from t on: the pairs on one side drop out exactly), what the rows from t on
+// read of H (q.d_q of the second term), what later chunks read of the rows before t
+// (k.d_k of the second term), and e^{a_end} <G, H>.
+//
+// A workgroup walks one chain's chunks in reverse with G in fp32 registers; H
+// comes from the copies that the forward (or a walk over k and x) left per chunk.
+#pragma once
+
+#include "kernels_attn.h"
+
+namespace mom {
+
+constexpr int ABT = 512;  // threads: eight waves
+constexpr int ABW = 8;
+
+template <typename T, int RT, int PT>   // PT tiles of 16 state rows p
+struct LdsB {
+  static constexpr int L = AV<T>::L;
+  // 128 rows of p in bf16: pitches of 8 (mod 64) elements, so that everything fits 160 KB
+  // (the transposing reads are then two-way bank conflicted)
+  static constexpr bool TIGHT = PT == 8 && RT == 8;
+  static constexpr int RP = TIGHT ? 16 * RT + 8 : AV<T>::pitch(16 * RT), PP = TIGHT ? 16 * PT + 8 : AV<T>::pitch(16 * PT),
+                       SP = TIGHT ? L + 8 : AV<T>::pitch(L);
+  static constexpr size_t E = sizeof(T);
+  static constexpr size_t tab = 0;
+  // rsum[4][64], csum[4][64], th[16], and up[8][64], vp[8][64], which with TIGHT lie in the
+  // four floats of padding behind each of the 128 rows of hs and gs instead
+  static constexpr size_t sums = sizeof(DecayTab);
+  static constexpr size_t k = sums + (4 + 4 + (TIGHT ? 0 : 16)) * 64 * 4 + 64;
+  static constexpr size_t q = k + (size_t)L * RP * E, x = q + (size_t)L * RP * E, dy = x + (size_t)L * PP * E,
+                          s = dy + (size_t)L * PP * E, t = s + (size_t)L * SP * E,
+                          hs = t + (size_t)L * SP * E, gs = hs + (size_t)16 * PT * RP * E,
+                          total = gs + (size_t)16 * PT * RP * E;
+};
+
+// The state copies that enter a chunk: tile pairs of two quads a lane (as k_attn_walk
+// saves them), in flight to the LDS tile [p][r].
+template <typename T, int RT, int PT>
+struct StageH {
+  static constexpr int PAIRS = PT * RT / 2 * 64, N = (PAIRS + ABT - 1) / ABT;
+  using quad = typename AV<T>::quad;
+  quad v[N][2];
+  __device__ __forceinline__ void load(const T* src) {
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int e = i * ABT + (int)threadIdx.x;
+      if (PAIRS % ABT == 0 || e < PAIRS) {
+        v[i][0] = *reinterpret_cast<const quad*>(src + (size_t)e * 8);
+        v[i][1] = *reinterpret_cast<const quad*>(src + (size_t)e * 8 + 4);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* t, int P) const {
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int e = i * ABT + (int)threadIdx.x, lane = e & 63, tp = e >> 6, m = tp % (RT / 2), pt = tp / (RT / 2);
+      if (PAIRS % ABT == 0 || e < PAIRS) {
+        st_quad(t, P, 16 * pt + (lane & 15), 8 * m + (lane >> 4), v[i][0]);
+        st_quad(t, P, 16 * pt + (lane & 15), 8 * m + 4 + (lane >> 4), v[i][1]);
+      }
+    }
+  }
+};
+
+// PART: d_q and d_k go, in float32, to a slice of their own for each head and p tile
+// (heads that share keys, or state rows in several tiles; k_attn_sum adds them), and
+// d_da likewise for each p tile; otherwise straight to the caller's tensors.
+template <typename T, int RT, int PT, bool PART>
+__global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
+    AttnGeo g, const T* __restrict__ x, const T* __restrict__ k, const T* __restrict__ q, const T* __restrict__ da,
+    const T* __restrict__ save, const T* __restrict__ dy, const float* __restrict__ d_last,
+    const float* __restrict__ seg_loc, const double* __restrict__ seg_dec, T* __restrict__ d_x, T* __restrict__ d_k,
+    T* __restrict__ d_q, T* __restrict__ d_da, float* __restrict__ d_h0, float* __restrict__ part_k,
+    float* __restrict__ part_q, float* __restrict__ part_da) {
+  using LD = LdsB<T, RT, PT>;
+  using V = AV<T>;
+  constexpr int L = V::L, NT = L / 16, NJ = L / 32;
+  constexpr int NG = ABW / PT > 0 ? ABW / PT : 1;   // wave groups: each has all p tiles of a share of the r tiles
+  constexpr int RW = RT / NG;                       // r tiles of G a wave owns
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  DecayTab* tab = reinterpret_cast<DecayTab*>(lds + LD::tab);
+  float* rsum = reinterpret_cast<float*>(lds + LD::sums);   // [jt][u]
+  float* csum = rsum + 4 * 64;                              // [ut][j]
+  float* th = csum + 4 * 64;                                // [wave]
+  T* ks = reinterpret_cast<T*>(lds + LD::k);
+  T* qs = reinterpret_cast<T*>(lds + LD::q);
+  T* xs = reinterpret_cast<T*>(lds + LD::x);
+  T* ys = reinterpret_cast<T*>(lds + LD::dy);
+  T* ss = reinterpret_cast<T*>(lds + LD::s);
+  T* ts = reinterpret_cast<T*>(lds + LD::t);
+  T* hs = reinterpret_cast<T*>(lds + LD::hs);
+  T* gs = reinterpret_cast<T*>(lds + LD::gs);
+  // sums over a tile of 16 columns r, [rt][u] and [rt][j]
+  auto up = [&](int rt, int u) -> float& {
+    if constexpr (LD::TIGHT) return reinterpret_cast<float*>(hs + (16 * rt + (u >> 2)) * LD::RP + 16 * RT)[u & 3];
+    return th[16 + rt * 64 + u];
+  };
+  auto vp = [&](int rt, int j) -> float& {
+    if constexpr (LD::TIGHT) return reinterpret_cast<float*>(gs + (16 * rt + (j >> 2)) * LD::RP + 16 * RT)[j & 3];
+    return th[16 + (8 + rt) * 64 + j];
+  };
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ln = lane & 15, lq = lane >> 4;
+
+  const int nch = g.b * g.h;
+  const int seg = g.nseg - 1 - (int)blockIdx.x / (nch * g.npt), rem = blockIdx.x % (nch * g.npt);
+  const int item = xcd_order(rem, nch * g.npt);
+  const int pt = item % g.npt, chain = item / g.npt;
+  const int bi = chain / g.h, hi = chain % g.h, gi = hi / g.hpg;
+  const int Vb = attn_len(g, bi), nkb = (Vb + g.CT - 1) / g.CT;
+  const int n0 = seg * g.SL, n1 = min(n0 + g.SL, g.NK);
+  const int p0 = pt * 16 * PT, pn = min(g.p - p0, 16 * PT);
+  const size_t kst = (size_t)g.g * g.r, xst = (size_t)g.h * g.p;
+  const size_t row0 = (size_t)bi * g.s * g.c;
+  const T* kb = k + row0 * kst + (size_t)gi * g.r;
+  const T* qb = q + row0 * kst + (size_t)gi * g.r;
+  const T* xb = x + row0 * xst + (size_t)hi * g.p + p0;
+  const T* yb = dy + row0 * xst + (size_t)hi * g.p + p0;
+  const T* dab = da + (size_t)bi * g.s * g.h + hi;
+  const bool vq = g.vq != 0, vx = g.vx != 0;
+  constexpr size_t TILES = (size_t)PT * RT * 256;
+  // slices: rows of h * npt * r values (d_q, d_k) and h * npt values a token (d_da)
+  const int slice = hi * g.npt + pt;
+  const size_t pst = (size_t)g.h * g.npt * g.r;
+
+  const int mp = wave % PT, mr = (wave / PT) * RW;   // this wave's p tile and first r tile of G
+  f4 G[RW];
+#pragma unroll
+  for (int i = 0; i < RW; i++) {
+    G[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (d_last != nullptr)
+      G[i] = ld_state4(d_last + (size_t)chain * g.p * g.r, g.p, g.r, p0 + 16 * mp + ln, 16 * (mr + i) + 4 * lq);
+  }
+  for (int s = g.nseg - 1; s > seg; s--) {   // what the segments after this one leave
+    const size_t at = ((size_t)chain * g.nseg + s) * g.npt + pt;
+    const float dec = ex2((float)seg_dec[at]);
+#pragma unroll
+    for (int i = 0; i < RW; i++)
+      G[i] = G[i] * dec + *reinterpret_cast<const f4*>(seg_loc + at * TILES + tile_off(RT, mp, mr + i, lane));
+  }
+
+  const int nlive = min(n1, nkb);
+  for (int n = nlive - 1; n >= n0; n--) {
+    const int t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
+    const size_t u0 = (size_t)t0 * g.c;
+    {
+      Stage<T, 16 * RT, ABT> sk, sq;
+      Stage<T, 16 * PT, ABT> sx, sy;
+      StageH<T, RT, PT> sh;
+      sk.load(kb + u0 * kst, kst, nrows, g.r, vq);
+      sq.load(qb + u0 * kst, kst, nrows, g.r, vq);
+      sx.load(xb + u0 * xst, xst, nrows, pn, vx);
+      sy.load(yb + u0 * xst, xst, nrows, pn, vx);
+      sh.load(save + (((size_t)chain * g.NK + n) * g.npt + pt) * TILES);
+      // (the barrier that ended the last chunk covers these writes)
+      sk.store(ks, LD::RP);
+      sq.store(qs, LD::RP);
+      sx.store(xs, LD::PP);
+      sy.store(ys, LD::PP);
+      sh.store(hs, LD::RP);
+    }
+#pragma unroll
+    for (int i = 0; i < RW; i++) st_quad(gs, LD::RP, 16 * mp + ln, 4 * (mr + i) + lq, to_quad<T>(G[i]));
+    if (wave == 0) {
+      const int tok = (lane * g.cinv) >> 16;
+      const bool opens = lane < nrows && tok * g.c == lane;
+      decay_table(tab, opens ? log2_decay(to_f(dab[(size_t)(t0 + tok) * g.h])) : 0.0, lane);
+    }
+    __syncthreads();
+    const float dec = ex2((float)tab->total);
+
+    // <G, H> of this wave's tiles
+    {
+      float v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < RW; i++) {
+        const f4 h = quad_f(ld_quad(hs, LD::RP, 16 * mp + ln, 4 * (mr + i) + lq));
+#pragma unroll
+        for (int e = 0; e < 4; e++) v += G[i][e] * h[e];
+      }
+      v = col4_sum(row16_sum(v));
+      if (lane == 0) th[wave] = v;
+    }
+    // s, t (stored [u][j]) and the sums of (q.k) t over pairs of different tokens
+#pragma unroll
+    for (int it = 0; it < (NT * NT + ABW - 1) / ABW; it++) {
+      const int id = it * ABW + wave, ut = id % NT, jt = id / NT;
+      if (NT * NT % ABW != 0 && id >= NT * NT) break;
+      f4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
+      float rs = 0.0f;
+      f4 cs = a;
+      if (jt <= ut || (g.c == 3 && jt == ut + 1)) {
+#pragma unroll
+        for (int m = 0; m < RT / 2; m++)
+          a = mma32(row_frag(ks, LD::RP, 16 * jt, m, lane), row_frag(qs, LD::RP, 16 * ut, m, lane), a);
+#pragma unroll
+        for (int m = 0; m < PT / 2; m++)
+          b = mma32(row_frag(xs, LD::PP, 16 * jt, m, lane), row_frag(ys, LD::PP, 16 * ut, m, lane), b);
+        const int u = 16 * ut + ln, tu = (u * g.cinv) >> 16;
+        const float uh = tab->hi[u], ul = tab->lo[u];
+        const f4 jh = *reinterpret_cast<const f4*>(tab->hi + 16 * jt + 4 * lq);
+        const f4 jl = *reinterpret_cast<const f4*>(tab->lo + 16 * jt + 4 * lq);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const int tj = ((16 * jt + 4 * lq + e) * g.cinv) >> 16;
+          const float w = tj <= tu ? ex2((uh - jh[e]) + (ul - jl[e])) : 0.0f;
+          const float qk = a[e];
+          a[e] = tj <= tu ? qk * w : 0.0f;
+          b[e] = tj <= tu ? b[e] * w : 0.0f;
+          cs[e] = tj < tu ? qk * b[e] : 0.0f;
+          rs += cs[e];
+        }
+      }
+      st_quad(ss, LD::SP, 16 * ut + ln, 4 * jt + lq, to_quad<T>(a));
+      st_quad(ts, LD::SP, 16 * ut + ln, 4 * jt + lq, to_quad<T>(b));
+      rs = col4_sum(rs);
+      if (lq == 0) rsum[jt * 64 + 16 * ut + ln] = rs;
+#pragma unroll
+      for (int e = 0; e < 4; e++) cs[e] = row16_sum(cs[e]);
+      if (ln == 0) *reinterpret_cast<f4*>(csum + ut * 64 + 16 * jt + 4 * lq) = cs;
+    }
+    __syncthreads();
+
+    // d_q and d_k, r tile by r tile (transposed: columns are rows u of the chunk)
+#pragma unroll
+    for (int it = 0; it < (RT * NT + ABW - 1) / ABW; it++) {
+      const int id = it * ABW + wave, rt = id % RT, ut = id / RT;
+      if (RT * NT % ABW != 0 && id >= RT * NT) break;
+      const int u = 16 * ut + ln, r0 = 16 * rt + 4 * lq;
+      const bool live = u < nrows;
+      const size_t at = row0 + u0 + u;
+      f4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int m = 0; m < PT / 2; m++)
+        a = mma32(col_frag(hs, LD::RP, m, 16 * rt, lane), row_frag(ys, LD::PP, 16 * ut, m, lane), a);
+      a *= tab->start[u];
+      const f4 qv = quad_f(ld_quad(qs, LD::RP, u, 4 * rt + lq));
+      const float us = col4_sum(a[0] * qv[0] + a[1] * qv[1] + a[2] * qv[2] + a[3] * qv[3]);
+      if (lq == 0) up(rt, u) = us;
+#pragma unroll
+      for (int m = 0; m < NJ; m++)
+        if (32 * m < 16 * (ut + 1) || g.c == 3)
+          a = mma32(col_frag(ks, LD::RP, m, 16 * rt, lane), row_frag(ts, LD::SP, 16 * ut, m, lane), a);
+      if (live) {
+        if constexpr (PART)
+          st_row4(part_q + at * pst + (size_t)slice * g.r, g.r, r0, a);
+        else if (d_q != nullptr)
+          st_row4(d_q + at * kst + (size_t)gi * g.r, g.r, r0, a);
+      }
+      f4 b = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int m = 0; m < PT / 2; m++)
+        b = mma32(col_frag(gs, LD::RP, m, 16 * rt, lane), row_frag(xs, LD::PP, 16 * ut, m, lane), b);
+      b *= tab->end[u];
+      const f4 kv = quad_f(ld_quad(ks, LD::RP, u, 4 * rt + lq));
+      const float vs = col4_sum(b[0] * kv[0] + b[1] * kv[1] + b[2] * kv[2] + b[3] * kv[3]);
+      if (lq == 0) vp(rt, u) = vs;
+#pragma unroll
+      for (int m = 0; m < NJ; m++)
+        if (32 * (m + 1) > 16 * ut || g.c == 3)
+          b = mma32(col_frag(qs, LD::RP, m, 16 * rt, lane), col_frag(ts, LD::SP, m, 16 * ut, lane), b);
+      if (live) {
+        if constexpr (PART)
+          st_row4(part_k + at * pst + (size_t)slice * g.r, g.r, r0, b);
+        else if (d_k != nullptr)
+          st_row4(d_k + at * kst + (size_t)gi * g.r, g.r, r0, b);
+      }
+    }
+    // d_x
+#pragma unroll
+    for (int it = 0; it < (PT * NT + ABW - 1) / ABW; it++) {
+      const int id = it * ABW + wave, pj = id % PT, ut = id / PT;
+      if (PT * NT % ABW != 0 && id >= PT * NT) break;
+      const int u = 16 * ut + ln;
+      f4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int m = 0; m < RT / 2; m++)
+        a = mma32(row_frag(gs, LD::RP, 16 * pj, m, lane), row_frag(ks, LD::RP, 16 * ut, m, lane), a);
+      a *= tab->end[u];
+#pragma unroll
+      for (int m = 0; m < NJ; m++)
+        if (32 * (m + 1) > 16 * ut || g.c == 3)
+          a = mma32(col_frag(ys, LD::PP, m, 16 * pj, lane), col_frag(ss, LD::SP, m, 16 * ut, lane), a);
+      if (u < nrows && d_x != nullptr) st_row4(d_x + (row0 + u0 + u) * xst + (size_t)hi * g.p, g.p, p0 + 16 * pj + 4 * lq, a);
+    }
+    // G'
+    {
+      Scaled<V::NSPLIT> yf[NJ];
+#pragma unroll
+      for (int m = 0; m < NJ; m++)
+        yf[m].make(col_frag(ys, LD::PP, m, 16 * mp, lane),
+                   *reinterpret_cast<const f4*>(tab->start + 32 * m + 4 * lq),
+                   *reinterpret_cast<const f4*>(tab->start + 32 * m + 16 + 4 * lq));
+#pragma unroll
+      for (int i = 0; i < RW; i++) {
+        G[i] *= dec;
+#pragma unroll
+        for (int m = 0; m < NJ; m++) G[i] = yf[m].mma(col_frag(qs, LD::RP, m, 16 * (mr + i), lane), G[i]);
+      }
+    }
+    __syncthreads();   // every tile has been read; the sums are complete
+    if (wave == 0) {
+      // suffix sums over the rows from a token on, prefix sums over the rows before it
+      double suf = 0.0, pre = 0.0, thr = 0.0;
+      if (lane < L) {
+#pragma unroll
+        for (int i = 0; i < NT; i++) suf += (double)rsum[i * 64 + lane] - (double)csum[i * 64 + lane];
+#pragma unroll
+        for (int i = 0; i < RT; i++) {
+          suf += (double)up(i, lane);
+          pre += (double)vp(i, lane);
+        }
+      }
+      for (int i = 0; i < (PT < ABW ? ABW : PT); i++) thr += (double)th[i];
+      const double si = wave_sum_incl(suf, lane), pi = wave_sum_incl(pre, lane);
+      const double v = __shfl(si, 63) - si + suf + pi - pre + thr * (double)dec;
+      const int tok = (lane * g.cinv) >> 16;
+      if (lane < nrows && tok * g.c == lane) {
+        if constexpr (PART)
+          part_da[((size_t)bi * g.s + t0 + tok) * g.h * g.npt + slice] = (float)v;
+        else if (d_da != nullptr)
+          d_da[((size_t)bi * g.s + t0 + tok) * g.h + hi] = to_t<T>((float)v);
+      }
+    }
+  }
+
+  // rows past the sequence's length are zero
+  {
+    const int z0 = max(n0 * g.CT, Vb), z1 = min(n1 * g.CT, g.s);
+    for (int u = z0 * g.c + wave; u < z1 * g.c; u += ABW) {
+      const size_t at = row0 + u;
+      for (int e = lane; e < pn && d_x != nullptr; e += 64) d_x[at * xst + (size_t)hi * g.p + p0 + e] = (T)0.0f;
+      for (int e = lane; e < g.r; e += 64) {
+        if constexpr (PART) {
+          part_q[at * pst + (size_t)slice * g.r + e] = 0.0f;
+          part_k[at * pst + (size_t)slice * g.r + e] = 0.0f;
+        } else {
+          if (d_q != nullptr) d_q[at * kst + (size_t)gi * g.r + e] = (T)0.0f;
+          if (d_k != nullptr) d_k[at * kst + (size_t)gi * g.r + e] = (T)0.0f;
+        }
+      }
+    }
+    for (int t = z0 + (int)threadIdx.x; t < z1; t += ABT) {
+      if constexpr (PART)
+        part_da[((size_t)bi * g.s + t) * g.h * g.npt + slice] = 0.0f;
+      else if (d_da != nullptr)
+        d_da[((size_t)bi * g.s + t) * g.h + hi] = (T)0.0f;
+    }
+  }
+  if (d_h0 != nullptr && seg == 0) {
+#pragma unroll
+    for (int i = 0; i < RW; i++)
+      st_state4(d_h0 + (size_t)chain * g.p * g.r, g.p, g.r, p0 + 16 * mp + ln, 16 * (mr + i) + 4 * lq, G[i]);
+  }
+}
+
+// out[row][group][w] = sum of the group's `n` consecutive slices of part[row][groups * n][w].
+template <typename T>
+__global__ __launch_bounds__(256) void k_attn_sum(const float* __restrict__ part, size_t total, int n, int w,
+                                                  T* __restrict__ out) {
+  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (size_t)gridDim.x * 256) {
+    const size_t grp = e / w;
+    const float* src = part + grp * n * w + e % w;
+    float s = 0.0f;
+    for (int i = 0; i < n; i++) s += src[(size_t)i * w];
+    out[e] = to_t<T>(s);
+  }
+}
+
+}  // namespace mom

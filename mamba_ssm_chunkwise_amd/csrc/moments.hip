@@ -19,6 +19,7 @@
 #include "kernels_reduce.h"
 #include "kernels_rot.h"
 #include "fwd4_launch.h"
+#include "host.h"
 
 using namespace mom;
 
@@ -32,18 +33,13 @@ namespace {
 
 std::atomic<int> g_last_hip{0};
 
-constexpr size_t kLdsLimit = 160 * 1024;
-constexpr long kCUs = 256;  // compute units of the part (MI355X)
-
 // ---- optional per-kernel event timing (moments_profile_*) -------------------
-enum KernelId {
-  KID_CARRY, KID_SCAN, KID_FWD, KID_REDUCE, KID_BWD, KID_DSCAN, KID_FIX, KID_ZERO, KID_PREP, KID_GSCAN, KID_GFIX,
-  KID_CSCAN, KID_ROTSEG, KID_ROTCARRY, KID_ROTAPPLY, KID_PAIR, KID_GENTRY, KID_CSUM, KID_CGRP, KID_N
-};
 const char* const kKernelNames[KID_N] = {"k_carry", "k_scan",      "k_fwd",      "k_reduce", "k_bwd",  "k_dscan",
                                          "k_fix",   "k_zero_tail", "k_prep_dm1", "k_gscan",  "k_gfix",
                                          "k_cscan", "k_rot_seg",   "k_rot_carry", "k_rot_apply",
-                                         "k_pair",  "k_gentry",    "k_cscan_sum", "k_cscan_grp"};
+                                         "k_pair",  "k_gentry",    "k_cscan_sum", "k_cscan_grp",
+                                         "k_attn_state", "k_attn_fwd", "k_attn_bwd", "k_attn_sum", "k_attn_step",
+                                         "k_qk_fwd", "k_qk_bwd", "k_qk_sum"};
 struct Prof {
   std::mutex mu;
   bool on = false;
@@ -68,29 +64,35 @@ hipEvent_t prof_event() {
   if (hipEventCreate(&e) != hipSuccess) return nullptr;
   return e;
 }
-// Brackets one launch with events when profiling is on.
-struct ProfScope {
-  int kid;
-  hipStream_t st;
-  hipEvent_t a = nullptr;
-  ProfScope(int k, hipStream_t s) : kid(k), st(s) {
-    Prof& P = prof();
-    std::lock_guard<std::mutex> g(P.mu);
-    if (P.on && (a = prof_event()) != nullptr) (void)hipEventRecord(a, st);
-  }
-  ~ProfScope() {
-    if (a == nullptr) return;
-    Prof& P = prof();
-    std::lock_guard<std::mutex> g(P.mu);
-    hipEvent_t b = prof_event();
-    if (b == nullptr) return;
-    (void)hipEventRecord(b, st);
-    P.pending.push_back({kid, a, b});
-  }
-};
 
-template <int V> using IC = std::integral_constant<int, V>;
-template <typename T> struct TT { using type = T; };
+}  // namespace
+
+namespace mom {
+
+ProfScope::ProfScope(int k, hipStream_t s) : kid(k), st(s) {
+  Prof& P = prof();
+  std::lock_guard<std::mutex> g(P.mu);
+  if (P.on && (a = prof_event()) != nullptr) (void)hipEventRecord(a, st);
+}
+
+ProfScope::~ProfScope() {
+  if (a == nullptr) return;
+  Prof& P = prof();
+  std::lock_guard<std::mutex> g(P.mu);
+  hipEvent_t b = prof_event();
+  if (b == nullptr) return;
+  (void)hipEventRecord(b, st);
+  P.pending.push_back({kid, a, b});
+}
+
+int hip_fail(hipError_t e) {
+  g_last_hip.store((int)e);
+  return MOMENTS_EHIP;
+}
+
+}  // namespace mom
+
+namespace {
 
 struct Plan {
   Geo g;
@@ -320,31 +322,6 @@ int make_plan(const moments_desc* d, Plan* P) {
   }
   return MOMENTS_OK;
 }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
-
-int hip_fail(hipError_t e) {
-  g_last_hip.store((int)e);
-  return MOMENTS_EHIP;
-}
-
-template <typename K>
-int set_lds(K kernel, size_t bytes) {
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  return e == hipSuccess ? 0 : hip_fail(e);
-}
-
-int check_launch() {
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? 0 : hip_fail(e);
-}
-
-#define MOM_TRY(x)          \
-  do {                      \
-    const int _rc = (x);    \
-    if (_rc != 0) return _rc; \
-  } while (0)
 
 // The carry walk's group forms with `grid` workgroups: one staging buffer when
 // that lets two workgroups share a CU where two double-buffered ones would not
@@ -700,6 +677,10 @@ int run_bwd(const Plan& P0, const void* xhat, const void* bhat, const void* da, 
   return 0;
 }
 
+}  // namespace
+
+namespace mom {
+
 // Debug finiteness check (the pages' san() on the outputs), on when the
 // environment variable MOMENTS_CHECK_FINITE is set to anything but "" or "0".
 // It waits for the stream and returns MOMENTS_ENONFINITE if any listed output
@@ -708,12 +689,6 @@ bool check_finite_on() {
   const char* e = getenv("MOMENTS_CHECK_FINITE");
   return e != nullptr && e[0] != 0 && !(e[0] == '0' && e[1] == 0);
 }
-
-struct OutSpan {
-  const void* p;
-  size_t n;
-  bool f32;
-};
 
 int check_finite(const OutSpan* outs, int nout, unsigned char* flag_mem, hipStream_t st) {
   int* flag = (int*)flag_mem;
@@ -736,6 +711,10 @@ int check_finite(const OutSpan* outs, int nout, unsigned char* flag_mem, hipStre
   if (e != hipSuccess) return hip_fail(e);
   return host ? MOMENTS_ENONFINITE : 0;
 }
+
+}  // namespace mom
+
+namespace {
 
 // Calls f(TT<T>, IC<NT>, IC<ROT>, IC<CK>) for the compiled variant matching the plan.
 template <class F>

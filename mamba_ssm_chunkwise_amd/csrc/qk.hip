@@ -1,0 +1,214 @@
+// C ABI of the norms of queries and keys with the position rotation: validation,
+// planning, dispatch. The operation and its conventions are stated in include/moments.h.
+#include "moments.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "host.h"
+#include "kernels_attn_bwd.h"
+#include "kernels_qk.h"
+
+using namespace mom;
+
+namespace {
+
+struct QkPlan {
+  QkGeo g;
+  bool bf, empty;
+  int LPR, C, NT;       // lanes a row; padded channels; threads of the backward
+  size_t lds;           // of the backward
+  size_t part_w, part_b, part_rot, ws, flag;
+};
+
+int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
+  if (d == nullptr) return MOMENTS_EINVAL;
+  if (d->b < 0 || d->s < 0 || d->h < 0 || d->c < 1 || d->g < 1 || d->r < 1 || d->h % d->g != 0) return MOMENTS_EINVAL;
+  if (d->dtype != MOMENTS_F32 && d->dtype != MOMENTS_BF16) return MOMENTS_EINVAL;
+  if (!(d->eps >= 0.0f)) return MOMENTS_EINVAL;
+  int A = 0, J = 0;
+  switch (d->rot_kind) {
+    case MOMENTS_ROT_NONE:
+      break;
+    case MOMENTS_ROT_COMPLEX_PAIRWISE:
+    case MOMENTS_ROT_COMPLEX_HALF:
+      if (d->rope_dim < 2 || d->rope_dim % 2 != 0 || d->rope_dim > d->r) return MOMENTS_EINVAL;
+      if (d->rot_kind == MOMENTS_ROT_COMPLEX_HALF && d->r % 2 != 0) return MOMENTS_EINVAL;
+      A = (int)(d->rope_dim / 2);
+      break;
+    case MOMENTS_ROT_QUATERNION:
+      if (d->quat_blocks < 1 || 4 * d->quat_blocks > d->r) return MOMENTS_EINVAL;
+      J = (int)d->quat_blocks;
+      break;
+    default:
+      return MOMENTS_EINVAL;
+  }
+  if (d->rot_kind != MOMENTS_ROT_NONE && d->rot_h != 1 && d->rot_h != d->h) return MOMENTS_EINVAL;
+  const int64_t row = d->c * d->g * d->r;
+  const int64_t qs = d->q_stride == 0 ? row : d->q_stride, ks = d->k_stride == 0 ? row : d->k_stride;
+  if (qs < row || ks < row) return MOMENTS_EINVAL;
+  if (d->r > 128 || d->c > 4 || d->g > 65535 || d->h / d->g > 128 || d->s > (int64_t)1 << 28 ||
+      d->b > (int64_t)1 << 24 || d->b * d->s > (int64_t)1 << 30)
+    return MOMENTS_ENOTSUP;
+  P->empty = d->b == 0 || d->h == 0;
+  P->bf = d->dtype == MOMENTS_BF16;
+  const int tsz = P->bf ? 2 : 4;
+  QkGeo& g = P->g;
+  g = QkGeo{};
+  g.b = (int)d->b; g.s = (int)d->s; g.c = (int)d->c; g.h = (int)d->h; g.g = (int)d->g; g.r = (int)d->r;
+  g.qs = (size_t)qs; g.ks = (size_t)ks;
+  g.rot_h = (int)d->rot_h; g.A = A; g.J = J; g.RW = J > 0 ? 4 * J : A;
+  g.eps = d->eps;
+  g.vin = g.r % 8 == 0 && qs * tsz % 16 == 0 && ks * tsz % 16 == 0;
+  g.vio = g.r % 8 == 0;
+  g.vrot = A % 4 == 0;
+  P->LPR = g.r <= 64 ? 8 : 16;
+  P->C = g.c <= 1 ? 1 : g.c <= 2 ? 2 : 4;
+  if (P->empty) return MOMENTS_OK;
+  g.hpg = g.h / g.g;
+  const int rpw = 64 / P->LPR;
+  g.HPP = 1;
+  while (g.HPP < g.hpg && g.HPP < rpw) g.HPP *= 2;
+  g.HL = (g.hpg + g.HPP - 1) / g.HPP;
+  // sums for each head in LDS when a head slot serves several heads: 64 bytes a thread and
+  // head, so fewer threads where there are many
+  P->NT = QKT;
+  while (P->NT > 64 && (size_t)(g.HL + 1) * 64 * P->NT > kLdsLimit) P->NT /= 2;
+  P->lds = (size_t)(g.HL > 1 ? g.HL + 1 : 1) * 64 * P->NT;
+  const int64_t per = (int64_t)(P->NT / 64) * (rpw / g.HPP);   // tokens a workgroup has at once
+  const int64_t most = std::max<int64_t>(1, ((int64_t)g.b * g.s + per - 1) / per);
+  g.nblk = (int)std::min<int64_t>(most, std::max<int64_t>(1, 2048 / g.g));
+  size_t o = 0;
+  P->part_w = o; o = align256(o + (size_t)2 * g.nblk * g.g * g.r * 4);
+  P->part_b = o; o = align256(o + (size_t)2 * g.nblk * g.h * g.r * 4);
+  P->part_rot = o;
+  if (g.RW > 0 && g.rot_h == 1 && g.h > 1) o = align256(o + (size_t)g.b * g.s * g.g * g.RW * 4);
+  P->flag = o;
+  P->ws = o + 256;
+  return MOMENTS_OK;
+}
+
+// Calls f(TT<T>, IC<LPR>, IC<ROT>, IC<C>) for the compiled variant of the plan.
+template <class F>
+int with_qk(const QkPlan& P, int rot_kind, F&& f) {
+  auto by_c = [&](auto tt, auto lpr, auto rot) -> int {
+    switch (P.C) {
+      case 1: return f(tt, lpr, rot, IC<1>{});
+      case 2: return f(tt, lpr, rot, IC<2>{});
+    }
+    return f(tt, lpr, rot, IC<4>{});
+  };
+  auto by_rot = [&](auto tt, auto lpr) -> int {
+    switch (rot_kind) {
+      case MOMENTS_ROT_NONE: return by_c(tt, lpr, IC<0>{});
+      case MOMENTS_ROT_COMPLEX_PAIRWISE: return by_c(tt, lpr, IC<1>{});
+      case MOMENTS_ROT_COMPLEX_HALF: return by_c(tt, lpr, IC<2>{});
+    }
+    return by_c(tt, lpr, IC<3>{});
+  };
+  if (P.bf) return P.LPR == 8 ? by_rot(TT<bf16>{}, IC<8>{}) : by_rot(TT<bf16>{}, IC<16>{});
+  return P.LPR == 8 ? by_rot(TT<float>{}, IC<8>{}) : by_rot(TT<float>{}, IC<16>{});
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t moments_qk_workspace_size(const moments_qk_desc* desc) {
+  QkPlan P;
+  const int rc = make_qk_plan(desc, &P);
+  if (rc != 0) return rc;
+  return P.empty ? 0 : (int64_t)P.ws;
+}
+
+int moments_qk_fwd(const moments_qk_desc* desc, const void* q, const void* k, const float* wq, const float* wk,
+                   const float* bq, const float* bk, const void* rot, void* qhat, void* khat, void* stream) {
+  QkPlan P;
+  MOM_TRY(make_qk_plan(desc, &P));
+  const QkGeo& g = P.g;
+  if (P.empty || g.s == 0) return 0;
+  if (!q || !k || !wq || !wk || !qhat || !khat) return MOMENTS_EINVAL;
+  if ((desc->rot_kind == MOMENTS_ROT_NONE) != (rot == nullptr)) return MOMENTS_EINVAL;
+  const void* ptrs[] = {q, k, wq, wk, bq, bk, rot, qhat, khat};
+  for (const void* p : ptrs)
+    if (p != nullptr && !aligned16(p)) return MOMENTS_EINVAL;
+  hipStream_t st = (hipStream_t)stream;
+  return with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc) -> int {
+    using T = typename decltype(tt)::type;
+    constexpr int LPR = decltype(lpr)::value, ROT = decltype(rk)::value, C = decltype(cc)::value;
+    const int64_t per = QKT / 64 * (64 / LPR / g.HPP);
+    const int64_t nb = ((int64_t)g.b * g.s + per - 1) / per;
+    ProfScope ps(KID_QK_FWD, st);
+    hipLaunchKernelGGL((k_qk_fwd<T, LPR, ROT, C>), dim3((unsigned)nb, (unsigned)g.g), dim3(QKT), 0, st, g,
+                       (const T*)q, (const T*)k, wq, wk, bq, bk, (const T*)rot, (T*)qhat, (T*)khat);
+    return check_launch();
+  });
+}
+
+int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, const float* wq, const float* wk,
+                   const float* bq, const float* bk, const void* rot, const void* d_qhat, const void* d_khat,
+                   void* d_q, void* d_k, float* d_wq, float* d_wk, float* d_bq, float* d_bk, void* d_rot,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  QkPlan P;
+  MOM_TRY(make_qk_plan(desc, &P));
+  const QkGeo& g = P.g;
+  if (P.empty) return 0;
+  if (g.s > 0 && (!q || !k || !wq || !wk || !d_qhat || !d_khat)) return MOMENTS_EINVAL;
+  if (g.s > 0 && (desc->rot_kind == MOMENTS_ROT_NONE) != (rot == nullptr)) return MOMENTS_EINVAL;
+  if (desc->rot_kind == MOMENTS_ROT_NONE && d_rot != nullptr) return MOMENTS_EINVAL;
+  if ((bq == nullptr && d_bq != nullptr) || (bk == nullptr && d_bk != nullptr)) return MOMENTS_EINVAL;
+  const void* ptrs[] = {q, k, wq, wk, bq, bk, rot, d_qhat, d_khat, d_q, d_k, d_wq, d_wk, d_bq, d_bk, d_rot, workspace};
+  for (const void* p : ptrs)
+    if (p != nullptr && !aligned16(p)) return MOMENTS_EINVAL;
+  if (workspace == nullptr || workspace_bytes < P.ws) return MOMENTS_EWORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  unsigned char* ws = (unsigned char*)workspace;
+  const bool rot1 = g.RW > 0 && g.rot_h == 1 && g.h > 1;
+  float* pw = d_wq || d_wk ? (float*)(ws + P.part_w) : nullptr;
+  float* pb = d_bq || d_bk ? (float*)(ws + P.part_b) : nullptr;
+  float* pr = rot1 && d_rot ? (float*)(ws + P.part_rot) : nullptr;
+  MOM_TRY(with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc) -> int {
+    using T = typename decltype(tt)::type;
+    constexpr int LPR = decltype(lpr)::value, ROT = decltype(rk)::value, C = decltype(cc)::value;
+    auto go = [&](auto ldsb) -> int {
+      constexpr bool LB = decltype(ldsb)::value != 0;
+      MOM_TRY(set_lds(k_qk_bwd<T, LPR, ROT, C, LB>, P.lds));
+      ProfScope ps(KID_QK_BWD, st);
+      hipLaunchKernelGGL((k_qk_bwd<T, LPR, ROT, C, LB>), dim3((unsigned)g.nblk, (unsigned)g.g), dim3(P.NT), P.lds, st,
+                         g, (const T*)q, (const T*)k, wq, wk, bq, bk, (const T*)rot, (const T*)d_qhat,
+                         (const T*)d_khat, (T*)d_q, (T*)d_k, (T*)(rot1 ? nullptr : d_rot), pr, pw, pb);
+      return check_launch();
+    };
+    MOM_TRY(g.HL > 1 ? go(IC<1>{}) : go(IC<0>{}));
+    if (pr != nullptr && g.s > 0) {
+      const size_t total = (size_t)g.b * g.s * g.RW;
+      ProfScope ps(KID_QK_SUM, st);
+      hipLaunchKernelGGL((k_attn_sum<T>), dim3((unsigned)std::min<size_t>((total + 255) / 256, 16384)), dim3(256), 0,
+                         st, pr, total, g.g, g.RW, (T*)d_rot);
+      MOM_TRY(check_launch());
+    }
+    return 0;
+  }));
+  if (pw != nullptr) {
+    ProfScope ps(KID_QK_SUM, st);
+    hipLaunchKernelGGL(k_qk_sum, dim3((g.r + 63) / 64, 2), dim3(256), 0, st, pw, g.nblk * g.g, g.r, d_wq, d_wk);
+    MOM_TRY(check_launch());
+  }
+  if (pb != nullptr) {
+    ProfScope ps(KID_QK_SUM, st);
+    hipLaunchKernelGGL(k_qk_sum, dim3((unsigned)(((int64_t)g.h * g.r + 63) / 64), 2), dim3(256), 0, st, pb, g.nblk,
+                       g.h * g.r, d_bq, d_bk);
+    MOM_TRY(check_launch());
+  }
+  if (check_finite_on()) {
+    const size_t raw = (size_t)g.b * g.s * g.c * g.g * g.r;
+    const OutSpan outs[] = {{d_q, raw, !P.bf}, {d_k, raw, !P.bf}, {d_rot, (size_t)g.b * g.s * g.rot_h * g.RW, !P.bf},
+                            {d_wq, (size_t)g.r, true}, {d_wk, (size_t)g.r, true},
+                            {d_bq, (size_t)g.h * g.r, true}, {d_bk, (size_t)g.h * g.r, true}};
+    return check_finite(outs, 7, ws + P.flag, st);
+  }
+  return 0;
+}
+
+}  // extern "C"
