@@ -28,7 +28,6 @@ struct QkGeo {
   size_t qs, ks;    // elements between tokens of q and k
   int rot_h, RW, A, J;
   int hpg, HPP, HL; // heads per group; head slots of a wave; times they are filled
-  int vin, vio, vrot;  // 16-byte pieces: raw rows, hat rows, angles
   int nblk;         // workgroups per group (backward)
   float eps;
 };
@@ -90,61 +89,123 @@ __device__ __forceinline__ void st8(T* row, int l, int r, bool vec, const float 
   }
 }
 
-// Sine and cosine, to fp32 rounding for |x| < 1e5: the nearest multiple of pi/2 is
-// taken off with pi/2 in three floats, and the rest, at most pi/4, goes through the
-// Taylor series to x^9 and x^10 (the next terms are below 2^-28). Larger angles go
-// to the library's functions.
+// A lane's eight values of a row, in flight: as loaded from memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16> {
+  uint4 v;
+  template <bool HALF>
+  __device__ __forceinline__ void load(const bf16* row, int l, int r, bool vec) {
+    if (vec) {
+      v = make_uint4(0, 0, 0, 0);
+      if (HALF ? 4 * l >= (r >> 1) : 8 * l >= r) return;
+      if constexpr (HALF) {
+        const uint2 a = *reinterpret_cast<const uint2*>(row + 4 * l);
+        const uint2 b = *reinterpret_cast<const uint2*>(row + (r >> 1) + 4 * l);
+        v = make_uint4(a.x, a.y, b.x, b.y);
+      } else {
+        v = *reinterpret_cast<const uint4*>(row + 8 * l);
+      }
+    } else {
+      bf16 e[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) e[i] = qk_has<HALF>(l, i, r) ? row[qk_col<HALF>(l, i, r)] : (bf16)0.0f;
+      v = __builtin_bit_cast(uint4, e);
+    }
+  }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      o[2 * i] = bf16_lo(w[i]);
+      o[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float v[8];
+  template <bool HALF>
+  __device__ __forceinline__ void load(const float* row, int l, int r, bool vec) { ld8<float, HALF>(row, l, r, vec, v); }
+  __device__ __forceinline__ void zero() {
+    for (int i = 0; i < 8; i++) v[i] = 0.0f;
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    for (int i = 0; i < 8; i++) o[i] = v[i];
+  }
+};
+
+// Sine and cosine, to fp32 rounding: the nearest multiple of pi/2 is taken off (in three
+// floats below 1e5, else in doubles, which reach to 2^50), and the rest, at most pi/4, goes
+// through the Taylor series to x^9 and x^10 (the next terms are below 2^-28). Beyond
+// 2^50 neighbouring floats are 2^27 radians apart; there the rest is taken as zero.
 __device__ __forceinline__ void sincos_f(float x, float& s, float& c) {
+  constexpr double kPi2 = 1.5707963267948966, kPi2Lo = 6.123233995736766e-17;   // pi/2: double and remainder
+  float t;
+  int n;
   if (fabsf(x) < 1e5f) {
     const float k = rintf(x * 0.636619772367581343f);
-    constexpr double kPi2 = 1.5707963267948966;
-    constexpr float P1 = (float)kPi2, P2 = (float)(kPi2 - (double)P1);
-    constexpr float P3 = 6.123233995736766e-17f;   // pi/2 beyond a double
-    float t = fmaf(-k, P1, x);
-    t = fmaf(-k, P2, t);
-    t = fmaf(-k, P3, t);
-    const float t2 = t * t;
-    float a = fmaf(t2, 2.75573192e-6f, -1.98412698e-4f);
-    a = fmaf(t2, a, 8.33333333e-3f);
-    a = fmaf(t2, a, -1.66666667e-1f);
-    a = fmaf(t2 * t, a, t);
-    float b = fmaf(t2, -2.75573192e-7f, 2.48015873e-5f);
-    b = fmaf(t2, b, -1.38888889e-3f);
-    b = fmaf(t2, b, 4.16666667e-2f);
-    b = fmaf(t2, b, -0.5f);
-    b = fmaf(t2, b, 1.0f);
-    const int n = (int)k;
-    const float u = (n & 1) ? b : a, v = (n & 1) ? a : b;
-    s = (n & 2) ? -u : u;
-    c = ((n + 1) & 2) ? -v : v;
+    constexpr float P1 = (float)kPi2, P2 = (float)(kPi2 - (double)P1), P3 = (float)kPi2Lo;
+    t = fmaf(-k, P3, fmaf(-k, P2, fmaf(-k, P1, x)));
+    n = (int)k;
   } else {
-    sincosf(x, &s, &c);
+    const double k = rint((double)x * 0.6366197723675814);
+    const double d = fma(-k, kPi2Lo, fma(-k, kPi2, (double)x));
+    t = fabs(d) <= 1.0 ? (float)d : x - x;   // zero; NaN for infinities and NaN
+    n = (int)(k - 4.0 * floor(0.25 * k));
   }
+  const float t2 = t * t;
+  float a = fmaf(t2, 2.75573192e-6f, -1.98412698e-4f);
+  a = fmaf(t2, a, 8.33333333e-3f);
+  a = fmaf(t2, a, -1.66666667e-1f);
+  a = fmaf(t2 * t, a, t);
+  float b = fmaf(t2, -2.75573192e-7f, 2.48015873e-5f);
+  b = fmaf(t2, b, -1.38888889e-3f);
+  b = fmaf(t2, b, 4.16666667e-2f);
+  b = fmaf(t2, b, -0.5f);
+  b = fmaf(t2, b, 1.0f);
+  const float u = (n & 1) ? b : a, v = (n & 1) ? a : b;
+  s = (n & 2) ? -u : u;
+  c = ((n + 1) & 2) ? -v : v;
 }
 
 // The rotation of one (token, head) as a lane needs it: ROT 1, 2: cos and sin of its
 // four angles; ROT 3: its two quaternions. Blocks past the rotated width are identity.
-template <typename T, int ROT>
+template <int ROT>
 struct QkRot {
   float v[ROT == 0 ? 1 : 8];
+  template <bool VEC, typename T>
   __device__ __forceinline__ void load(const T* row, int l, const QkGeo& g) {
     if constexpr (ROT == 1 || ROT == 2) {
-      float a[4];
-      if (g.vrot) {
+      if (VEC) {
         f4 t = {0.0f, 0.0f, 0.0f, 0.0f};
         if (4 * l < g.A) t = ld4(row + 4 * l);
-        for (int i = 0; i < 4; i++) a[i] = t[i];
+        for (int i = 0; i < 4; i++) v[i] = t[i];
       } else {
-        for (int i = 0; i < 4; i++) a[i] = 4 * l + i < g.A ? to_f(row[4 * l + i]) : 0.0f;
+        for (int i = 0; i < 4; i++) v[i] = 4 * l + i < g.A ? to_f(row[4 * l + i]) : 0.0f;
       }
-#pragma unroll
-      for (int i = 0; i < 4; i++) sincos_f(a[i], v[4 + i], v[i]);
     } else if constexpr (ROT == 3) {
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         f4 t = {1.0f, 0.0f, 0.0f, 0.0f};
         if (2 * l + i < g.J) t = ld4(row + 4 * (2 * l + i));
         for (int e = 0; e < 4; e++) v[4 * i + e] = t[e];
+      }
+    }
+  }
+  // Angles to their cosines and sines; lanes past the rotated width keep the identity.
+  __device__ __forceinline__ void make(int l, const QkGeo& g) {
+    if constexpr (ROT == 1 || ROT == 2) {
+      if (4 * l < g.A) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) sincos_f(v[i], v[4 + i], v[i]);
+      } else {
+        for (int i = 0; i < 4; i++) {
+          v[i] = 1.0f;
+          v[4 + i] = 0.0f;
+        }
       }
     }
   }
@@ -197,83 +258,155 @@ __device__ __forceinline__ float slot_sum(float v, int n) {
   return v;
 }
 
-// One row, normed: n = x rstd.
-template <typename T, bool HALF, int LPR>
-__device__ __forceinline__ float ld_norm(const T* row, int l, const QkGeo& g, bool vec, float (&n)[8]) {
-  ld8<T, HALF>(row, l, g.r, vec, n);
-  float ss = 0.0f;
-  for (int e = 0; e < 8; e++) ss += n[e] * n[e];
-  const float rstd = 1.0f / sqrtf(row_sum<LPR>(ss) / (float)g.r + g.eps);
-  for (int e = 0; e < 8; e++) n[e] *= rstd;
-  return rstd;
-}
-
-// C: channels padded to 1, 2 or 4.
-template <typename T, int LPR, int ROT, int C>
+// C: channels padded to 1, 2 or 4. HB: heads per row slot whose bias stays in registers
+// (0: HL is larger, it is read again for each token). VEC: rows, their strides and the
+// angles are whole 16-byte pieces (8 bytes, bf16 angles); others go one element at a time.
+// A wave takes tokens a grid apart, with the next one's rows already in flight.
+template <typename T, int LPR, int ROT, int C, int HB, bool VEC>
 __global__ __launch_bounds__(QKT) void k_qk_fwd(QkGeo g, const T* __restrict__ q, const T* __restrict__ k,
                                                 const float* __restrict__ wq, const float* __restrict__ wk,
                                                 const float* __restrict__ bq, const float* __restrict__ bk,
                                                 const T* __restrict__ rot, T* __restrict__ qhat,
                                                 T* __restrict__ khat) {
   constexpr bool HALF = ROT == 2;
-  constexpr int RPW = 64 / LPR;
+  constexpr int RPW = 64 / LPR, NB = HB > 0 ? HB : 1;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPR, slot = lane / LPR;
-  const int gi = blockIdx.y, TPW = RPW / g.HPP, hs = slot % g.HPP;
-  const size_t tok = ((size_t)blockIdx.x * (QKT / 64) + wave) * TPW + slot / g.HPP;
-  // whole waves of tokens past the end leave; single slots stay for the sums over lanes
-  const bool live = tok < (size_t)g.b * g.s;
-  float n[2][C][8], w[2][8];
+  const int gi = blockIdx.y, TPW = RPW / g.HPP, hs = slot % g.HPP, ts = slot / g.HPP;
+  const size_t ntok = (size_t)g.b * g.s, step = (size_t)gridDim.x * (QKT / 64) * TPW;
+  float w[2][8], bv[2][NB][8];
 #pragma unroll
   for (int x = 0; x < 2; x++) {
-    ld8<float, HALF>(x ? wk : wq, l, g.r, false, w[x]);
+    ld8<float, HALF>(x ? wk : wq, l, g.r, VEC, w[x]);
 #pragma unroll
-    for (int c = 0; c < C; c++) {
-      const T* row = (x ? k : q) + tok * (x ? g.ks : g.qs) + ((size_t)c * g.g + gi) * g.r;
-      if (live && c < g.c) {
-        ld8<T, HALF>(row, l, g.r, g.vin, n[x][c]);
-      } else {
-        for (int e = 0; e < 8; e++) n[x][c][e] = 0.0f;
-      }
+    for (int i = 0; i < NB; i++) {
+      const int hg = i * g.HPP + hs;
+      const float* bias = x ? bk : bq;
+      for (int e = 0; e < 8; e++) bv[x][i][e] = 0.0f;
+      if (HB > 0 && bias != nullptr && hg < g.hpg)
+        ld8<float, HALF>(bias + (size_t)(gi * g.hpg + hg) * g.r, l, g.r, VEC, bv[x][i]);
     }
   }
+  Raw8<T> raw[2][C];
+  QkRot<ROT> R0[NB];
+  auto fetch = [&](size_t tok) {
+    const bool live = tok < ntok;
 #pragma unroll
-  for (int x = 0; x < 2; x++)
+    for (int x = 0; x < 2; x++)
 #pragma unroll
-    for (int c = 0; c < C; c++) {
-      float ss = 0.0f;
-      for (int e = 0; e < 8; e++) ss += n[x][c][e] * n[x][c][e];
-      const float rstd = 1.0f / sqrtf(row_sum<LPR>(ss) / (float)g.r + g.eps);
-      for (int e = 0; e < 8; e++) n[x][c][e] *= rstd * w[x][e];
+      for (int c = 0; c < C; c++) {
+        raw[x][c].zero();
+        if (live && c < g.c)
+          raw[x][c].template load<HALF>((x ? k : q) + tok * (x ? g.ks : g.qs) + ((size_t)c * g.g + gi) * g.r, l, g.r,
+                                        VEC);
+      }
+    if constexpr (ROT != 0 && HB > 0) {
+#pragma unroll
+      for (int i = 0; i < NB; i++) {
+        const int hg = i * g.HPP + hs;
+        if (live && hg < g.hpg)
+          R0[i].template load<VEC>(rot + (tok * g.rot_h + (g.rot_h > 1 ? gi * g.hpg + hg : 0)) * g.RW, l, g);
+      }
     }
-  if (!live) return;
-  for (int i = 0; i < g.HL; i++) {
-    const int hg = i * g.HPP + hs;
-    if (hg >= g.hpg) return;
-    const int hi = gi * g.hpg + hg;
-    QkRot<T, ROT> R;
-    if constexpr (ROT != 0) R.load(rot + (tok * g.rot_h + (g.rot_h > 1 ? hi : 0)) * g.RW, l, g);
+  };
+  size_t t0 = ((size_t)blockIdx.x * (QKT / 64) + wave) * TPW;
+  if (t0 < ntok) fetch(t0 + ts);
+  for (; t0 < ntok; t0 += step) {
+    const size_t tok = t0 + ts;
+    float n[2][C][8];
+    QkRot<ROT> R[NB];
 #pragma unroll
-    for (int x = 0; x < 2; x++) {
-      const float* bias = x ? bk : bq;
-      float bv[8];
-      for (int e = 0; e < 8; e++) bv[e] = 0.0f;
-      if (bias != nullptr) ld8<float, HALF>(bias + (size_t)hi * g.r, l, g.r, false, bv);
+    for (int x = 0; x < 2; x++)
+#pragma unroll
+      for (int c = 0; c < C; c++) raw[x][c].get(n[x][c]);
+#pragma unroll
+    for (int i = 0; i < NB; i++) R[i] = R0[i];
+    if (t0 + step < ntok) fetch(tok + step);
+#pragma unroll
+    for (int x = 0; x < 2; x++)
 #pragma unroll
       for (int c = 0; c < C; c++) {
         if (c >= g.c) break;
-        float u[8];
-        for (int e = 0; e < 8; e++) u[e] = n[x][c][e] + bv[e];
-        R.template turn<true>(u);
-        st8<T, HALF>((x ? khat : qhat) + ((tok * g.c + c) * g.h + hi) * g.r, l, g.r, g.vio, u);
+        float ss = 0.0f;
+        for (int e = 0; e < 8; e++) ss += n[x][c][e] * n[x][c][e];
+        const float rstd = 1.0f / sqrtf(row_sum<LPR>(ss) / (float)g.r + g.eps);
+        for (int e = 0; e < 8; e++) n[x][c][e] *= rstd * w[x][e];
+      }
+    auto head = [&](int hg, QkRot<ROT>& Rh, auto bias) {
+      const int hi = gi * g.hpg + hg;
+      Rh.make(l, g);
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        float b8[8];
+        bias(x, hi, b8);
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+          if (c >= g.c) break;
+          float u[8];
+          for (int e = 0; e < 8; e++) u[e] = n[x][c][e] + b8[e];
+          Rh.template turn<true>(u);
+          st8<T, HALF>((x ? khat : qhat) + ((tok * g.c + c) * g.h + hi) * g.r, l, g.r, VEC, u);
+        }
+      }
+    };
+    if (tok >= ntok) continue;
+    if constexpr (HB > 0) {
+#pragma unroll
+      for (int i = 0; i < NB; i++)
+        if (i * g.HPP + hs < g.hpg)
+          head(i * g.HPP + hs, R[i], [&](int x, int, float (&b8)[8]) {
+            for (int e = 0; e < 8; e++) b8[e] = bv[x][i][e];
+          });
+    } else {
+      for (int i = 0; i < g.HL; i++) {
+        const int hg = i * g.HPP + hs;
+        if (hg >= g.hpg) break;
+        if constexpr (ROT != 0)
+          R[0].template load<VEC>(rot + (tok * g.rot_h + (g.rot_h > 1 ? gi * g.hpg + hg : 0)) * g.RW, l, g);
+        head(hg, R[0], [&](int x, int hi, float (&b8)[8]) {
+          for (int e = 0; e < 8; e++) b8[e] = 0.0f;
+          const float* bias = x ? bk : bq;
+          if (bias != nullptr) ld8<float, HALF>(bias + (size_t)hi * g.r, l, g.r, VEC, b8);
+        });
       }
     }
   }
 }
 
-// LDSB: the sums of du for each head stand in LDS (HL > 1), one place per thread and
-// head; otherwise in registers. part_b [2][nblk][h][r], part_w [2][nblk][g][r]; part_rot
-// [b,s,g][RW] where all heads share a rotation (d_rot is then their sum over g).
-template <typename T, int LPR, int ROT, int C, bool LDSB>
+// One row's share of the gradients: d, the cotangent of its hat, becomes du and is added
+// to sb (the head's) and ds (the group's); the rotation's goes to dr.
+template <int ROT>
+__device__ __forceinline__ void qk_row_grad(const QkRot<ROT>& R, const float (&n)[8], const float (&w)[8],
+                                            const float (&b)[8], float (&d)[8], float (&dr)[8], float (&sb)[8],
+                                            float (&ds)[8]) {
+  if constexpr (ROT == 3) {
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      f4 u;
+      for (int e = 0; e < 4; e++) u[e] = n[4 * j + e] * w[4 * j + e] + b[4 * j + e];
+      const f4 z = qmul(u, qconj(f4{d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]}));
+      for (int e = 0; e < 4; e++) dr[4 * j + e] += z[e];
+    }
+  }
+  R.template turn<false>(d);
+  if constexpr (ROT == 1 || ROT == 2) {
+    // in the frame before the turn: u_x du_y - u_y du_x (turning both keeps it)
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int ex = ROT == 1 ? 2 * j : j, ey = ROT == 1 ? 2 * j + 1 : j + 4;
+      dr[j] += (n[ex] * w[ex] + b[ex]) * d[ey] - (n[ey] * w[ey] + b[ey]) * d[ex];
+    }
+  }
+  for (int e = 0; e < 8; e++) {
+    sb[e] += d[e];
+    ds[e] += d[e];
+  }
+}
+
+// HB: heads per row slot (1, 2) whose sums of du stand in registers; 0: any number, they
+// stand in LDS, one place per thread and head. part_b [2][nblk][h][r], part_w
+// [2][nblk][g][r]; part_rot [b,s,g][RW] where all heads share a rotation (d_rot is then
+// their sum over g).
+template <typename T, int LPR, int ROT, int C, int HB, bool VEC>
 __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q, const T* __restrict__ k,
                                                 const float* __restrict__ wq, const float* __restrict__ wk,
                                                 const float* __restrict__ bq, const float* __restrict__ bk,
@@ -281,209 +414,279 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
                                                 const T* __restrict__ dkh, T* __restrict__ d_q, T* __restrict__ d_k,
                                                 T* __restrict__ d_rot, float* __restrict__ part_rot,
                                                 float* __restrict__ part_w, float* __restrict__ part_b) {
-  constexpr bool HALF = ROT == 2;
-  constexpr int RPW = 64 / LPR;
+  constexpr bool HALF = ROT == 2, LDSB = HB == 0;
+  constexpr int RPW = 64 / LPR, NB = HB > 0 ? HB : 1, NR = ROT == 3 ? 8 : 4;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   float* acc = reinterpret_cast<float*>(lds);   // LDSB: [HL][16][threads]; then the block's sums
   const int NT = blockDim.x, NWV = NT / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPR, slot = lane / LPR;
   const int gi = blockIdx.y, TPW = RPW / g.HPP, hs = slot % g.HPP, ts = slot / g.HPP;
   const size_t ntok = (size_t)g.b * g.s;
-  float w[2][8], bv[2][8], dw[2][8], db[2][8];
+  float w[2][8], dw[2][8], db[2][NB][8];
 #pragma unroll
   for (int x = 0; x < 2; x++) {
-    ld8<float, HALF>(x ? wk : wq, l, g.r, false, w[x]);
-    for (int e = 0; e < 8; e++) dw[x][e] = db[x][e] = bv[x][e] = 0.0f;
+    ld8<float, HALF>(x ? wk : wq, l, g.r, VEC, w[x]);
+    for (int e = 0; e < 8; e++) dw[x][e] = 0.0f;
+    for (int i = 0; i < NB; i++)
+      for (int e = 0; e < 8; e++) db[x][i][e] = 0.0f;
   }
   if constexpr (LDSB) {
     for (int i = 0; i < g.HL * 16; i++) acc[i * NT + threadIdx.x] = 0.0f;
   }
+  auto raw_row = [&](int x, int c, size_t tok) {
+    return (x ? k : q) + tok * (x ? g.ks : g.qs) + ((size_t)c * g.g + gi) * g.r;
+  };
+  auto hat_row = [&](int x, int c, size_t tok, int hi) { return (x ? dkh : dqh) + ((tok * g.c + c) * g.h + hi) * g.r; };
+  auto rot_row = [&](size_t tok, int hi) { return (tok * g.rot_h + (g.rot_h > 1 ? hi : 0)) * g.RW; };
+  auto ld_bias = [&](int x, int hi, float (&b8)[8]) {
+    const float* bias = x ? bk : bq;
+    for (int e = 0; e < 8; e++) b8[e] = 0.0f;
+    if (bias != nullptr) ld8<float, HALF>(bias + (size_t)hi * g.r, l, g.r, VEC, b8);
+  };
+  auto norm = [&](float (&n)[8]) {
+    float ss = 0.0f;
+    for (int e = 0; e < 8; e++) ss += n[e] * n[e];
+    const float rstd = 1.0f / sqrtf(row_sum<LPR>(ss) / (float)g.r + g.eps);
+    for (int e = 0; e < 8; e++) n[e] *= rstd;
+    return rstd;
+  };
+  // the group's raw row, from the sum of du over its heads
+  auto finish = [&](int x, int c, size_t tok, bool live, const float (&n)[8], float rstd, float (&ds)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      const float v = slot_sum<LPR>(ds[e], g.HPP);
+      dw[x][e] += v * n[e];
+      ds[e] = v * w[x][e];
+      m += ds[e] * n[e];
+    }
+    m = row_sum<LPR>(m) / (float)g.r;
+    T* out = x ? d_k : d_q;
+    if (live && hs == 0 && out != nullptr) {
+      float o[8];
+      for (int e = 0; e < 8; e++) o[e] = (ds[e] - n[e] * m) * rstd;
+      st8<T, HALF>(out + ((tok * g.c + c) * g.g + gi) * g.r, l, g.r, VEC, o);
+    }
+  };
+  // the rotation's: one head's own, or the group's share of the one for all heads
+  auto st_rot = [&](size_t tok, int hi, const float (&dr)[8]) {
+    if (d_rot == nullptr) return;
+    T* o = d_rot + rot_row(tok, hi);
+    if constexpr (ROT == 3) {
+      for (int j = 0; j < 2; j++)
+        if (2 * l + j < g.J) st4(o + 4 * (2 * l + j), f4{dr[4 * j], dr[4 * j + 1], dr[4 * j + 2], dr[4 * j + 3]});
+    } else if (VEC) {
+      if (4 * l < g.A) st4(o + 4 * l, f4{dr[0], dr[1], dr[2], dr[3]});
+    } else {
+      for (int j = 0; j < 4; j++)
+        if (4 * l + j < g.A) o[4 * l + j] = to_t<T>(dr[j]);
+    }
+  };
+  auto st_rot1 = [&](size_t tok, bool live, float (&dr)[8]) {
+#pragma unroll
+    for (int e = 0; e < NR; e++) dr[e] = slot_sum<LPR>(dr[e], g.HPP);
+    if (live && hs == 0) {
+      float* o = part_rot + (tok * g.g + gi) * g.RW;
+      for (int e = 0; e < NR; e++)
+        if (NR * l + e < g.RW) o[NR * l + e] = dr[e];
+    }
+  };
   for (size_t t0 = ((size_t)blockIdx.x * NWV + wave) * TPW; t0 < ntok; t0 += (size_t)g.nblk * NWV * TPW) {
     const size_t tok = t0 + ts;
     const bool live = tok < ntok;
-    float n[2][C][8], rstd[2][C], ds[2][C][8];
+    if constexpr (!LDSB) {
+      // every load of the token first
+      Raw8<T> raw[2][C], hat[2][NB][C];
+      QkRot<ROT> R[NB];
+      float dr[NB][8];
+      bool on[NB];
 #pragma unroll
-    for (int x = 0; x < 2; x++)
+      for (int x = 0; x < 2; x++)
 #pragma unroll
-      for (int c = 0; c < C; c++) {
-        const T* row = (x ? k : q) + tok * (x ? g.ks : g.qs) + ((size_t)c * g.g + gi) * g.r;
-        if (live && c < g.c) {
-          ld8<T, HALF>(row, l, g.r, g.vin, n[x][c]);
-        } else {
-          for (int e = 0; e < 8; e++) n[x][c][e] = 0.0f;
+        for (int c = 0; c < C; c++) {
+          raw[x][c].zero();
+          if (live && c < g.c) raw[x][c].template load<HALF>(raw_row(x, c, tok), l, g.r, VEC);
         }
-        for (int e = 0; e < 8; e++) ds[x][c][e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NB; i++) {
+        const int hg = i * g.HPP + hs, hi = gi * g.hpg + hg;
+        on[i] = live && hg < g.hpg;
+        for (int e = 0; e < 8; e++) dr[i][e] = 0.0f;
+        if constexpr (ROT != 0)
+          if (on[i]) R[i].template load<VEC>(rot + rot_row(tok, hi), l, g);
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+          for (int c = 0; c < C; c++) {
+            hat[x][i][c].zero();
+            if (on[i] && c < g.c) hat[x][i][c].template load<HALF>(hat_row(x, c, tok, hi), l, g.r, VEC);
+          }
       }
 #pragma unroll
-    for (int x = 0; x < 2; x++)
-#pragma unroll
-      for (int c = 0; c < C; c++) {
-        float ss = 0.0f;
-        for (int e = 0; e < 8; e++) ss += n[x][c][e] * n[x][c][e];
-        rstd[x][c] = 1.0f / sqrtf(row_sum<LPR>(ss) / (float)g.r + g.eps);
-        for (int e = 0; e < 8; e++) n[x][c][e] *= rstd[x][c];
-      }
-    float dr1[8];   // d_rot over the heads of the group (rot_h = 1)
-    for (int e = 0; e < 8; e++) dr1[e] = 0.0f;
-    for (int i = 0; i < g.HL; i++) {
-      const int hg = i * g.HPP + hs;
-      if (!live || hg >= g.hpg) continue;
-      const int hi = gi * g.hpg + hg;
-      QkRot<T, ROT> R;
-      const size_t rrow = (tok * g.rot_h + (g.rot_h > 1 ? hi : 0)) * g.RW;
-      if constexpr (ROT != 0) R.load(rot + rrow, l, g);
-      float dr[8];
-      for (int e = 0; e < 8; e++) dr[e] = 0.0f;
+      for (int i = 0; i < NB; i++)
+        if constexpr (ROT != 0)
+          if (on[i]) R[i].make(l, g);
 #pragma unroll
       for (int x = 0; x < 2; x++) {
-        if constexpr (ROT == 3) {
-          const float* bias = x ? bk : bq;
-          if (bias != nullptr) ld8<float, HALF>(bias + (size_t)hi * g.r, l, g.r, false, bv[x]);
+        float n[C][8], ds[C][8], rstd[C];
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+          raw[x][c].get(n[c]);
+          rstd[c] = c < g.c ? norm(n[c]) : 0.0f;
+          for (int e = 0; e < 8; e++) ds[c][e] = 0.0f;
         }
-        float sb[8];
-        for (int e = 0; e < 8; e++) sb[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NB; i++) {
+          if (!on[i]) continue;
+          float b8[8];
+          if constexpr (ROT != 0) ld_bias(x, gi * g.hpg + i * g.HPP + hs, b8);
+#pragma unroll
+          for (int c = 0; c < C; c++) {
+            if (c >= g.c) break;
+            float d[8];
+            hat[x][i][c].get(d);
+            qk_row_grad<ROT>(R[i], n[c], w[x], b8, d, dr[i], db[x][i], ds[c]);
+          }
+        }
 #pragma unroll
         for (int c = 0; c < C; c++) {
           if (c >= g.c) break;
-          float d[8];
-          ld8<T, HALF>((x ? dkh : dqh) + ((tok * g.c + c) * g.h + hi) * g.r, l, g.r, g.vio, d);
-          if constexpr (ROT == 3) {
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-              f4 u;
-              for (int e = 0; e < 4; e++) u[e] = n[x][c][4 * j + e] * w[x][4 * j + e] + bv[x][4 * j + e];
-              const f4 z = qmul(u, qconj(f4{d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]}));
-              for (int e = 0; e < 4; e++) dr[4 * j + e] += z[e];
-            }
-          }
-          R.template turn<false>(d);
-          if constexpr (ROT == 1 || ROT == 2) {
-            // in the frame before the turn: u_x du_y - u_y du_x (turning both keeps it)
-            const float* bias = x ? bk : bq;
-            if (c == 0 && bias != nullptr) ld8<float, HALF>(bias + (size_t)hi * g.r, l, g.r, false, bv[x]);
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-              const int ex = ROT == 1 ? 2 * j : j, ey = ROT == 1 ? 2 * j + 1 : j + 4;
-              const float ux = n[x][c][ex] * w[x][ex] + bv[x][ex], uy = n[x][c][ey] * w[x][ey] + bv[x][ey];
-              dr[j] += ux * d[ey] - uy * d[ex];
-            }
-          }
-          for (int e = 0; e < 8; e++) {
-            sb[e] += d[e];
-            ds[x][c][e] += d[e];
-          }
-        }
-        if constexpr (LDSB) {
-#pragma unroll
-          for (int e = 0; e < 8; e++) acc[(i * 16 + 8 * x + e) * NT + threadIdx.x] += sb[e];
-        } else {
-          for (int e = 0; e < 8; e++) db[x][e] += sb[e];
+          finish(x, c, tok, live, n[c], rstd[c], ds[c]);
         }
       }
       if constexpr (ROT != 0) {
-        if (g.rot_h > 1 || g.h == 1) {
-          if (d_rot != nullptr) {
-            T* o = d_rot + rrow;
-            if constexpr (ROT == 3) {
-              for (int j = 0; j < 2; j++)
-                if (2 * l + j < g.J) st4(o + 4 * (2 * l + j), f4{dr[4 * j], dr[4 * j + 1], dr[4 * j + 2], dr[4 * j + 3]});
-            } else if (g.vrot) {
-              if (4 * l < g.A) st4(o + 4 * l, f4{dr[0], dr[1], dr[2], dr[3]});
-            } else {
-              for (int j = 0; j < 4; j++)
-                if (4 * l + j < g.A) o[4 * l + j] = to_t<T>(dr[j]);
-            }
-          }
+        if (part_rot != nullptr) {
+#pragma unroll
+          for (int i = 1; i < NB; i++)
+            for (int e = 0; e < NR; e++) dr[0][e] += dr[i][e];
+          st_rot1(tok, live, dr[0]);
         } else {
+#pragma unroll
+          for (int i = 0; i < NB; i++)
+            if (on[i]) st_rot(tok, gi * g.hpg + i * g.HPP + hs, dr[i]);
+        }
+      }
+    } else {
+      float n[2][C][8], ds[2][C][8], rstd[2][C], dr1[8];
+#pragma unroll
+      for (int x = 0; x < 2; x++)
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+          for (int e = 0; e < 8; e++) n[x][c][e] = ds[x][c][e] = 0.0f;
+          if (live && c < g.c) ld8<T, HALF>(raw_row(x, c, tok), l, g.r, VEC, n[x][c]);
+          rstd[x][c] = c < g.c ? norm(n[x][c]) : 0.0f;
+        }
+      for (int e = 0; e < 8; e++) dr1[e] = 0.0f;
+      for (int i = 0; i < g.HL; i++) {
+        const int hg = i * g.HPP + hs, hi = gi * g.hpg + hg;
+        if (!live || hg >= g.hpg) continue;
+        QkRot<ROT> R;
+        if constexpr (ROT != 0) {
+          R.template load<VEC>(rot + rot_row(tok, hi), l, g);
+          R.make(l, g);
+        }
+        float dr[8];
+        for (int e = 0; e < 8; e++) dr[e] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+          float b8[8], sb[8];
+          ld_bias(x, hi, b8);
+          for (int e = 0; e < 8; e++) sb[e] = 0.0f;
+#pragma unroll
+          for (int c = 0; c < C; c++) {
+            if (c >= g.c) break;
+            float d[8];
+            ld8<T, HALF>(hat_row(x, c, tok, hi), l, g.r, VEC, d);
+            qk_row_grad<ROT>(R, n[x][c], w[x], b8, d, dr, sb, ds[x][c]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; e++) acc[(i * 16 + 8 * x + e) * NT + threadIdx.x] += sb[e];
+        }
+        if constexpr (ROT != 0) {
+          if (part_rot == nullptr) st_rot(tok, hi, dr);
           for (int e = 0; e < 8; e++) dr1[e] += dr[e];
         }
       }
-    }
-    if constexpr (ROT != 0) {
-      if (part_rot != nullptr) {
+      if constexpr (ROT != 0)
+        if (part_rot != nullptr) st_rot1(tok, live, dr1);
 #pragma unroll
-        for (int e = 0; e < (ROT == 3 ? 8 : 4); e++) dr1[e] = slot_sum<LPR>(dr1[e], g.HPP);
-        if (live && hs == 0) {
-          float* o = part_rot + (tok * g.g + gi) * g.RW;
-          for (int e = 0; e < (ROT == 3 ? 8 : 4); e++) {
-            const int at = (ROT == 3 ? 8 : 4) * l + e;
-            if (at < g.RW) o[at] = dr1[e];
-          }
+      for (int x = 0; x < 2; x++)
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+          if (c >= g.c) break;
+          finish(x, c, tok, live, n[x][c], rstd[x][c], ds[x][c]);
         }
-      }
     }
-    // the group's raw rows
+  }
+  // the block's sums, in a fixed order: over the token slots of its waves. src [16][threads];
+  // heads hs0 + (head slot) of the group, or (isw) d_w, which all head slots have alike
+  const int NTS = NWV * TPW;
+  float* red = acc + (LDSB ? (size_t)g.HL * 16 * NT : 0);
+  auto sum_block = [&](const float* src, int hs0, bool isw) {
+    float* part = isw ? part_w : part_b;
+    if (part == nullptr) return;
+    for (int id = threadIdx.x; id < g.HPP * 16 * LPR; id += NT) {
+      const int ll = id % LPR, ve = id / LPR % 16, hh = id / (16 * LPR), x = ve / 8, e = ve % 8;
+      if (!qk_has<HALF>(ll, e, g.r) || (isw ? hh > 0 : hs0 + hh >= g.hpg)) continue;
+      double s = 0.0;
+      for (int t = 0; t < NTS; t++) s += (double)src[ve * NT + (t / TPW) * 64 + ((t % TPW) * g.HPP + hh) * LPR + ll];
+      const size_t row = isw ? ((size_t)x * g.nblk + blockIdx.x) * g.g + gi
+                             : ((size_t)x * g.nblk + blockIdx.x) * g.h + gi * g.hpg + hs0 + hh;
+      part[row * g.r + qk_col<HALF>(ll, e, g.r)] = (float)s;
+    }
+  };
+  auto to_red = [&](const float (&v)[2][8]) {
+    __syncthreads();
 #pragma unroll
     for (int x = 0; x < 2; x++)
 #pragma unroll
-      for (int c = 0; c < C; c++) {
-        if (c >= g.c) break;
-        float m = 0.0f;
+      for (int e = 0; e < 8; e++) red[(8 * x + e) * NT + threadIdx.x] = v[x][e];
+    __syncthreads();
+  };
+  if constexpr (LDSB) {
+    __syncthreads();
+    for (int i = 0; i < g.HL; i++) sum_block(acc + (size_t)i * 16 * NT, i * g.HPP, false);
+  } else {
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-          const float s = slot_sum<LPR>(ds[x][c][e], g.HPP);
-          dw[x][e] += s * n[x][c][e];
-          ds[x][c][e] = s * w[x][e];
-          m += ds[x][c][e] * n[x][c][e];
-        }
-        m = row_sum<LPR>(m) / (float)g.r;
-        T* out = x ? d_k : d_q;
-        if (live && hs == 0 && out != nullptr) {
-          float o[8];
-          for (int e = 0; e < 8; e++) o[e] = (ds[x][c][e] - n[x][c][e] * m) * rstd[x][c];
-          st8<T, HALF>(out + ((tok * g.c + c) * g.g + gi) * g.r, l, g.r, g.vio, o);
-        }
-      }
-  }
-  // the block's sums, in a fixed order: over the token slots of its waves
-  __syncthreads();
-  const int NTS = NWV * TPW;   // token slots of the block
-  float* red = acc + (LDSB ? (size_t)g.HL * 16 * NT : 0);   // [16][threads]
-  for (int i = 0; i < (LDSB ? g.HL : 1) + 1; i++) {
-    const bool isw = i == (LDSB ? g.HL : 1);   // last: d_w, equal in all head slots
-    float* src = LDSB && !isw ? acc + (size_t)i * 16 * NT : red;
-    if (!LDSB || isw) {
-      __syncthreads();
-#pragma unroll
+    for (int i = 0; i < NB; i++) {
+      float v[2][8];
       for (int x = 0; x < 2; x++)
-        for (int e = 0; e < 8; e++) red[(8 * x + e) * NT + threadIdx.x] = isw ? dw[x][e] : db[x][e];
-      __syncthreads();
-    }
-    float* part = isw ? part_w : part_b;
-    if (part == nullptr) continue;
-    // thread -> (head slot, value, lane of the row)
-    for (int id = threadIdx.x; id < g.HPP * 16 * LPR; id += NT) {
-      const int ll = id % LPR, ve = id / LPR % 16, hh = id / (16 * LPR), x = ve / 8, e = ve % 8;
-      const int hg = i * g.HPP + hh;
-      if (!qk_has<HALF>(ll, e, g.r) || (isw ? hh > 0 : hg >= g.hpg)) continue;
-      double s = 0.0;
-      for (int t = 0; t < NTS; t++) {
-        const int th = (t / TPW) * 64 + ((t % TPW) * g.HPP + hh) * LPR + ll;
-        s += (double)src[ve * NT + th];
-      }
-      const int col = qk_col<HALF>(ll, e, g.r);
-      if (isw)
-        part[(((size_t)x * g.nblk + blockIdx.x) * g.g + gi) * g.r + col] = (float)s;
-      else
-        part[(((size_t)x * g.nblk + blockIdx.x) * g.h + gi * g.hpg + hg) * g.r + col] = (float)s;
+        for (int e = 0; e < 8; e++) v[x][e] = db[x][i][e];
+      to_red(v);
+      sum_block(red, i * g.HPP, false);
     }
   }
+  to_red(dw);
+  sum_block(red, 0, true);
 }
 
-// out_x[e] = sum over i < n of part[x][i][e] (x = 0: q, 1: k), e < w; in double, one
-// workgroup for 64 values: four lanes groups of the sum each, joined in LDS.
-__global__ __launch_bounds__(256) void k_qk_sum(const float* __restrict__ part, int n, int w,
-                                                float* __restrict__ out_q, float* __restrict__ out_k) {
-  __shared__ double red[4][64];
-  const int x = blockIdx.y, e = blockIdx.x * 64 + (threadIdx.x & 63), j = threadIdx.x >> 6;
-  float* out = x ? out_k : out_q;
+// The sums of the blocks' partials, in double and in a fixed order: d_w over the n_w
+// rows of part_w [2][n_w][r], d_b over the n_b rows of part_b [2][n_b][hr]. A workgroup
+// takes 16 columns of one of them, 64 threads each.
+__global__ __launch_bounds__(1024) void k_qk_sum(const float* __restrict__ part_w, int n_w, int r,
+                                                 float* __restrict__ d_wq, float* __restrict__ d_wk,
+                                                 const float* __restrict__ part_b, int n_b, int hr,
+                                                 float* __restrict__ d_bq, float* __restrict__ d_bk) {
+  __shared__ double red[64][17];
+  const int wb = (r + 15) / 16, x = blockIdx.y;
+  const bool isw = (int)blockIdx.x < wb;
+  const float* part = isw ? part_w : part_b;
+  const int n = isw ? n_w : n_b, w = isw ? r : hr;
+  float* out = isw ? (x ? d_wk : d_wq) : (x ? d_bk : d_bq);
   if (out == nullptr) return;
+  const int e = ((int)blockIdx.x - (isw ? 0 : wb)) * 16 + (int)(threadIdx.x & 15), j = threadIdx.x >> 4;
   double s = 0.0;
-  if (e < w)
-    for (int i = j; i < n; i += 4) s += (double)part[((size_t)x * n + i) * w + e];
-  red[j][threadIdx.x & 63] = s;
+  if (e < w) {
+    const float* src = part + (size_t)x * n * w + e;
+#pragma unroll 8
+    for (int i = j; i < n; i += 64) s += (double)src[(size_t)i * w];
+  }
+  red[j][threadIdx.x & 15] = s;
   __syncthreads();
-  if (j == 0 && e < w) out[e] = (float)(red[0][threadIdx.x] + red[1][threadIdx.x] + red[2][threadIdx.x] + red[3][threadIdx.x]);
+  if (j == 0 && e < w) {
+    for (int i = 1; i < 64; i++) s += red[i][threadIdx.x];
+    out[e] = (float)s;
+  }
 }
 
 }  // namespace mom

@@ -16,8 +16,10 @@ namespace {
 
 struct QkPlan {
   QkGeo g;
-  bool bf, empty;
+  bool bf, empty, vec;
+  int HB;               // heads a row slot keeps in registers (0: any number)
   int LPR, C, NT;       // lanes a row; padded channels; threads of the backward
+  int nfwd;             // workgroups per group of the forward
   size_t lds;           // of the backward
   size_t part_w, part_b, part_rot, ws, flag;
 };
@@ -60,10 +62,8 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
   g.qs = (size_t)qs; g.ks = (size_t)ks;
   g.rot_h = (int)d->rot_h; g.A = A; g.J = J; g.RW = J > 0 ? 4 * J : A;
   g.eps = d->eps;
-  g.vin = g.r % 8 == 0 && qs * tsz % 16 == 0 && ks * tsz % 16 == 0;
-  g.vio = g.r % 8 == 0;
-  g.vrot = A % 4 == 0;
-  P->LPR = g.r <= 64 ? 8 : 16;
+  P->vec = g.r % 8 == 0 && qs * tsz % 16 == 0 && ks * tsz % 16 == 0 && A % 4 == 0;
+  P->LPR = g.r <= 64 && P->vec ? 8 : 16;
   P->C = g.c <= 1 ? 1 : g.c <= 2 ? 2 : 4;
   if (P->empty) return MOMENTS_OK;
   g.hpg = g.h / g.g;
@@ -71,14 +71,17 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
   g.HPP = 1;
   while (g.HPP < g.hpg && g.HPP < rpw) g.HPP *= 2;
   g.HL = (g.hpg + g.HPP - 1) / g.HPP;
-  // sums for each head in LDS when a head slot serves several heads: 64 bytes a thread and
-  // head, so fewer threads where there are many
+  // sums for each head in registers while a head slot serves one or two heads, else in LDS:
+  // 64 bytes a thread and head, so fewer threads where there are many
+  P->HB = P->vec && g.HL <= (P->C == 4 ? 1 : 2) ? g.HL : 0;
   P->NT = QKT;
-  while (P->NT > 64 && (size_t)(g.HL + 1) * 64 * P->NT > kLdsLimit) P->NT /= 2;
-  P->lds = (size_t)(g.HL > 1 ? g.HL + 1 : 1) * 64 * P->NT;
+  while (P->HB == 0 && P->NT > 64 && (size_t)(g.HL + 1) * 64 * P->NT > kLdsLimit) P->NT /= 2;
+  P->lds = (size_t)(P->HB == 0 ? g.HL + 1 : 1) * 64 * P->NT;
   const int64_t per = (int64_t)(P->NT / 64) * (rpw / g.HPP);   // tokens a workgroup has at once
   const int64_t most = std::max<int64_t>(1, ((int64_t)g.b * g.s + per - 1) / per);
   g.nblk = (int)std::min<int64_t>(most, std::max<int64_t>(1, 2048 / g.g));
+  const int64_t perf = QKT / 64 * (rpw / g.HPP);
+  P->nfwd = (int)std::min<int64_t>(((int64_t)g.b * g.s + perf - 1) / perf, std::max<int64_t>(1, 4096 / g.g));
   size_t o = 0;
   P->part_w = o; o = align256(o + (size_t)2 * g.nblk * g.g * g.r * 4);
   P->part_b = o; o = align256(o + (size_t)2 * g.nblk * g.h * g.r * 4);
@@ -89,26 +92,37 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
   return MOMENTS_OK;
 }
 
-// Calls f(TT<T>, IC<LPR>, IC<ROT>, IC<C>) for the compiled variant of the plan.
+// Calls f(TT<T>, IC<LPR>, IC<ROT>, IC<C>, IC<HB>, IC<VEC>) for the compiled variant of the
+// plan. Rows that are not whole pieces have one variant for all widths, channels and heads.
 template <class F>
 int with_qk(const QkPlan& P, int rot_kind, F&& f) {
+  auto by_hb = [&](auto tt, auto lpr, auto rot, auto cc) -> int {
+    switch (P.HB) {
+      case 1: return f(tt, lpr, rot, cc, IC<1>{}, IC<1>{});
+      case 2: return f(tt, lpr, rot, cc, IC<2>{}, IC<1>{});
+    }
+    return f(tt, lpr, rot, cc, IC<0>{}, IC<1>{});
+  };
   auto by_c = [&](auto tt, auto lpr, auto rot) -> int {
     switch (P.C) {
-      case 1: return f(tt, lpr, rot, IC<1>{});
-      case 2: return f(tt, lpr, rot, IC<2>{});
+      case 1: return by_hb(tt, lpr, rot, IC<1>{});
+      case 2: return by_hb(tt, lpr, rot, IC<2>{});
     }
-    return f(tt, lpr, rot, IC<4>{});
+    return by_hb(tt, lpr, rot, IC<4>{});
   };
-  auto by_rot = [&](auto tt, auto lpr) -> int {
+  auto by_lpr = [&](auto tt, auto rot) -> int {
+    if (!P.vec) return f(tt, IC<16>{}, rot, IC<4>{}, IC<0>{}, IC<0>{});
+    return P.LPR == 8 ? by_c(tt, IC<8>{}, rot) : by_c(tt, IC<16>{}, rot);
+  };
+  auto by_rot = [&](auto tt) -> int {
     switch (rot_kind) {
-      case MOMENTS_ROT_NONE: return by_c(tt, lpr, IC<0>{});
-      case MOMENTS_ROT_COMPLEX_PAIRWISE: return by_c(tt, lpr, IC<1>{});
-      case MOMENTS_ROT_COMPLEX_HALF: return by_c(tt, lpr, IC<2>{});
+      case MOMENTS_ROT_NONE: return by_lpr(tt, IC<0>{});
+      case MOMENTS_ROT_COMPLEX_PAIRWISE: return by_lpr(tt, IC<1>{});
+      case MOMENTS_ROT_COMPLEX_HALF: return by_lpr(tt, IC<2>{});
     }
-    return by_c(tt, lpr, IC<3>{});
+    return by_lpr(tt, IC<3>{});
   };
-  if (P.bf) return P.LPR == 8 ? by_rot(TT<bf16>{}, IC<8>{}) : by_rot(TT<bf16>{}, IC<16>{});
-  return P.LPR == 8 ? by_rot(TT<float>{}, IC<8>{}) : by_rot(TT<float>{}, IC<16>{});
+  return P.bf ? by_rot(TT<bf16>{}) : by_rot(TT<float>{});
 }
 
 }  // namespace
@@ -134,14 +148,13 @@ int moments_qk_fwd(const moments_qk_desc* desc, const void* q, const void* k, co
   for (const void* p : ptrs)
     if (p != nullptr && !aligned16(p)) return MOMENTS_EINVAL;
   hipStream_t st = (hipStream_t)stream;
-  return with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc) -> int {
+  return with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto vec) -> int {
     using T = typename decltype(tt)::type;
     constexpr int LPR = decltype(lpr)::value, ROT = decltype(rk)::value, C = decltype(cc)::value;
-    const int64_t per = QKT / 64 * (64 / LPR / g.HPP);
-    const int64_t nb = ((int64_t)g.b * g.s + per - 1) / per;
     ProfScope ps(KID_QK_FWD, st);
-    hipLaunchKernelGGL((k_qk_fwd<T, LPR, ROT, C>), dim3((unsigned)nb, (unsigned)g.g), dim3(QKT), 0, st, g,
-                       (const T*)q, (const T*)k, wq, wk, bq, bk, (const T*)rot, (T*)qhat, (T*)khat);
+    hipLaunchKernelGGL((k_qk_fwd<T, LPR, ROT, C, decltype(hb)::value, decltype(vec)::value != 0>),
+                       dim3((unsigned)P.nfwd, (unsigned)g.g), dim3(QKT), 0, st, g, (const T*)q, (const T*)k, wq, wk,
+                       bq, bk, (const T*)rot, (T*)qhat, (T*)khat);
     return check_launch();
   });
 }
@@ -168,19 +181,18 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
   float* pw = d_wq || d_wk ? (float*)(ws + P.part_w) : nullptr;
   float* pb = d_bq || d_bk ? (float*)(ws + P.part_b) : nullptr;
   float* pr = rot1 && d_rot ? (float*)(ws + P.part_rot) : nullptr;
-  MOM_TRY(with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc) -> int {
+  MOM_TRY(with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto vec) -> int {
     using T = typename decltype(tt)::type;
     constexpr int LPR = decltype(lpr)::value, ROT = decltype(rk)::value, C = decltype(cc)::value;
-    auto go = [&](auto ldsb) -> int {
-      constexpr bool LB = decltype(ldsb)::value != 0;
-      MOM_TRY(set_lds(k_qk_bwd<T, LPR, ROT, C, LB>, P.lds));
+    {
+      auto kernel = k_qk_bwd<T, LPR, ROT, C, decltype(hb)::value, decltype(vec)::value != 0>;
+      MOM_TRY(set_lds(kernel, P.lds));
       ProfScope ps(KID_QK_BWD, st);
-      hipLaunchKernelGGL((k_qk_bwd<T, LPR, ROT, C, LB>), dim3((unsigned)g.nblk, (unsigned)g.g), dim3(P.NT), P.lds, st,
-                         g, (const T*)q, (const T*)k, wq, wk, bq, bk, (const T*)rot, (const T*)d_qhat,
-                         (const T*)d_khat, (T*)d_q, (T*)d_k, (T*)(rot1 ? nullptr : d_rot), pr, pw, pb);
-      return check_launch();
-    };
-    MOM_TRY(g.HL > 1 ? go(IC<1>{}) : go(IC<0>{}));
+      hipLaunchKernelGGL(kernel, dim3((unsigned)g.nblk, (unsigned)g.g), dim3(P.NT), P.lds, st, g, (const T*)q,
+                         (const T*)k, wq, wk, bq, bk, (const T*)rot, (const T*)d_qhat, (const T*)d_khat, (T*)d_q,
+                         (T*)d_k, (T*)(rot1 ? nullptr : d_rot), pr, pw, pb);
+      MOM_TRY(check_launch());
+    }
     if (pr != nullptr && g.s > 0) {
       const size_t total = (size_t)g.b * g.s * g.RW;
       ProfScope ps(KID_QK_SUM, st);
@@ -190,14 +202,10 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
     }
     return 0;
   }));
-  if (pw != nullptr) {
+  if (pw != nullptr || pb != nullptr) {
     ProfScope ps(KID_QK_SUM, st);
-    hipLaunchKernelGGL(k_qk_sum, dim3((g.r + 63) / 64, 2), dim3(256), 0, st, pw, g.nblk * g.g, g.r, d_wq, d_wk);
-    MOM_TRY(check_launch());
-  }
-  if (pb != nullptr) {
-    ProfScope ps(KID_QK_SUM, st);
-    hipLaunchKernelGGL(k_qk_sum, dim3((unsigned)(((int64_t)g.h * g.r + 63) / 64), 2), dim3(256), 0, st, pb, g.nblk,
+    const unsigned cols = (unsigned)((g.r + 15) / 16 + (pb != nullptr ? ((int64_t)g.h * g.r + 15) / 16 : 0));
+    hipLaunchKernelGGL(k_qk_sum, dim3(cols, 2), dim3(1024), 0, st, pw, g.nblk * g.g, g.r, d_wq, d_wk, pb, g.nblk,
                        g.h * g.r, d_bq, d_bk);
     MOM_TRY(check_launch());
   }
