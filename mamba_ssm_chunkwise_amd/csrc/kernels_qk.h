@@ -19,6 +19,8 @@
 #include "common.h"
 #include "kernels_rot.h"
 
+#include <type_traits>
+
 namespace mom {
 
 constexpr int QKT = 256;
@@ -29,7 +31,7 @@ struct QkGeo {
   int rot_h, RW, A, J;
   int hpg, HPP, HL; // heads per group; head slots of a wave; times they are filled
   int nblk;         // workgroups per group (backward)
-  float eps;
+  float eps, rinv;  // added to the mean square; 1 / r
 };
 
 // Column of value e (0..7) of lane l of a row.
@@ -137,38 +139,52 @@ struct Raw8<float> {
   }
 };
 
-// Sine and cosine, to fp32 rounding: the nearest multiple of pi/2 is taken off (in three
-// floats below 1e5, else in doubles, which reach to 2^50), and the rest, at most pi/4, goes
-// through the Taylor series to x^9 and x^10 (the next terms are below 2^-28). Beyond
-// 2^50 neighbouring floats are 2^27 radians apart; there the rest is taken as zero.
+// Sine and cosine. The nearest multiple of pi/2 is taken off (in three floats below 1e5,
+// else in doubles, which reach to 2^50; beyond, neighbouring floats are 2^27 radians apart,
+// and the rest is taken as zero). FAST (bf16 results): the rest, at most pi/4, goes through
+// the sine and cosine instructions, whose error of about 2^-20 is far below the result's
+// rounding of 2^-9; otherwise through the Taylor series to x^9 and x^10 (the next terms are
+// below 2^-28). Evaluated for bf16 rows the series costs 80 more instructions a lane and head.
+template <bool FAST>
 __device__ __forceinline__ void sincos_f(float x, float& s, float& c) {
   constexpr double kPi2 = 1.5707963267948966, kPi2Lo = 6.123233995736766e-17;   // pi/2: double and remainder
+  constexpr float P1 = (float)kPi2, P2 = (float)(kPi2 - (double)P1), P3 = (float)kPi2Lo;
   float t;
-  int n;
+  int n = 0;
   if (fabsf(x) < 1e5f) {
-    const float k = rintf(x * 0.636619772367581343f);
-    constexpr float P1 = (float)kPi2, P2 = (float)(kPi2 - (double)P1), P3 = (float)kPi2Lo;
-    t = fmaf(-k, P3, fmaf(-k, P2, fmaf(-k, P1, x)));
-    n = (int)k;
+    // FAST takes off whole turns
+    const float k = FAST ? 4.0f * rintf(x * 0.159154943091895336f) : rintf(x * 0.636619772367581343f);
+    t = fmaf(-k, P2, fmaf(-k, P1, x));
+    if constexpr (!FAST) {
+      t = fmaf(-k, P3, t);
+      n = (int)k;
+    }
   } else {
     const double k = rint((double)x * 0.6366197723675814);
     const double d = fma(-k, kPi2Lo, fma(-k, kPi2, (double)x));
     t = fabs(d) <= 1.0 ? (float)d : x - x;   // zero; NaN for infinities and NaN
     n = (int)(k - 4.0 * floor(0.25 * k));
+    if constexpr (FAST) t += (float)n * P1;
   }
-  const float t2 = t * t;
-  float a = fmaf(t2, 2.75573192e-6f, -1.98412698e-4f);
-  a = fmaf(t2, a, 8.33333333e-3f);
-  a = fmaf(t2, a, -1.66666667e-1f);
-  a = fmaf(t2 * t, a, t);
-  float b = fmaf(t2, -2.75573192e-7f, 2.48015873e-5f);
-  b = fmaf(t2, b, -1.38888889e-3f);
-  b = fmaf(t2, b, 4.16666667e-2f);
-  b = fmaf(t2, b, -0.5f);
-  b = fmaf(t2, b, 1.0f);
-  const float u = (n & 1) ? b : a, v = (n & 1) ? a : b;
-  s = (n & 2) ? -u : u;
-  c = ((n + 1) & 2) ? -v : v;
+  if constexpr (FAST) {
+    const float turns = t * 0.159154943091895336f;
+    s = __builtin_amdgcn_sinf(turns);
+    c = __builtin_amdgcn_cosf(turns);
+  } else {
+    const float t2 = t * t;
+    float a = fmaf(t2, 2.75573192e-6f, -1.98412698e-4f);
+    a = fmaf(t2, a, 8.33333333e-3f);
+    a = fmaf(t2, a, -1.66666667e-1f);
+    a = fmaf(t2 * t, a, t);
+    float b = fmaf(t2, -2.75573192e-7f, 2.48015873e-5f);
+    b = fmaf(t2, b, -1.38888889e-3f);
+    b = fmaf(t2, b, 4.16666667e-2f);
+    b = fmaf(t2, b, -0.5f);
+    b = fmaf(t2, b, 1.0f);
+    const float u = (n & 1) ? b : a, v = (n & 1) ? a : b;
+    s = (n & 2) ? -u : u;
+    c = ((n + 1) & 2) ? -v : v;
+  }
 }
 
 // The rotation of one (token, head) as a lane needs it: ROT 1, 2: cos and sin of its
@@ -196,11 +212,12 @@ struct QkRot {
     }
   }
   // Angles to their cosines and sines; lanes past the rotated width keep the identity.
+  template <bool FAST>
   __device__ __forceinline__ void make(int l, const QkGeo& g) {
     if constexpr (ROT == 1 || ROT == 2) {
       if (4 * l < g.A) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) sincos_f(v[i], v[4 + i], v[i]);
+        for (int i = 0; i < 4; i++) sincos_f<FAST>(v[i], v[4 + i], v[i]);
       } else {
         for (int i = 0; i < 4; i++) {
           v[i] = 1.0f;
@@ -256,6 +273,44 @@ __device__ __forceinline__ float slot_sum(float v, int n) {
     v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
   }
   return v;
+}
+
+// Sums of N rows over the n head slots of a token, each slot left with its share of the
+// rows: after it, v[0 .. N / n - 1] (v[0] where n >= N) are the rows from qk_own_row() on. The swaps
+// of gfx950 move two rows at once, so a row costs half a swap and half an add per step
+// instead of a full exchange; where slots outnumber rows, several hold the same one.
+__host__ __device__ __forceinline__ int qk_own_row(int N, int n, int hs) {
+  // head slots split the rows from the widest step down
+  int row = 0;
+  for (int d = n / 2, m = N; d >= 1 && m > 1; d /= 2, m /= 2)
+    if (hs & d) row += m / 2;
+  return row;
+}
+// Whether this slot is the one that writes its rows (the first of those that share them).
+__host__ __device__ __forceinline__ bool qk_own_writes(int N, int n, int hs) { return n <= N || (hs & (n / N - 1)) == 0; }
+// D: head slots apart in this step; M: rows that the slot holds before it.
+template <int LPR, int D, int M, int N>
+__device__ __forceinline__ void slot_scatter(float (&v)[N][8], int lane) {
+  if constexpr (D >= 1) {
+    constexpr int H = M > 1 ? M / 2 : 1;
+#pragma unroll
+    for (int i = 0; i < H; i++)
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const float a = v[i][e], b = M > 1 ? v[i + M / 2][e] : a;
+        if constexpr (D * LPR == 32) {
+          const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+          v[i][e] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+        } else if constexpr (D * LPR == 16) {
+          const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+          v[i][e] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+        } else {   // 8 lanes: rotate the 16 lanes of a row by 8
+          const bool hi = lane & 8;
+          v[i][e] = (hi ? b : a) + dpp<0x128>(hi ? a : b);
+        }
+      }
+    slot_scatter<LPR, D / 2, H, N>(v, lane);
+  }
 }
 
 // C: channels padded to 1, 2 or 4. HB: heads per row slot whose bias stays in registers
@@ -328,12 +383,12 @@ __global__ __launch_bounds__(QKT) void k_qk_fwd(QkGeo g, const T* __restrict__ q
         if (c >= g.c) break;
         float ss = 0.0f;
         for (int e = 0; e < 8; e++) ss += n[x][c][e] * n[x][c][e];
-        const float rstd = 1.0f / sqrtf(row_sum<LPR>(ss) / (float)g.r + g.eps);
+        const float rstd = __builtin_amdgcn_rsqf(row_sum<LPR>(ss) * g.rinv + g.eps);
         for (int e = 0; e < 8; e++) n[x][c][e] *= rstd * w[x][e];
       }
     auto head = [&](int hg, QkRot<ROT>& Rh, auto bias) {
       const int hi = gi * g.hpg + hg;
-      Rh.make(l, g);
+      Rh.template make<sizeof(T) == 2>(l, g);
 #pragma unroll
       for (int x = 0; x < 2; x++) {
         float b8[8];
@@ -405,8 +460,8 @@ __device__ __forceinline__ void qk_row_grad(const QkRot<ROT>& R, const float (&n
 // HB: heads per row slot (1, 2) whose sums of du stand in registers; 0: any number, they
 // stand in LDS, one place per thread and head. part_b [2][nblk][h][r], part_w
 // [2][nblk][g][r]; part_rot [b,s,g][RW] where all heads share a rotation (d_rot is then
-// their sum over g).
-template <typename T, int LPR, int ROT, int C, int HB, bool VEC>
+// their sum over g). HPP: head slots of a token (all a wave has, with HB = 0 or 2).
+template <typename T, int LPR, int ROT, int C, int HB, int HPP, bool VEC>
 __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q, const T* __restrict__ k,
                                                 const float* __restrict__ wq, const float* __restrict__ wk,
                                                 const float* __restrict__ bq, const float* __restrict__ bk,
@@ -415,12 +470,12 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
                                                 T* __restrict__ d_rot, float* __restrict__ part_rot,
                                                 float* __restrict__ part_w, float* __restrict__ part_b) {
   constexpr bool HALF = ROT == 2, LDSB = HB == 0;
-  constexpr int RPW = 64 / LPR, NB = HB > 0 ? HB : 1, NR = ROT == 3 ? 8 : 4;
+  constexpr int RPW = 64 / LPR, TPW = RPW / HPP, NB = HB > 0 ? HB : 1, NR = ROT == 3 ? 8 : 4;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   float* acc = reinterpret_cast<float*>(lds);   // LDSB: [HL][16][threads]; then the block's sums
   const int NT = blockDim.x, NWV = NT / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPR, slot = lane / LPR;
-  const int gi = blockIdx.y, TPW = RPW / g.HPP, hs = slot % g.HPP, ts = slot / g.HPP;
+  const int gi = blockIdx.y, hs = slot % HPP, ts = slot / HPP;
   const size_t ntok = (size_t)g.b * g.s;
   float w[2][8], dw[2][8], db[2][NB][8];
 #pragma unroll
@@ -446,26 +501,47 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
   auto norm = [&](float (&n)[8]) {
     float ss = 0.0f;
     for (int e = 0; e < 8; e++) ss += n[e] * n[e];
-    const float rstd = 1.0f / sqrtf(row_sum<LPR>(ss) / (float)g.r + g.eps);
+    const float rstd = __builtin_amdgcn_rsqf(row_sum<LPR>(ss) * g.rinv + g.eps);
     for (int e = 0; e < 8; e++) n[e] *= rstd;
     return rstd;
   };
-  // the group's raw row, from the sum of du over its heads
-  auto finish = [&](int x, int c, size_t tok, bool live, const float (&n)[8], float rstd, float (&ds)[8]) {
-    float m = 0.0f;
+  // the group's raw rows 0 .. 2C - 1 (q's channels, then k's), from the sums of du over its
+  // heads: each head slot finishes its share of them, and sums d_w for q or k by its rows
+  constexpr int N = 2 * C;
+  constexpr int own = N > HPP ? N / HPP : 1;
+  const int orow = qk_own_row(N, HPP, hs);
+  const bool writes = qk_own_writes(N, HPP, hs);
+  auto finish = [&](size_t tok, bool live, const float (&n)[N][8], const float (&rstd)[N], float (&ds)[N][8]) {
+    slot_scatter<LPR, HPP / 2, N, N>(ds, lane);
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const float v = slot_sum<LPR>(ds[e], g.HPP);
-      dw[x][e] += v * n[e];
-      ds[e] = v * w[x][e];
-      m += ds[e] * n[e];
-    }
-    m = row_sum<LPR>(m) / (float)g.r;
-    T* out = x ? d_k : d_q;
-    if (live && hs == 0 && out != nullptr) {
-      float o[8];
-      for (int e = 0; e < 8; e++) o[e] = (ds[e] - n[e] * m) * rstd;
-      st8<T, HALF>(out + ((tok * g.c + c) * g.g + gi) * g.r, l, g.r, VEC, o);
+    for (int i = 0; i < own; i++) {
+      const int row = orow + i, x = row / C, c = row % C;
+      float nn[8], rs = 0.0f, m = 0.0f, wx[8];
+#pragma unroll
+      for (int j = i; j < N; j += own) {            // row j is this slot's
+        const bool is = j == row;
+        rs = is ? rstd[j] : rs;
+        for (int e = 0; e < 8; e++) nn[e] = j == i || is ? n[j][e] : nn[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        wx[e] = x ? w[1][e] : w[0][e];
+        const float t = ds[i][e] * nn[e];
+        if constexpr (own > C) {                    // one slot for both q and k
+          dw[i / C][e] += t;
+        } else {
+          dw[0][e] += t;
+        }
+        ds[i][e] *= wx[e];
+        m += ds[i][e] * nn[e];
+      }
+      m = row_sum<LPR>(m) * g.rinv;
+      T* out = x ? d_k : d_q;
+      if (live && writes && c < g.c && out != nullptr) {
+        float o[8];
+        for (int e = 0; e < 8; e++) o[e] = (ds[i][e] - nn[e] * m) * rs;
+        st8<T, HALF>(out + ((tok * g.c + c) * g.g + gi) * g.r, l, g.r, VEC, o);
+      }
     }
   };
   // the rotation's: one head's own, or the group's share of the one for all heads
@@ -484,7 +560,7 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
   };
   auto st_rot1 = [&](size_t tok, bool live, float (&dr)[8]) {
 #pragma unroll
-    for (int e = 0; e < NR; e++) dr[e] = slot_sum<LPR>(dr[e], g.HPP);
+    for (int e = 0; e < NR; e++) dr[e] = slot_sum<LPR>(dr[e], HPP);
     if (live && hs == 0) {
       float* o = part_rot + (tok * g.g + gi) * g.RW;
       for (int e = 0; e < NR; e++)
@@ -509,7 +585,7 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
         }
 #pragma unroll
       for (int i = 0; i < NB; i++) {
-        const int hg = i * g.HPP + hs, hi = gi * g.hpg + hg;
+        const int hg = i * HPP + hs, hi = gi * g.hpg + hg;
         on[i] = live && hg < g.hpg;
         for (int e = 0; e < 8; e++) dr[i][e] = 0.0f;
         if constexpr (ROT != 0)
@@ -525,35 +601,32 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
 #pragma unroll
       for (int i = 0; i < NB; i++)
         if constexpr (ROT != 0)
-          if (on[i]) R[i].make(l, g);
+          if (on[i]) R[i].template make<sizeof(T) == 2>(l, g);
+      float n[N][8], ds[N][8], rstd[N];
 #pragma unroll
       for (int x = 0; x < 2; x++) {
-        float n[C][8], ds[C][8], rstd[C];
 #pragma unroll
         for (int c = 0; c < C; c++) {
-          raw[x][c].get(n[c]);
-          rstd[c] = c < g.c ? norm(n[c]) : 0.0f;
-          for (int e = 0; e < 8; e++) ds[c][e] = 0.0f;
+          const int j = x * C + c;
+          raw[x][c].get(n[j]);
+          rstd[j] = c < g.c ? norm(n[j]) : 0.0f;
+          for (int e = 0; e < 8; e++) ds[j][e] = 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < NB; i++) {
           if (!on[i]) continue;
           float b8[8];
-          if constexpr (ROT != 0) ld_bias(x, gi * g.hpg + i * g.HPP + hs, b8);
+          if constexpr (ROT != 0) ld_bias(x, gi * g.hpg + i * HPP + hs, b8);
 #pragma unroll
           for (int c = 0; c < C; c++) {
             if (c >= g.c) break;
             float d[8];
             hat[x][i][c].get(d);
-            qk_row_grad<ROT>(R[i], n[c], w[x], b8, d, dr[i], db[x][i], ds[c]);
+            qk_row_grad<ROT>(R[i], n[x * C + c], w[x], b8, d, dr[i], db[x][i], ds[x * C + c]);
           }
         }
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-          if (c >= g.c) break;
-          finish(x, c, tok, live, n[c], rstd[c], ds[c]);
-        }
       }
+      finish(tok, live, n, rstd, ds);
       if constexpr (ROT != 0) {
         if (part_rot != nullptr) {
 #pragma unroll
@@ -563,27 +636,28 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
         } else {
 #pragma unroll
           for (int i = 0; i < NB; i++)
-            if (on[i]) st_rot(tok, gi * g.hpg + i * g.HPP + hs, dr[i]);
+            if (on[i]) st_rot(tok, gi * g.hpg + i * HPP + hs, dr[i]);
         }
       }
     } else {
-      float n[2][C][8], ds[2][C][8], rstd[2][C], dr1[8];
+      float n[N][8], ds[N][8], rstd[N], dr1[8];
 #pragma unroll
       for (int x = 0; x < 2; x++)
 #pragma unroll
         for (int c = 0; c < C; c++) {
-          for (int e = 0; e < 8; e++) n[x][c][e] = ds[x][c][e] = 0.0f;
-          if (live && c < g.c) ld8<T, HALF>(raw_row(x, c, tok), l, g.r, VEC, n[x][c]);
-          rstd[x][c] = c < g.c ? norm(n[x][c]) : 0.0f;
+          const int j = x * C + c;
+          for (int e = 0; e < 8; e++) n[j][e] = ds[j][e] = 0.0f;
+          if (live && c < g.c) ld8<T, HALF>(raw_row(x, c, tok), l, g.r, VEC, n[j]);
+          rstd[j] = c < g.c ? norm(n[j]) : 0.0f;
         }
       for (int e = 0; e < 8; e++) dr1[e] = 0.0f;
       for (int i = 0; i < g.HL; i++) {
-        const int hg = i * g.HPP + hs, hi = gi * g.hpg + hg;
+        const int hg = i * HPP + hs, hi = gi * g.hpg + hg;
         if (!live || hg >= g.hpg) continue;
         QkRot<ROT> R;
         if constexpr (ROT != 0) {
           R.template load<VEC>(rot + rot_row(tok, hi), l, g);
-          R.make(l, g);
+          R.template make<sizeof(T) == 2>(l, g);
         }
         float dr[8];
         for (int e = 0; e < 8; e++) dr[e] = 0.0f;
@@ -597,7 +671,7 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
             if (c >= g.c) break;
             float d[8];
             ld8<T, HALF>(hat_row(x, c, tok, hi), l, g.r, VEC, d);
-            qk_row_grad<ROT>(R, n[x][c], w[x], b8, d, dr, sb, ds[x][c]);
+            qk_row_grad<ROT>(R, n[x * C + c], w[x], b8, d, dr, sb, ds[x * C + c]);
           }
 #pragma unroll
           for (int e = 0; e < 8; e++) acc[(i * 16 + 8 * x + e) * NT + threadIdx.x] += sb[e];
@@ -609,27 +683,33 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
       }
       if constexpr (ROT != 0)
         if (part_rot != nullptr) st_rot1(tok, live, dr1);
-#pragma unroll
-      for (int x = 0; x < 2; x++)
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-          if (c >= g.c) break;
-          finish(x, c, tok, live, n[x][c], rstd[x][c], ds[x][c]);
-        }
+      finish(tok, live, n, rstd, ds);
     }
   }
   // the block's sums, in a fixed order: over the token slots of its waves. src [16][threads];
-  // heads hs0 + (head slot) of the group, or (isw) d_w, which all head slots have alike
+  // heads hs0 + (head slot) of the group, or (isw) d_w, over the head slots that own rows of
+  // q (of k) and write them
   const int NTS = NWV * TPW;
   float* red = acc + (LDSB ? (size_t)g.HL * 16 * NT : 0);
   auto sum_block = [&](const float* src, int hs0, bool isw) {
     float* part = isw ? part_w : part_b;
     if (part == nullptr) return;
-    for (int id = threadIdx.x; id < g.HPP * 16 * LPR; id += NT) {
+    for (int id = threadIdx.x; id < HPP * 16 * LPR; id += NT) {
       const int ll = id % LPR, ve = id / LPR % 16, hh = id / (16 * LPR), x = ve / 8, e = ve % 8;
       if (!qk_has<HALF>(ll, e, g.r) || (isw ? hh > 0 : hs0 + hh >= g.hpg)) continue;
       double s = 0.0;
-      for (int t = 0; t < NTS; t++) s += (double)src[ve * NT + (t / TPW) * 64 + ((t % TPW) * g.HPP + hh) * LPR + ll];
+      for (int t = 0; t < NTS; t++) {
+        const int th = (t / TPW) * 64 + (t % TPW) * HPP * LPR + ll;
+        if (!isw) {
+          s += (double)src[ve * NT + th + hh * LPR];
+        } else {
+          for (int o = 0; o < HPP; o++) {
+            if (!qk_own_writes(N, HPP, o)) continue;
+            if (own > C) s += (double)src[ve * NT + th + o * LPR];
+            else if (qk_own_row(N, HPP, o) / C == x) s += (double)src[e * NT + th + o * LPR];
+          }
+        }
+      }
       const size_t row = isw ? ((size_t)x * g.nblk + blockIdx.x) * g.g + gi
                              : ((size_t)x * g.nblk + blockIdx.x) * g.h + gi * g.hpg + hs0 + hh;
       part[row * g.r + qk_col<HALF>(ll, e, g.r)] = (float)s;
@@ -645,7 +725,7 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
   };
   if constexpr (LDSB) {
     __syncthreads();
-    for (int i = 0; i < g.HL; i++) sum_block(acc + (size_t)i * 16 * NT, i * g.HPP, false);
+    for (int i = 0; i < g.HL; i++) sum_block(acc + (size_t)i * 16 * NT, i * HPP, false);
   } else {
 #pragma unroll
     for (int i = 0; i < NB; i++) {
@@ -653,7 +733,7 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
       for (int x = 0; x < 2; x++)
         for (int e = 0; e < 8; e++) v[x][e] = db[x][i][e];
       to_red(v);
-      sum_block(red, i * g.HPP, false);
+      sum_block(red, i * HPP, false);
     }
   }
   to_red(dw);

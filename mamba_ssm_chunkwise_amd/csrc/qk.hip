@@ -62,13 +62,14 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
   g.qs = (size_t)qs; g.ks = (size_t)ks;
   g.rot_h = (int)d->rot_h; g.A = A; g.J = J; g.RW = J > 0 ? 4 * J : A;
   g.eps = d->eps;
+  g.rinv = 1.0f / (float)d->r;
   P->vec = g.r % 8 == 0 && qs * tsz % 16 == 0 && ks * tsz % 16 == 0 && A % 4 == 0;
   P->LPR = g.r <= 64 && P->vec ? 8 : 16;
   P->C = g.c <= 1 ? 1 : g.c <= 2 ? 2 : 4;
   if (P->empty) return MOMENTS_OK;
   g.hpg = g.h / g.g;
   const int rpw = 64 / P->LPR;
-  g.HPP = 1;
+  g.HPP = P->vec ? 1 : rpw;
   while (g.HPP < g.hpg && g.HPP < rpw) g.HPP *= 2;
   g.HL = (g.hpg + g.HPP - 1) / g.HPP;
   // sums for each head in registers while a head slot serves one or two heads, else in LDS:
@@ -92,16 +93,27 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
   return MOMENTS_OK;
 }
 
-// Calls f(TT<T>, IC<LPR>, IC<ROT>, IC<C>, IC<HB>, IC<VEC>) for the compiled variant of the
+// Calls f(TT<T>, IC<LPR>, IC<ROT>, IC<C>, IC<HB>, IC<HPP>, IC<VEC>) for the compiled variant of the
 // plan. Rows that are not whole pieces have one variant for all widths, channels and heads.
 template <class F>
 int with_qk(const QkPlan& P, int rot_kind, F&& f) {
   auto by_hb = [&](auto tt, auto lpr, auto rot, auto cc) -> int {
+    constexpr int RPW = 64 / decltype(lpr)::value;
     switch (P.HB) {
-      case 1: return f(tt, lpr, rot, cc, IC<1>{}, IC<1>{});
-      case 2: return f(tt, lpr, rot, cc, IC<2>{}, IC<1>{});
+      case 0: return f(tt, lpr, rot, cc, IC<0>{}, IC<RPW>{}, IC<1>{});
+      case 2:
+        if constexpr (decltype(cc)::value < 4) return f(tt, lpr, rot, cc, IC<2>{}, IC<RPW>{}, IC<1>{});
+        break;
+      case 1:
+        switch (P.g.HPP) {
+          case 1: return f(tt, lpr, rot, cc, IC<1>{}, IC<1>{}, IC<1>{});
+          case 2: return f(tt, lpr, rot, cc, IC<1>{}, IC<2>{}, IC<1>{});
+          case 4: return f(tt, lpr, rot, cc, IC<1>{}, IC<4>{}, IC<1>{});
+          case 8:
+            if constexpr (RPW == 8) return f(tt, lpr, rot, cc, IC<1>{}, IC<8>{}, IC<1>{});
+        }
     }
-    return f(tt, lpr, rot, cc, IC<0>{}, IC<1>{});
+    return MOMENTS_ENOTSUP;   // no plan has another combination
   };
   auto by_c = [&](auto tt, auto lpr, auto rot) -> int {
     switch (P.C) {
@@ -111,7 +123,7 @@ int with_qk(const QkPlan& P, int rot_kind, F&& f) {
     return by_hb(tt, lpr, rot, IC<4>{});
   };
   auto by_lpr = [&](auto tt, auto rot) -> int {
-    if (!P.vec) return f(tt, IC<16>{}, rot, IC<4>{}, IC<0>{}, IC<0>{});
+    if (!P.vec) return f(tt, IC<16>{}, rot, IC<4>{}, IC<0>{}, IC<4>{}, IC<0>{});
     return P.LPR == 8 ? by_c(tt, IC<8>{}, rot) : by_c(tt, IC<16>{}, rot);
   };
   auto by_rot = [&](auto tt) -> int {
@@ -148,7 +160,7 @@ int moments_qk_fwd(const moments_qk_desc* desc, const void* q, const void* k, co
   for (const void* p : ptrs)
     if (p != nullptr && !aligned16(p)) return MOMENTS_EINVAL;
   hipStream_t st = (hipStream_t)stream;
-  return with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto vec) -> int {
+  return with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto hpp, auto vec) -> int {
     using T = typename decltype(tt)::type;
     constexpr int LPR = decltype(lpr)::value, ROT = decltype(rk)::value, C = decltype(cc)::value;
     ProfScope ps(KID_QK_FWD, st);
@@ -181,11 +193,11 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
   float* pw = d_wq || d_wk ? (float*)(ws + P.part_w) : nullptr;
   float* pb = d_bq || d_bk ? (float*)(ws + P.part_b) : nullptr;
   float* pr = rot1 && d_rot ? (float*)(ws + P.part_rot) : nullptr;
-  MOM_TRY(with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto vec) -> int {
+  MOM_TRY(with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto hpp, auto vec) -> int {
     using T = typename decltype(tt)::type;
     constexpr int LPR = decltype(lpr)::value, ROT = decltype(rk)::value, C = decltype(cc)::value;
     {
-      auto kernel = k_qk_bwd<T, LPR, ROT, C, decltype(hb)::value, decltype(vec)::value != 0>;
+      auto kernel = k_qk_bwd<T, LPR, ROT, C, decltype(hb)::value, decltype(hpp)::value, decltype(vec)::value != 0>;
       MOM_TRY(set_lds(kernel, P.lds));
       ProfScope ps(KID_QK_BWD, st);
       hipLaunchKernelGGL(kernel, dim3((unsigned)g.nblk, (unsigned)g.g), dim3(P.NT), P.lds, st, g, (const T*)q,
