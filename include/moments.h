@@ -236,7 +236,8 @@ int moments_rot_bwd(const moments_desc* desc, const void* inc, const void* d_rot
  * the kernels, as moments_attn_bwd_saved reads it (opaque; same descriptor and
  * inputs); moments_attn_bwd makes these itself from one more pass over xhat and bhat.
  *
- * Supported: 1 <= c <= 4, r <= 128, p <= 4096, s <= 2^28; h a multiple of g; b, s or h
+ * Supported: 1 <= c <= 4, r <= 128, p <= 4096, s <= 2^28, h * max(p, r) <= 2^23 (with the
+ * p/64 or p/128 tiles of 64 or 128 state rows: h * tiles * r too); h a multiple of g; b, s or h
  * may be 0 (nothing to do, but with s = 0 h_last is h0 and d_h0 is d_h_last). Rows of
  * r and p elements that are whole 16-byte pieces are read as such, others one element
  * at a time. Layout, alignment, ownership, errors and MOMENTS_CHECK_FINITE are those

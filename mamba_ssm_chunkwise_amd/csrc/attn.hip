@@ -18,6 +18,7 @@ struct AttnPlan {
   AttnGeo g;    // forward walk
   AttnGeo gb;   // backward walk (segments of its own)
   bool bf, empty;
+  bool vec;     // rows of r and of p are whole 16-byte pieces
   bool part;    // d_q, d_k (and d_da) by slices that k_attn_sum adds
   int RT;       // 16-column tiles of r: 4 or 8
   bool wide;    // 128 rows of p a workgroup (bf16, p > 64), else 64
@@ -44,6 +45,8 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   if (d->dtype != MOMENTS_F32 && d->dtype != MOMENTS_BF16) return MOMENTS_EINVAL;
   if (d->r > 128 || d->c > 4 || d->p > 4096 || d->s > (int64_t)1 << 28) return MOMENTS_ENOTSUP;
   if (d->b > (int64_t)1 << 24 || d->h > (int64_t)1 << 20 || d->b * d->h > (int64_t)1 << 24) return MOMENTS_ENOTSUP;
+  // a token row of a tensor: the kernels address the rows of a chunk with 32-bit offsets
+  if (d->h * d->p > (int64_t)1 << 23 || d->h * d->r > (int64_t)1 << 23) return MOMENTS_ENOTSUP;
   P->empty = d->b == 0 || d->h == 0;
   P->bf = d->dtype == MOMENTS_BF16;
   const int tsz = P->bf ? 2 : 4, L = P->bf ? AV<bf16>::L : AV<float>::L;
@@ -55,15 +58,15 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   g.CT = L / g.c;
   g.NK = (g.s + g.CT - 1) / g.CT;
   g.cinv = (65536 + g.c - 1) / g.c;
-  g.vq = (g.r * tsz) % 16 == 0;
-  g.vx = (g.p * tsz) % 16 == 0;
+  P->vec = (g.r * tsz) % 16 == 0 && (g.p * tsz) % 16 == 0;
   g.lens = (const int*)d->valid_lens;
   P->RT = g.r <= 64 ? 4 : 8;
   P->wide = P->bf && g.p > 64;
   g.PT = P->wide ? 128 : 64;
   g.npt = (g.p + g.PT - 1) / g.PT;
   P->items = g.b * g.h * g.npt;
-  if ((int64_t)g.b * g.h * g.npt > (int64_t)1 << 24) return MOMENTS_ENOTSUP;
+  if ((int64_t)g.b * g.h * g.npt > (int64_t)1 << 24 || (int64_t)g.h * g.npt * g.r > (int64_t)1 << 23)
+    return MOMENTS_ENOTSUP;
   P->gb = g;
   if (!P->empty) {
     split(g, P->items, 2 * kCUs);      // two workgroups of the walk share a CU
@@ -96,33 +99,36 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   return MOMENTS_OK;
 }
 
-// Calls f(TT<T>, IC<RT>, IC<PW>) for the compiled variant of the plan.
+// Calls f(TT<T>, IC<RT>, IC<PW>, IC<VEC>) for the compiled variant of the plan.
 template <class F>
 int with_attn(const AttnPlan& P, F&& f) {
+  auto by_vec = [&](auto tt, auto rt, auto pw) -> int {
+    return P.vec ? f(tt, rt, pw, IC<1>{}) : f(tt, rt, pw, IC<0>{});
+  };
   if (P.bf) {
-    if (P.RT == 4) return P.wide ? f(TT<bf16>{}, IC<4>{}, IC<2>{}) : f(TT<bf16>{}, IC<4>{}, IC<1>{});
-    return P.wide ? f(TT<bf16>{}, IC<8>{}, IC<2>{}) : f(TT<bf16>{}, IC<8>{}, IC<1>{});
+    if (P.RT == 4) return P.wide ? by_vec(TT<bf16>{}, IC<4>{}, IC<2>{}) : by_vec(TT<bf16>{}, IC<4>{}, IC<1>{});
+    return P.wide ? by_vec(TT<bf16>{}, IC<8>{}, IC<2>{}) : by_vec(TT<bf16>{}, IC<8>{}, IC<1>{});
   }
-  return P.RT == 4 ? f(TT<float>{}, IC<4>{}, IC<1>{}) : f(TT<float>{}, IC<8>{}, IC<1>{});
+  return P.RT == 4 ? by_vec(TT<float>{}, IC<4>{}, IC<1>{}) : by_vec(TT<float>{}, IC<8>{}, IC<1>{});
 }
 
-template <typename T, int RT, int PW, int MODE>
+template <typename T, int RT, int PW, int MODE, bool VEC>
 int launch_walk(const AttnGeo& g, int nseg, const T* x, const T* k, const T* q, const T* da, const float* h0, T* y,
                 float* h_last, T* save, float* seg_loc, double* seg_dec, hipStream_t st) {
   using LD = LdsA<T, RT, PW>;
   const size_t lds = MODE == 0 ? LD::total : LD::state_total;
-  MOM_TRY(set_lds(k_attn_walk<T, RT, PW, MODE>, lds));
+  MOM_TRY(set_lds(k_attn_walk<T, RT, PW, MODE, VEC>, lds));
   ProfScope ps(MODE == 0 ? KID_ATTN_FWD : KID_ATTN_STATE, st);
-  hipLaunchKernelGGL((k_attn_walk<T, RT, PW, MODE>), dim3((unsigned)((size_t)g.b * g.h * g.npt * nseg)), dim3(ATT),
+  hipLaunchKernelGGL((k_attn_walk<T, RT, PW, MODE, VEC>), dim3((unsigned)((size_t)g.b * g.h * g.npt * nseg)), dim3(ATT),
                      lds, st, g, x, k, q, da, h0, y, h_last, save, seg_loc, seg_dec);
   return check_launch();
 }
 
 // The states that the segments of the forward walk leave, each from zero.
-template <typename T, int RT, int PW>
+template <typename T, int RT, int PW, bool VEC>
 int run_segments(const AttnPlan& P, const T* x, const T* k, const T* da, unsigned char* ws, hipStream_t st) {
   if (P.g.nseg < 2) return 0;
-  return launch_walk<T, RT, PW, 1>(P.g, P.g.nseg - 1, x, k, nullptr, da, nullptr, nullptr, nullptr, nullptr,
+  return launch_walk<T, RT, PW, 1, VEC>(P.g, P.g.nseg - 1, x, k, nullptr, da, nullptr, nullptr, nullptr, nullptr,
                                    (float*)ws, (double*)(ws + P.seg_dec), st);
 }
 
@@ -143,11 +149,12 @@ int attn_fwd(const moments_attn_desc* desc, const void* x, const void* k, const 
   unsigned char* ws = (unsigned char*)workspace;
   float* seg = P.g.nseg > 1 ? (float*)ws : nullptr;
   double* sdec = P.g.nseg > 1 ? (double*)(ws + P.seg_dec) : nullptr;
-  MOM_TRY(with_attn(P, [&](auto tt, auto rt, auto pw) -> int {
+  MOM_TRY(with_attn(P, [&](auto tt, auto rt, auto pw, auto vec) -> int {
+    constexpr bool VEC = decltype(vec)::value != 0;
     using T = typename decltype(tt)::type;
     constexpr int RT = decltype(rt)::value, PW = decltype(pw)::value;
-    MOM_TRY((run_segments<T, RT, PW>(P, (const T*)x, (const T*)k, (const T*)da, ws, st)));
-    return launch_walk<T, RT, PW, 0>(P.g, P.g.nseg, (const T*)x, (const T*)k, (const T*)q, (const T*)da, h0, (T*)y,
+    MOM_TRY((run_segments<T, RT, PW, VEC>(P, (const T*)x, (const T*)k, (const T*)da, ws, st)));
+    return launch_walk<T, RT, PW, 0, VEC>(P.g, P.g.nseg, (const T*)x, (const T*)k, (const T*)q, (const T*)da, h0, (T*)y,
                                      h_last, want_saved ? (T*)saved : nullptr, seg, sdec, st);
   }));
   if (check_finite_on()) {
@@ -183,15 +190,16 @@ int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const 
   if (workspace == nullptr || workspace_bytes < P.ws_bwd) return MOMENTS_EWORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   unsigned char* ws = (unsigned char*)workspace;
-  MOM_TRY(with_attn(P, [&](auto tt, auto rt, auto pw) -> int {
+  MOM_TRY(with_attn(P, [&](auto tt, auto rt, auto pw, auto vec) -> int {
+    constexpr bool VEC = decltype(vec)::value != 0;
     using T = typename decltype(tt)::type;
     constexpr int RT = decltype(rt)::value, PW = decltype(pw)::value, PT = 4 * PW;
     const T *xt = (const T*)x, *kt = (const T*)k, *qt = (const T*)q, *dat = (const T*)da, *dyt = (const T*)d_y;
     const T* copies = (const T*)saved;
     if (!use_saved) {   // the states entering the chunks, by a walk over k and x
       T* own = (T*)(ws + P.save);
-      MOM_TRY((run_segments<T, RT, PW>(P, xt, kt, dat, ws, st)));
-      MOM_TRY((launch_walk<T, RT, PW, 1>(P.g, P.g.nseg, xt, kt, nullptr, dat, h0, nullptr, nullptr, own,
+      MOM_TRY((run_segments<T, RT, PW, VEC>(P, xt, kt, dat, ws, st)));
+      MOM_TRY((launch_walk<T, RT, PW, 1, VEC>(P.g, P.g.nseg, xt, kt, nullptr, dat, h0, nullptr, nullptr, own,
                                          P.g.nseg > 1 ? (float*)ws : nullptr,
                                          P.g.nseg > 1 ? (double*)(ws + P.seg_dec) : nullptr, st)));
       copies = own;
@@ -202,7 +210,7 @@ int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const 
     if (g.nseg > 1) {
       AttnGeo g2 = g;
       g2.seg0 = 1;
-      MOM_TRY((launch_walk<T, RT, PW, 2>(g2, g.nseg - 1, dyt, qt, nullptr, dat, nullptr, nullptr, nullptr, nullptr,
+      MOM_TRY((launch_walk<T, RT, PW, 2, VEC>(g2, g.nseg - 1, dyt, qt, nullptr, dat, nullptr, nullptr, nullptr, nullptr,
                                          seg, sdec, st)));
     }
     float* pq = (float*)(ws + P.part_q);
@@ -212,9 +220,9 @@ int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const 
       constexpr bool PART = decltype(part)::value != 0;
       const size_t lds = LdsB<T, RT, PT>::total;
       static_assert(LdsB<T, RT, PT>::total <= kLdsLimit, "LDS");
-      MOM_TRY(set_lds(k_attn_bwd<T, RT, PT, PART>, lds));
+      MOM_TRY(set_lds(k_attn_bwd<T, RT, PT, PART, VEC>, lds));
       ProfScope ps(KID_ATTN_BWD, st);
-      hipLaunchKernelGGL((k_attn_bwd<T, RT, PT, PART>), dim3((unsigned)((size_t)P.items * g.nseg)), dim3(ABT), lds, st,
+      hipLaunchKernelGGL((k_attn_bwd<T, RT, PT, PART, VEC>), dim3((unsigned)((size_t)P.items * g.nseg)), dim3(ABT), lds, st,
                          g, xt, kt, qt, dat, copies, dyt, d_last, seg, sdec, (T*)d_x, (T*)d_k, (T*)d_q, (T*)d_da,
                          d_h0, pk, pq, pa);
       return check_launch();

@@ -42,7 +42,6 @@ struct AttnGeo {
   int npt;      // column tiles of the state rows p that separate workgroups take
   int PT;       // rows of p in such a tile
   int cinv;     // ceil(65536 / c): u / c = (u * cinv) >> 16 for a row u of a chunk
-  int vq, vx;   // 16-byte pieces of a q/k row, of an x/y row: rows are whole pieces (else element-wise)
   const int* lens;  // per-sequence valid lengths [b] (device), or nullptr
 };
 
@@ -197,31 +196,22 @@ struct Scaled<1> {
 };
 
 // ---- staging ----------------------------------------------------------------
-// Piece `piece` (PE elements) of a row of n elements at `row`; zeros past n. `vec`:
-// rows are 16-byte aligned and whole pieces.
-template <typename T>
-__device__ __forceinline__ uint4 ld_piece(const T* row, int piece, int n, bool vec) {
-  constexpr int PE = AV<T>::PE;
-  const int c0 = piece * PE;
-  if (vec) return c0 < n ? *reinterpret_cast<const uint4*>(row + c0) : make_uint4(0, 0, 0, 0);
-  T e[PE];
-#pragma unroll
-  for (int i = 0; i < PE; i++) e[i] = c0 + i < n ? row[c0 + i] : (T)0.0f;
-  return __builtin_bit_cast(uint4, e);
-}
-
-// A [L][columns] block of rows in flight from global memory to an LDS tile:
-// NP = L * columns / (threads * PE) pieces a thread. Rows >= nrows are zeros,
-// whatever the memory there holds.
+// A [L][COLS] block of rows on its way from global memory to an LDS tile, in 16-byte
+// pieces. Rows >= nrows and columns >= n are zeros, whatever the memory there holds.
+// Rows that are whole pieces go through registers (load, later store), so that they can
+// be in flight while another chunk is worked on; others are fetched one element at a
+// time, straight into the tile. Offsets inside a chunk fit 32 bits (the plan refuses
+// wider rows), so that addresses are a scalar base and one register.
 template <typename T, int COLS, int NT>
 struct Stage {
-  static constexpr int L = AV<T>::L, PR = COLS / AV<T>::PE, N = (L * PR + NT - 1) / NT;
+  static constexpr int L = AV<T>::L, PE = AV<T>::PE, PR = COLS / PE, N = (L * PR + NT - 1) / NT;
   uint4 v[N];
-  __device__ __forceinline__ void load(const T* base, size_t stride, int nrows, int n, bool vec) {
+  __device__ __forceinline__ void load(const T* base, unsigned stride, int nrows, int n) {
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int e = i * NT + (int)threadIdx.x, row = e / PR, piece = e % PR;
-      v[i] = row < nrows ? ld_piece(base + row * stride, piece, n, vec) : make_uint4(0, 0, 0, 0);
+      const int e = i * NT + (int)threadIdx.x, row = e / PR, c0 = e % PR * PE;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (row < nrows && c0 < n) v[i] = *reinterpret_cast<const uint4*>(base + ((unsigned)row * stride + (unsigned)c0));
     }
   }
   __device__ __forceinline__ void store(T* t, int P) const {
@@ -229,6 +219,17 @@ struct Stage {
     for (int i = 0; i < N; i++) {
       const int e = i * NT + (int)threadIdx.x, row = e / PR, piece = e % PR;
       if (L * PR % NT == 0 || row < L) st_piece(t, P, row, piece, v[i]);
+    }
+  }
+  __device__ __forceinline__ static void direct(T* t, int P, const T* base, unsigned stride, int nrows, int n) {
+#pragma unroll 1
+    for (int e = (int)threadIdx.x; e < L * PR; e += NT) {
+      const int row = e / PR, c0 = e % PR * PE;
+      T x[PE];
+#pragma unroll
+      for (int i = 0; i < PE; i++)
+        x[i] = row < nrows && c0 + i < n ? base[(unsigned)row * stride + (unsigned)(c0 + i)] : (T)0.0f;
+      st_piece(t, P, row, e % PR, __builtin_bit_cast(uint4, x));
     }
   }
 };
@@ -300,15 +301,17 @@ __device__ __forceinline__ void st_state4(float* st, int p, int r, int pi, int r
       if (r0 + i < r) s[i] = v[i];
   }
 }
-// Four consecutive columns of a row of n elements (quad-aligned when n % 4 == 0).
+// Four consecutive columns c0.. of the row of n elements at base[off] (quad-aligned when
+// n % 4 == 0).
 template <typename T>
-__device__ __forceinline__ void st_row4(T* row, int n, int c0, f4 v) {
+__device__ __forceinline__ void st_row4(T* base, unsigned off, int n, int c0, f4 v) {
+  off += (unsigned)c0;
   if ((n & 3) == 0) {
-    if (c0 < n) *reinterpret_cast<typename AV<T>::quad*>(row + c0) = to_quad<T>(v);
+    if (c0 < n) *reinterpret_cast<typename AV<T>::quad*>(base + off) = to_quad<T>(v);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; i++)
-      if (c0 + i < n) row[c0 + i] = to_t<T>(v[i]);
+      if (c0 + i < n) base[off + i] = to_t<T>(v[i]);
   }
 }
 
@@ -359,9 +362,10 @@ __device__ __forceinline__ void state_update(f4 (&H)[PW][RT], const T* ks, const
 //         last state and log2 decay there; without, the walk that only saves;
 // MODE 2: the cotangent of the state alone, chunks in reverse: k is q, x is d_y,
 //         and the weights are e^{a_u}.
-// A chain split into segments starts each of them from the states that the
+// VEC: rows are whole 16-byte pieces; the next chunk's are then in flight while one is
+// worked on. A chain split into segments starts each of them from the states that the
 // segments before it (after it, MODE 2 users) left in seg_loc.
-template <typename T, int RT, int PW, int MODE>
+template <typename T, int RT, int PW, int MODE, bool VEC>
 __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __restrict__ x, const T* __restrict__ k,
                                                       const T* __restrict__ q, const T* __restrict__ da,
                                                       const float* __restrict__ h0, T* __restrict__ y,
@@ -388,13 +392,12 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
   const int Vb = attn_len(g, bi), nkb = (Vb + g.CT - 1) / g.CT;
   const int n0 = seg * g.SL, n1 = min(n0 + g.SL, g.NK);
   const int p0 = pt * LD::PT, pn = min(g.p - p0, LD::PT);
-  const size_t kst = (size_t)g.g * g.r, xst = (size_t)g.h * g.p;   // strides of a row u
+  const unsigned kst = (unsigned)(g.g * g.r), xst = (unsigned)(g.h * g.p);   // strides of a row u
   const size_t row0 = (size_t)bi * g.s * g.c;
   const T* kb = k + row0 * kst + (size_t)gi * g.r;
   const T* qb = MODE == 0 ? q + row0 * kst + (size_t)gi * g.r : nullptr;
   const T* xb = x + row0 * xst + (size_t)hi * g.p + p0;
   const T* dab = da + (size_t)bi * g.s * g.h + hi;
-  const bool vq = g.vq != 0, vx = g.vx != 0;
   constexpr size_t TILES = (size_t)PT16 * RT * 256;   // values of a state in tile order
 
   f4 H[PW][RT];
@@ -425,30 +428,39 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
   double acc_dec = 0.0;
 
   const int nlive = min(n1, nkb);
-  for (int i = n0; i < nlive; i++) {
-    const int n = MODE == 2 ? nlive - 1 - (i - n0) : i;
+  Stage<T, 16 * RT, ATT> sk, sq;
+  Stage<T, LD::PT, ATT> sx;
+  T dnext = (T)0.0f;                        // da of the token that row u = lane opens
+  const int ltok = (lane * g.cinv) >> 16;   // the token of row u = lane
+  auto chunk = [&](int i) { return MODE == 2 ? nlive - 1 - (i - n0) : i; };
+  auto fetch = [&](int n) {
     const int t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
     const size_t u0 = (size_t)t0 * g.c;
+    if constexpr (VEC) {
+      sk.load(kb + u0 * kst, kst, nrows, g.r);
+      sx.load(xb + u0 * xst, xst, nrows, pn);
+      if constexpr (MODE == 0) sq.load(qb + u0 * kst, kst, nrows, g.r);
+    }
+    dnext = (T)0.0f;
+    if (wave == 0 && lane < nrows && ltok * g.c == lane) dnext = dab[(size_t)(t0 + ltok) * g.h];
+  };
+  if (nlive > n0) fetch(chunk(n0));
+  for (int i = n0; i < nlive; i++) {
+    const int n = chunk(i), t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
+    const size_t u0 = (size_t)t0 * g.c;
     __syncthreads();   // the last chunk's tiles have been read
-    {
-      Stage<T, 16 * RT, ATT> sk;
-      Stage<T, LD::PT, ATT> sx;
-      sk.load(kb + u0 * kst, kst, nrows, g.r, vq);
-      sx.load(xb + u0 * xst, xst, nrows, pn, vx);
-      if constexpr (MODE == 0) {
-        Stage<T, 16 * RT, ATT> sq;
-        sq.load(qb + u0 * kst, kst, nrows, g.r, vq);
-        sq.store(qs, LD::RP);
-      }
+    if constexpr (VEC) {
       sk.store(ks, LD::RP);
       sx.store(xs, LD::PP);
+      if constexpr (MODE == 0) sq.store(qs, LD::RP);
+    } else {
+      sk.direct(ks, LD::RP, kb + u0 * kst, kst, nrows, g.r);
+      sx.direct(xs, LD::PP, xb + u0 * xst, xst, nrows, pn);
+      if constexpr (MODE == 0) sq.direct(qs, LD::RP, qb + u0 * kst, kst, nrows, g.r);
     }
-    if (wave == 0) {
-      const int tok = (lane * g.cinv) >> 16;
-      const bool opens = lane < nrows && tok * g.c == lane;
-      decay_table(tab, opens ? log2_decay(to_f(dab[(size_t)(t0 + tok) * g.h])) : 0.0, lane);
-    }
+    if (wave == 0) decay_table(tab, log2_decay(to_f(dnext)), lane);
     __syncthreads();
+    if (i + 1 < nlive) fetch(chunk(i + 1));
     const double total = tab->total;
     acc_dec += total;
 
@@ -526,9 +538,10 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
           }
         }
         if (u < nrows) {
-          T* yr = y + (row0 + u0 + u) * xst + (size_t)hi * g.p;
 #pragma unroll
-          for (int pw = 0; pw < PW; pw++) st_row4(yr, g.p, p0 + 16 * (wave * PW + pw) + 4 * lq, a[pw]);
+          for (int pw = 0; pw < PW; pw++)
+            st_row4(y + (row0 + u0) * xst + (size_t)hi * g.p, (unsigned)u * xst, g.p,
+                    p0 + 16 * (wave * PW + pw) + 4 * lq, a[pw]);
         }
       }
     }

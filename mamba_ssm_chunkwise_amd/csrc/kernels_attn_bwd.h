@@ -34,10 +34,8 @@ struct LdsB {
                        SP = TIGHT ? L + 8 : AV<T>::pitch(L);
   static constexpr size_t E = sizeof(T);
   static constexpr size_t tab = 0;
-  // rsum[4][64], csum[4][64], th[16], and up[8][64], vp[8][64], which with TIGHT lie in the
-  // four floats of padding behind each of the 128 rows of hs and gs instead
-  static constexpr size_t sums = sizeof(DecayTab);
-  static constexpr size_t k = sums + (4 + 4 + (TIGHT ? 0 : 16)) * 64 * 4 + 64;
+  static constexpr size_t sums = sizeof(DecayTab);   // rsum, csum, up, vp [4][64], th[8]
+  static constexpr size_t k = sums + 16 * 64 * 4 + 32;
   static constexpr size_t q = k + (size_t)L * RP * E, x = q + (size_t)L * RP * E, dy = x + (size_t)L * PP * E,
                           s = dy + (size_t)L * PP * E, t = s + (size_t)L * SP * E,
                           hs = t + (size_t)L * SP * E, gs = hs + (size_t)16 * PT * RP * E,
@@ -75,8 +73,9 @@ struct StageH {
 
 // PART: d_q and d_k go, in float32, to a slice of their own for each head and p tile
 // (heads that share keys, or state rows in several tiles; k_attn_sum adds them), and
-// d_da likewise for each p tile; otherwise straight to the caller's tensors.
-template <typename T, int RT, int PT, bool PART>
+// d_da likewise for each p tile; otherwise straight to the caller's tensors. VEC as in
+// k_attn_walk.
+template <typename T, int RT, int PT, bool PART, bool VEC>
 __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     AttnGeo g, const T* __restrict__ x, const T* __restrict__ k, const T* __restrict__ q, const T* __restrict__ da,
     const T* __restrict__ save, const T* __restrict__ dy, const float* __restrict__ d_last,
@@ -92,7 +91,9 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
   DecayTab* tab = reinterpret_cast<DecayTab*>(lds + LD::tab);
   float* rsum = reinterpret_cast<float*>(lds + LD::sums);   // [jt][u]
   float* csum = rsum + 4 * 64;                              // [ut][j]
-  float* th = csum + 4 * 64;                                // [wave]
+  float* up = csum + 4 * 64;                                // [wave along r][u]
+  float* vp = up + 4 * 64;                                  // [wave along r][j]
+  float* th = vp + 4 * 64;                                  // [wave]
   T* ks = reinterpret_cast<T*>(lds + LD::k);
   T* qs = reinterpret_cast<T*>(lds + LD::q);
   T* xs = reinterpret_cast<T*>(lds + LD::x);
@@ -101,15 +102,6 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
   T* ts = reinterpret_cast<T*>(lds + LD::t);
   T* hs = reinterpret_cast<T*>(lds + LD::hs);
   T* gs = reinterpret_cast<T*>(lds + LD::gs);
-  // sums over a tile of 16 columns r, [rt][u] and [rt][j]
-  auto up = [&](int rt, int u) -> float& {
-    if constexpr (LD::TIGHT) return reinterpret_cast<float*>(hs + (16 * rt + (u >> 2)) * LD::RP + 16 * RT)[u & 3];
-    return th[16 + rt * 64 + u];
-  };
-  auto vp = [&](int rt, int j) -> float& {
-    if constexpr (LD::TIGHT) return reinterpret_cast<float*>(gs + (16 * rt + (j >> 2)) * LD::RP + 16 * RT)[j & 3];
-    return th[16 + (8 + rt) * 64 + j];
-  };
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ln = lane & 15, lq = lane >> 4;
 
@@ -121,18 +113,17 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
   const int Vb = attn_len(g, bi), nkb = (Vb + g.CT - 1) / g.CT;
   const int n0 = seg * g.SL, n1 = min(n0 + g.SL, g.NK);
   const int p0 = pt * 16 * PT, pn = min(g.p - p0, 16 * PT);
-  const size_t kst = (size_t)g.g * g.r, xst = (size_t)g.h * g.p;
+  const unsigned kst = (unsigned)(g.g * g.r), xst = (unsigned)(g.h * g.p);
   const size_t row0 = (size_t)bi * g.s * g.c;
   const T* kb = k + row0 * kst + (size_t)gi * g.r;
   const T* qb = q + row0 * kst + (size_t)gi * g.r;
   const T* xb = x + row0 * xst + (size_t)hi * g.p + p0;
   const T* yb = dy + row0 * xst + (size_t)hi * g.p + p0;
   const T* dab = da + (size_t)bi * g.s * g.h + hi;
-  const bool vq = g.vq != 0, vx = g.vx != 0;
   constexpr size_t TILES = (size_t)PT * RT * 256;
   // slices: rows of h * npt * r values (d_q, d_k) and h * npt values a token (d_da)
   const int slice = hi * g.npt + pt;
-  const size_t pst = (size_t)g.h * g.npt * g.r;
+  const unsigned pst = (unsigned)(g.h * g.npt * g.r);
 
   const int mp = wave % PT, mr = (wave / PT) * RW;   // this wave's p tile and first r tile of G
   f4 G[RW];
@@ -151,33 +142,47 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
   }
 
   const int nlive = min(n1, nkb);
+  // the next chunk's rows, in flight while this one is worked on
+  Stage<T, 16 * RT, ABT> sk, sq;
+  Stage<T, 16 * PT, ABT> sx, sy;
+  StageH<T, RT, PT> sh;
+  T dnext = (T)0.0f;
+  const int ltok = (lane * g.cinv) >> 16;   // the token of row u = lane
+  auto fetch = [&](int n) {
+    const int t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
+    const size_t u0 = (size_t)t0 * g.c;
+    if constexpr (VEC) {
+      sk.load(kb + u0 * kst, kst, nrows, g.r);
+      sq.load(qb + u0 * kst, kst, nrows, g.r);
+      sx.load(xb + u0 * xst, xst, nrows, pn);
+      sy.load(yb + u0 * xst, xst, nrows, pn);
+    }
+    sh.load(save + (((size_t)chain * g.NK + n) * g.npt + pt) * TILES);
+    dnext = (T)0.0f;
+    if (wave == 0 && lane < nrows && ltok * g.c == lane) dnext = dab[(size_t)(t0 + ltok) * g.h];
+  };
+  if (nlive > n0) fetch(nlive - 1);
   for (int n = nlive - 1; n >= n0; n--) {
     const int t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
     const size_t u0 = (size_t)t0 * g.c;
-    {
-      Stage<T, 16 * RT, ABT> sk, sq;
-      Stage<T, 16 * PT, ABT> sx, sy;
-      StageH<T, RT, PT> sh;
-      sk.load(kb + u0 * kst, kst, nrows, g.r, vq);
-      sq.load(qb + u0 * kst, kst, nrows, g.r, vq);
-      sx.load(xb + u0 * xst, xst, nrows, pn, vx);
-      sy.load(yb + u0 * xst, xst, nrows, pn, vx);
-      sh.load(save + (((size_t)chain * g.NK + n) * g.npt + pt) * TILES);
-      // (the barrier that ended the last chunk covers these writes)
+    // (the barrier that ended the last chunk covers these writes)
+    if constexpr (VEC) {
       sk.store(ks, LD::RP);
       sq.store(qs, LD::RP);
       sx.store(xs, LD::PP);
       sy.store(ys, LD::PP);
-      sh.store(hs, LD::RP);
+    } else {
+      sk.direct(ks, LD::RP, kb + u0 * kst, kst, nrows, g.r);
+      sq.direct(qs, LD::RP, qb + u0 * kst, kst, nrows, g.r);
+      sx.direct(xs, LD::PP, xb + u0 * xst, xst, nrows, pn);
+      sy.direct(ys, LD::PP, yb + u0 * xst, xst, nrows, pn);
     }
+    sh.store(hs, LD::RP);
 #pragma unroll
     for (int i = 0; i < RW; i++) st_quad(gs, LD::RP, 16 * mp + ln, 4 * (mr + i) + lq, to_quad<T>(G[i]));
-    if (wave == 0) {
-      const int tok = (lane * g.cinv) >> 16;
-      const bool opens = lane < nrows && tok * g.c == lane;
-      decay_table(tab, opens ? log2_decay(to_f(dab[(size_t)(t0 + tok) * g.h])) : 0.0, lane);
-    }
+    if (wave == 0) decay_table(tab, log2_decay(to_f(dnext)), lane);
     __syncthreads();
+    if (n > n0) fetch(n - 1);
     const float dec = ex2((float)tab->total);
 
     // <G, H> of this wave's tiles
@@ -232,69 +237,152 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     }
     __syncthreads();
 
-    // d_q and d_k, r tile by r tile (transposed: columns are rows u of the chunk)
+    // d_q and d_k (transposed: columns are rows u of the chunk). A wave takes RB r tiles by
+    // UB tiles of rows, and keeps the operands of its r tiles.
+    {
+      constexpr int RB = RT * NT >= 16 ? 2 : 1, WR = RT / RB, WU = ABW / WR, UB = NT / WU;
+      static_assert(WR * WU == ABW && UB * WU == NT && WR <= 4, "tiles and waves");
+      const int wr = wave % WR, rt0 = wr * RB, ut0 = wave / WR * UB;
+      {
+        typename V::frag hf[RB][PT / 2], kf[RB][NJ];
 #pragma unroll
-    for (int it = 0; it < (RT * NT + ABW - 1) / ABW; it++) {
-      const int id = it * ABW + wave, rt = id % RT, ut = id / RT;
-      if (RT * NT % ABW != 0 && id >= RT * NT) break;
-      const int u = 16 * ut + ln, r0 = 16 * rt + 4 * lq;
-      const bool live = u < nrows;
-      const size_t at = row0 + u0 + u;
-      f4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < RB; i++) {
 #pragma unroll
-      for (int m = 0; m < PT / 2; m++)
-        a = mma32(col_frag(hs, LD::RP, m, 16 * rt, lane), row_frag(ys, LD::PP, 16 * ut, m, lane), a);
-      a *= tab->start[u];
-      const f4 qv = quad_f(ld_quad(qs, LD::RP, u, 4 * rt + lq));
-      const float us = col4_sum(a[0] * qv[0] + a[1] * qv[1] + a[2] * qv[2] + a[3] * qv[3]);
-      if (lq == 0) up(rt, u) = us;
+          for (int m = 0; m < PT / 2; m++) hf[i][m] = col_frag(hs, LD::RP, m, 16 * (rt0 + i), lane);
 #pragma unroll
-      for (int m = 0; m < NJ; m++)
-        if (32 * m < 16 * (ut + 1) || g.c == 3)
-          a = mma32(col_frag(ks, LD::RP, m, 16 * rt, lane), row_frag(ts, LD::SP, 16 * ut, m, lane), a);
-      if (live) {
-        if constexpr (PART)
-          st_row4(part_q + at * pst + (size_t)slice * g.r, g.r, r0, a);
-        else if (d_q != nullptr)
-          st_row4(d_q + at * kst + (size_t)gi * g.r, g.r, r0, a);
+          for (int m = 0; m < NJ; m++) kf[i][m] = col_frag(ks, LD::RP, m, 16 * (rt0 + i), lane);
+        }
+#pragma unroll
+        for (int j = 0; j < UB; j++) {
+          const int ut = ut0 + j, u = 16 * ut + ln;
+          f4 a[RB];
+#pragma unroll
+          for (int i = 0; i < RB; i++) a[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int m = 0; m < PT / 2; m++) {
+            const auto yf = row_frag(ys, LD::PP, 16 * ut, m, lane);
+#pragma unroll
+            for (int i = 0; i < RB; i++) a[i] = mma32(hf[i][m], yf, a[i]);
+          }
+          const float st = tab->start[u];
+          float us = 0.0f;
+#pragma unroll
+          for (int i = 0; i < RB; i++) {
+            a[i] *= st;
+            const f4 qv = quad_f(ld_quad(qs, LD::RP, u, 4 * (rt0 + i) + lq));
+            us += a[i][0] * qv[0] + a[i][1] * qv[1] + a[i][2] * qv[2] + a[i][3] * qv[3];
+          }
+          us = col4_sum(us);
+          if (lq == 0) up[wr * 64 + u] = us;
+#pragma unroll
+          for (int m = 0; m < NJ; m++)
+            if (32 * m < 16 * (ut + 1) || g.c == 3) {
+              const auto tf = row_frag(ts, LD::SP, 16 * ut, m, lane);
+#pragma unroll
+              for (int i = 0; i < RB; i++) a[i] = mma32(kf[i][m], tf, a[i]);
+            }
+          if (u < nrows) {
+#pragma unroll
+            for (int i = 0; i < RB; i++) {
+              const int r0 = 16 * (rt0 + i) + 4 * lq;
+              if constexpr (PART)
+                st_row4(part_q + (row0 + u0) * pst + (size_t)slice * g.r, (unsigned)u * pst, g.r, r0, a[i]);
+              else if (d_q != nullptr)
+                st_row4(d_q + (row0 + u0) * kst + (size_t)gi * g.r, (unsigned)u * kst, g.r, r0, a[i]);
+            }
+          }
+        }
       }
-      f4 b = {0.0f, 0.0f, 0.0f, 0.0f};
+      __builtin_amdgcn_sched_barrier(0);
+      {
+        typename V::frag gf[RB][PT / 2], qf[RB][NJ];
 #pragma unroll
-      for (int m = 0; m < PT / 2; m++)
-        b = mma32(col_frag(gs, LD::RP, m, 16 * rt, lane), row_frag(xs, LD::PP, 16 * ut, m, lane), b);
-      b *= tab->end[u];
-      const f4 kv = quad_f(ld_quad(ks, LD::RP, u, 4 * rt + lq));
-      const float vs = col4_sum(b[0] * kv[0] + b[1] * kv[1] + b[2] * kv[2] + b[3] * kv[3]);
-      if (lq == 0) vp(rt, u) = vs;
+        for (int i = 0; i < RB; i++) {
 #pragma unroll
-      for (int m = 0; m < NJ; m++)
-        if (32 * (m + 1) > 16 * ut || g.c == 3)
-          b = mma32(col_frag(qs, LD::RP, m, 16 * rt, lane), col_frag(ts, LD::SP, m, 16 * ut, lane), b);
-      if (live) {
-        if constexpr (PART)
-          st_row4(part_k + at * pst + (size_t)slice * g.r, g.r, r0, b);
-        else if (d_k != nullptr)
-          st_row4(d_k + at * kst + (size_t)gi * g.r, g.r, r0, b);
+          for (int m = 0; m < PT / 2; m++) gf[i][m] = col_frag(gs, LD::RP, m, 16 * (rt0 + i), lane);
+#pragma unroll
+          for (int m = 0; m < NJ; m++) qf[i][m] = col_frag(qs, LD::RP, m, 16 * (rt0 + i), lane);
+        }
+#pragma unroll
+        for (int j = 0; j < UB; j++) {
+          const int ut = ut0 + j, u = 16 * ut + ln;
+          f4 b[RB];
+#pragma unroll
+          for (int i = 0; i < RB; i++) b[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int m = 0; m < PT / 2; m++) {
+            const auto xf = row_frag(xs, LD::PP, 16 * ut, m, lane);
+#pragma unroll
+            for (int i = 0; i < RB; i++) b[i] = mma32(gf[i][m], xf, b[i]);
+          }
+          const float en = tab->end[u];
+          float vs = 0.0f;
+#pragma unroll
+          for (int i = 0; i < RB; i++) {
+            b[i] *= en;
+            const f4 kv = quad_f(ld_quad(ks, LD::RP, u, 4 * (rt0 + i) + lq));
+            vs += b[i][0] * kv[0] + b[i][1] * kv[1] + b[i][2] * kv[2] + b[i][3] * kv[3];
+          }
+          vs = col4_sum(vs);
+          if (lq == 0) vp[wr * 64 + u] = vs;
+#pragma unroll
+          for (int m = 0; m < NJ; m++)
+            if (32 * (m + 1) > 16 * ut || g.c == 3) {
+              const auto tf = col_frag(ts, LD::SP, m, 16 * ut, lane);
+#pragma unroll
+              for (int i = 0; i < RB; i++) b[i] = mma32(qf[i][m], tf, b[i]);
+            }
+          if (u < nrows) {
+#pragma unroll
+            for (int i = 0; i < RB; i++) {
+              const int r0 = 16 * (rt0 + i) + 4 * lq;
+              if constexpr (PART)
+                st_row4(part_k + (row0 + u0) * pst + (size_t)slice * g.r, (unsigned)u * pst, g.r, r0, b[i]);
+              else if (d_k != nullptr)
+                st_row4(d_k + (row0 + u0) * kst + (size_t)gi * g.r, (unsigned)u * kst, g.r, r0, b[i]);
+            }
+          }
+        }
       }
     }
-    // d_x
+    // d_x, likewise over PB tiles of rows p
+    __builtin_amdgcn_sched_barrier(0);
+    {
+      constexpr int PB = PT * NT >= 16 ? 2 : 1, WP = PT / PB, WU = ABW / WP, UB = NT / WU > 0 ? NT / WU : 1;
+      static_assert(WP * WU == ABW && UB * WU == NT, "tiles and waves");
+      const int pj0 = wave % WP * PB, ut0 = wave / WP * UB;
 #pragma unroll
-    for (int it = 0; it < (PT * NT + ABW - 1) / ABW; it++) {
-      const int id = it * ABW + wave, pj = id % PT, ut = id / PT;
-      if (PT * NT % ABW != 0 && id >= PT * NT) break;
-      const int u = 16 * ut + ln;
-      f4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < UB; j++) {
+        const int ut = ut0 + j, u = 16 * ut + ln;
+        f4 a[PB];
 #pragma unroll
-      for (int m = 0; m < RT / 2; m++)
-        a = mma32(row_frag(gs, LD::RP, 16 * pj, m, lane), row_frag(ks, LD::RP, 16 * ut, m, lane), a);
-      a *= tab->end[u];
+        for (int i = 0; i < PB; i++) a[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int m = 0; m < NJ; m++)
-        if (32 * (m + 1) > 16 * ut || g.c == 3)
-          a = mma32(col_frag(ys, LD::PP, m, 16 * pj, lane), col_frag(ss, LD::SP, m, 16 * ut, lane), a);
-      if (u < nrows && d_x != nullptr) st_row4(d_x + (row0 + u0 + u) * xst + (size_t)hi * g.p, g.p, p0 + 16 * pj + 4 * lq, a);
+        for (int m = 0; m < RT / 2; m++) {
+          const auto kf = row_frag(ks, LD::RP, 16 * ut, m, lane);
+#pragma unroll
+          for (int i = 0; i < PB; i++) a[i] = mma32(row_frag(gs, LD::RP, 16 * (pj0 + i), m, lane), kf, a[i]);
+        }
+        const float en = tab->end[u];
+#pragma unroll
+        for (int i = 0; i < PB; i++) a[i] *= en;
+#pragma unroll
+        for (int m = 0; m < NJ; m++)
+          if (32 * (m + 1) > 16 * ut || g.c == 3) {
+            const auto sf = col_frag(ss, LD::SP, m, 16 * ut, lane);
+#pragma unroll
+            for (int i = 0; i < PB; i++) a[i] = mma32(col_frag(ys, LD::PP, m, 16 * (pj0 + i), lane), sf, a[i]);
+          }
+        if (u < nrows && d_x != nullptr) {
+#pragma unroll
+          for (int i = 0; i < PB; i++)
+            st_row4(d_x + (row0 + u0) * xst + (size_t)hi * g.p, (unsigned)u * xst, g.p, p0 + 16 * (pj0 + i) + 4 * lq,
+                    a[i]);
+        }
+      }
     }
     // G'
+    __builtin_amdgcn_sched_barrier(0);
     {
       Scaled<V::NSPLIT> yf[NJ];
 #pragma unroll
@@ -317,20 +405,19 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
         for (int i = 0; i < NT; i++) suf += (double)rsum[i * 64 + lane] - (double)csum[i * 64 + lane];
 #pragma unroll
-        for (int i = 0; i < RT; i++) {
-          suf += (double)up(i, lane);
-          pre += (double)vp(i, lane);
+        for (int i = 0; i < (RT * NT >= 16 ? RT / 2 : RT); i++) {
+          suf += (double)up[i * 64 + lane];
+          pre += (double)vp[i * 64 + lane];
         }
       }
-      for (int i = 0; i < (PT < ABW ? ABW : PT); i++) thr += (double)th[i];
+      for (int i = 0; i < ABW; i++) thr += (double)th[i];
       const double si = wave_sum_incl(suf, lane), pi = wave_sum_incl(pre, lane);
       const double v = __shfl(si, 63) - si + suf + pi - pre + thr * (double)dec;
-      const int tok = (lane * g.cinv) >> 16;
-      if (lane < nrows && tok * g.c == lane) {
+      if (lane < nrows && ltok * g.c == lane) {
         if constexpr (PART)
-          part_da[((size_t)bi * g.s + t0 + tok) * g.h * g.npt + slice] = (float)v;
+          part_da[((size_t)bi * g.s + t0 + ltok) * g.h * g.npt + slice] = (float)v;
         else if (d_da != nullptr)
-          d_da[((size_t)bi * g.s + t0 + tok) * g.h + hi] = to_t<T>((float)v);
+          d_da[((size_t)bi * g.s + t0 + ltok) * g.h + hi] = to_t<T>((float)v);
       }
     }
   }
