@@ -331,61 +331,38 @@ def moments_rot_bwd(desc: Desc, inc, d_rot, d_inc=None):
 
 
 # ---------------------------------------------------------------- linear attention
-def _dt(desc):
-    return torch.bfloat16 if desc.dtype == BF16 else torch.float32
+# These entry points also serve single tokens, where the host's time counts: tensors are
+# checked in one pass and pointers go to the library as plain integers.
+_DTYPES = {F32: torch.float32, BF16: torch.bfloat16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def attn_desc(xhat, bhat, valid_len=None, valid_lens=None, dtype=None) -> AttnDesc:
-    """Descriptor of linear attention for xhat [b,s,c,h,p] and keys bhat
-    [b,s,c,g,r] of g groups of heads. ``valid_len`` defaults to s; ``valid_lens``
-    as in make_desc."""
-    for name, t in (("xhat", xhat), ("bhat", bhat)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 5:
-            raise ValueError(f"{name} must be a torch.Tensor of five dimensions")
-    b, s, c, h, p = xhat.shape
-    if dtype is None:
-        dtype = BF16 if xhat.dtype == torch.bfloat16 else F32
-    d = AttnDesc(b, s, c, h, bhat.shape[3], p, bhat.shape[4], s if valid_len is None else int(valid_len), int(dtype))
-    return set_valid_lens(d, valid_lens) if valid_lens is not None else d
+def _stream_of(dev):
+    """torch's current stream on dev as an integer handle."""
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
-def moments_attn_validate(desc: AttnDesc) -> int:
-    return _lib.load().moments_attn_validate(ctypes.byref(desc))
+def _tensors_ok(dev, specs):
+    """Checks (name, tensor, shape, dtype, optional) each as _expect does; returns the
+    tensors' addresses (None for an absent optional one)."""
+    out = []
+    for name, t, shape, dtype, optional in specs:
+        if t is None and optional:
+            out.append(None)
+            continue
+        if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev
+                and t.is_contiguous()):
+            _expect(name, t, shape, dtype, dev)   # names what is wrong
+        out.append(t.data_ptr())
+    return out
 
 
-def _size(n):
-    if n < 0:
-        _lib.check(int(n))
-    return int(n)
-
-
-def moments_attn_workspace_size(desc: AttnDesc, is_bwd: bool) -> int:
-    return _size(_lib.load().moments_attn_workspace_size(ctypes.byref(desc), int(bool(is_bwd))))
-
-
-def moments_attn_saved_size(desc: AttnDesc) -> int:
-    """Bytes of the buffer of moments_attn_fwd_save / moments_attn_bwd_saved."""
-    return _size(_lib.load().moments_attn_saved_size(ctypes.byref(desc)))
-
-
-def _attn_inputs(desc: AttnDesc, xhat, bhat, qhat, da, h0):
-    """Checks the inputs against the descriptor (all on xhat's device, a GPU)."""
-    if not isinstance(xhat, torch.Tensor):
-        raise ValueError("xhat must be a torch.Tensor")
-    dev, dt = xhat.device, _dt(desc)
-    if desc.valid_lens:
-        ref = getattr(desc, "_valid_lens_ref", None)
-        if ref is None or ref.data_ptr() != desc.valid_lens:
-            raise ValueError("set per-sequence lengths with set_valid_lens (the descriptor keeps the tensor)")
-        if ref.device != dev:
-            raise ValueError(f"valid_lens is on {ref.device}, the inputs on {dev}")
-    b, s, c, h, g, p, r = desc.b, desc.s, desc.c, desc.h, desc.g, desc.p, desc.r
-    _expect("xhat", xhat, (b, s, c, h, p), dt, dev)
-    _expect("bhat", bhat, (b, s, c, g, r), dt, dev)
-    _expect("qhat", qhat, (b, s, c, g, r), dt, dev)
-    _expect("da", da, (b, s, h), dt, dev)
-    _expect("h0", h0, (b, h, p, r), torch.float32, dev, optional=True)
-    return dev
+def _gpu(dev):
+    if dev.type != "cuda":
+        raise ValueError(f"the inputs are on {dev}; the kernels need GPU tensors")
+    return _lib.load()
 
 
 def _buffer(name, n, device, t):
@@ -403,23 +380,74 @@ def _bytes(t):
     return t.numel() * t.element_size()
 
 
+def _size(n):
+    if n < 0:
+        _lib.check(int(n))
+    return int(n)
+
+
+def attn_desc(xhat, bhat, valid_len=None, valid_lens=None, dtype=None) -> AttnDesc:
+    """Descriptor of linear attention for xhat [b,s,c,h,p] and keys bhat
+    [b,s,c,g,r] of g groups of heads. ``valid_len`` defaults to s; ``valid_lens``
+    as in make_desc."""
+    for name, t in (("xhat", xhat), ("bhat", bhat)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 5:
+            raise ValueError(f"{name} must be a torch.Tensor of five dimensions")
+    b, s, c, h, p = xhat.shape
+    g, r = bhat.shape[3:]
+    if dtype is None:
+        dtype = BF16 if xhat.dtype is torch.bfloat16 else F32
+    d = AttnDesc(b, s, c, h, g, p, r, s if valid_len is None else int(valid_len), int(dtype))
+    return set_valid_lens(d, valid_lens) if valid_lens is not None else d
+
+
+def moments_attn_validate(desc: AttnDesc) -> int:
+    return _lib.load().moments_attn_validate(ctypes.byref(desc))
+
+
+def moments_attn_workspace_size(desc: AttnDesc, is_bwd: bool) -> int:
+    return _size(_lib.load().moments_attn_workspace_size(ctypes.byref(desc), int(bool(is_bwd))))
+
+
+def moments_attn_saved_size(desc: AttnDesc) -> int:
+    """Bytes of the buffer of moments_attn_fwd_save / moments_attn_bwd_saved."""
+    return _size(_lib.load().moments_attn_saved_size(ctypes.byref(desc)))
+
+
+def _attn_inputs(desc: AttnDesc, xhat, bhat, qhat, da, h0):
+    """Checks the inputs against the descriptor (all on xhat's device). Returns the
+    device and their addresses."""
+    if not isinstance(xhat, torch.Tensor):
+        raise ValueError("xhat must be a torch.Tensor")
+    dev, dt = xhat.device, _DTYPES.get(desc.dtype)
+    if desc.valid_lens:
+        ref = getattr(desc, "_valid_lens_ref", None)
+        if ref is None or ref.data_ptr() != desc.valid_lens:
+            raise ValueError("set per-sequence lengths with set_valid_lens (the descriptor keeps the tensor)")
+        if ref.device != dev:
+            raise ValueError(f"valid_lens is on {ref.device}, the inputs on {dev}")
+    b, s, c, h, p = desc.b, desc.s, desc.c, desc.h, desc.p
+    keys = (b, s, c, desc.g, desc.r)
+    return dev, _tensors_ok(dev, (
+        ("xhat", xhat, (b, s, c, h, p), dt, False), ("bhat", bhat, keys, dt, False), ("qhat", qhat, keys, dt, False),
+        ("da", da, (b, s, h), dt, False), ("h0", h0, (b, h, p, desc.r), torch.float32, True)))
+
+
 def _attn_forward(desc, xhat, bhat, qhat, da, h0, y, h_last, saved, want_saved, workspace):
-    dev = _attn_inputs(desc, xhat, bhat, qhat, da, h0)
-    _expect("y", y, xhat.shape, xhat.dtype, dev, optional=True)
-    _expect("h_last", h_last, (desc.b, desc.h, desc.p, desc.r), torch.float32, dev, optional=True)
-    _require_gpu(dev)
-    lib = _lib.load()
+    dev, ins = _attn_inputs(desc, xhat, bhat, qhat, da, h0)
+    state = (desc.b, desc.h, desc.p, desc.r)
+    _tensors_ok(dev, (("y", y, xhat.shape, xhat.dtype, True), ("h_last", h_last, state, torch.float32, True)))
+    lib = _gpu(dev)
     ws = _buffer("workspace", moments_attn_workspace_size(desc, False), dev, workspace)
-    if want_saved:
-        saved = _buffer("saved", moments_attn_saved_size(desc), dev, saved)
     if y is None:
         y = torch.empty_like(xhat)
     if h_last is None:
-        h_last = torch.empty(desc.b, desc.h, desc.p, desc.r, dtype=torch.float32, device=dev)
-    head = (ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(qhat), _ptr(da), _ptr(h0), _ptr(y), _ptr(h_last))
-    tail = (_ptr(ws), _bytes(ws), _stream(dev))
+        h_last = torch.empty(state, dtype=torch.float32, device=dev)
+    head = (ctypes.byref(desc), *ins, y.data_ptr(), h_last.data_ptr())
+    tail = (ws.data_ptr(), _bytes(ws), _stream_of(dev))
     if want_saved:
-        _lib.check(lib.moments_attn_fwd_save(*head, _ptr(saved), _bytes(saved), *tail))
+        saved = _buffer("saved", moments_attn_saved_size(desc), dev, saved)
+        _lib.check(lib.moments_attn_fwd_save(*head, saved.data_ptr(), _bytes(saved), *tail))
         return y, h_last, saved
     _lib.check(lib.moments_attn_fwd(*head, *tail))
     return y, h_last
@@ -438,35 +466,37 @@ def moments_attn_fwd_save(desc: AttnDesc, xhat, bhat, qhat, da, h0=None, y=None,
     return _attn_forward(desc, xhat, bhat, qhat, da, h0, y, h_last, saved, True, workspace)
 
 
+def _gradients(dev, want, out, like):
+    """The dict of gradients d_<name> for the inputs in ``like``: the caller's tensors
+    (checked) or new ones; None where not wanted or the input is absent."""
+    out = dict(out or {})
+    _tensors_ok(dev, [("d_" + k, out.get("d_" + k), t.shape, t.dtype, True) for k, t in like.items()
+                      if k in want and t is not None])
+    _gpu(dev)
+    for k, t in like.items():
+        if k not in want or t is None:
+            out["d_" + k] = None
+        elif out.get("d_" + k) is None:
+            out["d_" + k] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+    return out, [None if out["d_" + k] is None else out["d_" + k].data_ptr() for k in like]
+
+
 def moments_attn_bwd(desc: AttnDesc, xhat, bhat, qhat, da, h0, d_y, d_h_last=None,
                      want=("xhat", "bhat", "qhat", "da", "h0"), out=None, workspace=None, _saved=None):
     """Returns dict d_xhat, d_bhat, d_qhat, d_da (input dtype), d_h0 (float32); None
     when not wanted (d_h0: or when there is no h0)."""
-    dev = _attn_inputs(desc, xhat, bhat, qhat, da, h0)
-    _expect("d_y", d_y, xhat.shape, xhat.dtype, dev)
-    state = (desc.b, desc.h, desc.p, desc.r)
-    _expect("d_h_last", d_h_last, state, torch.float32, dev, optional=True)
-    out = dict(out or {})
-    like = {"xhat": xhat, "bhat": bhat, "qhat": qhat, "da": da, "h0": h0}
-    for k, t in like.items():
-        if k in want and t is not None:
-            _expect("d_" + k, out.get("d_" + k), t.shape, t.dtype, dev, optional=True)
-        else:
-            out["d_" + k] = None
-    _require_gpu(dev)
-    for k, t in like.items():
-        if k in want and t is not None and out.get("d_" + k) is None:
-            out["d_" + k] = torch.empty_like(t)
+    dev, ins = _attn_inputs(desc, xhat, bhat, qhat, da, h0)
+    cot = _tensors_ok(dev, (("d_y", d_y, xhat.shape, xhat.dtype, False),
+                            ("d_h_last", d_h_last, (desc.b, desc.h, desc.p, desc.r), torch.float32, True)))
+    out, grads = _gradients(dev, want, out, {"xhat": xhat, "bhat": bhat, "qhat": qhat, "da": da, "h0": h0})
     lib = _lib.load()
     ws = _buffer("workspace", moments_attn_workspace_size(desc, True), dev, workspace)
-    head = (ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(qhat), _ptr(da), _ptr(h0))
-    grads = (_ptr(d_y), _ptr(d_h_last), _ptr(out["d_xhat"]), _ptr(out["d_bhat"]), _ptr(out["d_qhat"]),
-             _ptr(out["d_da"]), _ptr(out["d_h0"]), _ptr(ws), _bytes(ws), _stream(dev))
+    tail = (*cot, *grads, ws.data_ptr(), _bytes(ws), _stream_of(dev))
     if _saved is None:
-        _lib.check(lib.moments_attn_bwd(*head, *grads))
+        _lib.check(lib.moments_attn_bwd(ctypes.byref(desc), *ins, *tail))
     else:
         sv = _buffer("saved", moments_attn_saved_size(desc), dev, _saved)
-        _lib.check(lib.moments_attn_bwd_saved(*head, _ptr(sv), _bytes(sv), *grads))
+        _lib.check(lib.moments_attn_bwd_saved(ctypes.byref(desc), *ins, sv.data_ptr(), _bytes(sv), *tail))
     return out
 
 
@@ -483,18 +513,18 @@ def moments_attn_step(desc: AttnDesc, xhat, bhat, qhat, da, state, slots=None, y
     """One token of each sequence (s = 1) on a pool of states, state [nslots,h,p,r]
     float32, updated in place; ``slots`` int32 [b] (None: slot i for sequence i; a
     slot outside the pool marks an unused row, whose y is zero). Returns y."""
-    dev = _attn_inputs(desc, xhat, bhat, qhat, da, None)
+    dev, ins = _attn_inputs(desc, xhat, bhat, qhat, da, None)
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be a torch.Tensor [nslots,h,p,r]")
     n = state.shape[0]
-    _expect("state", state, (n, desc.h, desc.p, desc.r), torch.float32, dev)
-    _expect("slots", slots, (desc.b,), torch.int32, dev, optional=True)
-    _expect("y", y, xhat.shape, xhat.dtype, dev, optional=True)
-    _require_gpu(dev)
+    st, sl, out = _tensors_ok(dev, (("state", state, (n, desc.h, desc.p, desc.r), torch.float32, False),
+                                    ("slots", slots, (desc.b,), torch.int32, True),
+                                    ("y", y, xhat.shape, xhat.dtype, True)))
+    lib = _gpu(dev)
     if y is None:
         y = torch.empty_like(xhat)
-    _lib.check(_lib.load().moments_attn_step(ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(qhat), _ptr(da),
-                                             _ptr(slots), n, _ptr(state), _ptr(y), _stream(dev)))
+        out = y.data_ptr()
+    _lib.check(lib.moments_attn_step(ctypes.byref(desc), *ins[:4], sl, n, st, out, _stream_of(dev)))
     return y
 
 
@@ -504,11 +534,7 @@ def qk_desc(q, k, h, rot_kind, rot=None, eps=1e-5, rope_dim=None, quat_blocks=No
     q and k may be columns of a wider projection: each token's values together,
     tokens a fixed stride apart. The rotated width and the heads of the rotation
     are taken from ``rot`` ([b,s,h or 1,a] angles or [b,s,h or 1,J,4])."""
-    strides = []
-    for name, t in (("q", q), ("k", k)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 5:
-            raise ValueError(f"{name} must be a torch.Tensor of five dimensions")
-        strides.append(_token_stride(name, t))
+    strides = [_token_stride("q", q), _token_stride("k", k)]
     b, s, c, g, r = q.shape
     rot_h = h
     if rot_kind != ROT_NONE:
@@ -520,45 +546,54 @@ def qk_desc(q, k, h, rot_kind, rot=None, eps=1e-5, rope_dim=None, quat_blocks=No
         else:
             rope_dim = 2 * rot.shape[3] if rope_dim is None else rope_dim
     return QkDesc(b, s, c, h, g, r, strides[0], strides[1], rope_dim or 0, quat_blocks or 0, rot_h,
-                  BF16 if q.dtype == torch.bfloat16 else F32, int(rot_kind), float(eps))
+                  BF16 if q.dtype is torch.bfloat16 else F32, int(rot_kind), float(eps))
 
 
 def _token_stride(name, t):
     """Elements between tokens of t [b,s,c,g,r] (0 where any would do)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 5:
+        raise ValueError(f"{name} must be a torch.Tensor of five dimensions")
     b, s, c, g, r = t.shape
+    if t.is_contiguous():
+        return c * g * r if b * s > 1 else 0
     if t.numel() == 0:
         return 0
-    inner = t[0, 0]
-    step = t.stride(1) if s > 1 else (t.stride(0) if b > 1 else c * g * r)
-    if not inner.is_contiguous() or step < c * g * r or (b > 1 and s > 1 and t.stride(0) != s * step):
+    sb, ss, sc, sg, sr = t.stride()
+    step = ss if s > 1 else (sb if b > 1 else c * g * r)
+    inner = (r == 1 or sr == 1) and (g == 1 or sg == r) and (c == 1 or sc == g * r)
+    if not inner or step < c * g * r or (b > 1 and s > 1 and sb != s * step):
         raise ValueError(f"{name} must hold each token's values together, tokens a fixed stride apart")
     return step
 
 
 def _qk_inputs(desc: QkDesc, q, k, wq, wk, bq, bk, rot):
+    """Checks the inputs against the descriptor; returns the device, the dtype and the
+    inputs' addresses."""
     if not isinstance(q, torch.Tensor):
         raise ValueError("q must be a torch.Tensor")
-    dev, dt = q.device, _dt(desc)
+    dev, dt = q.device, _DTYPES.get(desc.dtype)
     b, s, c, h, g, r = desc.b, desc.s, desc.c, desc.h, desc.g, desc.r
+    row = c * g * r
     for name, t, stride in (("q", q, desc.q_stride), ("k", k, desc.k_stride)):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a torch.Tensor")
-        if tuple(t.shape) != (b, s, c, g, r) or t.dtype != dt or t.device != dev:
+        if t.shape != (b, s, c, g, r) or t.dtype is not dt or t.device != dev:
             raise ValueError(f"{name} must be {dt} of shape {(b, s, c, g, r)} on {dev}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
-        if t.numel() and _token_stride(name, t) != (stride or c * g * r):
-            raise ValueError(f"{name} has another token stride than the descriptor ({stride or c * g * r})")
-    for name, t in (("wq", wq), ("wk", wk)):
-        _expect(name, t, (r,), torch.float32, dev)
-    for name, t in (("bq", bq), ("bk", bk)):
-        _expect(name, t, (h, r), torch.float32, dev, optional=True)
-    if desc.rot_kind == ROT_NONE:
+        if b * s > 1 and (_token_stride(name, t) or row) != (stride or row):
+            raise ValueError(f"{name} has another token stride than the descriptor ({stride or row})")
+    f32, kind = torch.float32, desc.rot_kind
+    specs = [("wq", wq, (r,), f32, False), ("wk", wk, (r,), f32, False), ("bq", bq, (h, r), f32, True),
+             ("bk", bk, (h, r), f32, True)]
+    if kind == ROT_NONE:
         if rot is not None:
             raise ValueError("rot must be None when the descriptor has no rotation")
+    elif kind == ROT_QUAT:
+        specs.append(("rot", rot, (b, s, desc.rot_h, desc.quat_blocks, 4), dt, False))
     else:
-        _expect("rot", rot, (b, s, desc.rot_h, desc.quat_blocks, 4) if desc.rot_kind == ROT_QUAT
-                else (b, s, desc.rot_h, desc.rope_dim // 2), dt, dev)
-    return dev, dt
+        specs.append(("rot", rot, (b, s, desc.rot_h, desc.rope_dim // 2), dt, False))
+    ptrs = [q.data_ptr(), k.data_ptr(), *_tensors_ok(dev, specs)]
+    return dev, dt, ptrs if kind != ROT_NONE else [*ptrs, None]
 
 
 def moments_qk_workspace_size(desc: QkDesc) -> int:
@@ -569,17 +604,15 @@ def moments_qk_workspace_size(desc: QkDesc) -> int:
 def moments_qk_fwd(desc: QkDesc, q, k, wq, wk, bq=None, bk=None, rot=None, qhat=None, khat=None):
     """Returns (qhat, khat) [b,s,c,h,r]: normed, weighted, biased and turned into the
     frame of the cached states (khat is what the moments path takes as bhat)."""
-    dev, dt = _qk_inputs(desc, q, k, wq, wk, bq, bk, rot)
+    dev, dt, ins = _qk_inputs(desc, q, k, wq, wk, bq, bk, rot)
     shape = (desc.b, desc.s, desc.c, desc.h, desc.r)
-    _expect("qhat", qhat, shape, dt, dev, optional=True)
-    _expect("khat", khat, shape, dt, dev, optional=True)
-    _require_gpu(dev)
+    _tensors_ok(dev, (("qhat", qhat, shape, dt, True), ("khat", khat, shape, dt, True)))
+    lib = _gpu(dev)
     if qhat is None:
         qhat = torch.empty(shape, dtype=dt, device=dev)
     if khat is None:
-        khat = torch.empty(shape, dtype=dt, device=dev)
-    _lib.check(_lib.load().moments_qk_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(bq),
-                                          _ptr(bk), _ptr(rot), _ptr(qhat), _ptr(khat), _stream(dev)))
+        khat = torch.empty_like(qhat)
+    _lib.check(lib.moments_qk_fwd(ctypes.byref(desc), *ins, qhat.data_ptr(), khat.data_ptr(), _stream_of(dev)))
     return qhat, khat
 
 
@@ -587,26 +620,13 @@ def moments_qk_bwd(desc: QkDesc, q, k, wq, wk, bq, bk, rot, d_qhat, d_khat,
                    want=("q", "k", "wq", "wk", "bq", "bk", "rot"), out=None, workspace=None):
     """Returns dict d_q, d_k, d_rot (input dtype, dense), d_wq, d_wk, d_bq, d_bk
     (float32); None when not wanted or not defined."""
-    dev, dt = _qk_inputs(desc, q, k, wq, wk, bq, bk, rot)
+    dev, dt, ins = _qk_inputs(desc, q, k, wq, wk, bq, bk, rot)
     shape = (desc.b, desc.s, desc.c, desc.h, desc.r)
-    _expect("d_qhat", d_qhat, shape, dt, dev)
-    _expect("d_khat", d_khat, shape, dt, dev)
-    out = dict(out or {})
-    like = {"q": q, "k": k, "wq": wq, "wk": wk, "bq": bq, "bk": bk, "rot": rot}
-    for n, t in like.items():
-        if n in want and t is not None:
-            _expect("d_" + n, out.get("d_" + n), t.shape, t.dtype, dev, optional=True)
-        else:
-            out["d_" + n] = None
-    _require_gpu(dev)
-    for n, t in like.items():
-        if n in want and t is not None and out.get("d_" + n) is None:
-            out["d_" + n] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+    cot = _tensors_ok(dev, (("d_qhat", d_qhat, shape, dt, False), ("d_khat", d_khat, shape, dt, False)))
+    out, grads = _gradients(dev, want, out, {"q": q, "k": k, "wq": wq, "wk": wk, "bq": bq, "bk": bk, "rot": rot})
     ws = _buffer("workspace", moments_qk_workspace_size(desc), dev, workspace)
-    _lib.check(_lib.load().moments_qk_bwd(
-        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(bq), _ptr(bk), _ptr(rot), _ptr(d_qhat),
-        _ptr(d_khat), _ptr(out["d_q"]), _ptr(out["d_k"]), _ptr(out["d_wq"]), _ptr(out["d_wk"]), _ptr(out["d_bq"]),
-        _ptr(out["d_bk"]), _ptr(out["d_rot"]), _ptr(ws), _bytes(ws), _stream(dev)))
+    _lib.check(_lib.load().moments_qk_bwd(ctypes.byref(desc), *ins, *cot, *grads, ws.data_ptr(), _bytes(ws),
+                                          _stream_of(dev)))
     return out
 
 

@@ -117,7 +117,8 @@ int launch_walk(const AttnGeo& g, int nseg, const T* x, const T* k, const T* q, 
                 float* h_last, T* save, float* seg_loc, double* seg_dec, hipStream_t st) {
   using LD = LdsA<T, RT, PW>;
   const size_t lds = MODE == 0 ? LD::total : LD::state_total;
-  MOM_TRY(set_lds(k_attn_walk<T, RT, PW, MODE, VEC>, lds));
+  static std::atomic<uint64_t> done{0};
+  MOM_TRY(set_lds_once(done, k_attn_walk<T, RT, PW, MODE, VEC>, lds));
   ProfScope ps(MODE == 0 ? KID_ATTN_FWD : KID_ATTN_STATE, st);
   hipLaunchKernelGGL((k_attn_walk<T, RT, PW, MODE, VEC>), dim3((unsigned)((size_t)g.b * g.h * g.npt * nseg)), dim3(ATT),
                      lds, st, g, x, k, q, da, h0, y, h_last, save, seg_loc, seg_dec);
@@ -220,7 +221,8 @@ int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const 
       constexpr bool PART = decltype(part)::value != 0;
       const size_t lds = LdsB<T, RT, PT>::total;
       static_assert(LdsB<T, RT, PT>::total <= kLdsLimit, "LDS");
-      MOM_TRY(set_lds(k_attn_bwd<T, RT, PT, PART, VEC>, lds));
+      static std::atomic<uint64_t> done{0};
+      MOM_TRY(set_lds_once(done, k_attn_bwd<T, RT, PT, PART, VEC>, lds));
       ProfScope ps(KID_ATTN_BWD, st);
       hipLaunchKernelGGL((k_attn_bwd<T, RT, PT, PART, VEC>), dim3((unsigned)((size_t)P.items * g.nseg)), dim3(ABT), lds, st,
                          g, xt, kt, qt, dat, copies, dyt, d_last, seg, sdec, (T*)d_x, (T*)d_k, (T*)d_q, (T*)d_da,

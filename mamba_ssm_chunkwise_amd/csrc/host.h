@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "moments.h"
@@ -47,6 +48,20 @@ int set_lds(K kernel, size_t bytes) {
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   return e == hipSuccess ? 0 : hip_fail(e);
+}
+
+// set_lds once for each device instead of at every launch: `done` is a static of the
+// launch site (one bit a device; devices past 63 are set every time).
+template <typename K>
+int set_lds_once(std::atomic<uint64_t>& done, K kernel, size_t bytes) {
+  int dev = 0;
+  const hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return hip_fail(e);
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return 0;
+  const int rc = set_lds(kernel, bytes);
+  if (rc == 0) done.fetch_or(bit, std::memory_order_relaxed);
+  return rc;
 }
 
 #define MOM_TRY(x)          \

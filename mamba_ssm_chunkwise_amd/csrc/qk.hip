@@ -198,7 +198,7 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
     constexpr int LPR = decltype(lpr)::value, ROT = decltype(rk)::value, C = decltype(cc)::value;
     {
       auto kernel = k_qk_bwd<T, LPR, ROT, C, decltype(hb)::value, decltype(hpp)::value, decltype(vec)::value != 0>;
-      MOM_TRY(set_lds(kernel, P.lds));
+      if (P.lds > 64 * 1024) MOM_TRY(set_lds(kernel, P.lds));
       ProfScope ps(KID_QK_BWD, st);
       hipLaunchKernelGGL(kernel, dim3((unsigned)g.nblk, (unsigned)g.g), dim3(P.NT), P.lds, st, g, (const T*)q,
                          (const T*)k, wq, wk, bq, bk, (const T*)rot, (const T*)d_qhat, (const T*)d_khat, (T*)d_q,
