@@ -27,14 +27,13 @@ struct AttnPlan {
   size_t ws_fwd, ws_bwd, flag_fwd, flag_bwd, saved;
 };
 
-// Segments a chain's walk is split into: one when the chains alone give every
-// compute unit `want` workgroups, or nearly; else as many as that takes, of eight chunks
-// or more each (a segment's own start costs it one more read of k and x).
-void split(AttnGeo& g, int items, long want) {
+// Segments a chain's walk is split into: one when the chains alone nearly fill the
+// `want` places that the chip has for workgroups of the walk.
+void split(AttnGeo& g, int items, long want, const char* env) {
   int n = 1;
-  if ((long)items * 4 < want * 3) n = (int)std::min<long>((want + items - 1) / items, std::max(1, g.NK / 8));
-  g.SL = std::max(1, (g.NK + n - 1) / n);
-  g.nseg = std::max(1, (g.NK + g.SL - 1) / g.SL);
+  if ((long)items * 4 < want * 3) n = (int)std::min<long>((want + items - 1) / items, std::max(1, g.NK / 2));
+  if (getenv(env)) n = std::min(atoi(getenv(env)), std::max(1, g.NK));
+  g.nseg = std::max(1, n);
   g.seg0 = 0;
 }
 
@@ -56,7 +55,7 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   g.V = (int)std::min(d->valid_len, d->s);
   g.hpg = P->empty ? 1 : g.h / g.g;
   g.CT = L / g.c;
-  g.NK = (g.s + g.CT - 1) / g.CT;
+  g.NK = (g.V + g.CT - 1) / g.CT;
   g.cinv = (65536 + g.c - 1) / g.c;
   P->vec = (g.r * tsz) % 16 == 0 && (g.p * tsz) % 16 == 0;
   g.lens = (const int*)d->valid_lens;
@@ -69,8 +68,8 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
     return MOMENTS_ENOTSUP;
   P->gb = g;
   if (!P->empty) {
-    split(g, P->items, 2 * kCUs);      // two workgroups of the walk share a CU
-    split(P->gb, P->items, kCUs);      // one of the backward
+    split(g, P->items, 2 * kCUs, "NSEGF");      // two workgroups of the walk share a CU
+    split(P->gb, P->items, kCUs, "NSEGB");      // one of the backward
   }
   P->part = g.hpg > 1 || g.npt > 1;
   const size_t tiles = (size_t)(g.PT / 16) * P->RT * 256;
@@ -125,12 +124,28 @@ int launch_walk(const AttnGeo& g, int nseg, const T* x, const T* k, const T* q, 
   return check_launch();
 }
 
-// The states that the segments of the forward walk leave, each from zero.
+int launch_scan(const AttnPlan& P, const AttnGeo& g, bool back, const float* first, float* seg_loc,
+                const double* seg_dec, hipStream_t st) {
+  const int tiles = (g.PT / 16) * P.RT * 256;
+  const dim3 grid((unsigned)P.items, (unsigned)((tiles / 4 + 255) / 256));
+  ProfScope ps(KID_ATTN_SCAN, st);
+  if (back)
+    hipLaunchKernelGGL(k_attn_scan<true>, grid, dim3(256), 0, st, g, P.RT, tiles, first, seg_loc, seg_dec);
+  else
+    hipLaunchKernelGGL(k_attn_scan<false>, grid, dim3(256), 0, st, g, P.RT, tiles, first, seg_loc, seg_dec);
+  return check_launch();
+}
+
+// The states that the segments of the forward walk start from.
 template <typename T, int RT, int PW, bool VEC>
-int run_segments(const AttnPlan& P, const T* x, const T* k, const T* da, unsigned char* ws, hipStream_t st) {
+int run_segments(const AttnPlan& P, const T* x, const T* k, const T* da, const float* h0, unsigned char* ws,
+                 hipStream_t st) {
   if (P.g.nseg < 2) return 0;
-  return launch_walk<T, RT, PW, 1, VEC>(P.g, P.g.nseg - 1, x, k, nullptr, da, nullptr, nullptr, nullptr, nullptr,
-                                   (float*)ws, (double*)(ws + P.seg_dec), st);
+  float* seg = (float*)ws;
+  double* dec = (double*)(ws + P.seg_dec);
+  MOM_TRY((launch_walk<T, RT, PW, 1, VEC>(P.g, P.g.nseg - 1, x, k, nullptr, da, nullptr, nullptr, nullptr, nullptr,
+                                          seg, dec, st)));
+  return launch_scan(P, P.g, false, h0, seg, dec, st);
 }
 
 int attn_fwd(const moments_attn_desc* desc, const void* x, const void* k, const void* q, const void* da,
@@ -154,7 +169,7 @@ int attn_fwd(const moments_attn_desc* desc, const void* x, const void* k, const 
     constexpr bool VEC = decltype(vec)::value != 0;
     using T = typename decltype(tt)::type;
     constexpr int RT = decltype(rt)::value, PW = decltype(pw)::value;
-    MOM_TRY((run_segments<T, RT, PW, VEC>(P, (const T*)x, (const T*)k, (const T*)da, ws, st)));
+    MOM_TRY((run_segments<T, RT, PW, VEC>(P, (const T*)x, (const T*)k, (const T*)da, h0, ws, st)));
     return launch_walk<T, RT, PW, 0, VEC>(P.g, P.g.nseg, (const T*)x, (const T*)k, (const T*)q, (const T*)da, h0, (T*)y,
                                      h_last, want_saved ? (T*)saved : nullptr, seg, sdec, st);
   }));
@@ -199,7 +214,7 @@ int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const 
     const T* copies = (const T*)saved;
     if (!use_saved) {   // the states entering the chunks, by a walk over k and x
       T* own = (T*)(ws + P.save);
-      MOM_TRY((run_segments<T, RT, PW, VEC>(P, xt, kt, dat, ws, st)));
+      MOM_TRY((run_segments<T, RT, PW, VEC>(P, xt, kt, dat, h0, ws, st)));
       MOM_TRY((launch_walk<T, RT, PW, 1, VEC>(P.g, P.g.nseg, xt, kt, nullptr, dat, h0, nullptr, nullptr, own,
                                          P.g.nseg > 1 ? (float*)ws : nullptr,
                                          P.g.nseg > 1 ? (double*)(ws + P.seg_dec) : nullptr, st)));
@@ -213,6 +228,7 @@ int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const 
       g2.seg0 = 1;
       MOM_TRY((launch_walk<T, RT, PW, 2, VEC>(g2, g.nseg - 1, dyt, qt, nullptr, dat, nullptr, nullptr, nullptr, nullptr,
                                          seg, sdec, st)));
+      MOM_TRY(launch_scan(P, g, true, d_last, seg, sdec, st));
     }
     float* pq = (float*)(ws + P.part_q);
     float* pk = (float*)(ws + P.part_k);
@@ -225,7 +241,7 @@ int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const 
       MOM_TRY(set_lds_once(done, k_attn_bwd<T, RT, PT, PART, VEC>, lds));
       ProfScope ps(KID_ATTN_BWD, st);
       hipLaunchKernelGGL((k_attn_bwd<T, RT, PT, PART, VEC>), dim3((unsigned)((size_t)P.items * g.nseg)), dim3(ABT), lds, st,
-                         g, xt, kt, qt, dat, copies, dyt, d_last, seg, sdec, (T*)d_x, (T*)d_k, (T*)d_q, (T*)d_da,
+                         g, xt, kt, qt, dat, copies, dyt, d_last, seg, (T*)d_x, (T*)d_k, (T*)d_q, (T*)d_da,
                          d_h0, pk, pq, pa);
       return check_launch();
     };

@@ -20,7 +20,7 @@ constexpr long kCUs = 256;  // compute units of the part (MI355X)
 enum KernelId {
   KID_CARRY, KID_SCAN, KID_FWD, KID_REDUCE, KID_BWD, KID_DSCAN, KID_FIX, KID_ZERO, KID_PREP, KID_GSCAN, KID_GFIX,
   KID_CSCAN, KID_ROTSEG, KID_ROTCARRY, KID_ROTAPPLY, KID_PAIR, KID_GENTRY, KID_CSUM, KID_CGRP,
-  KID_ATTN_STATE, KID_ATTN_FWD, KID_ATTN_BWD, KID_ATTN_SUM, KID_ATTN_STEP, KID_QK_FWD, KID_QK_BWD, KID_QK_SUM,
+  KID_ATTN_STATE, KID_ATTN_SCAN, KID_ATTN_FWD, KID_ATTN_BWD, KID_ATTN_SUM, KID_ATTN_STEP, KID_QK_FWD, KID_QK_BWD, KID_QK_SUM,
   KID_N
 };
 

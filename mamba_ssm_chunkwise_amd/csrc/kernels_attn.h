@@ -35,10 +35,9 @@ struct AttnGeo {
   int V;        // min(valid_len, s)
   int hpg;      // heads per key group
   int CT;       // tokens per chunk: L / c
-  int NK;       // chunks over all s tokens
-  int nseg;     // segments a chain's walk is split into
+  int NK;       // chunks over V tokens
+  int nseg;     // segments a chain's walk is split into (each sequence splits its own length)
   int seg0;     // first segment of this launch
-  int SL;       // chunks per segment
   int npt;      // column tiles of the state rows p that separate workgroups take
   int PT;       // rows of p in such a tile
   int cinv;     // ceil(65536 / c): u / c = (u * cinv) >> 16 for a row u of a chunk
@@ -50,6 +49,19 @@ __device__ __forceinline__ int attn_len(const AttnGeo& g, int bi) {
   const int v = g.lens[bi];
   return v < 0 ? 0 : (v < g.V ? v : g.V);
 }
+
+// Chunks [n0, n1) of a segment of a sequence of nkb chunks, and the share [z0, z1) of the
+// tokens past its length whose outputs the segment clears.
+struct Segment {
+  int n0, n1, z0, z1;
+  __device__ __forceinline__ Segment(const AttnGeo& g, int seg, int Vb, int nkb) {
+    const int sl = (nkb + g.nseg - 1) / g.nseg, zl = (g.s - Vb + g.nseg - 1) / g.nseg;
+    n0 = min(seg * sl, nkb);
+    n1 = min(n0 + sl, nkb);
+    z0 = min(Vb + seg * zl, g.s);
+    z1 = min(z0 + zl, g.s);
+  }
+};
 
 // Decays. Sums of da are kept in units of log2 as a float and its remainder
 // (from a sum in double), so that differences of long sums keep 24 bits of the
@@ -157,9 +169,8 @@ __device__ __forceinline__ AV<float>::frag col_frag(const float* t, int P, int m
   return f;
 }
 
-// c + a (B operand x scaled by w per slot), to fp32 accuracy of the scaled values:
-// in bf16 the scaled operand is split into three bf16 pieces, each exact in the rest
-// of the one before.
+// An operand scaled by w per slot, to fp32 accuracy of the scaled values: in bf16 it is
+// split into three bf16 pieces, each the rounded rest of those before.
 template <int N>
 struct Scaled;
 template <>
@@ -182,43 +193,64 @@ struct Scaled<3> {
     }
     for (int i = 0; i < 3; i++) p[i] = as_bf8(o[i]);
   }
-  __device__ __forceinline__ f4 mma(bf8 a, f4 c) const {
-#pragma unroll
-    for (int i = 2; i >= 0; i--) c = mma32(a, p[i], c);
-    return c;
-  }
+  __device__ __forceinline__ bf8 piece(int i) const { return p[2 - i]; }   // the smallest first
 };
 template <>
 struct Scaled<1> {
   AV<float>::frag p;
   __device__ __forceinline__ void make(const AV<float>::frag& x, f4 w0, f4 w1) { p = AV<float>::frag{{x.v[0] * w0, x.v[1] * w1}}; }
-  __device__ __forceinline__ f4 mma(const AV<float>::frag& a, f4 c) const { return mma32(a, p, c); }
+  __device__ __forceinline__ const AV<float>::frag& piece(int) const { return p; }
 };
 
 // ---- staging ----------------------------------------------------------------
+// Rows of a chunk in global memory through a buffer descriptor that ends with the last
+// valid row: loads past it return zeros and stores past it are dropped by the hardware, so
+// that neither needs a branch. (With branches the compiler cannot count what is in flight,
+// and waiting for a chunk's loads would wait for the last chunk's stores too.) Offsets
+// inside a chunk fit 32 bits: the plan refuses wider rows.
+constexpr unsigned kPast = 0xFFFFFFF0u;   // an offset past every descriptor's end
+using Rsrc = __amdgpu_buffer_rsrc_t;
+// Rows of n elements, `stride` elements apart; none where nrows = 0 or base is nullptr.
+template <typename T>
+__device__ __forceinline__ Rsrc row_rsrc(const T* base, unsigned stride, int nrows, int n) {
+  const unsigned bytes = base == nullptr || nrows == 0 ? 0u : ((unsigned)(nrows - 1) * stride + (unsigned)n) * (unsigned)sizeof(T);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, 0x00027000);
+}
+__device__ __forceinline__ uint4 buf_load(Rsrc r, unsigned off) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ void buf_store(Rsrc r, unsigned off, uint2 v) {
+  __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(unsigned __attribute__((ext_vector_type(2))), v), r, off, 0, 0);
+}
+__device__ __forceinline__ void buf_store(Rsrc r, unsigned off, f4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), r, off, 0, 0);
+}
+
 // A [L][COLS] block of rows on its way from global memory to an LDS tile, in 16-byte
 // pieces. Rows >= nrows and columns >= n are zeros, whatever the memory there holds.
 // Rows that are whole pieces go through registers (load, later store), so that they can
 // be in flight while another chunk is worked on; others are fetched one element at a
-// time, straight into the tile. Offsets inside a chunk fit 32 bits (the plan refuses
-// wider rows), so that addresses are a scalar base and one register.
+// time, straight into the tile.
 template <typename T, int COLS, int NT>
 struct Stage {
   static constexpr int L = AV<T>::L, PE = AV<T>::PE, PR = COLS / PE, N = (L * PR + NT - 1) / NT;
+  static_assert(L * PR % NT == 0 && NT % PR == 0, "whole rows of pieces");
   uint4 v[N];
-  __device__ __forceinline__ void load(const T* base, unsigned stride, int nrows, int n) {
+  unsigned off0, step;   // byte offset of the thread's first piece, and from one to the next
+  __device__ __forceinline__ void setup(unsigned stride, int n) {
+    const int row = (int)threadIdx.x / PR, c0 = (int)threadIdx.x % PR * PE;
+    off0 = c0 < n ? ((unsigned)row * stride + (unsigned)c0) * (unsigned)sizeof(T) : kPast;
+    step = c0 < n ? (unsigned)(NT / PR) * stride * (unsigned)sizeof(T) : 0u;
+  }
+  __device__ __forceinline__ void load(Rsrc r) {
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-      const int e = i * NT + (int)threadIdx.x, row = e / PR, c0 = e % PR * PE;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (row < nrows && c0 < n) v[i] = *reinterpret_cast<const uint4*>(base + ((unsigned)row * stride + (unsigned)c0));
-    }
+    for (int i = 0; i < N; i++) v[i] = buf_load(r, off0 + (unsigned)i * step);
   }
   __device__ __forceinline__ void store(T* t, int P) const {
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int e = i * NT + (int)threadIdx.x, row = e / PR, piece = e % PR;
-      if (L * PR % NT == 0 || row < L) st_piece(t, P, row, piece, v[i]);
+      const int e = i * NT + (int)threadIdx.x;
+      st_piece(t, P, e / PR, e % PR, v[i]);
     }
   }
   __device__ __forceinline__ static void direct(T* t, int P, const T* base, unsigned stride, int nrows, int n) {
@@ -234,6 +266,29 @@ struct Stage {
   }
 };
 
+// Rows u of a chunk on their way out: four columns c0.. of one row at a time.
+template <typename T, bool VEC>
+struct RowOut {
+  Rsrc r;
+  T* base;
+  unsigned stride;
+  int nrows, n;
+  __device__ __forceinline__ RowOut(T* b, unsigned st, int nr, int cols) : base(b), stride(st), nrows(nr), n(cols) {
+    if constexpr (VEC) r = row_rsrc(b, st, nr, cols);
+  }
+  __device__ __forceinline__ void put(int u, int c0, f4 v) const {
+    if constexpr (VEC) {
+      const unsigned off = c0 < n ? ((unsigned)u * stride + (unsigned)c0) * (unsigned)sizeof(T) : kPast;
+      buf_store(r, off, to_quad<T>(v));
+    } else {
+      if (base == nullptr || u >= nrows) return;
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (c0 + i < n) base[(unsigned)u * stride + (unsigned)(c0 + i)] = to_t<T>(v[i]);
+    }
+  }
+};
+
 // Per-row decay tables of a chunk, written by one wave (lane u = row u).
 struct DecayTab {
   float hi[64], lo[64];   // a_u in log2 units: hi + lo
@@ -242,17 +297,31 @@ struct DecayTab {
   double total;           // a_end in log2 units
   double pad;             // tiles behind it start at 16 bytes
 };
-// v: log2 decay of row u = lane (zero where the row does not open a token).
-__device__ __forceinline__ double wave_sum_incl(double v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const double o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
+// Inclusive sum over the 64 lanes, in the vector unit: within rows of 16 by shifts, then
+// each row's total into the next one, then the lower half's into the upper.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+  const long long b = __builtin_bit_cast(long long, v);
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xF, true);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xF, true);
+  return v + __builtin_bit_cast(double, ((long long)hi << 32) | (unsigned)lo);
 }
+__device__ __forceinline__ double wave_sum_incl(double v) {
+  v = dpp_add<0x111, 0xF>(v);   // row_shr:1, 2, 4, 8 (zero shifted in)
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);   // row_bcast:15 into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);   // row_bcast:31 into rows 2 and 3
+}
+__device__ __forceinline__ double lane63(double v) {
+  const long long b = __builtin_bit_cast(long long, v);
+  const unsigned lo = __builtin_amdgcn_readlane((int)b, 63), hi = __builtin_amdgcn_readlane((int)(b >> 32), 63);
+  return __builtin_bit_cast(double, ((long long)hi << 32) | lo);
+}
+// v: log2 decay of row u = lane (zero where the row does not open a token).
 __device__ __forceinline__ void decay_table(DecayTab* t, double v, int lane) {
-  const double a = wave_sum_incl(v, lane), e = __shfl(a, 63);
+  const double a = wave_sum_incl(v), e = lane63(a);
   const float hi = (float)a;
   t->hi[lane] = hi;
   t->lo[lane] = (float)(a - hi);
@@ -301,18 +370,14 @@ __device__ __forceinline__ void st_state4(float* st, int p, int r, int pi, int r
       if (r0 + i < r) s[i] = v[i];
   }
 }
-// Four consecutive columns c0.. of the row of n elements at base[off] (quad-aligned when
-// n % 4 == 0).
-template <typename T>
-__device__ __forceinline__ void st_row4(T* base, unsigned off, int n, int c0, f4 v) {
-  off += (unsigned)c0;
-  if ((n & 3) == 0) {
-    if (c0 < n) *reinterpret_cast<typename AV<T>::quad*>(base + off) = to_quad<T>(v);
-  } else {
+// N stores that the hardware drops. A walk issues as many behind its first loads as each of
+// its chunks has stores behind the next chunk's loads, so that waiting for loads at the top
+// of the loop means the same number of younger operations on both ways in.
+template <typename T, int N>
+__device__ __forceinline__ void dropped_stores() {
+  const Rsrc r = __builtin_amdgcn_make_buffer_rsrc(nullptr, 0, 0, 0x00027000);
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-      if (c0 + i < n) base[off + i] = to_t<T>(v[i]);
-  }
+  for (int i = 0; i < N; i++) buf_store(r, kPast, typename AV<T>::quad{});
 }
 
 // LDS of the walks.
@@ -320,7 +385,7 @@ template <typename T, int RT, int PW>
 struct LdsA {
   static constexpr int L = AV<T>::L, RP = AV<T>::pitch(16 * RT), PT = 16 * ATW * PW, PP = AV<T>::pitch(PT),
                        SP = AV<T>::pitch(L);
-  static constexpr size_t tab = 0, k = sizeof(DecayTab), x = k + (size_t)L * RP * sizeof(T),
+  static constexpr size_t tab = 0, k = 2 * sizeof(DecayTab), x = k + (size_t)L * RP * sizeof(T),
                           state_total = x + (size_t)L * PP * sizeof(T), q = state_total,
                           s = q + (size_t)L * RP * sizeof(T), total = s + (size_t)L * SP * sizeof(T);
   static_assert(sizeof(DecayTab) % 16 == 0, "tiles start at 16 bytes");
@@ -343,28 +408,53 @@ __device__ __forceinline__ void state_update(f4 (&H)[PW][RT], const T* ks, const
     for (int pw = 0; pw < PW; pw++) xf[pw][m].make(col_frag(xs, LD::PP, m, 16 * (wave * PW + pw), lane), w0, w1);
   }
 #pragma unroll
-  for (int rt = 0; rt < RT; rt++) {
+  for (int rt = 0; rt < RT; rt++)
 #pragma unroll
     for (int pw = 0; pw < PW; pw++) H[pw][rt] *= dec;
+  // tile by tile within each piece of the scaled rows, so that consecutive matrix
+  // instructions do not wait for one another's sums
 #pragma unroll
-    for (int m = 0; m < NJ; m++) {
-      const auto kf = col_frag(ks, LD::RP, m, 16 * rt, lane);
+  for (int m = 0; m < NJ; m++) {
+    typename AV<T>::frag kf[RT];
 #pragma unroll
-      for (int pw = 0; pw < PW; pw++) H[pw][rt] = xf[pw][m].mma(kf, H[pw][rt]);
-    }
+    for (int rt = 0; rt < RT; rt++) kf[rt] = col_frag(ks, LD::RP, m, 16 * rt, lane);
+#pragma unroll
+    for (int i = 0; i < AV<T>::NSPLIT; i++)
+#pragma unroll
+      for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+        for (int pw = 0; pw < PW; pw++) H[pw][rt] = mma32(kf[rt], xf[pw][m].piece(i), H[pw][rt]);
   }
 }
+
+// The 16x16 tiles (ut, jt) of the scores that hold pairs j <= u, four bits each: the lower
+// triangle, and, with three channels, whose tokens straddle 16 rows, the tile right of the
+// diagonal too. The others stay zero.
+template <int NT> struct ScoreTiles;
+template <> struct ScoreTiles<4> {
+  static constexpr int SB = 3;   // tiles that a wave of four has in work together
+  unsigned long long list;
+  int n;
+  __device__ __forceinline__ ScoreTiles(int c)
+      : list(c == 3 ? 0xB61FEDCA98540ull : 0xFEDCA98540ull), n(c == 3 ? 13 : 10) {}
+};
+template <> struct ScoreTiles<2> {
+  static constexpr int SB = 1;
+  unsigned long long list;
+  int n;
+  __device__ __forceinline__ ScoreTiles(int c) : list(0x1540ull), n(c == 3 ? 4 : 3) {}
+};
 
 // ---- walks --------------------------------------------------------------------
 // MODE 0: the forward, writing y, the last state, and with `save` the state that
 //         enters each chunk as an operand copy (T, tile order);
-// MODE 1: the state alone (k, x): with seg_loc each segment from zero, leaving its
-//         last state and log2 decay there; without, the walk that only saves;
+// MODE 1: the state alone (k, x): each segment from zero, leaving its last state and
+//         log2 decay in seg_loc and seg_dec, or (with save) the walk that only saves;
 // MODE 2: the cotangent of the state alone, chunks in reverse: k is q, x is d_y,
 //         and the weights are e^{a_u}.
 // VEC: rows are whole 16-byte pieces; the next chunk's are then in flight while one is
-// worked on. A chain split into segments starts each of them from the states that the
-// segments before it (after it, MODE 2 users) left in seg_loc.
+// worked on. A chain split into segments takes three launches: the segments' own states
+// (MODE 1 or 2), k_attn_scan, which joins them, and the walk itself.
 template <typename T, int RT, int PW, int MODE, bool VEC>
 __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __restrict__ x, const T* __restrict__ k,
                                                       const T* __restrict__ q, const T* __restrict__ da,
@@ -375,7 +465,7 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
   using V = AV<T>;
   constexpr int L = V::L, NT = L / 16, NJ = L / 32, PT16 = ATW * PW;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  DecayTab* tab = reinterpret_cast<DecayTab*>(lds + LD::tab);
+  DecayTab* tabs = reinterpret_cast<DecayTab*>(lds + LD::tab);   // this chunk's and the next one's
   T* ks = reinterpret_cast<T*>(lds + LD::k);
   T* xs = reinterpret_cast<T*>(lds + LD::x);
   T* qs = reinterpret_cast<T*>(lds + LD::q);
@@ -390,7 +480,8 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
   const int pt = item % g.npt, chain = item / g.npt;
   const int bi = chain / g.h, hi = chain % g.h, gi = hi / g.hpg;
   const int Vb = attn_len(g, bi), nkb = (Vb + g.CT - 1) / g.CT;
-  const int n0 = seg * g.SL, n1 = min(n0 + g.SL, g.NK);
+  const Segment sg(g, seg, Vb, nkb);
+  const int n0 = sg.n0, nlive = sg.n1;
   const int p0 = pt * LD::PT, pn = min(g.p - p0, LD::PT);
   const unsigned kst = (unsigned)(g.g * g.r), xst = (unsigned)(g.h * g.p);   // strides of a row u
   const size_t row0 = (size_t)bi * g.s * g.c;
@@ -405,8 +496,15 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
   for (int pw = 0; pw < PW; pw++)
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) H[pw][rt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (MODE == 0 || seg_loc == nullptr || save != nullptr) {
-    if (h0 != nullptr) {
+  if (MODE == 0 || save != nullptr) {
+    if (seg > 0) {   // k_attn_scan left it there
+      const float* src = seg_loc + (((size_t)chain * g.nseg + seg) * g.npt + pt) * TILES;
+#pragma unroll
+      for (int pw = 0; pw < PW; pw++)
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++)
+          H[pw][rt] = *reinterpret_cast<const f4*>(src + tile_off(RT, wave * PW + pw, rt, lane));
+    } else if (h0 != nullptr) {
 #pragma unroll
       for (int pw = 0; pw < PW; pw++)
 #pragma unroll
@@ -414,22 +512,14 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
           H[pw][rt] = ld_state4(h0 + (size_t)chain * g.p * g.r, g.p, g.r, p0 + 16 * (wave * PW + pw) + ln,
                                 16 * rt + 4 * lq);
     }
-    for (int s = 0; s < seg; s++) {   // what the segments before this one leave
-      const size_t at = ((size_t)chain * g.nseg + s) * g.npt + pt;
-      const float dec = ex2((float)seg_dec[at]);
-#pragma unroll
-      for (int pw = 0; pw < PW; pw++)
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++)
-          H[pw][rt] = H[pw][rt] * dec +
-                      *reinterpret_cast<const f4*>(seg_loc + at * TILES + tile_off(RT, wave * PW + pw, rt, lane));
-    }
   }
   double acc_dec = 0.0;
 
-  const int nlive = min(n1, nkb);
   Stage<T, 16 * RT, ATT> sk, sq;
   Stage<T, LD::PT, ATT> sx;
+  sk.setup(kst, g.r);
+  sq.setup(kst, g.r);
+  sx.setup(xst, pn);
   T dnext = (T)0.0f;                        // da of the token that row u = lane opens
   const int ltok = (lane * g.cinv) >> 16;   // the token of row u = lane
   auto chunk = [&](int i) { return MODE == 2 ? nlive - 1 - (i - n0) : i; };
@@ -437,17 +527,35 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
     const int t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
     const size_t u0 = (size_t)t0 * g.c;
     if constexpr (VEC) {
-      sk.load(kb + u0 * kst, kst, nrows, g.r);
-      sx.load(xb + u0 * xst, xst, nrows, pn);
-      if constexpr (MODE == 0) sq.load(qb + u0 * kst, kst, nrows, g.r);
+      sk.load(row_rsrc(kb + u0 * kst, kst, nrows, g.r));
+      sx.load(row_rsrc(xb + u0 * xst, xst, nrows, pn));
+      if constexpr (MODE == 0) sq.load(row_rsrc(qb + u0 * kst, kst, nrows, g.r));
     }
-    dnext = (T)0.0f;
-    if (wave == 0 && lane < nrows && ltok * g.c == lane) dnext = dab[(size_t)(t0 + ltok) * g.h];
   };
-  if (nlive > n0) fetch(chunk(n0));
+  // the last wave makes each chunk's decay table while the chunk before is worked on
+  constexpr int TWAVE = ATW - 1;
+  auto fetch_da = [&](int n) {
+    const int t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
+    dnext = (T)0.0f;
+    if (lane < nrows && ltok * g.c == lane) dnext = dab[(size_t)(t0 + ltok) * g.h];
+  };
+  if (nlive > n0) {
+    if (wave == TWAVE) {
+      fetch_da(chunk(n0));
+      decay_table(tabs, log2_decay(to_f(dnext)), lane);
+      if (n0 + 1 < nlive) fetch_da(chunk(n0 + 1));
+    }
+    fetch(chunk(n0));
+    if constexpr (VEC && MODE == 0) dropped_stores<T, NT * PW>();
+  }
+  if constexpr (MODE == 0) {
+    for (int e = threadIdx.x; e < L * LD::SP / 4; e += ATT)
+      reinterpret_cast<typename V::quad*>(ss)[e] = typename V::quad{};
+  }
   for (int i = n0; i < nlive; i++) {
     const int n = chunk(i), t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
     const size_t u0 = (size_t)t0 * g.c;
+    const DecayTab* tab = tabs + ((i - n0) & 1);
     __syncthreads();   // the last chunk's tiles have been read
     if constexpr (VEC) {
       sk.store(ks, LD::RP);
@@ -458,12 +566,7 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
       sx.direct(xs, LD::PP, xb + u0 * xst, xst, nrows, pn);
       if constexpr (MODE == 0) sq.direct(qs, LD::RP, qb + u0 * kst, kst, nrows, g.r);
     }
-    if (wave == 0) decay_table(tab, log2_decay(to_f(dnext)), lane);
     __syncthreads();
-    if (i + 1 < nlive) fetch(chunk(i + 1));
-    const double total = tab->total;
-    acc_dec += total;
-
     if constexpr (MODE != 2) {
       if (save != nullptr) {
         T* dst = save + (((size_t)chain * g.NK + n) * g.npt + pt) * TILES;
@@ -479,79 +582,101 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
       }
     }
 
+    if (i + 1 < nlive) {
+      fetch(chunk(i + 1));
+      if (wave == TWAVE) {
+        decay_table(tabs + ((i + 1 - n0) & 1), log2_decay(to_f(dnext)), lane);
+        if (i + 2 < nlive) fetch_da(chunk(i + 2));
+      }
+    }
+    const double total = tab->total;
+    acc_dec += total;
+
     if constexpr (MODE == 0) {
-      // scores s[u][j] = (q[u].k[j]) e^{a_u - a_j}, one 16x16 tile (columns u) at a time
+      // scores s[u][j] = (q[u].k[j]) e^{a_u - a_j} in 16x16 tiles (columns u)
+      const ScoreTiles<NT> tl(g.c);
+      constexpr int SB = ScoreTiles<NT>::SB;
+#pragma unroll 1
+      for (int b0 = 0; b0 < tl.n; b0 += ATW * SB) {
+        f4 a[SB];
+        int ut[SB], jt[SB];
 #pragma unroll
-      for (int it = 0; it < (NT * NT + ATW - 1) / ATW; it++) {
-        const int id = it * ATW + wave, ut = id % NT, jt = id / NT;
-        f4 a = {0.0f, 0.0f, 0.0f, 0.0f};
-        // rows of a token never straddle 16 rows unless c = 3 (then up to two rows further)
-        if (jt <= ut || (g.c == 3 && jt == ut + 1)) {
+        for (int k2 = 0; k2 < SB; k2++) {
+          const int at = min(b0 + k2 * ATW + wave, tl.n - 1);   // past the end: the last tile once more
+          const int code = (int)(tl.list >> (4 * at)) & 15;
+          ut[k2] = 16 * (code >> 2);
+          jt[k2] = 16 * (code & 3);
+          a[k2] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
 #pragma unroll
-          for (int m = 0; m < RT / 2; m++)
-            a = mma32(row_frag(ks, LD::RP, 16 * jt, m, lane), row_frag(qs, LD::RP, 16 * ut, m, lane), a);
-          const int u = 16 * ut + ln, tu = (u * g.cinv) >> 16;
+        for (int m = 0; m < RT / 2; m++)
+#pragma unroll
+          for (int k2 = 0; k2 < SB; k2++)
+            a[k2] = mma32(row_frag(ks, LD::RP, jt[k2], m, lane), row_frag(qs, LD::RP, ut[k2], m, lane), a[k2]);
+#pragma unroll
+        for (int k2 = 0; k2 < SB; k2++) {
+          const int u = ut[k2] + ln, tu = (u * g.cinv) >> 16;
           const float uh = tab->hi[u], ul = tab->lo[u];
-          const f4 jh = *reinterpret_cast<const f4*>(tab->hi + 16 * jt + 4 * lq);
-          const f4 jl = *reinterpret_cast<const f4*>(tab->lo + 16 * jt + 4 * lq);
+          const f4 jh = *reinterpret_cast<const f4*>(tab->hi + jt[k2] + 4 * lq);
+          const f4 jl = *reinterpret_cast<const f4*>(tab->lo + jt[k2] + 4 * lq);
 #pragma unroll
           for (int e = 0; e < 4; e++) {
-            const int tj = ((16 * jt + 4 * lq + e) * g.cinv) >> 16;
-            a[e] = tj <= tu ? a[e] * ex2((uh - jh[e]) + (ul - jl[e])) : 0.0f;
+            const int tj = ((jt[k2] + 4 * lq + e) * g.cinv) >> 16;
+            a[k2][e] = tj <= tu ? a[k2][e] * ex2((uh - jh[e]) + (ul - jl[e])) : 0.0f;
           }
+          st_quad(ss, LD::SP, u, jt[k2] / 4 + lq, to_quad<T>(a[k2]));
         }
-        st_quad(ss, LD::SP, 16 * ut + ln, 4 * jt + lq, to_quad<T>(a));
       }
-      __syncthreads();
-      // y[u] for this wave's rows p
       typename V::frag hf[PW][RT / 2];
 #pragma unroll
       for (int pw = 0; pw < PW; pw++)
 #pragma unroll
         for (int m = 0; m < RT / 2; m++) hf[pw][m] = acc_frag<T>(H[pw][2 * m], H[pw][2 * m + 1]);
-      typename V::frag xf[PW][NJ];
+      __syncthreads();
+      // y[u] for this wave's rows p, all row tiles together
+      f4 a[NT][PW];
 #pragma unroll
-      for (int pw = 0; pw < PW; pw++)
+      for (int ut = 0; ut < NT; ut++)
 #pragma unroll
-        for (int m = 0; m < NJ; m++) xf[pw][m] = col_frag(xs, LD::PP, m, 16 * (wave * PW + pw), lane);
+        for (int pw = 0; pw < PW; pw++) a[ut][pw] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int ut = 0; ut < NT; ut++) {
-        f4 a[PW];
+      for (int m = 0; m < RT / 2; m++)
 #pragma unroll
-        for (int pw = 0; pw < PW; pw++) a[pw] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int m = 0; m < RT / 2; m++) {
+        for (int ut = 0; ut < NT; ut++) {
           const auto qf = row_frag(qs, LD::RP, 16 * ut, m, lane);
 #pragma unroll
-          for (int pw = 0; pw < PW; pw++) a[pw] = mma32(hf[pw][m], qf, a[pw]);
+          for (int pw = 0; pw < PW; pw++) a[ut][pw] = mma32(hf[pw][m], qf, a[ut][pw]);
         }
-        const int u = 16 * ut + ln;
-        const float st = tab->start[u];
 #pragma unroll
-        for (int pw = 0; pw < PW; pw++) a[pw] *= st;
+      for (int ut = 0; ut < NT; ut++) {
+        const float st = tab->start[16 * ut + ln];
 #pragma unroll
-        for (int m = 0; m < NJ; m++) {
-          if (32 * m < 16 * (ut + 1) || g.c == 3) {
-            const auto sf = row_frag(ss, LD::SP, 16 * ut, m, lane);
+        for (int pw = 0; pw < PW; pw++) a[ut][pw] *= st;
+      }
 #pragma unroll
-            for (int pw = 0; pw < PW; pw++) a[pw] = mma32(xf[pw][m], sf, a[pw]);
-          }
-        }
-        if (u < nrows) {
+      for (int m = 0; m < NJ; m++) {
+        typename V::frag xf[PW];
 #pragma unroll
-          for (int pw = 0; pw < PW; pw++)
-            st_row4(y + (row0 + u0) * xst + (size_t)hi * g.p, (unsigned)u * xst, g.p,
-                    p0 + 16 * (wave * PW + pw) + 4 * lq, a[pw]);
+        for (int pw = 0; pw < PW; pw++) xf[pw] = col_frag(xs, LD::PP, m, 16 * (wave * PW + pw), lane);
+#pragma unroll
+        for (int ut = 0; ut < NT; ut++) {
+          const auto sf = row_frag(ss, LD::SP, 16 * ut, m, lane);
+#pragma unroll
+          for (int pw = 0; pw < PW; pw++) a[ut][pw] = mma32(xf[pw], sf, a[ut][pw]);
         }
       }
+      const RowOut<T, VEC> yo(y + (row0 + u0) * xst + (size_t)hi * g.p + p0, xst, nrows, pn);
+#pragma unroll
+      for (int ut = 0; ut < NT; ut++)
+#pragma unroll
+        for (int pw = 0; pw < PW; pw++) yo.put(16 * ut + ln, 16 * (wave * PW + pw) + 4 * lq, a[ut][pw]);
     }
     state_update<T, RT, PW>(H, ks, xs, MODE == 2 ? tab->start : tab->end, ex2((float)total), wave, lane);
   }
 
   if constexpr (MODE == 0) {
     // rows past the sequence's length are zero
-    const int z0 = max(n0 * g.CT, Vb), z1 = min(n1 * g.CT, g.s);
-    for (int u = z0 * g.c + (int)(threadIdx.x / 16); u < z1 * g.c; u += ATT / 16) {
+    for (int u = sg.z0 * g.c + (int)(threadIdx.x / 16); u < sg.z1 * g.c; u += ATT / 16) {
       T* yr = y + (row0 + u) * xst + (size_t)hi * g.p + p0;
       for (int e = threadIdx.x % 16; e < pn; e += 16) yr[e] = (T)0.0f;
     }
@@ -563,7 +688,7 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
           st_state4(h_last + (size_t)chain * g.p * g.r, g.p, g.r, p0 + 16 * (wave * PW + pw) + ln, 16 * rt + 4 * lq,
                     H[pw][rt]);
     }
-  } else if (seg_loc != nullptr && save == nullptr) {
+  } else if (save == nullptr) {
     const size_t at = ((size_t)chain * g.nseg + seg) * g.npt + pt;
     if (threadIdx.x == 0) seg_dec[at] = acc_dec;
 #pragma unroll
@@ -571,6 +696,42 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
 #pragma unroll
       for (int rt = 0; rt < RT; rt++)
         *reinterpret_cast<f4*>(seg_loc + at * TILES + tile_off(RT, wave * PW + pw, rt, lane)) = H[pw][rt];
+  }
+}
+
+// Joins the segments of each chain: seg_loc[seg], the state that the segment leaves from
+// zero, becomes the state that it starts from (from `first`, or zeros; BACK: the segments
+// in reverse). One thread for four values of a state.
+template <bool BACK>
+__global__ __launch_bounds__(256) void k_attn_scan(AttnGeo g, int RT, int tiles, const float* __restrict__ first,
+                                                   float* __restrict__ seg_loc, const double* __restrict__ seg_dec) {
+  const int pt = blockIdx.x % g.npt, chain = blockIdx.x / g.npt, e = blockIdx.y * 256 + threadIdx.x;
+  if (4 * e >= tiles) return;
+  const int lane = e & 63, tile = e >> 6, rt = tile % RT, pi = pt * g.PT + 16 * (tile / RT) + (lane & 15);
+  f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (first != nullptr)
+    v = ld_state4(first + (size_t)chain * g.p * g.r, g.p, g.r, pi, 16 * rt + 4 * (lane >> 4));
+  constexpr int U = 8;   // segments whose loads are in flight together
+  for (int s0 = 0; s0 < g.nseg; s0 += U) {
+    f4 loc[U];
+    float dec[U];
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+      if (s0 + i < g.nseg - 1) {   // the last one's own state is not needed
+        const int s = BACK ? g.nseg - 1 - s0 - i : s0 + i;
+        const size_t at = ((size_t)chain * g.nseg + s) * g.npt + pt;
+        loc[i] = *reinterpret_cast<const f4*>(seg_loc + at * tiles + 4 * e);
+        dec[i] = ex2((float)seg_dec[at]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+      if (s0 + i < g.nseg) {
+        const int s = BACK ? g.nseg - 1 - s0 - i : s0 + i;
+        *reinterpret_cast<f4*>(seg_loc + (((size_t)chain * g.nseg + s) * g.npt + pt) * tiles + 4 * e) = v;
+        if (s0 + i < g.nseg - 1) v = v * dec[i] + loc[i];
+      }
+    }
   }
 }
 

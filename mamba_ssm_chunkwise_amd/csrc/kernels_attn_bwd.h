@@ -17,6 +17,8 @@
 // comes from the copies that the forward (or a walk over k and x) left per chunk.
 #pragma once
 
+#include <type_traits>
+
 #include "kernels_attn.h"
 
 namespace mom {
@@ -79,7 +81,7 @@ template <typename T, int RT, int PT, bool PART, bool VEC>
 __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     AttnGeo g, const T* __restrict__ x, const T* __restrict__ k, const T* __restrict__ q, const T* __restrict__ da,
     const T* __restrict__ save, const T* __restrict__ dy, const float* __restrict__ d_last,
-    const float* __restrict__ seg_loc, const double* __restrict__ seg_dec, T* __restrict__ d_x, T* __restrict__ d_k,
+    const float* __restrict__ seg_loc, T* __restrict__ d_x, T* __restrict__ d_k,
     T* __restrict__ d_q, T* __restrict__ d_da, float* __restrict__ d_h0, float* __restrict__ part_k,
     float* __restrict__ part_q, float* __restrict__ part_da) {
   using LD = LdsB<T, RT, PT>;
@@ -111,7 +113,8 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
   const int pt = item % g.npt, chain = item / g.npt;
   const int bi = chain / g.h, hi = chain % g.h, gi = hi / g.hpg;
   const int Vb = attn_len(g, bi), nkb = (Vb + g.CT - 1) / g.CT;
-  const int n0 = seg * g.SL, n1 = min(n0 + g.SL, g.NK);
+  const Segment sg(g, seg, Vb, nkb);
+  const int n0 = sg.n0, nlive = sg.n1;
   const int p0 = pt * 16 * PT, pn = min(g.p - p0, 16 * PT);
   const unsigned kst = (unsigned)(g.g * g.r), xst = (unsigned)(g.h * g.p);
   const size_t row0 = (size_t)bi * g.s * g.c;
@@ -130,38 +133,37 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
   for (int i = 0; i < RW; i++) {
     G[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (d_last != nullptr)
+    if (seg < g.nseg - 1)   // k_attn_scan left it there
+      G[i] = *reinterpret_cast<const f4*>(seg_loc + (((size_t)chain * g.nseg + seg) * g.npt + pt) * TILES +
+                                          tile_off(RT, mp, mr + i, lane));
+    else if (d_last != nullptr)
       G[i] = ld_state4(d_last + (size_t)chain * g.p * g.r, g.p, g.r, p0 + 16 * mp + ln, 16 * (mr + i) + 4 * lq);
   }
-  for (int s = g.nseg - 1; s > seg; s--) {   // what the segments after this one leave
-    const size_t at = ((size_t)chain * g.nseg + s) * g.npt + pt;
-    const float dec = ex2((float)seg_dec[at]);
-#pragma unroll
-    for (int i = 0; i < RW; i++)
-      G[i] = G[i] * dec + *reinterpret_cast<const f4*>(seg_loc + at * TILES + tile_off(RT, mp, mr + i, lane));
-  }
-
-  const int nlive = min(n1, nkb);
   // the next chunk's rows, in flight while this one is worked on
   Stage<T, 16 * RT, ABT> sk, sq;
   Stage<T, 16 * PT, ABT> sx, sy;
   StageH<T, RT, PT> sh;
+  sk.setup(kst, g.r);
+  sq.setup(kst, g.r);
+  sx.setup(xst, pn);
+  sy.setup(xst, pn);
   T dnext = (T)0.0f;
   const int ltok = (lane * g.cinv) >> 16;   // the token of row u = lane
   auto fetch = [&](int n) {
     const int t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
     const size_t u0 = (size_t)t0 * g.c;
     if constexpr (VEC) {
-      sk.load(kb + u0 * kst, kst, nrows, g.r);
-      sq.load(qb + u0 * kst, kst, nrows, g.r);
-      sx.load(xb + u0 * xst, xst, nrows, pn);
-      sy.load(yb + u0 * xst, xst, nrows, pn);
+      sk.load(row_rsrc(kb + u0 * kst, kst, nrows, g.r));
+      sq.load(row_rsrc(qb + u0 * kst, kst, nrows, g.r));
+      sx.load(row_rsrc(xb + u0 * xst, xst, nrows, pn));
+      sy.load(row_rsrc(yb + u0 * xst, xst, nrows, pn));
     }
     sh.load(save + (((size_t)chain * g.NK + n) * g.npt + pt) * TILES);
     dnext = (T)0.0f;
     if (wave == 0 && lane < nrows && ltok * g.c == lane) dnext = dab[(size_t)(t0 + ltok) * g.h];
   };
   if (nlive > n0) fetch(nlive - 1);
+  if constexpr (VEC) dropped_stores<T, (2 * RT + PT) * NT / ABW>();
   for (int n = nlive - 1; n >= n0; n--) {
     const int t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
     const size_t u0 = (size_t)t0 * g.c;
@@ -237,6 +239,14 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     }
     __syncthreads();
 
+    using TO = typename std::conditional<PART, float, T>::type;
+    auto chunk_rows = [&](T* out, float* part) -> TO* {
+      if constexpr (PART) return part + (row0 + u0) * pst + (size_t)slice * g.r;
+      else return out == nullptr ? nullptr : out + (row0 + u0) * kst + (size_t)gi * g.r;
+    };
+    const RowOut<TO, VEC> oq(chunk_rows(d_q, part_q), PART ? pst : kst, nrows, g.r);
+    const RowOut<TO, VEC> ok(chunk_rows(d_k, part_k), PART ? pst : kst, nrows, g.r);
+    const RowOut<T, VEC> ox(d_x == nullptr ? nullptr : d_x + (row0 + u0) * xst + (size_t)hi * g.p + p0, xst, nrows, pn);
     // d_q and d_k (transposed: columns are rows u of the chunk). A wave takes RB r tiles by
     // UB tiles of rows, and keeps the operands of its r tiles.
     {
@@ -281,16 +291,8 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
               for (int i = 0; i < RB; i++) a[i] = mma32(kf[i][m], tf, a[i]);
             }
-          if (u < nrows) {
 #pragma unroll
-            for (int i = 0; i < RB; i++) {
-              const int r0 = 16 * (rt0 + i) + 4 * lq;
-              if constexpr (PART)
-                st_row4(part_q + (row0 + u0) * pst + (size_t)slice * g.r, (unsigned)u * pst, g.r, r0, a[i]);
-              else if (d_q != nullptr)
-                st_row4(d_q + (row0 + u0) * kst + (size_t)gi * g.r, (unsigned)u * kst, g.r, r0, a[i]);
-            }
-          }
+          for (int i = 0; i < RB; i++) oq.put(u, 16 * (rt0 + i) + 4 * lq, a[i]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -332,16 +334,8 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
               for (int i = 0; i < RB; i++) b[i] = mma32(qf[i][m], tf, b[i]);
             }
-          if (u < nrows) {
 #pragma unroll
-            for (int i = 0; i < RB; i++) {
-              const int r0 = 16 * (rt0 + i) + 4 * lq;
-              if constexpr (PART)
-                st_row4(part_k + (row0 + u0) * pst + (size_t)slice * g.r, (unsigned)u * pst, g.r, r0, b[i]);
-              else if (d_k != nullptr)
-                st_row4(d_k + (row0 + u0) * kst + (size_t)gi * g.r, (unsigned)u * kst, g.r, r0, b[i]);
-            }
-          }
+          for (int i = 0; i < RB; i++) ok.put(u, 16 * (rt0 + i) + 4 * lq, b[i]);
         }
       }
     }
@@ -373,12 +367,8 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
             for (int i = 0; i < PB; i++) a[i] = mma32(col_frag(ys, LD::PP, m, 16 * (pj0 + i), lane), sf, a[i]);
           }
-        if (u < nrows && d_x != nullptr) {
 #pragma unroll
-          for (int i = 0; i < PB; i++)
-            st_row4(d_x + (row0 + u0) * xst + (size_t)hi * g.p, (unsigned)u * xst, g.p, p0 + 16 * (pj0 + i) + 4 * lq,
-                    a[i]);
-        }
+        for (int i = 0; i < PB; i++) ox.put(u, 16 * (pj0 + i) + 4 * lq, a[i]);
       }
     }
     // G'
@@ -394,7 +384,11 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
       for (int i = 0; i < RW; i++) {
         G[i] *= dec;
 #pragma unroll
-        for (int m = 0; m < NJ; m++) G[i] = yf[m].mma(col_frag(qs, LD::RP, m, 16 * (mr + i), lane), G[i]);
+        for (int m = 0; m < NJ; m++) {
+          const auto qf = col_frag(qs, LD::RP, m, 16 * (mr + i), lane);
+#pragma unroll
+          for (int k2 = 0; k2 < V::NSPLIT; k2++) G[i] = mma32(qf, yf[m].piece(k2), G[i]);
+        }
       }
     }
     __syncthreads();   // every tile has been read; the sums are complete
@@ -411,8 +405,8 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
         }
       }
       for (int i = 0; i < ABW; i++) thr += (double)th[i];
-      const double si = wave_sum_incl(suf, lane), pi = wave_sum_incl(pre, lane);
-      const double v = __shfl(si, 63) - si + suf + pi - pre + thr * (double)dec;
+      const double si = wave_sum_incl(suf), pi = wave_sum_incl(pre);
+      const double v = lane63(si) - si + suf + pi - pre + thr * (double)dec;
       if (lane < nrows && ltok * g.c == lane) {
         if constexpr (PART)
           part_da[((size_t)bi * g.s + t0 + ltok) * g.h * g.npt + slice] = (float)v;
@@ -424,7 +418,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 
   // rows past the sequence's length are zero
   {
-    const int z0 = max(n0 * g.CT, Vb), z1 = min(n1 * g.CT, g.s);
+    const int z0 = sg.z0, z1 = sg.z1;
     for (int u = z0 * g.c + wave; u < z1 * g.c; u += ABW) {
       const size_t at = row0 + u;
       for (int e = lane; e < pn && d_x != nullptr; e += 64) d_x[at * xst + (size_t)hi * g.p + p0 + e] = (T)0.0f;

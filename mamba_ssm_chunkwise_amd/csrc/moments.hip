@@ -38,7 +38,7 @@ const char* const kKernelNames[KID_N] = {"k_carry", "k_scan",      "k_fwd",     
                                          "k_fix",   "k_zero_tail", "k_prep_dm1", "k_gscan",  "k_gfix",
                                          "k_cscan", "k_rot_seg",   "k_rot_carry", "k_rot_apply",
                                          "k_pair",  "k_gentry",    "k_cscan_sum", "k_cscan_grp",
-                                         "k_attn_state", "k_attn_fwd", "k_attn_bwd", "k_attn_sum", "k_attn_step",
+                                         "k_attn_state", "k_attn_scan", "k_attn_fwd", "k_attn_bwd", "k_attn_sum", "k_attn_step",
                                          "k_qk_fwd", "k_qk_bwd", "k_qk_sum"};
 struct Prof {
   std::mutex mu;
