@@ -79,7 +79,7 @@ template <> struct AV<bf16> {
   static constexpr int NSPLIT = 3;
   using quad = uint2;
   using frag = bf8;
-  __host__ __device__ static constexpr int pitch(int n) { return n + ((16 - n % 64) + 64) % 64; }
+  __host__ __device__ static constexpr int pitch(int n) { return n; }
 };
 template <> struct AV<float> {
   static constexpr int L = 32;
@@ -115,36 +115,37 @@ template <typename T> __device__ __forceinline__ typename AV<T>::frag acc_frag(f
 }
 
 // ---- LDS tiles [row][column] ---------------------------------------------------
-// Rows of `pitch` elements. In bf16 tiles the 4-element quads of rows 8..15 of
-// each 16 are swapped pairwise (quad v sits at v ^ 1): with rows 8 banks apart,
-// reads of one quad from 16 rows, and transposing reads of 4 rows, are then both
-// free of bank conflicts.
-template <typename T> __device__ __forceinline__ int swz(int row);
-template <> __device__ __forceinline__ int swz<bf16>(int row) { return (row >> 3) & 1; }
-template <> __device__ __forceinline__ int swz<float>(int) { return 0; }
-
-template <typename T>
-__device__ __forceinline__ typename AV<T>::quad ld_quad(const T* t, int P, int row, int v) {
-  return *reinterpret_cast<const typename AV<T>::quad*>(t + row * P + 4 * (v ^ swz<T>(row)));
+// COLS is 64 or 128 (32 for the float scores). bf16 rows are not padded: quad v (four
+// columns, 8 bytes) of a row sits at v ^ swz(row). What 32 lanes read together, one quad
+// and its neighbour of 16 rows, or (transposing reads) four quads of eight rows, then
+// touches each of the 64 banks once (measured: no conflicts), and the pairs of quads that
+// 16-byte pieces are stay together. Float rows are padded by one quad instead.
+template <typename T, int COLS> __device__ __forceinline__ int swz(int row) {
+  if constexpr (sizeof(T) != 2) return 0;
+  else if constexpr (COLS >= 128) return ((row & 7) << 2) | (((row >> 3) & 1) << 1);
+  else return (((row >> 1) & 3) << 2) | (((row >> 3) & 1) << 1);
 }
-template <typename T>
-__device__ __forceinline__ void st_quad(T* t, int P, int row, int v, typename AV<T>::quad x) {
-  *reinterpret_cast<typename AV<T>::quad*>(t + row * P + 4 * (v ^ swz<T>(row))) = x;
+template <int COLS, typename T>
+__device__ __forceinline__ typename AV<T>::quad ld_quad(const T* t, int row, int v) {
+  return *reinterpret_cast<const typename AV<T>::quad*>(t + row * AV<T>::pitch(COLS) + 4 * (v ^ swz<T, COLS>(row)));
 }
-// One 16-byte piece (column piece * PE) of a row.
-__device__ __forceinline__ void st_piece(bf16* t, int P, int row, int piece, uint4 x) {
-  if (swz<bf16>(row)) x = make_uint4(x.z, x.w, x.x, x.y);
-  *reinterpret_cast<uint4*>(t + row * P + 8 * piece) = x;
+template <int COLS, typename T>
+__device__ __forceinline__ void st_quad(T* t, int row, int v, typename AV<T>::quad x) {
+  *reinterpret_cast<typename AV<T>::quad*>(t + row * AV<T>::pitch(COLS) + 4 * (v ^ swz<T, COLS>(row))) = x;
 }
-__device__ __forceinline__ void st_piece(float* t, int P, int row, int piece, uint4 x) {
-  *reinterpret_cast<uint4*>(t + row * P + 4 * piece) = x;
+// One 16-byte piece (columns piece * PE ..) of a row.
+template <int COLS, typename T>
+__device__ __forceinline__ void st_piece(T* t, int row, int piece, uint4 x) {
+  constexpr int PE = AV<T>::PE;
+  *reinterpret_cast<uint4*>(t + row * AV<T>::pitch(COLS) + 4 * ((piece * (PE / 4)) ^ swz<T, COLS>(row))) = x;
 }
 
 // Fragment of rows row0 + lane % 16, contracted over columns 32m .. 32m + 31.
-template <typename T>
-__device__ __forceinline__ typename AV<T>::frag row_frag(const T* t, int P, int row0, int m, int lane) {
-  const int row = row0 + (lane & 15), q = lane >> 4;
-  return join(ld_quad(t, P, row, 8 * m + q), ld_quad(t, P, row, 8 * m + 4 + q));
+template <int COLS, typename T>
+__device__ __forceinline__ typename AV<T>::frag row_frag(const T* t, int row0, int m, int lane) {
+  const int row = lane & 15, q = lane >> 4;
+  const T* t0 = t + row0 * AV<T>::pitch(COLS);   // row0 is a multiple of 16: no change of swz
+  return join(ld_quad<COLS>(t0, row, 8 * m + q), ld_quad<COLS>(t0, row, 8 * m + 4 + q));
 }
 // Fragment of columns col0 + lane % 16, contracted over rows 32m .. 32m + 31.
 // bf16: transposing reads; in each 16-lane group, lane j receives element j % 4
@@ -153,13 +154,17 @@ typedef short as4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ as4 lds_tr16(const bf16* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) as4*)p);
 }
-__device__ __forceinline__ bf8 col_frag(const bf16* t, int P, int m, int col0, int lane) {
-  const int row = 32 * m + 4 * (lane >> 4) + ((lane >> 2) & 3);
-  const bf16* p0 = t + row * P + col0 + 4 * ((lane & 3) ^ swz<bf16>(row));
+template <int COLS>
+__device__ __forceinline__ bf8 col_frag(const bf16* t, int m, int col0, int lane) {
+  constexpr int P = AV<bf16>::pitch(COLS);
+  const int row = 4 * (lane >> 4) + ((lane >> 2) & 3);
+  const bf16* p0 = t + 32 * m * P + row * P + 4 * ((col0 / 4 + (lane & 3)) ^ swz<bf16, COLS>(row));
   const as4 v[2] = {lds_tr16(p0), lds_tr16(p0 + 16 * P)};
   return __builtin_bit_cast(bf8, v);
 }
-__device__ __forceinline__ AV<float>::frag col_frag(const float* t, int P, int m, int col0, int lane) {
+template <int COLS>
+__device__ __forceinline__ AV<float>::frag col_frag(const float* t, int m, int col0, int lane) {
+  constexpr int P = AV<float>::pitch(COLS);
   AV<float>::frag f;
   const float* p0 = t + (32 * m + 4 * (lane >> 4)) * P + col0 + (lane & 15);
 #pragma unroll
@@ -246,14 +251,14 @@ struct Stage {
 #pragma unroll
     for (int i = 0; i < N; i++) v[i] = buf_load(r, off0 + (unsigned)i * step);
   }
-  __device__ __forceinline__ void store(T* t, int P) const {
+  __device__ __forceinline__ void store(T* t) const {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int e = i * NT + (int)threadIdx.x;
-      st_piece(t, P, e / PR, e % PR, v[i]);
+      st_piece<COLS>(t, e / PR, e % PR, v[i]);
     }
   }
-  __device__ __forceinline__ static void direct(T* t, int P, const T* base, unsigned stride, int nrows, int n) {
+  __device__ __forceinline__ static void direct(T* t, const T* base, unsigned stride, int nrows, int n) {
 #pragma unroll 1
     for (int e = (int)threadIdx.x; e < L * PR; e += NT) {
       const int row = e / PR, c0 = e % PR * PE;
@@ -261,7 +266,7 @@ struct Stage {
 #pragma unroll
       for (int i = 0; i < PE; i++)
         x[i] = row < nrows && c0 + i < n ? base[(unsigned)row * stride + (unsigned)(c0 + i)] : (T)0.0f;
-      st_piece(t, P, row, e % PR, __builtin_bit_cast(uint4, x));
+      st_piece<COLS>(t, row, e % PR, __builtin_bit_cast(uint4, x));
     }
   }
 };
@@ -330,6 +335,24 @@ __device__ __forceinline__ void decay_table(DecayTab* t, double v, int lane) {
   if (lane == 0) t->total = e;
 }
 
+// The lane number as a value that the compiler takes for a new one: LDS addresses are then
+// made again for each phase of a chunk, from a few instructions, instead of being kept in
+// dozens of registers over the whole loop.
+template <bool ON = true>
+__device__ __forceinline__ int fresh(int lane) {
+  if constexpr (ON) asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+// Nothing is scheduled across: the loads before it are all issued before the matrix
+// instructions behind it, which then wait for them one by one. (Left to itself the compiler
+// saves registers by loading one operand pair, waiting out its latency, and so on.)
+__device__ __forceinline__ void issue_fence() { __builtin_amdgcn_sched_barrier(0); }
+// v where keep, else zero, whatever v is; without a branch.
+__device__ __forceinline__ float keep_if(bool keep, float v) {
+  return __uint_as_float(__float_as_uint(v) & (keep ? 0xFFFFFFFFu : 0u));
+}
+
 // Work of a block: workgroups are handed out round-robin to the eight XCDs, so
 // consecutive chains (heads of one key group read the same rows) are given to one
 // XCD and share its L2.
@@ -383,8 +406,8 @@ __device__ __forceinline__ void dropped_stores() {
 // LDS of the walks.
 template <typename T, int RT, int PW>
 struct LdsA {
-  static constexpr int L = AV<T>::L, RP = AV<T>::pitch(16 * RT), PT = 16 * ATW * PW, PP = AV<T>::pitch(PT),
-                       SP = AV<T>::pitch(L);
+  static constexpr int L = AV<T>::L, RC = 16 * RT, PC = 16 * ATW * PW;   // columns of the tiles
+  static constexpr int RP = AV<T>::pitch(RC), PP = AV<T>::pitch(PC), SP = AV<T>::pitch(L);
   static constexpr size_t tab = 0, k = 2 * sizeof(DecayTab), x = k + (size_t)L * RP * sizeof(T),
                           state_total = x + (size_t)L * PP * sizeof(T), q = state_total,
                           s = q + (size_t)L * RP * sizeof(T), total = s + (size_t)L * SP * sizeof(T);
@@ -399,31 +422,45 @@ __device__ __forceinline__ void state_update(f4 (&H)[PW][RT], const T* ks, const
   using LD = LdsA<T, RT, PW>;
   constexpr int NJ = AV<T>::L / 32;
   const int q = lane >> 4;
-  Scaled<AV<T>::NSPLIT> xf[PW][NJ];
+  // the rows of both halves of the chunk in flight together, as registers allow
+  constexpr int MB = PW == 1 ? NJ : 1;
 #pragma unroll
-  for (int m = 0; m < NJ; m++) {
-    const f4 w0 = *reinterpret_cast<const f4*>(w + 32 * m + 4 * q);
-    const f4 w1 = *reinterpret_cast<const f4*>(w + 32 * m + 16 + 4 * q);
+  for (int m0 = 0; m0 < NJ; m0 += MB) {
+    typename AV<T>::frag kf[MB][RT], xr[MB][PW];
+    f4 w0[MB], w1[MB];
 #pragma unroll
-    for (int pw = 0; pw < PW; pw++) xf[pw][m].make(col_frag(xs, LD::PP, m, 16 * (wave * PW + pw), lane), w0, w1);
-  }
+    for (int m = 0; m < MB; m++) {
+      w0[m] = *reinterpret_cast<const f4*>(w + 32 * (m0 + m) + 4 * q);
+      w1[m] = *reinterpret_cast<const f4*>(w + 32 * (m0 + m) + 16 + 4 * q);
 #pragma unroll
-  for (int rt = 0; rt < RT; rt++)
+      for (int pw = 0; pw < PW; pw++) xr[m][pw] = col_frag<LD::PC>(xs, m0 + m, 16 * (wave * PW + pw), lane);
+    }
 #pragma unroll
-    for (int pw = 0; pw < PW; pw++) H[pw][rt] *= dec;
-  // tile by tile within each piece of the scaled rows, so that consecutive matrix
-  // instructions do not wait for one another's sums
+    for (int m = 0; m < MB; m++)
 #pragma unroll
-  for (int m = 0; m < NJ; m++) {
-    typename AV<T>::frag kf[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) kf[rt] = col_frag(ks, LD::RP, m, 16 * rt, lane);
-#pragma unroll
-    for (int i = 0; i < AV<T>::NSPLIT; i++)
+      for (int rt = 0; rt < RT; rt++) kf[m][rt] = col_frag<LD::RC>(ks, m0 + m, 16 * rt, lane);
+    issue_fence();
+    if (m0 == 0) {
 #pragma unroll
       for (int rt = 0; rt < RT; rt++)
 #pragma unroll
-        for (int pw = 0; pw < PW; pw++) H[pw][rt] = mma32(kf[rt], xf[pw][m].piece(i), H[pw][rt]);
+        for (int pw = 0; pw < PW; pw++) H[pw][rt] *= dec;
+    }
+    Scaled<AV<T>::NSPLIT> xf[MB][PW];
+#pragma unroll
+    for (int m = 0; m < MB; m++)
+#pragma unroll
+      for (int pw = 0; pw < PW; pw++) xf[m][pw].make(xr[m][pw], w0[m], w1[m]);
+    // tile by tile within each piece of the scaled rows, so that consecutive matrix
+    // instructions do not wait for one another's sums
+#pragma unroll
+    for (int m = 0; m < MB; m++)
+#pragma unroll
+      for (int i = 0; i < AV<T>::NSPLIT; i++)
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+          for (int pw = 0; pw < PW; pw++) H[pw][rt] = mma32(kf[m][rt], xf[m][pw].piece(i), H[pw][rt]);
   }
 }
 
@@ -482,7 +519,7 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
   const int Vb = attn_len(g, bi), nkb = (Vb + g.CT - 1) / g.CT;
   const Segment sg(g, seg, Vb, nkb);
   const int n0 = sg.n0, nlive = sg.n1;
-  const int p0 = pt * LD::PT, pn = min(g.p - p0, LD::PT);
+  const int p0 = pt * LD::PC, pn = min(g.p - p0, LD::PC);
   const unsigned kst = (unsigned)(g.g * g.r), xst = (unsigned)(g.h * g.p);   // strides of a row u
   const size_t row0 = (size_t)bi * g.s * g.c;
   const T* kb = k + row0 * kst + (size_t)gi * g.r;
@@ -516,7 +553,7 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
   double acc_dec = 0.0;
 
   Stage<T, 16 * RT, ATT> sk, sq;
-  Stage<T, LD::PT, ATT> sx;
+  Stage<T, LD::PC, ATT> sx;
   sk.setup(kst, g.r);
   sq.setup(kst, g.r);
   sx.setup(xst, pn);
@@ -558,13 +595,13 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
     const DecayTab* tab = tabs + ((i - n0) & 1);
     __syncthreads();   // the last chunk's tiles have been read
     if constexpr (VEC) {
-      sk.store(ks, LD::RP);
-      sx.store(xs, LD::PP);
-      if constexpr (MODE == 0) sq.store(qs, LD::RP);
+      sk.store(ks);
+      sx.store(xs);
+      if constexpr (MODE == 0) sq.store(qs);
     } else {
-      sk.direct(ks, LD::RP, kb + u0 * kst, kst, nrows, g.r);
-      sx.direct(xs, LD::PP, xb + u0 * xst, xst, nrows, pn);
-      if constexpr (MODE == 0) sq.direct(qs, LD::RP, qb + u0 * kst, kst, nrows, g.r);
+      sk.direct(ks, kb + u0 * kst, kst, nrows, g.r);
+      sx.direct(xs, xb + u0 * xst, xst, nrows, pn);
+      if constexpr (MODE == 0) sq.direct(qs, qb + u0 * kst, kst, nrows, g.r);
     }
     __syncthreads();
     if constexpr (MODE != 2) {
@@ -594,37 +631,54 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
 
     if constexpr (MODE == 0) {
       // scores s[u][j] = (q[u].k[j]) e^{a_u - a_j} in 16x16 tiles (columns u)
+      const int la = fresh(lane), ln = la & 15, lq = la >> 4;
       const ScoreTiles<NT> tl(g.c);
       constexpr int SB = ScoreTiles<NT>::SB;
 #pragma unroll 1
       for (int b0 = 0; b0 < tl.n; b0 += ATW * SB) {
+        constexpr int MB = PW == 1 ? RT / 2 : RT / 4;   // operand pairs in flight: as registers allow
         f4 a[SB];
         int ut[SB], jt[SB];
 #pragma unroll
         for (int k2 = 0; k2 < SB; k2++) {
-          const int at = min(b0 + k2 * ATW + wave, tl.n - 1);   // past the end: the last tile once more
-          const int code = (int)(tl.list >> (4 * at)) & 15;
+          const int code = (int)(tl.list >> (4 * min(b0 + k2 * ATW + wave, tl.n - 1))) & 15;   // past the end: the last one
           ut[k2] = 16 * (code >> 2);
           jt[k2] = 16 * (code & 3);
           a[k2] = f4{0.0f, 0.0f, 0.0f, 0.0f};
         }
 #pragma unroll
-        for (int m = 0; m < RT / 2; m++)
+        for (int m0 = 0; m0 < RT / 2; m0 += MB) {
+          typename V::frag kf[SB][MB], qf[SB][MB];
 #pragma unroll
-          for (int k2 = 0; k2 < SB; k2++)
-            a[k2] = mma32(row_frag(ks, LD::RP, jt[k2], m, lane), row_frag(qs, LD::RP, ut[k2], m, lane), a[k2]);
+          for (int m = 0; m < MB; m++)
+#pragma unroll
+            for (int k2 = 0; k2 < SB; k2++) {
+              kf[k2][m] = row_frag<LD::RC>(ks, jt[k2], m0 + m, la);
+              qf[k2][m] = row_frag<LD::RC>(qs, ut[k2], m0 + m, la);
+            }
+          issue_fence();
+#pragma unroll
+          for (int m = 0; m < MB; m++)
+#pragma unroll
+            for (int k2 = 0; k2 < SB; k2++) a[k2] = mma32(kf[k2][m], qf[k2][m], a[k2]);
+        }
+        f4 jh[SB], jl[SB];
+        float uh[SB], ul[SB];
 #pragma unroll
         for (int k2 = 0; k2 < SB; k2++) {
-          const int u = ut[k2] + ln, tu = (u * g.cinv) >> 16;
-          const float uh = tab->hi[u], ul = tab->lo[u];
-          const f4 jh = *reinterpret_cast<const f4*>(tab->hi + jt[k2] + 4 * lq);
-          const f4 jl = *reinterpret_cast<const f4*>(tab->lo + jt[k2] + 4 * lq);
+          uh[k2] = tab->hi[ut[k2] + ln];
+          ul[k2] = tab->lo[ut[k2] + ln];
+          jh[k2] = *reinterpret_cast<const f4*>(tab->hi + jt[k2] + 4 * lq);
+          jl[k2] = *reinterpret_cast<const f4*>(tab->lo + jt[k2] + 4 * lq);
+        }
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const int tj = ((jt[k2] + 4 * lq + e) * g.cinv) >> 16;
-            a[k2][e] = tj <= tu ? a[k2][e] * ex2((uh - jh[e]) + (ul - jl[e])) : 0.0f;
-          }
-          st_quad(ss, LD::SP, u, jt[k2] / 4 + lq, to_quad<T>(a[k2]));
+        for (int k2 = 0; k2 < SB; k2++) {
+          // j <= u: up to the last row of u's token
+          const int u = ut[k2] + ln, last = ((u * g.cinv) >> 16) * g.c + g.c - 1 - jt[k2] - 4 * lq;
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            a[k2][e] = keep_if(e <= last, a[k2][e] * ex2((uh[k2] - jh[k2][e]) + (ul[k2] - jl[k2][e])));
+          st_quad<LD::L>(ss, u, jt[k2] / 4 + lq, to_quad<T>(a[k2]));
         }
       }
       typename V::frag hf[PW][RT / 2];
@@ -634,36 +688,51 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
         for (int m = 0; m < RT / 2; m++) hf[pw][m] = acc_frag<T>(H[pw][2 * m], H[pw][2 * m + 1]);
       __syncthreads();
       // y[u] for this wave's rows p, all row tiles together
+      constexpr int MB = PW == 1 ? RT / 2 : RT / 4;
+      const int lb = fresh(lane);
       f4 a[NT][PW];
 #pragma unroll
       for (int ut = 0; ut < NT; ut++)
 #pragma unroll
         for (int pw = 0; pw < PW; pw++) a[ut][pw] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int m = 0; m < RT / 2; m++)
+      for (int m0 = 0; m0 < RT / 2; m0 += MB) {
+        typename V::frag qf[MB][NT];
 #pragma unroll
-        for (int ut = 0; ut < NT; ut++) {
-          const auto qf = row_frag(qs, LD::RP, 16 * ut, m, lane);
+        for (int m = 0; m < MB; m++)
 #pragma unroll
-          for (int pw = 0; pw < PW; pw++) a[ut][pw] = mma32(hf[pw][m], qf, a[ut][pw]);
-        }
+          for (int ut = 0; ut < NT; ut++) qf[m][ut] = row_frag<LD::RC>(qs, 16 * ut, m0 + m, lb);
+        issue_fence();
 #pragma unroll
-      for (int ut = 0; ut < NT; ut++) {
-        const float st = tab->start[16 * ut + ln];
+        for (int m = 0; m < MB; m++)
 #pragma unroll
-        for (int pw = 0; pw < PW; pw++) a[ut][pw] *= st;
+          for (int ut = 0; ut < NT; ut++)
+#pragma unroll
+            for (int pw = 0; pw < PW; pw++) a[ut][pw] = mma32(hf[pw][m0 + m], qf[m][ut], a[ut][pw]);
       }
+      {
+        typename V::frag xf[NJ][PW], sf[NJ][NT];
+        float st[NT];
 #pragma unroll
-      for (int m = 0; m < NJ; m++) {
-        typename V::frag xf[PW];
+        for (int ut = 0; ut < NT; ut++) st[ut] = tab->start[16 * ut + (lb & 15)];
 #pragma unroll
-        for (int pw = 0; pw < PW; pw++) xf[pw] = col_frag(xs, LD::PP, m, 16 * (wave * PW + pw), lane);
+        for (int m = 0; m < NJ; m++) {
 #pragma unroll
-        for (int ut = 0; ut < NT; ut++) {
-          const auto sf = row_frag(ss, LD::SP, 16 * ut, m, lane);
+          for (int pw = 0; pw < PW; pw++) xf[m][pw] = col_frag<LD::PC>(xs, m, 16 * (wave * PW + pw), lb);
 #pragma unroll
-          for (int pw = 0; pw < PW; pw++) a[ut][pw] = mma32(xf[pw], sf, a[ut][pw]);
+          for (int ut = 0; ut < NT; ut++) sf[m][ut] = row_frag<LD::L>(ss, 16 * ut, m, lb);
         }
+        issue_fence();
+#pragma unroll
+        for (int ut = 0; ut < NT; ut++)
+#pragma unroll
+          for (int pw = 0; pw < PW; pw++) a[ut][pw] *= st[ut];
+#pragma unroll
+        for (int m = 0; m < NJ; m++)
+#pragma unroll
+          for (int ut = 0; ut < NT; ut++)
+#pragma unroll
+            for (int pw = 0; pw < PW; pw++) a[ut][pw] = mma32(xf[m][pw], sf[m][ut], a[ut][pw]);
       }
       const RowOut<T, VEC> yo(y + (row0 + u0) * xst + (size_t)hi * g.p + p0, xst, nrows, pn);
 #pragma unroll
@@ -671,7 +740,7 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
 #pragma unroll
         for (int pw = 0; pw < PW; pw++) yo.put(16 * ut + ln, 16 * (wave * PW + pw) + 4 * lq, a[ut][pw]);
     }
-    state_update<T, RT, PW>(H, ks, xs, MODE == 2 ? tab->start : tab->end, ex2((float)total), wave, lane);
+    state_update<T, RT, PW>(H, ks, xs, MODE == 2 ? tab->start : tab->end, ex2((float)total), wave, fresh(lane));
   }
 
   if constexpr (MODE == 0) {

@@ -29,11 +29,8 @@ constexpr int ABW = 8;
 template <typename T, int RT, int PT>   // PT tiles of 16 state rows p
 struct LdsB {
   static constexpr int L = AV<T>::L;
-  // 128 rows of p in bf16: pitches of 8 (mod 64) elements, so that everything fits 160 KB
-  // (the transposing reads are then two-way bank conflicted)
-  static constexpr bool TIGHT = PT == 8 && RT == 8;
-  static constexpr int RP = TIGHT ? 16 * RT + 8 : AV<T>::pitch(16 * RT), PP = TIGHT ? 16 * PT + 8 : AV<T>::pitch(16 * PT),
-                       SP = TIGHT ? L + 8 : AV<T>::pitch(L);
+  static constexpr int RC = 16 * RT, PC = 16 * PT;
+  static constexpr int RP = AV<T>::pitch(RC), PP = AV<T>::pitch(PC), SP = AV<T>::pitch(L);
   static constexpr size_t E = sizeof(T);
   static constexpr size_t tab = 0;
   static constexpr size_t sums = sizeof(DecayTab);   // rsum, csum, up, vp [4][64], th[8]
@@ -61,13 +58,13 @@ struct StageH {
       }
     }
   }
-  __device__ __forceinline__ void store(T* t, int P) const {
+  __device__ __forceinline__ void store(T* t) const {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int e = i * ABT + (int)threadIdx.x, lane = e & 63, tp = e >> 6, m = tp % (RT / 2), pt = tp / (RT / 2);
       if (PAIRS % ABT == 0 || e < PAIRS) {
-        st_quad(t, P, 16 * pt + (lane & 15), 8 * m + (lane >> 4), v[i][0]);
-        st_quad(t, P, 16 * pt + (lane & 15), 8 * m + 4 + (lane >> 4), v[i][1]);
+        st_quad<16 * RT>(t, 16 * pt + (lane & 15), 8 * m + (lane >> 4), v[i][0]);
+        st_quad<16 * RT>(t, 16 * pt + (lane & 15), 8 * m + 4 + (lane >> 4), v[i][1]);
       }
     }
   }
@@ -169,19 +166,19 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     const size_t u0 = (size_t)t0 * g.c;
     // (the barrier that ended the last chunk covers these writes)
     if constexpr (VEC) {
-      sk.store(ks, LD::RP);
-      sq.store(qs, LD::RP);
-      sx.store(xs, LD::PP);
-      sy.store(ys, LD::PP);
+      sk.store(ks);
+      sq.store(qs);
+      sx.store(xs);
+      sy.store(ys);
     } else {
-      sk.direct(ks, LD::RP, kb + u0 * kst, kst, nrows, g.r);
-      sq.direct(qs, LD::RP, qb + u0 * kst, kst, nrows, g.r);
-      sx.direct(xs, LD::PP, xb + u0 * xst, xst, nrows, pn);
-      sy.direct(ys, LD::PP, yb + u0 * xst, xst, nrows, pn);
+      sk.direct(ks, kb + u0 * kst, kst, nrows, g.r);
+      sq.direct(qs, qb + u0 * kst, kst, nrows, g.r);
+      sx.direct(xs, xb + u0 * xst, xst, nrows, pn);
+      sy.direct(ys, yb + u0 * xst, xst, nrows, pn);
     }
-    sh.store(hs, LD::RP);
+    sh.store(hs);
 #pragma unroll
-    for (int i = 0; i < RW; i++) st_quad(gs, LD::RP, 16 * mp + ln, 4 * (mr + i) + lq, to_quad<T>(G[i]));
+    for (int i = 0; i < RW; i++) st_quad<LD::RC>(gs, 16 * mp + ln, 4 * (mr + i) + lq, to_quad<T>(G[i]));
     if (wave == 0) decay_table(tab, log2_decay(to_f(dnext)), lane);
     __syncthreads();
     if (n > n0) fetch(n - 1);
@@ -192,7 +189,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
       float v = 0.0f;
 #pragma unroll
       for (int i = 0; i < RW; i++) {
-        const f4 h = quad_f(ld_quad(hs, LD::RP, 16 * mp + ln, 4 * (mr + i) + lq));
+        const f4 h = quad_f(ld_quad<LD::RC>(hs, 16 * mp + ln, 4 * (mr + i) + lq));
 #pragma unroll
         for (int e = 0; e < 4; e++) v += G[i][e] * h[e];
       }
@@ -200,6 +197,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
       if (lane == 0) th[wave] = v;
     }
     // s, t (stored [u][j]) and the sums of (q.k) t over pairs of different tokens
+    const int la = fresh<PT == 8>(lane);
 #pragma unroll
     for (int it = 0; it < (NT * NT + ABW - 1) / ABW; it++) {
       const int id = it * ABW + wave, ut = id % NT, jt = id / NT;
@@ -210,10 +208,10 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
       if (jt <= ut || (g.c == 3 && jt == ut + 1)) {
 #pragma unroll
         for (int m = 0; m < RT / 2; m++)
-          a = mma32(row_frag(ks, LD::RP, 16 * jt, m, lane), row_frag(qs, LD::RP, 16 * ut, m, lane), a);
+          a = mma32(row_frag<LD::RC>(ks, 16 * jt, m, la), row_frag<LD::RC>(qs, 16 * ut, m, la), a);
 #pragma unroll
         for (int m = 0; m < PT / 2; m++)
-          b = mma32(row_frag(xs, LD::PP, 16 * jt, m, lane), row_frag(ys, LD::PP, 16 * ut, m, lane), b);
+          b = mma32(row_frag<LD::PC>(xs, 16 * jt, m, la), row_frag<LD::PC>(ys, 16 * ut, m, la), b);
         const int u = 16 * ut + ln, tu = (u * g.cinv) >> 16;
         const float uh = tab->hi[u], ul = tab->lo[u];
         const f4 jh = *reinterpret_cast<const f4*>(tab->hi + 16 * jt + 4 * lq);
@@ -229,8 +227,8 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
           rs += cs[e];
         }
       }
-      st_quad(ss, LD::SP, 16 * ut + ln, 4 * jt + lq, to_quad<T>(a));
-      st_quad(ts, LD::SP, 16 * ut + ln, 4 * jt + lq, to_quad<T>(b));
+      st_quad<LD::L>(ss, 16 * ut + ln, 4 * jt + lq, to_quad<T>(a));
+      st_quad<LD::L>(ts, 16 * ut + ln, 4 * jt + lq, to_quad<T>(b));
       rs = col4_sum(rs);
       if (lq == 0) rsum[jt * 64 + 16 * ut + ln] = rs;
 #pragma unroll
@@ -254,13 +252,14 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
       static_assert(WR * WU == ABW && UB * WU == NT && WR <= 4, "tiles and waves");
       const int wr = wave % WR, rt0 = wr * RB, ut0 = wave / WR * UB;
       {
+        const int lb = fresh<PT == 8>(lane);
         typename V::frag hf[RB][PT / 2], kf[RB][NJ];
 #pragma unroll
         for (int i = 0; i < RB; i++) {
 #pragma unroll
-          for (int m = 0; m < PT / 2; m++) hf[i][m] = col_frag(hs, LD::RP, m, 16 * (rt0 + i), lane);
+          for (int m = 0; m < PT / 2; m++) hf[i][m] = col_frag<LD::RC>(hs, m, 16 * (rt0 + i), lb);
 #pragma unroll
-          for (int m = 0; m < NJ; m++) kf[i][m] = col_frag(ks, LD::RP, m, 16 * (rt0 + i), lane);
+          for (int m = 0; m < NJ; m++) kf[i][m] = col_frag<LD::RC>(ks, m, 16 * (rt0 + i), lb);
         }
 #pragma unroll
         for (int j = 0; j < UB; j++) {
@@ -270,7 +269,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
           for (int i = 0; i < RB; i++) a[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int m = 0; m < PT / 2; m++) {
-            const auto yf = row_frag(ys, LD::PP, 16 * ut, m, lane);
+            const auto yf = row_frag<LD::PC>(ys, 16 * ut, m, lb);
 #pragma unroll
             for (int i = 0; i < RB; i++) a[i] = mma32(hf[i][m], yf, a[i]);
           }
@@ -279,7 +278,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
           for (int i = 0; i < RB; i++) {
             a[i] *= st;
-            const f4 qv = quad_f(ld_quad(qs, LD::RP, u, 4 * (rt0 + i) + lq));
+            const f4 qv = quad_f(ld_quad<LD::RC>(qs, u, 4 * (rt0 + i) + lq));
             us += a[i][0] * qv[0] + a[i][1] * qv[1] + a[i][2] * qv[2] + a[i][3] * qv[3];
           }
           us = col4_sum(us);
@@ -287,7 +286,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
           for (int m = 0; m < NJ; m++)
             if (32 * m < 16 * (ut + 1) || g.c == 3) {
-              const auto tf = row_frag(ts, LD::SP, 16 * ut, m, lane);
+              const auto tf = row_frag<LD::L>(ts, 16 * ut, m, lb);
 #pragma unroll
               for (int i = 0; i < RB; i++) a[i] = mma32(kf[i][m], tf, a[i]);
             }
@@ -297,13 +296,14 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
       }
       __builtin_amdgcn_sched_barrier(0);
       {
+        const int lc = fresh<PT == 8>(lane);
         typename V::frag gf[RB][PT / 2], qf[RB][NJ];
 #pragma unroll
         for (int i = 0; i < RB; i++) {
 #pragma unroll
-          for (int m = 0; m < PT / 2; m++) gf[i][m] = col_frag(gs, LD::RP, m, 16 * (rt0 + i), lane);
+          for (int m = 0; m < PT / 2; m++) gf[i][m] = col_frag<LD::RC>(gs, m, 16 * (rt0 + i), lc);
 #pragma unroll
-          for (int m = 0; m < NJ; m++) qf[i][m] = col_frag(qs, LD::RP, m, 16 * (rt0 + i), lane);
+          for (int m = 0; m < NJ; m++) qf[i][m] = col_frag<LD::RC>(qs, m, 16 * (rt0 + i), lc);
         }
 #pragma unroll
         for (int j = 0; j < UB; j++) {
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
           for (int i = 0; i < RB; i++) b[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int m = 0; m < PT / 2; m++) {
-            const auto xf = row_frag(xs, LD::PP, 16 * ut, m, lane);
+            const auto xf = row_frag<LD::PC>(xs, 16 * ut, m, lc);
 #pragma unroll
             for (int i = 0; i < RB; i++) b[i] = mma32(gf[i][m], xf, b[i]);
           }
@@ -322,7 +322,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
           for (int i = 0; i < RB; i++) {
             b[i] *= en;
-            const f4 kv = quad_f(ld_quad(ks, LD::RP, u, 4 * (rt0 + i) + lq));
+            const f4 kv = quad_f(ld_quad<LD::RC>(ks, u, 4 * (rt0 + i) + lq));
             vs += b[i][0] * kv[0] + b[i][1] * kv[1] + b[i][2] * kv[2] + b[i][3] * kv[3];
           }
           vs = col4_sum(vs);
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
           for (int m = 0; m < NJ; m++)
             if (32 * (m + 1) > 16 * ut || g.c == 3) {
-              const auto tf = col_frag(ts, LD::SP, m, 16 * ut, lane);
+              const auto tf = col_frag<LD::L>(ts, m, 16 * ut, lc);
 #pragma unroll
               for (int i = 0; i < RB; i++) b[i] = mma32(qf[i][m], tf, b[i]);
             }
@@ -344,6 +344,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     {
       constexpr int PB = PT * NT >= 16 ? 2 : 1, WP = PT / PB, WU = ABW / WP, UB = NT / WU > 0 ? NT / WU : 1;
       static_assert(WP * WU == ABW && UB * WU == NT, "tiles and waves");
+      const int ld = fresh<PT == 8>(lane);
       const int pj0 = wave % WP * PB, ut0 = wave / WP * UB;
 #pragma unroll
       for (int j = 0; j < UB; j++) {
@@ -353,9 +354,9 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
         for (int i = 0; i < PB; i++) a[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int m = 0; m < RT / 2; m++) {
-          const auto kf = row_frag(ks, LD::RP, 16 * ut, m, lane);
+          const auto kf = row_frag<LD::RC>(ks, 16 * ut, m, ld);
 #pragma unroll
-          for (int i = 0; i < PB; i++) a[i] = mma32(row_frag(gs, LD::RP, 16 * (pj0 + i), m, lane), kf, a[i]);
+          for (int i = 0; i < PB; i++) a[i] = mma32(row_frag<LD::RC>(gs, 16 * (pj0 + i), m, ld), kf, a[i]);
         }
         const float en = tab->end[u];
 #pragma unroll
@@ -363,9 +364,9 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
         for (int m = 0; m < NJ; m++)
           if (32 * (m + 1) > 16 * ut || g.c == 3) {
-            const auto sf = col_frag(ss, LD::SP, m, 16 * ut, lane);
+            const auto sf = col_frag<LD::L>(ss, m, 16 * ut, ld);
 #pragma unroll
-            for (int i = 0; i < PB; i++) a[i] = mma32(col_frag(ys, LD::PP, m, 16 * (pj0 + i), lane), sf, a[i]);
+            for (int i = 0; i < PB; i++) a[i] = mma32(col_frag<LD::PC>(ys, m, 16 * (pj0 + i), ld), sf, a[i]);
           }
 #pragma unroll
         for (int i = 0; i < PB; i++) ox.put(u, 16 * (pj0 + i) + 4 * lq, a[i]);
@@ -374,10 +375,11 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     // G'
     __builtin_amdgcn_sched_barrier(0);
     {
+      const int le = fresh<PT == 8>(lane);
       Scaled<V::NSPLIT> yf[NJ];
 #pragma unroll
       for (int m = 0; m < NJ; m++)
-        yf[m].make(col_frag(ys, LD::PP, m, 16 * mp, lane),
+        yf[m].make(col_frag<LD::PC>(ys, m, 16 * mp, le),
                    *reinterpret_cast<const f4*>(tab->start + 32 * m + 4 * lq),
                    *reinterpret_cast<const f4*>(tab->start + 32 * m + 16 + 4 * lq));
 #pragma unroll
@@ -385,7 +387,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
         G[i] *= dec;
 #pragma unroll
         for (int m = 0; m < NJ; m++) {
-          const auto qf = col_frag(qs, LD::RP, m, 16 * (mr + i), lane);
+          const auto qf = col_frag<LD::RC>(qs, m, 16 * (mr + i), le);
 #pragma unroll
           for (int k2 = 0; k2 < V::NSPLIT; k2++) G[i] = mma32(qf, yf[m].piece(k2), G[i]);
         }
