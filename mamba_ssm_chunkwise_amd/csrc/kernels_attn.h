@@ -469,17 +469,18 @@ __device__ __forceinline__ void state_update(f4 (&H)[PW][RT], const T* ks, const
 // diagonal too. The others stay zero.
 template <int NT> struct ScoreTiles;
 template <> struct ScoreTiles<4> {
-  static constexpr int SB = 3;   // tiles that a wave of four has in work together
-  unsigned long long list;
-  int n;
+  static constexpr int SB = 3;       // tiles that a wave of four has in work together
+  unsigned long long list, lower;    // tile k of wave w of four: entry 4k + w; the last wave (decay tables) has least
+  int n, pairs;                      // entries of `list`; of `lower`, each tile once
   __device__ __forceinline__ ScoreTiles(int c)
-      : list(c == 3 ? 0xB61FEDCA98540ull : 0xFEDCA98540ull), n(c == 3 ? 13 : 10) {}
+      : list(c == 3 ? 0xB61FEDCA98540ull : 0x5AE049D0F8Cull), lower(0xB61FEDCA98540ull), n(c == 3 ? 13 : 12),
+        pairs(c == 3 ? 13 : 10) {}
 };
 template <> struct ScoreTiles<2> {
   static constexpr int SB = 1;
-  unsigned long long list;
-  int n;
-  __device__ __forceinline__ ScoreTiles(int c) : list(0x1540ull), n(c == 3 ? 4 : 3) {}
+  unsigned long long list, lower;
+  int n, pairs;
+  __device__ __forceinline__ ScoreTiles(int c) : list(0x1540ull), lower(0x1540ull), n(c == 3 ? 4 : 3), pairs(n) {}
 };
 
 // ---- walks --------------------------------------------------------------------

@@ -159,6 +159,13 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     dnext = (T)0.0f;
     if (wave == 0 && lane < nrows && ltok * g.c == lane) dnext = dab[(size_t)(t0 + ltok) * g.h];
   };
+  // tiles of the scores without pairs j <= u are never written: zeros throughout
+  for (int e = threadIdx.x; e < L * LD::SP / 4; e += ABT) {
+    reinterpret_cast<typename V::quad*>(ss)[e] = typename V::quad{};
+    reinterpret_cast<typename V::quad*>(ts)[e] = typename V::quad{};
+  }
+  rsum[threadIdx.x] = 0.0f;   // and csum behind it
+  const ScoreTiles<NT> tl(g.c);
   if (nlive > n0) fetch(nlive - 1);
   if constexpr (VEC) dropped_stores<T, (2 * RT + PT) * NT / ABW>();
   for (int n = nlive - 1; n >= n0; n--) {
@@ -198,42 +205,50 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     }
     // s, t (stored [u][j]) and the sums of (q.k) t over pairs of different tokens
     const int la = fresh<PT == 8>(lane);
-#pragma unroll
-    for (int it = 0; it < (NT * NT + ABW - 1) / ABW; it++) {
-      const int id = it * ABW + wave, ut = id % NT, jt = id / NT;
-      if (NT * NT % ABW != 0 && id >= NT * NT) break;
+#pragma unroll 1
+    for (int at = wave; at < tl.pairs; at += ABW) {
+      const int code = (int)(tl.lower >> (4 * at)) & 15, ut = 16 * (code >> 2), jt = 16 * (code & 3);
       f4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
-      float rs = 0.0f;
-      f4 cs = a;
-      if (jt <= ut || (g.c == 3 && jt == ut + 1)) {
+      typename V::frag kf[RT / 2], qf[RT / 2], xf[PT / 2], yf[PT / 2];
 #pragma unroll
-        for (int m = 0; m < RT / 2; m++)
-          a = mma32(row_frag<LD::RC>(ks, 16 * jt, m, la), row_frag<LD::RC>(qs, 16 * ut, m, la), a);
-#pragma unroll
-        for (int m = 0; m < PT / 2; m++)
-          b = mma32(row_frag<LD::PC>(xs, 16 * jt, m, la), row_frag<LD::PC>(ys, 16 * ut, m, la), b);
-        const int u = 16 * ut + ln, tu = (u * g.cinv) >> 16;
-        const float uh = tab->hi[u], ul = tab->lo[u];
-        const f4 jh = *reinterpret_cast<const f4*>(tab->hi + 16 * jt + 4 * lq);
-        const f4 jl = *reinterpret_cast<const f4*>(tab->lo + 16 * jt + 4 * lq);
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const int tj = ((16 * jt + 4 * lq + e) * g.cinv) >> 16;
-          const float w = tj <= tu ? ex2((uh - jh[e]) + (ul - jl[e])) : 0.0f;
-          const float qk = a[e];
-          a[e] = tj <= tu ? qk * w : 0.0f;
-          b[e] = tj <= tu ? b[e] * w : 0.0f;
-          cs[e] = tj < tu ? qk * b[e] : 0.0f;
-          rs += cs[e];
-        }
+      for (int m = 0; m < RT / 2; m++) {
+        kf[m] = row_frag<LD::RC>(ks, jt, m, la);
+        qf[m] = row_frag<LD::RC>(qs, ut, m, la);
       }
-      st_quad<LD::L>(ss, 16 * ut + ln, 4 * jt + lq, to_quad<T>(a));
-      st_quad<LD::L>(ts, 16 * ut + ln, 4 * jt + lq, to_quad<T>(b));
+#pragma unroll
+      for (int m = 0; m < PT / 2; m++) {
+        xf[m] = row_frag<LD::PC>(xs, jt, m, la);
+        yf[m] = row_frag<LD::PC>(ys, ut, m, la);
+      }
+      const int u = ut + ln, tok = (u * g.cinv) >> 16;
+      const float uh = tab->hi[u], ul = tab->lo[u];
+      const f4 jh = *reinterpret_cast<const f4*>(tab->hi + jt + 4 * lq);
+      const f4 jl = *reinterpret_cast<const f4*>(tab->lo + jt + 4 * lq);
+      issue_fence();
+#pragma unroll
+      for (int m = 0; m < (RT > PT ? RT : PT) / 2; m++) {
+        if (m < RT / 2) a = mma32(kf[m], qf[m], a);
+        if (m < PT / 2) b = mma32(xf[m], yf[m], b);
+      }
+      // j <= u: up to the last row of u's token; another token: below its first row
+      const int first = tok * g.c - jt - 4 * lq, last = first + g.c - 1;
+      float rs = 0.0f;
+      f4 cs;
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const float w = ex2((uh - jh[e]) + (ul - jl[e])), qk = a[e];
+        a[e] = keep_if(e <= last, qk * w);
+        b[e] = keep_if(e <= last, b[e] * w);
+        cs[e] = keep_if(e < first, qk * b[e]);
+        rs += cs[e];
+      }
+      st_quad<LD::L>(ss, u, jt / 4 + lq, to_quad<T>(a));
+      st_quad<LD::L>(ts, u, jt / 4 + lq, to_quad<T>(b));
       rs = col4_sum(rs);
-      if (lq == 0) rsum[jt * 64 + 16 * ut + ln] = rs;
+      if (lq == 0) rsum[4 * jt + u] = rs;
 #pragma unroll
       for (int e = 0; e < 4; e++) cs[e] = row16_sum(cs[e]);
-      if (ln == 0) *reinterpret_cast<f4*>(csum + ut * 64 + 16 * jt + 4 * lq) = cs;
+      if (ln == 0) *reinterpret_cast<f4*>(csum + 4 * ut + jt + 4 * lq) = cs;
     }
     __syncthreads();
 
@@ -251,92 +266,82 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
       constexpr int RB = RT * NT >= 16 ? 2 : 1, WR = RT / RB, WU = ABW / WR, UB = NT / WU;
       static_assert(WR * WU == ABW && UB * WU == NT && WR <= 4, "tiles and waves");
       const int wr = wave % WR, rt0 = wr * RB, ut0 = wave / WR * UB;
-      {
-        const int lb = fresh<PT == 8>(lane);
-        typename V::frag hf[RB][PT / 2], kf[RB][NJ];
+      // row tiles whose operands are in flight together: as registers allow
+      constexpr int JB = PT == 4 ? UB : 1;
+      // `in`, the operands contracted over p (with the state or its cotangent) and over the
+      // rows of the chunk; out: their rows' tiles, and the sums of what the first gives
+      auto rows_grad = [&](const T* st, const T* cs, auto first, auto second, const float* w, const T* own, float* sums,
+                           const RowOut<TO, VEC>& out, int l) {
+        typename V::frag sf[RB][PT / 2], cf[RB][NJ];
 #pragma unroll
         for (int i = 0; i < RB; i++) {
 #pragma unroll
-          for (int m = 0; m < PT / 2; m++) hf[i][m] = col_frag<LD::RC>(hs, m, 16 * (rt0 + i), lb);
+          for (int m = 0; m < PT / 2; m++) sf[i][m] = col_frag<LD::RC>(st, m, 16 * (rt0 + i), l);
 #pragma unroll
-          for (int m = 0; m < NJ; m++) kf[i][m] = col_frag<LD::RC>(ks, m, 16 * (rt0 + i), lb);
+          for (int m = 0; m < NJ; m++) cf[i][m] = col_frag<LD::RC>(cs, m, 16 * (rt0 + i), l);
         }
 #pragma unroll
-        for (int j = 0; j < UB; j++) {
-          const int ut = ut0 + j, u = 16 * ut + ln;
-          f4 a[RB];
+        for (int j0 = 0; j0 < UB; j0 += JB) {
+          typename V::frag ff[JB][PT / 2], gf[JB][NJ];
+          typename V::quad ow[JB][RB];
+          float wu[JB];
 #pragma unroll
-          for (int i = 0; i < RB; i++) a[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int j = 0; j < JB; j++) {
+            const int ut = ut0 + j0 + j;
 #pragma unroll
-          for (int m = 0; m < PT / 2; m++) {
-            const auto yf = row_frag<LD::PC>(ys, 16 * ut, m, lb);
+            for (int m = 0; m < PT / 2; m++) ff[j][m] = first(ut, m);
 #pragma unroll
-            for (int i = 0; i < RB; i++) a[i] = mma32(hf[i][m], yf, a[i]);
+            for (int m = 0; m < NJ; m++) gf[j][m] = second(ut, m);
+            wu[j] = w[16 * ut + ln];
+#pragma unroll
+            for (int i = 0; i < RB; i++) ow[j][i] = ld_quad<LD::RC>(own + 16 * ut * LD::RP, l & 15, 4 * (rt0 + i) + lq);
           }
-          const float st = tab->start[u];
-          float us = 0.0f;
+          issue_fence();
+          f4 a[JB][RB];
 #pragma unroll
-          for (int i = 0; i < RB; i++) {
-            a[i] *= st;
-            const f4 qv = quad_f(ld_quad<LD::RC>(qs, u, 4 * (rt0 + i) + lq));
-            us += a[i][0] * qv[0] + a[i][1] * qv[1] + a[i][2] * qv[2] + a[i][3] * qv[3];
+          for (int j = 0; j < JB; j++)
+#pragma unroll
+            for (int i = 0; i < RB; i++) a[j][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int m = 0; m < PT / 2; m++)
+#pragma unroll
+            for (int j = 0; j < JB; j++)
+#pragma unroll
+              for (int i = 0; i < RB; i++) a[j][i] = mma32(sf[i][m], ff[j][m], a[j][i]);
+#pragma unroll
+          for (int j = 0; j < JB; j++) {
+            float us = 0.0f;
+#pragma unroll
+            for (int i = 0; i < RB; i++) {
+              a[j][i] *= wu[j];
+              const f4 v = quad_f(ow[j][i]);
+              us += a[j][i][0] * v[0] + a[j][i][1] * v[1] + a[j][i][2] * v[2] + a[j][i][3] * v[3];
+            }
+            us = col4_sum(us);
+            if (lq == 0) sums[wr * 64 + 16 * (ut0 + j0 + j) + ln] = us;
           }
-          us = col4_sum(us);
-          if (lq == 0) up[wr * 64 + u] = us;
 #pragma unroll
           for (int m = 0; m < NJ; m++)
-            if (32 * m < 16 * (ut + 1) || g.c == 3) {
-              const auto tf = row_frag<LD::L>(ts, 16 * ut, m, lb);
 #pragma unroll
-              for (int i = 0; i < RB; i++) a[i] = mma32(kf[i][m], tf, a[i]);
-            }
+            for (int j = 0; j < JB; j++)
 #pragma unroll
-          for (int i = 0; i < RB; i++) oq.put(u, 16 * (rt0 + i) + 4 * lq, a[i]);
+              for (int i = 0; i < RB; i++) a[j][i] = mma32(cf[i][m], gf[j][m], a[j][i]);
+#pragma unroll
+          for (int j = 0; j < JB; j++)
+#pragma unroll
+            for (int i = 0; i < RB; i++) out.put(16 * (ut0 + j0 + j) + ln, 16 * (rt0 + i) + 4 * lq, a[j][i]);
         }
+      };
+      {
+        const int lb = fresh<PT == 8>(lane);
+        rows_grad(hs, ks, [&](int ut, int m) { return row_frag<LD::PC>(ys, 16 * ut, m, lb); },
+                  [&](int ut, int m) { return row_frag<LD::L>(ts, 16 * ut, m, lb); }, tab->start, qs, up, oq, lb);
       }
       __builtin_amdgcn_sched_barrier(0);
       {
         const int lc = fresh<PT == 8>(lane);
-        typename V::frag gf[RB][PT / 2], qf[RB][NJ];
-#pragma unroll
-        for (int i = 0; i < RB; i++) {
-#pragma unroll
-          for (int m = 0; m < PT / 2; m++) gf[i][m] = col_frag<LD::RC>(gs, m, 16 * (rt0 + i), lc);
-#pragma unroll
-          for (int m = 0; m < NJ; m++) qf[i][m] = col_frag<LD::RC>(qs, m, 16 * (rt0 + i), lc);
-        }
-#pragma unroll
-        for (int j = 0; j < UB; j++) {
-          const int ut = ut0 + j, u = 16 * ut + ln;
-          f4 b[RB];
-#pragma unroll
-          for (int i = 0; i < RB; i++) b[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int m = 0; m < PT / 2; m++) {
-            const auto xf = row_frag<LD::PC>(xs, 16 * ut, m, lc);
-#pragma unroll
-            for (int i = 0; i < RB; i++) b[i] = mma32(gf[i][m], xf, b[i]);
-          }
-          const float en = tab->end[u];
-          float vs = 0.0f;
-#pragma unroll
-          for (int i = 0; i < RB; i++) {
-            b[i] *= en;
-            const f4 kv = quad_f(ld_quad<LD::RC>(ks, u, 4 * (rt0 + i) + lq));
-            vs += b[i][0] * kv[0] + b[i][1] * kv[1] + b[i][2] * kv[2] + b[i][3] * kv[3];
-          }
-          vs = col4_sum(vs);
-          if (lq == 0) vp[wr * 64 + u] = vs;
-#pragma unroll
-          for (int m = 0; m < NJ; m++)
-            if (32 * (m + 1) > 16 * ut || g.c == 3) {
-              const auto tf = col_frag<LD::L>(ts, m, 16 * ut, lc);
-#pragma unroll
-              for (int i = 0; i < RB; i++) b[i] = mma32(qf[i][m], tf, b[i]);
-            }
-#pragma unroll
-          for (int i = 0; i < RB; i++) ok.put(u, 16 * (rt0 + i) + 4 * lq, b[i]);
-        }
+        rows_grad(gs, qs, [&](int ut, int m) { return row_frag<LD::PC>(xs, 16 * ut, m, lc); },
+                  [&](int ut, int m) { return col_frag<LD::L>(ts, m, 16 * ut, lc); }, tab->end, ks, vp, ok, lc);
       }
     }
     // d_x, likewise over PB tiles of rows p
@@ -349,25 +354,34 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
       for (int j = 0; j < UB; j++) {
         const int ut = ut0 + j, u = 16 * ut + ln;
+        typename V::frag kf[RT / 2], gf[PB][RT / 2], sf[NJ], yf[PB][NJ];
+#pragma unroll
+        for (int m = 0; m < RT / 2; m++) {
+          kf[m] = row_frag<LD::RC>(ks, 16 * ut, m, ld);
+#pragma unroll
+          for (int i = 0; i < PB; i++) gf[i][m] = row_frag<LD::RC>(gs, 16 * (pj0 + i), m, ld);
+        }
+#pragma unroll
+        for (int m = 0; m < NJ; m++) {
+          sf[m] = col_frag<LD::L>(ss, m, 16 * ut, ld);
+#pragma unroll
+          for (int i = 0; i < PB; i++) yf[i][m] = col_frag<LD::PC>(ys, m, 16 * (pj0 + i), ld);
+        }
+        const float en = tab->end[u];
+        issue_fence();
         f4 a[PB];
 #pragma unroll
         for (int i = 0; i < PB; i++) a[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int m = 0; m < RT / 2; m++) {
-          const auto kf = row_frag<LD::RC>(ks, 16 * ut, m, ld);
+        for (int m = 0; m < RT / 2; m++)
 #pragma unroll
-          for (int i = 0; i < PB; i++) a[i] = mma32(row_frag<LD::RC>(gs, 16 * (pj0 + i), m, ld), kf, a[i]);
-        }
-        const float en = tab->end[u];
+          for (int i = 0; i < PB; i++) a[i] = mma32(gf[i][m], kf[m], a[i]);
 #pragma unroll
         for (int i = 0; i < PB; i++) a[i] *= en;
 #pragma unroll
         for (int m = 0; m < NJ; m++)
-          if (32 * (m + 1) > 16 * ut || g.c == 3) {
-            const auto sf = col_frag<LD::L>(ss, m, 16 * ut, ld);
 #pragma unroll
-            for (int i = 0; i < PB; i++) a[i] = mma32(col_frag<LD::PC>(ys, m, 16 * (pj0 + i), ld), sf, a[i]);
-          }
+          for (int i = 0; i < PB; i++) a[i] = mma32(yf[i][m], sf[m], a[i]);
 #pragma unroll
         for (int i = 0; i < PB; i++) ox.put(u, 16 * (pj0 + i) + 4 * lq, a[i]);
       }
@@ -376,22 +390,28 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     __builtin_amdgcn_sched_barrier(0);
     {
       const int le = fresh<PT == 8>(lane);
+      typename V::frag qf[NJ][RW], yr[NJ];
+      f4 w0[NJ], w1[NJ];
+#pragma unroll
+      for (int m = 0; m < NJ; m++) {
+        yr[m] = col_frag<LD::PC>(ys, m, 16 * mp, le);
+        w0[m] = *reinterpret_cast<const f4*>(tab->start + 32 * m + 4 * lq);
+        w1[m] = *reinterpret_cast<const f4*>(tab->start + 32 * m + 16 + 4 * lq);
+#pragma unroll
+        for (int i = 0; i < RW; i++) qf[m][i] = col_frag<LD::RC>(qs, m, 16 * (mr + i), le);
+      }
+      issue_fence();
       Scaled<V::NSPLIT> yf[NJ];
 #pragma unroll
+      for (int m = 0; m < NJ; m++) yf[m].make(yr[m], w0[m], w1[m]);
+#pragma unroll
+      for (int i = 0; i < RW; i++) G[i] *= dec;
+#pragma unroll
       for (int m = 0; m < NJ; m++)
-        yf[m].make(col_frag<LD::PC>(ys, m, 16 * mp, le),
-                   *reinterpret_cast<const f4*>(tab->start + 32 * m + 4 * lq),
-                   *reinterpret_cast<const f4*>(tab->start + 32 * m + 16 + 4 * lq));
 #pragma unroll
-      for (int i = 0; i < RW; i++) {
-        G[i] *= dec;
+        for (int k2 = 0; k2 < V::NSPLIT; k2++)
 #pragma unroll
-        for (int m = 0; m < NJ; m++) {
-          const auto qf = col_frag<LD::RC>(qs, m, 16 * (mr + i), le);
-#pragma unroll
-          for (int k2 = 0; k2 < V::NSPLIT; k2++) G[i] = mma32(qf, yf[m].piece(k2), G[i]);
-        }
-      }
+          for (int i = 0; i < RW; i++) G[i] = mma32(qf[m][i], yf[m].piece(k2), G[i]);
     }
     __syncthreads();   // every tile has been read; the sums are complete
     if (wave == 0) {
