@@ -181,15 +181,6 @@ int attn_fwd(const moments_attn_desc* desc, const void* x, const void* k, const 
   return 0;
 }
 
-template <typename T>
-int launch_sum(const float* part, size_t total, int n, int w, T* out, hipStream_t st) {
-  if (total == 0) return 0;
-  ProfScope ps(KID_ATTN_SUM, st);
-  const unsigned blocks = (unsigned)std::min<size_t>((total + 255) / 256, 16384);
-  hipLaunchKernelGGL((k_attn_sum<T>), dim3(blocks), dim3(256), 0, st, part, total, n, w, out);
-  return check_launch();
-}
-
 int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const void* q, const void* da,
              const float* h0, const void* saved, size_t saved_bytes, bool use_saved, const void* d_y,
              const float* d_last, void* d_x, void* d_k, void* d_q, void* d_da, float* d_h0, void* workspace,
@@ -247,10 +238,15 @@ int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const 
     };
     if (!P.part) return go(IC<0>{});
     MOM_TRY(go(IC<1>{}));
-    const size_t rows = (size_t)g.b * g.s * g.c * g.g * g.r;
-    if (d_q != nullptr) MOM_TRY(launch_sum<T>(pq, rows, g.hpg * g.npt, g.r, (T*)d_q, st));
-    if (d_k != nullptr) MOM_TRY(launch_sum<T>(pk, rows, g.hpg * g.npt, g.r, (T*)d_k, st));
-    return d_da == nullptr ? 0 : launch_sum<T>(pa, (size_t)g.b * g.s * g.h, g.npt, 1, (T*)d_da, st);
+    const size_t keys = (size_t)g.b * g.s * g.c * g.g * g.r, toks = (size_t)g.b * g.s * g.h;
+    const SumJobs jobs = {{{pq, d_q, d_q != nullptr ? keys : 0, g.hpg * g.npt, g.r},
+                           {pk, d_k, d_k != nullptr ? keys : 0, g.hpg * g.npt, g.r},
+                           {pa, d_da, d_da != nullptr ? toks : 0, g.npt, 1}}};
+    const unsigned blocks = (unsigned)std::min<size_t>((std::max(keys, toks) + 255) / 256, 16384);
+    if (blocks == 0) return 0;
+    ProfScope ps(KID_ATTN_SUM, st);
+    hipLaunchKernelGGL((k_attn_sum<T>), dim3(blocks, 3), dim3(256), 0, st, jobs);
+    return check_launch();
   }));
   if (check_finite_on()) {
     const AttnGeo& g = P.g;

@@ -233,9 +233,10 @@ __device__ __forceinline__ void buf_store(Rsrc r, unsigned off, f4 v) {
 
 // A [L][COLS] block of rows on its way from global memory to an LDS tile, in 16-byte
 // pieces. Rows >= nrows and columns >= n are zeros, whatever the memory there holds.
-// Rows that are whole pieces go through registers (load, later store), so that they can
-// be in flight while another chunk is worked on; others are fetched one element at a
-// time, straight into the tile.
+// Pieces go through registers (load, later store), so that they can be in flight while
+// another chunk is worked on. VEC: rows are whole pieces. Others are fetched one element
+// at a time: as many registers for floats; bf16 elements, a register each until they are
+// packed, go straight into the tile (direct) instead.
 template <typename T, int COLS, int NT>
 struct Stage {
   static constexpr int L = AV<T>::L, PE = AV<T>::PE, PR = COLS / PE, N = (L * PR + NT - 1) / NT;
@@ -251,6 +252,18 @@ struct Stage {
 #pragma unroll
     for (int i = 0; i < N; i++) v[i] = buf_load(r, off0 + (unsigned)i * step);
   }
+  // One element at a time: floats of rows that are not whole pieces.
+  __device__ __forceinline__ void load_each(Rsrc r, int n) {
+    const int c0 = (int)threadIdx.x % PR * PE;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      unsigned x[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        x[e] = __builtin_amdgcn_raw_buffer_load_b32(r, c0 + e < n ? off0 + (unsigned)i * step + 4u * e : kPast, 0, 0);
+      v[i] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+  }
   __device__ __forceinline__ void store(T* t) const {
 #pragma unroll
     for (int i = 0; i < N; i++) {
@@ -258,15 +271,21 @@ struct Stage {
       st_piece<COLS>(t, e / PR, e % PR, v[i]);
     }
   }
-  __device__ __forceinline__ static void direct(T* t, const T* base, unsigned stride, int nrows, int n) {
-#pragma unroll 1
-    for (int e = (int)threadIdx.x; e < L * PR; e += NT) {
-      const int row = e / PR, c0 = e % PR * PE;
-      T x[PE];
+  __device__ __forceinline__ void direct(T* t, Rsrc r, int n) const {
+    static_assert(sizeof(T) == 2, "bf16 elements");
+    const int c0 = (int)threadIdx.x % PR * PE;
+    unsigned short x[N][PE];
 #pragma unroll
-      for (int i = 0; i < PE; i++)
-        x[i] = row < nrows && c0 + i < n ? base[(unsigned)row * stride + (unsigned)(c0 + i)] : (T)0.0f;
-      st_piece<COLS>(t, row, e % PR, __builtin_bit_cast(uint4, x));
+    for (int i = 0; i < N; i++)
+#pragma unroll
+      for (int e = 0; e < PE; e++)
+        x[i][e] = __builtin_amdgcn_raw_buffer_load_b16(r, c0 + e < n ? off0 + (unsigned)i * step + 2u * e : kPast, 0, 0);
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int e = i * NT + (int)threadIdx.x;
+      st_piece<COLS>(t, e / PR, e % PR,
+                     make_uint4(x[i][0] | (unsigned)x[i][1] << 16, x[i][2] | (unsigned)x[i][3] << 16,
+                                x[i][4] | (unsigned)x[i][5] << 16, x[i][6] | (unsigned)x[i][7] << 16));
     }
   }
 };
@@ -275,21 +294,22 @@ struct Stage {
 template <typename T, bool VEC>
 struct RowOut {
   Rsrc r;
-  T* base;
   unsigned stride;
-  int nrows, n;
-  __device__ __forceinline__ RowOut(T* b, unsigned st, int nr, int cols) : base(b), stride(st), nrows(nr), n(cols) {
-    if constexpr (VEC) r = row_rsrc(b, st, nr, cols);
-  }
+  int n;
+  __device__ __forceinline__ RowOut(T* b, unsigned st, int nr, int cols) : r(row_rsrc(b, st, nr, cols)), stride(st), n(cols) {}
   __device__ __forceinline__ void put(int u, int c0, f4 v) const {
+    const unsigned off = ((unsigned)u * stride + (unsigned)c0) * (unsigned)sizeof(T);
     if constexpr (VEC) {
-      const unsigned off = c0 < n ? ((unsigned)u * stride + (unsigned)c0) * (unsigned)sizeof(T) : kPast;
-      buf_store(r, off, to_quad<T>(v));
+      buf_store(r, c0 < n ? off : kPast, to_quad<T>(v));
     } else {
-      if (base == nullptr || u >= nrows) return;
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (c0 + i < n) base[(unsigned)u * stride + (unsigned)(c0 + i)] = to_t<T>(v[i]);
+      for (int i = 0; i < 4; i++) {
+        const unsigned o = c0 + i < n ? off + (unsigned)(i * sizeof(T)) : kPast;
+        if constexpr (sizeof(T) == 2)
+          __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, to_t<T>(v[i])), r, o, 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, o, 0, 0);
+      }
     }
   }
 };
@@ -568,6 +588,10 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
       sk.load(row_rsrc(kb + u0 * kst, kst, nrows, g.r));
       sx.load(row_rsrc(xb + u0 * xst, xst, nrows, pn));
       if constexpr (MODE == 0) sq.load(row_rsrc(qb + u0 * kst, kst, nrows, g.r));
+    } else if constexpr (sizeof(T) == 4) {
+      sk.load_each(row_rsrc(kb + u0 * kst, kst, nrows, g.r), g.r);
+      sx.load_each(row_rsrc(xb + u0 * xst, xst, nrows, pn), pn);
+      if constexpr (MODE == 0) sq.load_each(row_rsrc(qb + u0 * kst, kst, nrows, g.r), g.r);
     }
   };
   // the last wave makes each chunk's decay table while the chunk before is worked on
@@ -595,14 +619,14 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
     const size_t u0 = (size_t)t0 * g.c;
     const DecayTab* tab = tabs + ((i - n0) & 1);
     __syncthreads();   // the last chunk's tiles have been read
-    if constexpr (VEC) {
+    if constexpr (VEC || sizeof(T) == 4) {
       sk.store(ks);
       sx.store(xs);
       if constexpr (MODE == 0) sq.store(qs);
     } else {
-      sk.direct(ks, kb + u0 * kst, kst, nrows, g.r);
-      sx.direct(xs, xb + u0 * xst, xst, nrows, pn);
-      if constexpr (MODE == 0) sq.direct(qs, qb + u0 * kst, kst, nrows, g.r);
+      sk.direct(ks, row_rsrc(kb + u0 * kst, kst, nrows, g.r), g.r);
+      sx.direct(xs, row_rsrc(xb + u0 * xst, xst, nrows, pn), pn);
+      if constexpr (MODE == 0) sq.direct(qs, row_rsrc(qb + u0 * kst, kst, nrows, g.r), g.r);
     }
     __syncthreads();
     if constexpr (MODE != 2) {

@@ -154,6 +154,11 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
       sq.load(row_rsrc(qb + u0 * kst, kst, nrows, g.r));
       sx.load(row_rsrc(xb + u0 * xst, xst, nrows, pn));
       sy.load(row_rsrc(yb + u0 * xst, xst, nrows, pn));
+    } else if constexpr (sizeof(T) == 4) {
+      sk.load_each(row_rsrc(kb + u0 * kst, kst, nrows, g.r), g.r);
+      sq.load_each(row_rsrc(qb + u0 * kst, kst, nrows, g.r), g.r);
+      sx.load_each(row_rsrc(xb + u0 * xst, xst, nrows, pn), pn);
+      sy.load_each(row_rsrc(yb + u0 * xst, xst, nrows, pn), pn);
     }
     sh.load(save + (((size_t)chain * g.NK + n) * g.npt + pt) * TILES);
     dnext = (T)0.0f;
@@ -172,16 +177,16 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     const int t0 = n * g.CT, nrows = min(g.CT, Vb - t0) * g.c;
     const size_t u0 = (size_t)t0 * g.c;
     // (the barrier that ended the last chunk covers these writes)
-    if constexpr (VEC) {
+    if constexpr (VEC || sizeof(T) == 4) {
       sk.store(ks);
       sq.store(qs);
       sx.store(xs);
       sy.store(ys);
     } else {
-      sk.direct(ks, kb + u0 * kst, kst, nrows, g.r);
-      sq.direct(qs, qb + u0 * kst, kst, nrows, g.r);
-      sx.direct(xs, xb + u0 * xst, xst, nrows, pn);
-      sy.direct(ys, yb + u0 * xst, xst, nrows, pn);
+      sk.direct(ks, row_rsrc(kb + u0 * kst, kst, nrows, g.r), g.r);
+      sq.direct(qs, row_rsrc(qb + u0 * kst, kst, nrows, g.r), g.r);
+      sx.direct(xs, row_rsrc(xb + u0 * xst, xst, nrows, pn), pn);
+      sy.direct(ys, row_rsrc(yb + u0 * xst, xst, nrows, pn), pn);
     }
     sh.store(hs);
 #pragma unroll
@@ -468,15 +473,27 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
   }
 }
 
-// out[row][group][w] = sum of the group's `n` consecutive slices of part[row][groups * n][w].
+// Jobs of sums: out[row][group][w] = sum of the group's n consecutive slices of
+// part[row][groups * n][w], `total` values of out. One launch for all of them.
+struct SumJob {
+  const float* part;
+  void* out;
+  size_t total;
+  int n, w;
+};
+struct SumJobs {
+  SumJob job[3];
+};
 template <typename T>
-__global__ __launch_bounds__(256) void k_attn_sum(const float* __restrict__ part, size_t total, int n, int w,
-                                                  T* __restrict__ out) {
-  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (size_t)gridDim.x * 256) {
-    const size_t grp = e / w;
-    const float* src = part + grp * n * w + e % w;
+__global__ __launch_bounds__(256) void k_attn_sum(SumJobs jobs) {
+  const SumJob j = jobs.job[blockIdx.y];
+  T* out = reinterpret_cast<T*>(j.out);
+  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < j.total; e += (size_t)gridDim.x * 256) {
+    const size_t grp = e / j.w;
+    const float* src = j.part + grp * j.n * j.w + e % j.w;
     float s = 0.0f;
-    for (int i = 0; i < n; i++) s += src[(size_t)i * w];
+#pragma unroll 4
+    for (int i = 0; i < j.n; i++) s += src[(size_t)i * j.w];
     out[e] = to_t<T>(s);
   }
 }

@@ -208,8 +208,9 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
     if (pr != nullptr && g.s > 0) {
       const size_t total = (size_t)g.b * g.s * g.RW;
       ProfScope ps(KID_QK_SUM, st);
+      const SumJobs jobs = {{{pr, d_rot, total, g.g, g.RW}, {}, {}}};
       hipLaunchKernelGGL((k_attn_sum<T>), dim3((unsigned)std::min<size_t>((total + 255) / 256, 16384)), dim3(256), 0,
-                         st, pr, total, g.g, g.RW, (T*)d_rot);
+                         st, jobs);
       MOM_TRY(check_launch());
     }
     return 0;
