@@ -241,7 +241,7 @@ int moments_rot_bwd(const moments_desc* desc, const void* inc, const void* d_rot
  * may be 0 (nothing to do, but with s = 0 h_last is h0 and d_h0 is d_h_last). Rows of
  * r and p elements that are whole 16-byte pieces are read as such, others one element
  * at a time. Layout, alignment, ownership, errors and MOMENTS_CHECK_FINITE are those
- * stated above; the workspace is never optional. */
+ * stated above; moments_attn_fwd may need no workspace (its size is then 0). */
 typedef struct {
   int64_t b, s, c, h, g, p, r; /* batch, sequence, channels, heads, key groups, rows, state rank */
   int64_t valid_len;           /* positions >= valid_len are padding; >= s acts as s */

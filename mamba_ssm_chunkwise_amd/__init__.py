@@ -348,14 +348,16 @@ def _tensors_ok(dev, specs):
     """Checks (name, tensor, shape, dtype, optional) each as _expect does; returns the
     tensors' addresses (None for an absent optional one)."""
     out = []
+    at = -1 if dev.index is None else dev.index
     for name, t, shape, dtype, optional in specs:
         if t is None and optional:
             out.append(None)
-            continue
-        if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev
-                and t.is_contiguous()):
+        elif (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == at
+              and t.is_contiguous() and (at >= 0 or t.device == dev)):
+            out.append(t.data_ptr())
+        else:
             _expect(name, t, shape, dtype, dev)   # names what is wrong
-        out.append(t.data_ptr())
+            out.append(t.data_ptr())
     return out
 
 
@@ -366,9 +368,9 @@ def _gpu(dev):
 
 
 def _buffer(name, n, device, t):
-    """The caller's scratch tensor, checked, or a new one of n bytes."""
+    """The caller's scratch tensor, checked, or a new one of n bytes (None for none)."""
     if t is None:
-        return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+        return torch.empty(n, dtype=torch.uint8, device=device) if n else None
     if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on {device}")
     if t.numel() * t.element_size() < n:
@@ -376,8 +378,9 @@ def _buffer(name, n, device, t):
     return t
 
 
-def _bytes(t):
-    return t.numel() * t.element_size()
+def _scratch(t):
+    """(address, bytes) of a scratch tensor or None."""
+    return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
 
 
 def _size(n):
@@ -386,15 +389,18 @@ def _size(n):
     return int(n)
 
 
+def _shape5(name, t):
+    if not isinstance(t, torch.Tensor) or t.dim() != 5:
+        raise ValueError(f"{name} must be a torch.Tensor of five dimensions")
+    return t.shape
+
+
 def attn_desc(xhat, bhat, valid_len=None, valid_lens=None, dtype=None) -> AttnDesc:
     """Descriptor of linear attention for xhat [b,s,c,h,p] and keys bhat
     [b,s,c,g,r] of g groups of heads. ``valid_len`` defaults to s; ``valid_lens``
     as in make_desc."""
-    for name, t in (("xhat", xhat), ("bhat", bhat)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 5:
-            raise ValueError(f"{name} must be a torch.Tensor of five dimensions")
-    b, s, c, h, p = xhat.shape
-    g, r = bhat.shape[3:]
+    b, s, c, h, p = _shape5("xhat", xhat)
+    _, _, _, g, r = _shape5("bhat", bhat)
     if dtype is None:
         dtype = BF16 if xhat.dtype is torch.bfloat16 else F32
     d = AttnDesc(b, s, c, h, g, p, r, s if valid_len is None else int(valid_len), int(dtype))
@@ -436,7 +442,8 @@ def _attn_inputs(desc: AttnDesc, xhat, bhat, qhat, da, h0):
 def _attn_forward(desc, xhat, bhat, qhat, da, h0, y, h_last, saved, want_saved, workspace):
     dev, ins = _attn_inputs(desc, xhat, bhat, qhat, da, h0)
     state = (desc.b, desc.h, desc.p, desc.r)
-    _tensors_ok(dev, (("y", y, xhat.shape, xhat.dtype, True), ("h_last", h_last, state, torch.float32, True)))
+    if y is not None or h_last is not None:
+        _tensors_ok(dev, (("y", y, xhat.shape, xhat.dtype, True), ("h_last", h_last, state, torch.float32, True)))
     lib = _gpu(dev)
     ws = _buffer("workspace", moments_attn_workspace_size(desc, False), dev, workspace)
     if y is None:
@@ -444,11 +451,11 @@ def _attn_forward(desc, xhat, bhat, qhat, da, h0, y, h_last, saved, want_saved, 
     if h_last is None:
         h_last = torch.empty(state, dtype=torch.float32, device=dev)
     head = (ctypes.byref(desc), *ins, y.data_ptr(), h_last.data_ptr())
-    tail = (ws.data_ptr(), _bytes(ws), _stream_of(dev))
+    tail = (*_scratch(ws), _stream_of(dev))
     if want_saved:
         saved = _buffer("saved", moments_attn_saved_size(desc), dev, saved)
-        _lib.check(lib.moments_attn_fwd_save(*head, saved.data_ptr(), _bytes(saved), *tail))
-        return y, h_last, saved
+        _lib.check(lib.moments_attn_fwd_save(*head, *_scratch(saved), *tail))
+        return y, h_last, torch.empty(0, dtype=torch.uint8, device=dev) if saved is None else saved
     _lib.check(lib.moments_attn_fwd(*head, *tail))
     return y, h_last
 
@@ -491,12 +498,12 @@ def moments_attn_bwd(desc: AttnDesc, xhat, bhat, qhat, da, h0, d_y, d_h_last=Non
     out, grads = _gradients(dev, want, out, {"xhat": xhat, "bhat": bhat, "qhat": qhat, "da": da, "h0": h0})
     lib = _lib.load()
     ws = _buffer("workspace", moments_attn_workspace_size(desc, True), dev, workspace)
-    tail = (*cot, *grads, ws.data_ptr(), _bytes(ws), _stream_of(dev))
+    tail = (*cot, *grads, *_scratch(ws), _stream_of(dev))
     if _saved is None:
         _lib.check(lib.moments_attn_bwd(ctypes.byref(desc), *ins, *tail))
     else:
         sv = _buffer("saved", moments_attn_saved_size(desc), dev, _saved)
-        _lib.check(lib.moments_attn_bwd_saved(ctypes.byref(desc), *ins, sv.data_ptr(), _bytes(sv), *tail))
+        _lib.check(lib.moments_attn_bwd_saved(ctypes.byref(desc), *ins, *_scratch(sv), *tail))
     return out
 
 
@@ -551,9 +558,7 @@ def qk_desc(q, k, h, rot_kind, rot=None, eps=1e-5, rope_dim=None, quat_blocks=No
 
 def _token_stride(name, t):
     """Elements between tokens of t [b,s,c,g,r] (0 where any would do)."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 5:
-        raise ValueError(f"{name} must be a torch.Tensor of five dimensions")
-    b, s, c, g, r = t.shape
+    b, s, c, g, r = _shape5(name, t)
     if t.is_contiguous():
         return c * g * r if b * s > 1 else 0
     if t.numel() == 0:
@@ -573,11 +578,11 @@ def _qk_inputs(desc: QkDesc, q, k, wq, wk, bq, bk, rot):
         raise ValueError("q must be a torch.Tensor")
     dev, dt = q.device, _DTYPES.get(desc.dtype)
     b, s, c, h, g, r = desc.b, desc.s, desc.c, desc.h, desc.g, desc.r
-    row = c * g * r
+    row, raw = c * g * r, (b, s, c, g, r)
     for name, t, stride in (("q", q, desc.q_stride), ("k", k, desc.k_stride)):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a torch.Tensor")
-        if t.shape != (b, s, c, g, r) or t.dtype is not dt or t.device != dev:
+        if t.shape != raw or t.dtype is not dt or t.device != dev:
             raise ValueError(f"{name} must be {dt} of shape {(b, s, c, g, r)} on {dev}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
         if b * s > 1 and (_token_stride(name, t) or row) != (stride or row):
@@ -606,7 +611,8 @@ def moments_qk_fwd(desc: QkDesc, q, k, wq, wk, bq=None, bk=None, rot=None, qhat=
     frame of the cached states (khat is what the moments path takes as bhat)."""
     dev, dt, ins = _qk_inputs(desc, q, k, wq, wk, bq, bk, rot)
     shape = (desc.b, desc.s, desc.c, desc.h, desc.r)
-    _tensors_ok(dev, (("qhat", qhat, shape, dt, True), ("khat", khat, shape, dt, True)))
+    if qhat is not None or khat is not None:
+        _tensors_ok(dev, (("qhat", qhat, shape, dt, True), ("khat", khat, shape, dt, True)))
     lib = _gpu(dev)
     if qhat is None:
         qhat = torch.empty(shape, dtype=dt, device=dev)
@@ -625,8 +631,7 @@ def moments_qk_bwd(desc: QkDesc, q, k, wq, wk, bq, bk, rot, d_qhat, d_khat,
     cot = _tensors_ok(dev, (("d_qhat", d_qhat, shape, dt, False), ("d_khat", d_khat, shape, dt, False)))
     out, grads = _gradients(dev, want, out, {"q": q, "k": k, "wq": wq, "wk": wk, "bq": bq, "bk": bk, "rot": rot})
     ws = _buffer("workspace", moments_qk_workspace_size(desc), dev, workspace)
-    _lib.check(_lib.load().moments_qk_bwd(ctypes.byref(desc), *ins, *cot, *grads, ws.data_ptr(), _bytes(ws),
-                                          _stream_of(dev)))
+    _lib.check(_lib.load().moments_qk_bwd(ctypes.byref(desc), *ins, *cot, *grads, *_scratch(ws), _stream_of(dev)))
     return out
 
 

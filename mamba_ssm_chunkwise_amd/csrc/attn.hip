@@ -79,8 +79,9 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   if (g.nseg > 1) o = align256(o + (size_t)P->items * g.nseg * tiles * 4);
   P->seg_dec = o;
   if (g.nseg > 1) o = align256(o + (size_t)P->items * g.nseg * 8);
+  // the finiteness check's flag: only calls with one segment and no check need no workspace
   P->flag_fwd = o;
-  P->ws_fwd = o + 256;
+  P->ws_fwd = o > 0 || check_finite_on() ? o + 256 : 0;
   P->saved = (size_t)P->items * g.NK * tiles * tsz;
   P->save = o;
   o = align256(o + P->saved);
@@ -162,7 +163,7 @@ int attn_fwd(const moments_attn_desc* desc, const void* x, const void* k, const 
   const void* ptrs[] = {x, k, q, da, h0, y, h_last, saved, workspace};
   for (const void* p : ptrs)
     if (p != nullptr && !aligned16(p)) return MOMENTS_EINVAL;
-  if (workspace == nullptr || workspace_bytes < P.ws_fwd) return MOMENTS_EWORKSPACE;
+  if (workspace_bytes < P.ws_fwd || (P.ws_fwd > 0 && workspace == nullptr)) return MOMENTS_EWORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   unsigned char* ws = (unsigned char*)workspace;
   float* seg = P.g.nseg > 1 ? (float*)ws : nullptr;

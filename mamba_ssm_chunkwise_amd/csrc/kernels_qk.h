@@ -145,13 +145,13 @@ struct Raw8<float> {
 // the sine and cosine instructions, whose error of about 2^-20 is far below the result's
 // rounding of 2^-9; otherwise through the Taylor series to x^9 and x^10 (the next terms are
 // below 2^-28). Evaluated for bf16 rows the series costs 80 more instructions a lane and head.
-template <bool FAST>
+template <bool FAST, bool BIG>
 __device__ __forceinline__ void sincos_f(float x, float& s, float& c) {
   constexpr double kPi2 = 1.5707963267948966, kPi2Lo = 6.123233995736766e-17;   // pi/2: double and remainder
   constexpr float P1 = (float)kPi2, P2 = (float)(kPi2 - (double)P1), P3 = (float)kPi2Lo;
   float t;
   int n = 0;
-  if (fabsf(x) < 1e5f) {
+  if constexpr (!BIG) {
     // FAST takes off whole turns
     const float k = FAST ? 4.0f * rintf(x * 0.159154943091895336f) : rintf(x * 0.636619772367581343f);
     t = fmaf(-k, P2, fmaf(-k, P1, x));
@@ -211,18 +211,18 @@ struct QkRot {
       }
     }
   }
-  // Angles to their cosines and sines; lanes past the rotated width keep the identity.
+  // Angles to their cosines and sines.
   template <bool FAST>
   __device__ __forceinline__ void make(int l, const QkGeo& g) {
     if constexpr (ROT == 1 || ROT == 2) {
-      if (4 * l < g.A) {
+      // angles past the rotated width were loaded as zero: the identity
+      const float big = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+      if (big < 1e5f) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) sincos_f<FAST>(v[i], v[4 + i], v[i]);
+        for (int i = 0; i < 4; i++) sincos_f<FAST, false>(v[i], v[4 + i], v[i]);
       } else {
-        for (int i = 0; i < 4; i++) {
-          v[i] = 1.0f;
-          v[4 + i] = 0.0f;
-        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) sincos_f<FAST, true>(v[i], v[4 + i], v[i]);
       }
     }
   }
