@@ -59,9 +59,18 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   g.CT = L / g.c;
   g.NK = (g.V + g.CT - 1) / g.CT;
   g.cinv = (65536 + g.c - 1) / g.c;
+  // Rows of whole 16-byte pieces are fetched a chunk ahead; others, which such loads cannot
+  // address, element by element. Aligned shapes, either way (forward, backward): float, 32
+  // chains of 3800 rows, 44 and 56 us; bf16, 512 of 16384, 1.87 and 3.94 ms, 3.3 and 10.6 ms.
   P->vec = (g.r * tsz) % 16 == 0 && (g.p * tsz) % 16 == 0;
   g.lens = (const int*)d->valid_lens;
+  // Half the columns where they do: r = 64, float, 32 chains of 3800 rows, 4 tiles 21 us for
+  // the segments' states and 44 for the walk, 8 tiles 31 and 68.
   P->RT = g.r <= 64 ? 4 : 8;
+  // All of up to 128 state rows to a workgroup, so that keys and scores are made once:
+  // 32 chains of 240000 rows, p = 128, 0.84 ms for the segments' states and 2.05 for the walk;
+  // two workgroups of 64 each 0.96 and 2.62. Float, whose LDS tiles are
+  // twice as large, stays at 64.
   P->wide = P->bf && g.p > 64;
   g.PT = P->wide ? 128 : 64;
   g.npt = (g.p + g.PT - 1) / g.PT;

@@ -513,6 +513,17 @@ template <> struct ScoreTiles<2> {
 // VEC: rows are whole 16-byte pieces; the next chunk's are then in flight while one is
 // worked on. A chain split into segments takes three launches: the segments' own states
 // (MODE 1 or 2), k_attn_scan, which joins them, and the walk itself.
+//
+// Why so: scores cost L (r + p) operations a row beside the state's 4 p r, so L is the
+// smallest that keeps the matrix instructions in whole tiles for all four waves (64 rows in
+// bf16; 32 in float, whose tiles are twice as large). Two workgroups share a CU, one's loads
+// under the other's barriers; three measured no faster.
+// Bound: memory where the chains fill the card. bf16, r = 128: 512 chains of 16384 rows,
+// p = 64, with the saved copies, 8.6 GB in 1.87 ms (4.6 TB/s; a large copy reaches 4.75);
+// 32 chains of 240000 rows, p = 128, 8.0 GB in 2.05 ms (3.9 TB/s) behind a MODE 1 pass of
+// 3.9 GB in 0.85 ms (4.6 TB/s), matrix pipes 31 % and vector pipes 51 % busy. Else the
+// latency of a chunk: its phases depend on one another through LDS and three barriers (128
+// chains of 4096 rows, p = 64: 109 us; of ragged rows, the longest deciding: 96 us).
 template <typename T, int RT, int PW, int MODE, bool VEC>
 __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __restrict__ x, const T* __restrict__ k,
                                                       const T* __restrict__ q, const T* __restrict__ da,
@@ -795,7 +806,9 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
 
 // Joins the segments of each chain: seg_loc[seg], the state that the segment leaves from
 // zero, becomes the state that it starts from (from `first`, or zeros; BACK: the segments
-// in reverse). One thread for four values of a state.
+// in reverse). One thread for four values of a state. A chain of dependent reads: bound by
+// their latency, so eight segments' are in flight together. 32 chains, p = r = 128, 16
+// segments: 13 us.
 template <bool BACK>
 __global__ __launch_bounds__(256) void k_attn_scan(AttnGeo g, int RT, int tiles, const float* __restrict__ first,
                                                    float* __restrict__ seg_loc, const double* __restrict__ seg_dec) {
@@ -834,7 +847,9 @@ __global__ __launch_bounds__(256) void k_attn_scan(AttnGeo g, int RT, int tiles,
 // LPR lanes share a state row, four columns each (r <= 4 LPR); a wave takes
 // 64 / LPR rows at a time and NB such batches, with all their loads in flight first:
 // the state is read and written once and is all that counts (2 * 4 p r bytes against
-// 2 (2 r + 2 p) for the rest).
+// 2 (2 r + 2 p) for the rest). Bound by memory: 256 sequences of 64 heads, p = 64, r = 128
+// (1.08 GB): 226 us, 4.8 TB/s, as a large copy. One sequence: the launch's own time (4 us
+// of the 11 that the call takes on the host).
 template <typename T, int LPR, int NB>
 __global__ __launch_bounds__(256) void k_attn_step(AttnGeo g, int nslots, const T* __restrict__ x,
                                                    const T* __restrict__ k, const T* __restrict__ q,

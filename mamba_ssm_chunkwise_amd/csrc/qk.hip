@@ -40,19 +40,19 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
       A = (int)(d->rope_dim / 2);
       break;
     case MOMENTS_ROT_QUATERNION:
-      if (d->quat_blocks < 1 || 4 * d->quat_blocks > d->r) return MOMENTS_EINVAL;
+      if (d->quat_blocks < 1 || d->quat_blocks > d->r / 4) return MOMENTS_EINVAL;
       J = (int)d->quat_blocks;
       break;
     default:
       return MOMENTS_EINVAL;
   }
   if (d->rot_kind != MOMENTS_ROT_NONE && d->rot_h != 1 && d->rot_h != d->h) return MOMENTS_EINVAL;
-  const int64_t row = d->c * d->g * d->r;
-  const int64_t qs = d->q_stride == 0 ? row : d->q_stride, ks = d->k_stride == 0 ? row : d->k_stride;
-  if (qs < row || ks < row) return MOMENTS_EINVAL;
   if (d->r > 128 || d->c > 4 || d->g > 65535 || d->h / d->g > 128 || d->s > (int64_t)1 << 28 ||
       d->b > (int64_t)1 << 24 || d->b * d->s > (int64_t)1 << 30)
     return MOMENTS_ENOTSUP;
+  const int64_t row = d->c * d->g * d->r;
+  const int64_t qs = d->q_stride == 0 ? row : d->q_stride, ks = d->k_stride == 0 ? row : d->k_stride;
+  if (qs < row || ks < row) return MOMENTS_EINVAL;
   P->empty = d->b == 0 || d->h == 0;
   P->bf = d->dtype == MOMENTS_BF16;
   const int tsz = P->bf ? 2 : 4;
@@ -63,8 +63,14 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
   g.rot_h = (int)d->rot_h; g.A = A; g.J = J; g.RW = J > 0 ? 4 * J : A;
   g.eps = d->eps;
   g.rinv = 1.0f / (float)d->r;
+  // The rules below on 8 x 8192 tokens of two channels, 64 heads in 8 groups, r = 128, bf16
+  // ("large"), and 2 x 2048 of two, 16 heads, r = 64, float ("small"), forward and backward.
+  // Whole pieces, or, where alignment does not allow them, element by element: large 1.26 and
+  // 1.66 ms against 4.4 and 10.1, small 25 and 48 us against 148 and 543.
   P->vec = g.r % 8 == 0 && qs * tsz % 16 == 0 && ks * tsz % 16 == 0 && A % 4 == 0;
+  // 16 lanes for rows that 8 would do: small 29 and 58 us.
   P->LPR = g.r <= 64 && P->vec ? 8 : 16;
+  // Channels are held in registers; four places for two: large 2.1 and 5.5 ms, small 28 and 71 us.
   P->C = g.c <= 1 ? 1 : g.c <= 2 ? 2 : 4;
   if (P->empty) return MOMENTS_OK;
   g.hpg = g.h / g.g;
@@ -73,7 +79,8 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
   while (g.HPP < g.hpg && g.HPP < rpw) g.HPP *= 2;
   g.HL = (g.hpg + g.HPP - 1) / g.HPP;
   // sums for each head in registers while a head slot serves one or two heads, else in LDS:
-  // 64 bytes a thread and head, so fewer threads where there are many
+  // 64 bytes a thread and head, so fewer threads where there are many. LDS always: large 1.6
+  // and 2.8 ms, small 27 and 213 us.
   P->HB = P->vec && g.HL <= (P->C == 4 ? 1 : 2) ? g.HL : 0;
   P->NT = QKT;
   while (P->HB == 0 && P->NT > 64 && (size_t)(g.HL + 1) * 64 * P->NT > kLdsLimit) P->NT /= 2;
