@@ -94,6 +94,14 @@ def test_qk_descriptor(kw, code):
     assert (n > 0) if code == 0 else (n == code)
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(rot_kind=M.ROT_QUAT, rope_dim=0, quat_blocks=2 ** 62), -1),        # four times it is zero in 64 bits
+    (dict(c=2 ** 62), -2), (dict(r=2 ** 62), -2), (dict(b=2 ** 40, s=2 ** 40), -2),
+])
+def test_qk_sizes_that_would_wrap(kw, code):
+    assert _lib.load().moments_qk_workspace_size(ctypes.byref(_qk(**kw))) == code
+
+
 def test_qk_pointers():
     lib = _lib.load()
     d = ctypes.byref(_qk())
