@@ -505,10 +505,13 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
     for (int e = 0; e < 8; e++) b8[e] = 0.0f;
     if (bias != nullptr) ld8<float, HALF>(bias + (size_t)hi * g.r, l, g.r, VEC, b8);
   };
-  auto norm = [&](float (&n)[8]) {
+  // A row slot without a row (past the last token) has rstd = 0: with eps = 0 its zeros would
+  // become 0 * inf = NaN, which the sums of d_w would take up.
+  auto norm = [&](float (&n)[8], bool live) {
     float ss = 0.0f;
     for (int e = 0; e < 8; e++) ss += n[e] * n[e];
-    const float rstd = __builtin_amdgcn_rsqf(row_sum<LPR>(ss) * g.rinv + g.eps);
+    const float ms = row_sum<LPR>(ss) * g.rinv + g.eps;
+    const float rstd = live ? __builtin_amdgcn_rsqf(ms) : 0.0f;
     for (int e = 0; e < 8; e++) n[e] *= rstd;
     return rstd;
   };
@@ -616,7 +619,7 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
         for (int c = 0; c < C; c++) {
           const int j = x * C + c;
           raw[x][c].get(n[j]);
-          rstd[j] = c < g.c ? norm(n[j]) : 0.0f;
+          rstd[j] = c < g.c ? norm(n[j], live) : 0.0f;
           for (int e = 0; e < 8; e++) ds[j][e] = 0.0f;
         }
 #pragma unroll
@@ -655,7 +658,7 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
           const int j = x * C + c;
           for (int e = 0; e < 8; e++) n[j][e] = ds[j][e] = 0.0f;
           if (live && c < g.c) ld8<T, HALF>(raw_row(x, c, tok), l, g.r, VEC, n[j]);
-          rstd[j] = c < g.c ? norm(n[j]) : 0.0f;
+          rstd[j] = c < g.c ? norm(n[j], live) : 0.0f;
         }
       for (int e = 0; e < 8; e++) dr1[e] = 0.0f;
       for (int i = 0; i < g.HL; i++) {

