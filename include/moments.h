@@ -235,6 +235,8 @@ int moments_rot_bwd(const moments_desc* desc, const void* inc, const void* d_rot
  * `saved` of moments_attn_saved_size() bytes, the state that enters each chunk of
  * the kernels, as moments_attn_bwd_saved reads it (opaque; same descriptor and
  * inputs); moments_attn_bwd makes these itself from one more pass over xhat and bhat.
+ * h_last may be the buffer h0, and d_h0 the buffer d_h_last; no other output may
+ * overlap an input or another output.
  *
  * Supported: 1 <= c <= 4, r <= 128, p <= 4096, s <= 2^28, h * max(p, r) <= 2^23 (with the
  * p/64 or p/128 tiles of 64 or 128 state rows: h * tiles * r too); h a multiple of g; b, s or h

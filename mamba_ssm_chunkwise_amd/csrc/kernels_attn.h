@@ -527,8 +527,8 @@ template <> struct ScoreTiles<2> {
 template <typename T, int RT, int PW, int MODE, bool VEC>
 __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __restrict__ x, const T* __restrict__ k,
                                                       const T* __restrict__ q, const T* __restrict__ da,
-                                                      const float* __restrict__ h0, T* __restrict__ y,
-                                                      float* __restrict__ h_last, T* __restrict__ save,
+                                                      const float* h0, T* __restrict__ y,
+                                                      float* h_last, T* __restrict__ save,
                                                       float* __restrict__ seg_loc, double* __restrict__ seg_dec) {
   using LD = LdsA<T, RT, PW>;
   using V = AV<T>;
@@ -566,7 +566,9 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) H[pw][rt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
   if (MODE == 0 || save != nullptr) {
-    if (seg > 0) {   // k_attn_scan left it there
+    // Where k_attn_scan ran, it left every segment's there, the first one's too: h_last may be h0
+    // itself, and the last segment's workgroup may be done before the first one's has started.
+    if (g.nseg > 1) {
       const float* src = seg_loc + (((size_t)chain * g.nseg + seg) * g.npt + pt) * TILES;
 #pragma unroll
       for (int pw = 0; pw < PW; pw++)

@@ -86,9 +86,9 @@ struct StageH {
 template <typename T, int RT, int PT, bool PART, bool VEC>
 __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     AttnGeo g, const T* __restrict__ x, const T* __restrict__ k, const T* __restrict__ q, const T* __restrict__ da,
-    const T* __restrict__ save, const T* __restrict__ dy, const float* __restrict__ d_last,
+    const T* __restrict__ save, const T* __restrict__ dy, const float* d_last,
     const float* __restrict__ seg_loc, T* __restrict__ d_x, T* __restrict__ d_k,
-    T* __restrict__ d_q, T* __restrict__ d_da, float* __restrict__ d_h0, float* __restrict__ part_k,
+    T* __restrict__ d_q, T* __restrict__ d_da, float* d_h0, float* __restrict__ part_k,
     float* __restrict__ part_q, float* __restrict__ part_da) {
   using LD = LdsB<T, RT, PT>;
   using V = AV<T>;
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
   for (int i = 0; i < RW; i++) {
     G[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (seg < g.nseg - 1)   // k_attn_scan left it there
+    if (g.nseg > 1)   // k_attn_scan left every segment's there (d_h0 may be d_last itself)
       G[i] = *reinterpret_cast<const f4*>(seg_loc + (((size_t)chain * g.nseg + seg) * g.npt + pt) * TILES +
                                           tile_off(RT, mp, mr + i, lane));
     else if (d_last != nullptr)

@@ -1,0 +1,44 @@
+"""Linear attention at its edges: values that are not finite, cleared states, buffers
+that a caller uses twice, empty inputs, the finite check of single tokens.
+
+Tolerances are those of test_gpu_attn.py."""
+import pytest
+import torch
+
+import mamba_ssm_chunkwise_amd as M
+from test_gpu_attn import BF16, DEV, F32, _make
+
+pytestmark = pytest.mark.gpu
+INPUTS = ("xhat", "bhat", "qhat", "da")
+
+
+def _args(t):
+    return [t[n] for n in INPUTS]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("b,s,h,p,lens", [(2, 50, 3, 24, None), (1, 2300, 2, 96, None), (4, 2300, 2, 32, [5, 2300, 0, 900])])
+def test_states_written_over_the_ones_that_were_read(dtype, b, s, h, p, lens):
+    """h_last on h0, and d_h0 on d_h_last: one segment, several, and lengths that leave segments empty."""
+    print(f"[case] in place b={b} s={s} {dtype}", flush=True)
+    t = _make(b, s, 1, h, 1, p, 40, dtype, seed=b + s)
+    a = _args(t)
+    n = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=DEV)
+    d = M.attn_desc(a[0], a[1], valid_lens=n)
+    y, last, saved = M.moments_attn_fwd_save(d, *a, t["h0"])
+    g = M.moments_attn_bwd_saved(d, *a, t["h0"], saved, t["d_y"], t["d_last"])
+    for save in (False, True):
+        h0 = t["h0"].clone()
+        if save:
+            y2, last2, saved2 = M.moments_attn_fwd_save(d, *a, h0, h_last=h0)
+        else:
+            y2, last2 = M.moments_attn_fwd(d, *a, h0, h_last=h0)
+        assert last2 is h0 and torch.equal(y, y2) and torch.equal(last, h0)
+    for save in (False, True):
+        dl = t["d_last"].clone()
+        if save:
+            g2 = M.moments_attn_bwd_saved(d, *a, t["h0"], saved2, t["d_y"], dl, out={"d_h0": dl})
+        else:
+            g2 = M.moments_attn_bwd(d, *a, t["h0"], t["d_y"], dl, out={"d_h0": dl})
+        for k in g:
+            assert torch.equal(g[k], g2[k]), k
