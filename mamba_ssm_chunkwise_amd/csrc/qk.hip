@@ -200,7 +200,10 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
   float* pw = d_wq || d_wk ? (float*)(ws + P.part_w) : nullptr;
   float* pb = d_bq || d_bk ? (float*)(ws + P.part_b) : nullptr;
   float* pr = rot1 && d_rot ? (float*)(ws + P.part_rot) : nullptr;
-  MOM_TRY(with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto hpp, auto vec) -> int {
+  // Without tokens there is nothing to read (q, k, the weights and rot may be NULL): the sums
+  // over tokens, of no partials, are all that is left.
+  const int nblk = g.s > 0 ? g.nblk : 0;
+  auto rows = [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto hpp, auto vec) -> int {
     using T = typename decltype(tt)::type;
     constexpr int LPR = decltype(lpr)::value, ROT = decltype(rk)::value, C = decltype(cc)::value;
     {
@@ -212,7 +215,7 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
                          (T*)d_k, (T*)(rot1 ? nullptr : d_rot), pr, pw, pb);
       MOM_TRY(check_launch());
     }
-    if (pr != nullptr && g.s > 0) {
+    if (pr != nullptr) {
       const size_t total = (size_t)g.b * g.s * g.RW;
       ProfScope ps(KID_QK_SUM, st);
       const SumJobs jobs = {{{pr, d_rot, total, g.g, g.RW}, {}, {}}};
@@ -221,11 +224,12 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
       MOM_TRY(check_launch());
     }
     return 0;
-  }));
+  };
+  if (nblk > 0) MOM_TRY(with_qk(P, desc->rot_kind, rows));
   if (pw != nullptr || pb != nullptr) {
     ProfScope ps(KID_QK_SUM, st);
     const unsigned cols = (unsigned)((g.r + 15) / 16 + (pb != nullptr ? ((int64_t)g.h * g.r + 15) / 16 : 0));
-    hipLaunchKernelGGL(k_qk_sum, dim3(cols, 2), dim3(1024), 0, st, pw, g.nblk * g.g, g.r, d_wq, d_wk, pb, g.nblk,
+    hipLaunchKernelGGL(k_qk_sum, dim3(cols, 2), dim3(1024), 0, st, pw, nblk * g.g, g.r, d_wq, d_wk, pb, nblk,
                        g.h * g.r, d_bq, d_bk);
     MOM_TRY(check_launch());
   }

@@ -2,11 +2,13 @@
 large angles, empty batches, rows cut out of a projection at any element.
 
 Tolerances are those of test_gpu_qk.py unless a test states its own."""
-import numpy as np
+import ctypes
+
 import pytest
 import torch
 
 import mamba_ssm_chunkwise_amd as M
+from mamba_ssm_chunkwise_amd import _lib
 from oracle import qk_norm
 from test_gpu_qk import BF16, DEV, F32, KINDS, TOL, _check, _make, _np
 
@@ -42,3 +44,15 @@ def test_without_eps(dtype, kind, width, c, h, g, r):
         pytest.skip("half-split rows are even")
     print(f"[case] eps=0 kind={kind} c={c} h={h} g={g} r={r} {dtype}", flush=True)
     _against_oracle(_make(1, 9, c, h, g, r, kind, width, dtype, seed=r), h, kind, 0.0)
+
+
+def test_gradients_of_no_tokens_need_no_weights():
+    """The C call with s = 0 and every input NULL: the parameters' gradients are zero."""
+    h, r = 4, 24
+    d = M.QkDesc(2, 0, 1, h, 2, r, 0, 0, 8, 0, h, _lib.F32, M.ROT_PAIRWISE, 1e-5)
+    ws = torch.empty(M.moments_qk_workspace_size(d), dtype=torch.uint8, device=DEV)
+    d_w = [torch.full((r,), float("nan"), device=DEV) for _ in range(2)]
+    rc = _lib.load().moments_qk_bwd(ctypes.byref(d), *[None] * 11, d_w[0].data_ptr(), d_w[1].data_ptr(), None, None,
+                                    None, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0 and all(torch.count_nonzero(v) == 0 for v in d_w)
