@@ -585,7 +585,8 @@ def _qk_inputs(desc: QkDesc, q, k, wq, wk, bq, bk, rot):
         if t.shape != raw or t.dtype is not dt or t.device != dev:
             raise ValueError(f"{name} must be {dt} of shape {(b, s, c, g, r)} on {dev}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
-        if b * s > 1 and (_token_stride(name, t) or row) != (stride or row):
+        step = _token_stride(name, t) or row   # also one token's values have to lie together
+        if b * s > 1 and step != (stride or row):
             raise ValueError(f"{name} has another token stride than the descriptor ({stride or row})")
     f32, kind = torch.float32, desc.rot_kind
     specs = [("wq", wq, (r,), f32, False), ("wk", wk, (r,), f32, False), ("bq", bq, (h, r), f32, True),

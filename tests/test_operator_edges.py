@@ -2,6 +2,10 @@
 what an empty call may leave out, layouts, sizes. No GPU is touched."""
 import ctypes
 
+import pytest
+import torch
+
+import mamba_ssm_chunkwise_amd as M
 from mamba_ssm_chunkwise_amd import _lib
 from test_attn_abi import BIG, FAKE, NULL, _qk
 
@@ -11,3 +15,30 @@ def test_norm_gradients_of_no_tokens_launch_nothing():
     lib = _lib.load()
     d = ctypes.byref(_qk(s=0))
     assert lib.moments_qk_bwd(d, *[NULL] * 16, FAKE, BIG, NULL) == 0
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("kind", ["transposed", "expanded", "strided"])
+def test_one_token_of_another_layout_is_refused(which, kind):
+    """One token (b = s = 1) under a descriptor made earlier, as decoding has it: its values have to lie
+    together there too."""
+    t = {n: torch.zeros(1, 1, 1, 2, 16) for n in ("q", "k")}
+    w = torch.zeros(16)
+    d = M.qk_desc(t["q"], t["k"], 4, M.ROT_NONE)
+    t[which] = {"transposed": torch.zeros(1, 1, 1, 16, 2).transpose(3, 4),
+                "expanded": torch.zeros(1, 1, 1, 1, 16).expand(1, 1, 1, 2, 16),
+                "strided": torch.zeros(1, 1, 1, 2, 32)[..., ::2]}[kind]
+    with pytest.raises(ValueError, match=f"{which} must hold each token's values together"):
+        M.moments_qk_fwd(d, t["q"], t["k"], w, w)
+    hat = torch.zeros(1, 1, 1, 4, 16)
+    with pytest.raises(ValueError, match=f"{which} must hold each token's values together"):
+        M.moments_qk_bwd(d, t["q"], t["k"], w, w, None, None, None, hat, hat)
+
+
+def test_one_token_cut_out_of_a_projection_is_taken():
+    """Any step to a next token that is not there: the checks pass as far as the device."""
+    q = torch.zeros(1, 1, 100)[:, :, :32].view(1, 1, 1, 2, 16)
+    d = M.qk_desc(torch.zeros(1, 1, 1, 2, 16), q, 4, M.ROT_NONE)
+    w = torch.zeros(16)
+    with pytest.raises(ValueError, match="GPU"):
+        M.moments_qk_fwd(d, q, q, w, w)
