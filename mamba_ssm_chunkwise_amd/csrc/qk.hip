@@ -144,6 +144,39 @@ int with_qk(const QkPlan& P, int rot_kind, F&& f) {
   return P.bf ? by_rot(TT<bf16>{}) : by_rot(TT<float>{});
 }
 
+// The parameters' gradients from the partials of nblk workgroups a group (zeros for none).
+int launch_qk_sum(const QkGeo& g, const float* pw, const float* pb, int nblk, float* d_wq, float* d_wk, float* d_bq,
+                  float* d_bk, hipStream_t st) {
+  if (!d_wq && !d_wk && !d_bq && !d_bk) return 0;
+  ProfScope ps(KID_QK_SUM, st);
+  const unsigned cols = (unsigned)((g.r + 15) / 16 + (d_bq || d_bk ? ((int64_t)g.h * g.r + 15) / 16 : 0));
+  hipLaunchKernelGGL(k_qk_sum, dim3(cols, 2), dim3(1024), 0, st, pw, nblk * g.g, g.r, d_wq, d_wk, pb, nblk,
+                     g.h * g.r, d_bq, d_bk);
+  return check_launch();
+}
+
+// Gradients where there are no sequences or no heads: those that hold values are zero (sums
+// of no slices).
+int qk_bwd_empty(const QkPlan& P, void* d_q, void* d_k, float* d_wq, float* d_wk, float* d_bq, float* d_bk,
+                 void* d_rot, hipStream_t st) {
+  const QkGeo& g = P.g;
+  const size_t tok = (size_t)g.b * g.s, raw = tok * g.c * g.g * g.r, rot = tok * g.rot_h * g.RW;
+  const SumJobs jobs = {{{nullptr, d_q, d_q ? raw : 0, 0, g.r},
+                         {nullptr, d_k, d_k ? raw : 0, 0, g.r},
+                         {nullptr, d_rot, d_rot ? rot : 0, 0, std::max(g.RW, 1)}}};
+  const size_t most = std::max({jobs.job[0].total, jobs.job[1].total, jobs.job[2].total});
+  if (most > 0) {
+    ProfScope ps(KID_QK_SUM, st);
+    const dim3 grid((unsigned)std::min<size_t>((most + 255) / 256, 16384), 3);
+    if (P.bf)
+      hipLaunchKernelGGL((k_attn_sum<bf16>), grid, dim3(256), 0, st, jobs);
+    else
+      hipLaunchKernelGGL((k_attn_sum<float>), grid, dim3(256), 0, st, jobs);
+    MOM_TRY(check_launch());
+  }
+  return launch_qk_sum(g, nullptr, nullptr, 0, d_wq, d_wk, d_bq, d_bk, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -185,7 +218,7 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
   QkPlan P;
   MOM_TRY(make_qk_plan(desc, &P));
   const QkGeo& g = P.g;
-  if (P.empty) return 0;
+  if (P.empty) return qk_bwd_empty(P, d_q, d_k, d_wq, d_wk, d_bq, d_bk, d_rot, (hipStream_t)stream);
   if (g.s > 0 && (!q || !k || !wq || !wk || !d_qhat || !d_khat)) return MOMENTS_EINVAL;
   if (g.s > 0 && (desc->rot_kind == MOMENTS_ROT_NONE) != (rot == nullptr)) return MOMENTS_EINVAL;
   if (desc->rot_kind == MOMENTS_ROT_NONE && d_rot != nullptr) return MOMENTS_EINVAL;
@@ -226,13 +259,7 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
     return 0;
   };
   if (nblk > 0) MOM_TRY(with_qk(P, desc->rot_kind, rows));
-  if (pw != nullptr || pb != nullptr) {
-    ProfScope ps(KID_QK_SUM, st);
-    const unsigned cols = (unsigned)((g.r + 15) / 16 + (pb != nullptr ? ((int64_t)g.h * g.r + 15) / 16 : 0));
-    hipLaunchKernelGGL(k_qk_sum, dim3(cols, 2), dim3(1024), 0, st, pw, nblk * g.g, g.r, d_wq, d_wk, pb, nblk,
-                       g.h * g.r, d_bq, d_bk);
-    MOM_TRY(check_launch());
-  }
+  MOM_TRY(launch_qk_sum(g, pw, pb, nblk, d_wq, d_wk, d_bq, d_bk, st));
   if (check_finite_on()) {
     const size_t raw = (size_t)g.b * g.s * g.c * g.g * g.r;
     const OutSpan outs[] = {{d_q, raw, !P.bf}, {d_k, raw, !P.bf}, {d_rot, (size_t)g.b * g.s * g.rot_h * g.RW, !P.bf},

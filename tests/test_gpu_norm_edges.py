@@ -56,3 +56,20 @@ def test_gradients_of_no_tokens_need_no_weights():
                                     None, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert rc == 0 and all(torch.count_nonzero(v) == 0 for v in d_w)
+
+
+def _poisoned(t, h):
+    """Gradients to be written over: each holds NaN."""
+    return {"d_" + n: torch.full_like(t[n], float("nan")) for n in NAMES if t[n] is not None}
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rot_h", [1, None])
+@pytest.mark.parametrize("b,s,h", [(0, 5, 4), (2, 0, 4), (2, 5, 0)])
+def test_gradients_of_empty_inputs(dtype, rot_h, b, s, h):
+    """No sequences, no tokens, no heads: what is left of the gradients is zero."""
+    t = _make(b, s, 2, h, 2, 24, M.ROT_PAIRWISE, 4, dtype, rot_h=rot_h, seed=1)
+    _, got = _run(t, h, M.ROT_PAIRWISE, 1e-5, out=_poisoned(t, h))
+    torch.cuda.synchronize()
+    for k, v in got.items():
+        assert torch.equal(v, torch.zeros_like(v)), k
