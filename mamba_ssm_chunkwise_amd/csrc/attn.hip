@@ -48,6 +48,7 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   if (d->b > (int64_t)1 << 24 || d->h > (int64_t)1 << 20 || d->b * d->h > (int64_t)1 << 24) return MOMENTS_ENOTSUP;
   // a token row of a tensor: the kernels address the rows of a chunk with 32-bit offsets
   if (d->h * d->p > (int64_t)1 << 23 || d->h * d->r > (int64_t)1 << 23) return MOMENTS_ENOTSUP;
+  if (d->g > (int64_t)1 << 20) return MOMENTS_ENOTSUP;   // with h = 0, that is: else g <= h
   P->empty = d->b == 0 || d->h == 0;
   P->bf = d->dtype == MOMENTS_BF16;
   const int tsz = P->bf ? 2 : 4, L = P->bf ? AV<bf16>::L : AV<float>::L;
@@ -193,13 +194,29 @@ int attn_fwd(const moments_attn_desc* desc, const void* x, const void* k, const 
   return 0;
 }
 
+// Gradients where there are no sequences or no heads: those of keys and queries may hold
+// values, and are zero (sums of no slices).
+int attn_bwd_empty(const AttnPlan& P, void* d_k, void* d_q, hipStream_t st) {
+  const AttnGeo& g = P.g;
+  const size_t keys = (size_t)g.b * g.s * g.c * g.g * g.r;
+  if (keys == 0 || (d_k == nullptr && d_q == nullptr)) return 0;
+  const SumJobs jobs = {{{nullptr, d_q, d_q ? keys : 0, 0, g.r}, {nullptr, d_k, d_k ? keys : 0, 0, g.r}, {}}};
+  ProfScope ps(KID_ATTN_SUM, st);
+  const dim3 grid((unsigned)std::min<size_t>((keys + 255) / 256, 16384), 2);
+  if (P.bf)
+    hipLaunchKernelGGL((k_attn_sum<bf16>), grid, dim3(256), 0, st, jobs);
+  else
+    hipLaunchKernelGGL((k_attn_sum<float>), grid, dim3(256), 0, st, jobs);
+  return check_launch();
+}
+
 int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const void* q, const void* da,
              const float* h0, const void* saved, size_t saved_bytes, bool use_saved, const void* d_y,
              const float* d_last, void* d_x, void* d_k, void* d_q, void* d_da, float* d_h0, void* workspace,
              size_t workspace_bytes, void* stream) {
   AttnPlan P;
   MOM_TRY(make_attn_plan(desc, &P));
-  if (P.empty) return 0;
+  if (P.empty) return attn_bwd_empty(P, d_k, d_q, (hipStream_t)stream);
   if (P.g.s > 0 && (!x || !k || !q || !da || !d_y)) return MOMENTS_EINVAL;
   if (use_saved && P.saved > 0 && saved == nullptr) return MOMENTS_EINVAL;
   if (use_saved && saved_bytes < P.saved) return MOMENTS_EWORKSPACE;

@@ -9,6 +9,7 @@ import mamba_ssm_chunkwise_amd as M
 from test_gpu_attn import BF16, DEV, F32, _make
 
 pytestmark = pytest.mark.gpu
+NAN = float("nan")
 INPUTS = ("xhat", "bhat", "qhat", "da")
 
 
@@ -42,3 +43,17 @@ def test_states_written_over_the_ones_that_were_read(dtype, b, s, h, p, lens):
             g2 = M.moments_attn_bwd(d, *a, t["h0"], t["d_y"], dl, out={"d_h0": dl})
         for k in g:
             assert torch.equal(g[k], g2[k]), k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradients_without_heads(dtype):
+    """h = 0: keys and queries still have gradients, and they are zero."""
+    t = _make(2, 5, 1, 1, 1, 4, 8, dtype, seed=1)
+    k, q = (torch.randn(2, 5, 1, 2, 8, device=DEV).to(dtype) for _ in range(2))
+    x, da = t["xhat"][:, :, :, :0].contiguous(), t["da"][:, :, :0].contiguous()
+    d = M.attn_desc(x, k)
+    out = {"d_bhat": torch.full_like(k, NAN), "d_qhat": torch.full_like(q, NAN)}
+    got = M.moments_attn_bwd(d, x, k, q, da, None, x, out=out)
+    torch.cuda.synchronize()
+    for n in ("d_bhat", "d_qhat"):
+        assert torch.equal(got[n], torch.zeros_like(k)), n
