@@ -313,6 +313,14 @@ __device__ __forceinline__ void slot_scatter(float (&v)[N][8], int lane) {
   }
 }
 
+// 1 / sqrt(v): the instruction, right to one unit in the last place, which is of the size of
+// the sum's and the products' own roundings (float rows use it too). It takes subnormal
+// inputs for zero: those are brought into its range by a power of two, and back.
+__device__ __forceinline__ float recip_sqrt(float v) {
+  const bool small = v < 0x1p-100f;
+  return __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v) * (small ? 0x1p32f : 1.0f);
+}
+
 // C: channels padded to 1, 2 or 4. HB: heads per row slot whose bias stays in registers
 // (0: HL is larger, it is read again for each token). VEC: rows, their strides and the
 // angles are whole 16-byte pieces (8 bytes, bf16 angles); others go one element at a time.
@@ -386,7 +394,7 @@ __global__ __launch_bounds__(QKT) void k_qk_fwd(QkGeo g, const T* __restrict__ q
         if (c >= g.c) break;
         float ss = 0.0f;
         for (int e = 0; e < 8; e++) ss += n[x][c][e] * n[x][c][e];
-        const float rstd = __builtin_amdgcn_rsqf(row_sum<LPR>(ss) * g.rinv + g.eps);
+        const float rstd = recip_sqrt(row_sum<LPR>(ss) * g.rinv + g.eps);
         for (int e = 0; e < 8; e++) n[x][c][e] *= rstd * w[x][e];
       }
     auto head = [&](int hg, QkRot<ROT>& Rh, auto bias) {
@@ -511,7 +519,7 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
     float ss = 0.0f;
     for (int e = 0; e < 8; e++) ss += n[e] * n[e];
     const float ms = row_sum<LPR>(ss) * g.rinv + g.eps;
-    const float rstd = live ? __builtin_amdgcn_rsqf(ms) : 0.0f;
+    const float rstd = live ? recip_sqrt(ms) : 0.0f;
     for (int e = 0; e < 8; e++) n[e] *= rstd;
     return rstd;
   };

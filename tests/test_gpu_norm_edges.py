@@ -73,3 +73,18 @@ def test_gradients_of_empty_inputs(dtype, rot_h, b, s, h):
     torch.cuda.synchronize()
     for k, v in got.items():
         assert torch.equal(v, torch.zeros_like(v)), k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("r", [24, 45])
+def test_rows_of_zeros_under_a_subnormal_eps(dtype, r):
+    """Their mean square plus eps is subnormal: 1 / sqrt is 2^65, and the rows' norm is zero, not NaN."""
+    t = _make(1, 10, 1, 2, 2, r, M.ROT_PAIRWISE, 4, dtype, seed=3)
+    for n in ("q", "k"):
+        t[n][:, ::2] = 0.0
+    hats, got = _against_oracle(t, 2, M.ROT_PAIRWISE, 2.0 ** -130)
+    o = {k: _np(v) for k, v in t.items()}
+    for n in ("q", "k"):      # the other rows' gradients, which are 2^65 times smaller
+        d_x = qk_norm.qk_bwd(o[n], o["w" + n], o["b" + n], o["rot"], M.ROT_PAIRWISE, 2, 2.0 ** -130,
+                             o["d_%shat" % n])[0]
+        _check("d_" + n, got["d_" + n][:, 1::2], d_x[:, 1::2], TOL[dtype])
