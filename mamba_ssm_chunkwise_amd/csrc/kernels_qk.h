@@ -139,16 +139,19 @@ struct Raw8<float> {
   }
 };
 
-// Sine and cosine. The nearest multiple of pi/2 is taken off (in three floats below 1e5,
-// else in doubles, which reach to 2^50; beyond, neighbouring floats are 2^27 radians apart,
-// and the rest is taken as zero). FAST (bf16 results): the rest, at most pi/4, goes through
-// the sine and cosine instructions, whose error of about 2^-20 is far below the result's
-// rounding of 2^-9; otherwise through the Taylor series to x^9 and x^10 (the next terms are
-// below 2^-28). Evaluated for bf16 rows the series costs 80 more instructions a lane and head.
+// Sine and cosine. The nearest multiple of pi/2 (FAST: the whole turns) is taken off, below
+// 1e5 in three floats, which hold pi/2 to 2^-76 (FAST: in two), else in doubles, which reach
+// to 2^50; beyond, neighbouring floats are 2^27 radians apart, and the rest is taken as zero.
+// FAST (bf16 results): the rest, up to half a turn (from 1e5 on the quarters are put back, up
+// to a whole one), goes through the sine and cosine instructions, whose error of about 2^-20
+// is far below the result's rounding of 2^-9; otherwise, at most pi/4, through the Taylor
+// series to x^9 and x^10 (the next terms are below 2^-28). Evaluated for bf16 rows the series
+// costs 80 more instructions a lane and head.
 template <bool FAST, bool BIG>
 __device__ __forceinline__ void sincos_f(float x, float& s, float& c) {
   constexpr double kPi2 = 1.5707963267948966, kPi2Lo = 6.123233995736766e-17;   // pi/2: double and remainder
-  constexpr float P1 = (float)kPi2, P2 = (float)(kPi2 - (double)P1), P3 = (float)kPi2Lo;
+  constexpr float P1 = (float)kPi2, P2 = (float)(kPi2 - (double)P1),
+                  P3 = (float)(kPi2 - (double)P1 - (double)P2 + kPi2Lo);
   float t;
   int n = 0;
   if constexpr (!BIG) {

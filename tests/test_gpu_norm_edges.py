@@ -4,6 +4,7 @@ large angles, empty batches, rows cut out of a projection at any element.
 Tolerances are those of test_gpu_qk.py unless a test states its own."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -88,3 +89,31 @@ def test_rows_of_zeros_under_a_subnormal_eps(dtype, r):
         d_x = qk_norm.qk_bwd(o[n], o["w" + n], o["b" + n], o["rot"], M.ROT_PAIRWISE, 2, 2.0 ** -130,
                              o["d_%shat" % n])[0]
         _check("d_" + n, got["d_" + n][:, 1::2], d_x[:, 1::2], TOL[dtype])
+
+
+def test_angles_next_to_multiples_of_a_right_angle():
+    """float32 angles next to k pi/2 up to 1e5: the sine or cosine is tiny, and is right to its own last bits.
+
+    The rows are (1, 0), so that hat is (cos, sin) times 1 up to a dozen roundings of 2^-24: 2^-20 bounds them."""
+    x = (np.arange(1, 63000) * (np.pi / 2)).astype(np.float32)
+    n = x.size
+    q = torch.zeros(1, n, 1, 1, 2, device=DEV)
+    q[..., 0] = 1.0
+    w = torch.full((2,), 0.5 ** 0.5, device=DEV)
+    rot = torch.from_numpy(x).to(DEV).view(1, n, 1, 1)
+    hat, _ = M.moments_qk_fwd(M.qk_desc(q, q, 1, M.ROT_PAIRWISE, rot=rot, eps=0.0), q, q, w, w, rot=rot)
+    got = _np(hat)[0, :, 0, 0]
+    ref = np.stack([np.cos(x.astype(np.float64)), np.sin(x.astype(np.float64))], -1)
+    err = np.abs(got - ref) / np.abs(ref)
+    print(f"[compare] relative error of the smallest values: {err.max():.2e}", flush=True)
+    assert err.max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("kind", [M.ROT_PAIRWISE, M.ROT_HALF])
+def test_large_angles_in_bf16(kind):
+    """Both of the reductions that bf16 rows use: below 1e5 and from there on."""
+    t = _make(1, 64, 1, 2, 2, 16, kind, 8, BF16, seed=5)
+    rot = torch.logspace(0, 6, 64, device=DEV).view(1, 64, 1, 1) * torch.linspace(-1.0, 1.0, 8, device=DEV)
+    t["rot"] = rot.expand(1, 64, 2, 8).to(BF16).contiguous()
+    assert (t["rot"].abs() > 1e5).any() and (t["rot"].abs() < 1e5).any()
+    _against_oracle(t, 2, kind, 1e-5)
