@@ -239,7 +239,8 @@ int moments_rot_bwd(const moments_desc* desc, const void* inc, const void* d_rot
  * overlap an input or another output.
  *
  * Supported: 1 <= c <= 4, r <= 128, p <= 4096, s <= 2^28, h * max(p, r) <= 2^23 (with the
- * p/64 or p/128 tiles of 64 or 128 state rows: h * tiles * r too); h a multiple of g; b, s or h
+ * p/64 or p/128 tiles of 64 or 128 state rows: h * tiles * r too); b * h * tiles below 2^24, for
+ * the gradients 2^23 (MOMENTS_ENOTSUP from their workspace size); h a multiple of g; b, s or h
  * may be 0 (nothing to do, but with s = 0 h_last is h0 and d_h0 is d_h_last). Rows of
  * r and p elements that are whole 16-byte pieces are read as such, others one element
  * at a time. Layout, alignment, ownership, errors and MOMENTS_CHECK_FINITE are those

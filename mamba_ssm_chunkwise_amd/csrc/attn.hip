@@ -18,6 +18,7 @@ struct AttnPlan {
   AttnGeo g;    // forward walk
   AttnGeo gb;   // backward walk (segments of its own)
   bool bf, empty;
+  bool bwd;     // few enough items for the gradients' launch
   bool vec;     // rows of r and of p are whole 16-byte pieces
   bool part;    // d_q, d_k (and d_da) by slices that k_attn_sum adds
   int RT;       // 16-column tiles of r: 4 or 8
@@ -76,8 +77,11 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   g.PT = P->wide ? 128 : 64;
   g.npt = (g.p + g.PT - 1) / g.PT;
   P->items = g.b * g.h * g.npt;
-  if ((int64_t)g.b * g.h * g.npt > (int64_t)1 << 24 || (int64_t)g.h * g.npt * g.r > (int64_t)1 << 23)
-    return MOMENTS_ENOTSUP;
+  // A launch holds fewer than 2^32 threads: the walks take 256 for each item, the gradients 512
+  // (attn_bwd and the size of its workspace refuse those that are too many for them alone).
+  const int64_t items = (int64_t)g.b * g.h * g.npt;
+  if (items >= ((int64_t)1 << 32) / ATT || (int64_t)g.h * g.npt * g.r > (int64_t)1 << 23) return MOMENTS_ENOTSUP;
+  P->bwd = items < ((int64_t)1 << 32) / ABT;
   P->gb = g;
   if (!P->empty) {
     split(g, P->items, 2 * kCUs);      // two workgroups of the walk share a CU
@@ -217,6 +221,7 @@ int attn_bwd(const moments_attn_desc* desc, const void* x, const void* k, const 
   AttnPlan P;
   MOM_TRY(make_attn_plan(desc, &P));
   if (P.empty) return attn_bwd_empty(P, d_k, d_q, (hipStream_t)stream);
+  if (!P.bwd) return MOMENTS_ENOTSUP;
   if (P.g.s > 0 && (!x || !k || !q || !da || !d_y)) return MOMENTS_EINVAL;
   if (use_saved && P.saved > 0 && saved == nullptr) return MOMENTS_EINVAL;
   if (use_saved && saved_bytes < P.saved) return MOMENTS_EWORKSPACE;
@@ -301,6 +306,7 @@ int64_t moments_attn_workspace_size(const moments_attn_desc* desc, int is_bwd) {
   AttnPlan P;
   const int rc = make_attn_plan(desc, &P);
   if (rc != 0) return rc;
+  if (is_bwd && !P.bwd) return MOMENTS_ENOTSUP;
   return P.empty ? 0 : (int64_t)(is_bwd ? P.ws_bwd : P.ws_fwd);
 }
 

@@ -57,3 +57,19 @@ def test_gradients_without_heads(dtype):
     torch.cuda.synchronize()
     for n in ("d_bhat", "d_qhat"):
         assert torch.equal(got[n], torch.zeros_like(k)), n
+
+
+def test_the_largest_launches():
+    """As many chains as a launch holds: forwards and single tokens 2^24 - 1, gradients 2^23 - 1."""
+    n = 2 ** 24 - 1
+    one = lambda *shape: torch.ones(n, *shape, device=DEV)  # noqa: E731
+    x, k, da = one(1, 1, 1, 1), one(1, 1, 1, 1), torch.zeros(n, 1, 1, device=DEV)
+    h0 = torch.arange(n, dtype=torch.float32, device=DEV).view(n, 1, 1, 1) % 1024
+    d = M.attn_desc(x, k)
+    y, last = M.moments_attn_fwd(d, x, k, k, da, h0)
+    assert torch.equal(last, h0 + 1) and torch.equal(y.view(-1), last.view(-1))
+    assert torch.equal(M.moments_attn_step(d, x, k, k, da, last).view(-1), h0.view(-1) + 2)
+    n = 2 ** 23 - 1
+    x, k, da, h0 = x[:n, :0], k[:n, :0], da[:n, :0], h0[:n].contiguous()
+    got = M.moments_attn_bwd(M.attn_desc(x, k), x, k, k, da, h0, x, h0)
+    assert torch.equal(got["d_h0"], h0)

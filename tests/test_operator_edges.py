@@ -7,7 +7,7 @@ import torch
 
 import mamba_ssm_chunkwise_amd as M
 from mamba_ssm_chunkwise_amd import _lib
-from test_attn_abi import BIG, FAKE, NULL, _qk
+from test_attn_abi import BIG, FAKE, NULL, _attn, _qk
 
 
 def test_norm_gradients_of_no_tokens_launch_nothing():
@@ -42,3 +42,24 @@ def test_one_token_cut_out_of_a_projection_is_taken():
     w = torch.zeros(16)
     with pytest.raises(ValueError, match="GPU"):
         M.moments_qk_fwd(d, q, q, w, w)
+
+
+@pytest.mark.parametrize("p", [1, 64, 65])
+@pytest.mark.parametrize("chains,fwd,bwd", [(2 ** 22 - 1, 0, 0), (2 ** 22, 0, 0), (2 ** 23 - 1, 0, 0), (2 ** 23, 0, -2),
+                                            (2 ** 24 - 1, 0, -2), (2 ** 24, -2, -2)])
+def test_sizes_that_a_launch_cannot_hold(p, chains, fwd, bwd):
+    """2^32 threads and more: 256 for each 64 state rows of a chain forwards, 512 for the gradients."""
+    if p > 64:      # two workgroups a chain
+        fwd, bwd = (0 if 2 * chains < 2 ** 24 else -2), (0 if 2 * chains < 2 ** 23 else -2)
+    d = ctypes.byref(_attn(b=chains, h=1, g=1, s=1, p=p, r=1, valid_len=1))
+    lib = _lib.load()
+    assert lib.moments_attn_validate(d) == fwd
+    for n, code in ((lib.moments_attn_workspace_size(d, 0), fwd), (lib.moments_attn_saved_size(d), fwd),
+                    (lib.moments_attn_workspace_size(d, 1), bwd)):
+        assert (n >= 0) if code == 0 else (n == code)
+    if bwd != 0:
+        assert lib.moments_attn_bwd(d, *[FAKE] * 12, FAKE, BIG, NULL) == bwd
+        assert lib.moments_attn_bwd_saved(d, *[FAKE] * 5, FAKE, BIG, *[FAKE] * 7, FAKE, BIG, NULL) == bwd
+    if fwd != 0:
+        assert lib.moments_attn_fwd(d, *[FAKE] * 7, FAKE, BIG, NULL) == fwd
+        assert lib.moments_attn_step(d, *[FAKE] * 5, chains, FAKE, FAKE, NULL) == fwd
