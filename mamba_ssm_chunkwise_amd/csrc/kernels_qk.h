@@ -767,26 +767,29 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
 __global__ __launch_bounds__(1024) void k_qk_sum(const float* __restrict__ part_w, int n_w, int r,
                                                  float* __restrict__ d_wq, float* __restrict__ d_wk,
                                                  const float* __restrict__ part_b, int n_b, int hr,
-                                                 float* __restrict__ d_bq, float* __restrict__ d_bk) {
+                                                 float* __restrict__ d_bq, float* __restrict__ d_bk, int cols) {
   __shared__ double red[64][17];
-  const int wb = (r + 15) / 16, x = blockIdx.y;
-  const bool isw = (int)blockIdx.x < wb;
-  const float* part = isw ? part_w : part_b;
-  const int n = isw ? n_w : n_b, w = isw ? r : hr;
-  float* out = isw ? (x ? d_wk : d_wq) : (x ? d_bk : d_bq);
-  if (out == nullptr) return;
-  const int e = ((int)blockIdx.x - (isw ? 0 : wb)) * 16 + (int)(threadIdx.x & 15), j = threadIdx.x >> 4;
-  double s = 0.0;
-  if (e < w) {
-    const float* src = part + (size_t)x * n * w + e;
+  const int wb = (r + 15) / 16, x = blockIdx.y, j = threadIdx.x >> 4;
+  for (int cb = blockIdx.x; cb < cols; cb += gridDim.x) {
+    const bool isw = cb < wb;
+    const float* part = isw ? part_w : part_b;
+    const int n = isw ? n_w : n_b, w = isw ? r : hr;
+    float* out = isw ? (x ? d_wk : d_wq) : (x ? d_bk : d_bq);
+    if (out == nullptr) continue;   // all threads alike
+    const int e = (cb - (isw ? 0 : wb)) * 16 + (int)(threadIdx.x & 15);
+    double s = 0.0;
+    if (e < w) {
+      const float* src = part + (size_t)x * n * w + e;
 #pragma unroll 8
-    for (int i = j; i < n; i += 64) s += (double)src[(size_t)i * w];
-  }
-  red[j][threadIdx.x & 15] = s;
-  __syncthreads();
-  if (j == 0 && e < w) {
-    for (int i = 1; i < 64; i++) s += red[i][threadIdx.x];
-    out[e] = (float)s;
+      for (int i = j; i < n; i += 64) s += (double)src[(size_t)i * w];
+    }
+    red[j][threadIdx.x & 15] = s;
+    __syncthreads();
+    if (j == 0 && e < w) {
+      for (int i = 1; i < 64; i++) s += red[i][threadIdx.x];
+      out[e] = (float)s;
+    }
+    __syncthreads();   // read before the next columns' sums are written
   }
 }
 

@@ -149,9 +149,10 @@ int launch_qk_sum(const QkGeo& g, const float* pw, const float* pb, int nblk, fl
                   float* d_bk, hipStream_t st) {
   if (!d_wq && !d_wk && !d_bq && !d_bk) return 0;
   ProfScope ps(KID_QK_SUM, st);
-  const unsigned cols = (unsigned)((g.r + 15) / 16 + (d_bq || d_bk ? ((int64_t)g.h * g.r + 15) / 16 : 0));
-  hipLaunchKernelGGL(k_qk_sum, dim3(cols, 2), dim3(1024), 0, st, pw, nblk * g.g, g.r, d_wq, d_wk, pb, nblk,
-                     g.h * g.r, d_bq, d_bk);
+  const int cols = (g.r + 15) / 16 + (d_bq || d_bk ? (int)(((int64_t)g.h * g.r + 15) / 16) : 0);
+  // a launch holds fewer than 2^32 threads
+  hipLaunchKernelGGL(k_qk_sum, dim3((unsigned)std::min(cols, 1 << 20), 2), dim3(1024), 0, st, pw, nblk * g.g, g.r,
+                     d_wq, d_wk, pb, nblk, g.h * g.r, d_bq, d_bk, cols);
   return check_launch();
 }
 

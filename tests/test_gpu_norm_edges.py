@@ -117,3 +117,18 @@ def test_large_angles_in_bf16(kind):
     t["rot"] = rot.expand(1, 64, 2, 8).to(BF16).contiguous()
     assert (t["rot"].abs() > 1e5).any() and (t["rot"].abs() < 1e5).any()
     _against_oracle(t, 2, kind, 1e-5)
+
+
+def test_bias_gradients_of_very_many_heads():
+    """2^26 of them: more columns than one launch of the sums has threads for. One token, no rotation:
+    each bias gradient is its cotangent."""
+    g, h, r = 8192, 524_288, 128
+    x = torch.randn(1, 1, 1, g, r, device=DEV).to(BF16)
+    w, bias = torch.ones(r, device=DEV), torch.zeros(h, r, device=DEV)
+    d_q, d_k = (torch.randn(1, 1, 1, h, r, device=DEV).to(BF16) for _ in range(2))
+    d = M.qk_desc(x, x, h, M.ROT_NONE)
+    got = M.moments_qk_bwd(d, x, x, w, w, bias, bias, None, d_q, d_k, want=("wq", "bq", "bk"))
+    assert torch.equal(got["d_bq"], d_q.float().view(h, r)) and torch.equal(got["d_bk"], d_k.float().view(h, r))
+    n = x.double() / (x.double().square().mean(-1, keepdim=True) + 1e-5).sqrt()
+    ref = (n * d_q.double().view(1, 1, 1, g, h // g, r).sum(4)).sum((0, 1, 2, 3))
+    _check("d_wq", got["d_wq"], _np(ref), TOL[F32])
