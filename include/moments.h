@@ -286,15 +286,19 @@ int moments_attn_step(const moments_attn_desc* desc, const void* xhat, const voi
  * quaternion blocks by the conjugate), for x = q and x = k alike. q and k are
  * [b,s,c,g,r] in desc->dtype, each token's c*g*r values together and tokens q_stride
  * and k_stride elements apart (0: c*g*r), so they may be columns of a wider
- * projection. w[r] and bias[h,r] (NULL: none) are float32. rot is [b,s,rot_h,a] or
- * [b,s,rot_h,J,4] in desc->dtype with rot_h = h, or 1 (all heads turn alike). qhat and
- * khat are [b,s,c,h,r]: head hi takes group hi / (h/g), with its own bias and rotation.
+ * projection; they may start at any element (rows of whole 16-byte pieces, with
+ * bases and strides alike, are read as such, others one element at a time). w[r] and
+ * bias[h,r] (NULL: none) are float32. rot is [b,s,rot_h,a] or [b,s,rot_h,J,4] in
+ * desc->dtype with rot_h = h, or 1 (all heads turn alike). All but q and k start at 16
+ * bytes. qhat and khat are [b,s,c,h,r]: head hi takes group hi / (h/g), with its own
+ * bias and rotation.
  *
  * moments_qk_bwd is the vector-Jacobian product at d_qhat, d_khat: d_q, d_k
  * [b,s,c,g,r] and d_rot in desc->dtype (dense), d_wq, d_wk[r] and d_bq, d_bk[h,r] in
  * float32 (summed over tokens in a fixed order). d_rot must be NULL without a
  * rotation, d_bq (d_bk) without that bias; any gradient may be NULL. Every position is
- * computed (there is no valid_len here). Supported: r <= 128, c <= 4, s, b, h as above. */
+ * computed (there is no valid_len here). Supported: r <= 128, c <= 4, g <= 65535, h <= 128 g,
+ * s <= 2^28, b <= 2^24, b * s <= 2^30; b, s or h may be 0. */
 typedef struct {
   int64_t b, s, c, h, g, r;
   int64_t q_stride, k_stride;    /* elements between tokens of q and of k, or 0: c*g*r */

@@ -24,7 +24,8 @@ struct QkPlan {
   size_t part_w, part_b, part_rot, ws, flag;
 };
 
-int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
+// bases: q and k start at 16 bytes (else their rows cannot be read in whole pieces).
+int make_qk_plan(const moments_qk_desc* d, QkPlan* P, bool bases) {
   if (d == nullptr) return MOMENTS_EINVAL;
   if (d->b < 0 || d->s < 0 || d->h < 0 || d->c < 1 || d->g < 1 || d->r < 1 || d->h % d->g != 0) return MOMENTS_EINVAL;
   if (d->dtype != MOMENTS_F32 && d->dtype != MOMENTS_BF16) return MOMENTS_EINVAL;
@@ -67,7 +68,7 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P) {
   // ("large"), and 2 x 2048 of two, 16 heads, r = 64, float ("small"), forward and backward.
   // Whole pieces, or, where alignment does not allow them, element by element: large 1.26 and
   // 1.66 ms against 4.4 and 10.1, small 25 and 48 us against 148 and 543.
-  P->vec = g.r % 8 == 0 && qs * tsz % 16 == 0 && ks * tsz % 16 == 0 && A % 4 == 0;
+  P->vec = bases && g.r % 8 == 0 && qs * tsz % 16 == 0 && ks * tsz % 16 == 0 && A % 4 == 0;
   // 16 lanes for rows that 8 would do: small 29 and 58 us.
   P->LPR = g.r <= 64 && P->vec ? 8 : 16;
   // Channels are held in registers; four places for two: large 2.1 and 5.5 ms, small 28 and 71 us.
@@ -144,6 +145,8 @@ int with_qk(const QkPlan& P, int rot_kind, F&& f) {
   return P.bf ? by_rot(TT<bf16>{}) : by_rot(TT<float>{});
 }
 
+bool at_element(const void* p, bool bf) { return ((uintptr_t)p & (bf ? 1 : 3)) == 0; }
+
 // The parameters' gradients from the partials of nblk workgroups a group (zeros for none).
 int launch_qk_sum(const QkGeo& g, const float* pw, const float* pb, int nblk, float* d_wq, float* d_wk, float* d_bq,
                   float* d_bk, hipStream_t st) {
@@ -183,21 +186,23 @@ int qk_bwd_empty(const QkPlan& P, void* d_q, void* d_k, float* d_wq, float* d_wk
 extern "C" {
 
 int64_t moments_qk_workspace_size(const moments_qk_desc* desc) {
-  QkPlan P;
-  const int rc = make_qk_plan(desc, &P);
+  QkPlan P, U;   // where q and k start is not known here
+  const int rc = make_qk_plan(desc, &P, true);
   if (rc != 0) return rc;
-  return P.empty ? 0 : (int64_t)P.ws;
+  MOM_TRY(make_qk_plan(desc, &U, false));
+  return P.empty ? 0 : (int64_t)std::max(P.ws, U.ws);
 }
 
 int moments_qk_fwd(const moments_qk_desc* desc, const void* q, const void* k, const float* wq, const float* wk,
                    const float* bq, const float* bk, const void* rot, void* qhat, void* khat, void* stream) {
   QkPlan P;
-  MOM_TRY(make_qk_plan(desc, &P));
+  MOM_TRY(make_qk_plan(desc, &P, aligned16(q) && aligned16(k)));
   const QkGeo& g = P.g;
   if (P.empty || g.s == 0) return 0;
   if (!q || !k || !wq || !wk || !qhat || !khat) return MOMENTS_EINVAL;
   if ((desc->rot_kind == MOMENTS_ROT_NONE) != (rot == nullptr)) return MOMENTS_EINVAL;
-  const void* ptrs[] = {q, k, wq, wk, bq, bk, rot, qhat, khat};
+  if (!at_element(q, P.bf) || !at_element(k, P.bf)) return MOMENTS_EINVAL;
+  const void* ptrs[] = {wq, wk, bq, bk, rot, qhat, khat};
   for (const void* p : ptrs)
     if (p != nullptr && !aligned16(p)) return MOMENTS_EINVAL;
   hipStream_t st = (hipStream_t)stream;
@@ -217,14 +222,15 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
                    void* d_q, void* d_k, float* d_wq, float* d_wk, float* d_bq, float* d_bk, void* d_rot,
                    void* workspace, size_t workspace_bytes, void* stream) {
   QkPlan P;
-  MOM_TRY(make_qk_plan(desc, &P));
+  MOM_TRY(make_qk_plan(desc, &P, aligned16(q) && aligned16(k)));
   const QkGeo& g = P.g;
   if (P.empty) return qk_bwd_empty(P, d_q, d_k, d_wq, d_wk, d_bq, d_bk, d_rot, (hipStream_t)stream);
   if (g.s > 0 && (!q || !k || !wq || !wk || !d_qhat || !d_khat)) return MOMENTS_EINVAL;
   if (g.s > 0 && (desc->rot_kind == MOMENTS_ROT_NONE) != (rot == nullptr)) return MOMENTS_EINVAL;
   if (desc->rot_kind == MOMENTS_ROT_NONE && d_rot != nullptr) return MOMENTS_EINVAL;
   if ((bq == nullptr && d_bq != nullptr) || (bk == nullptr && d_bk != nullptr)) return MOMENTS_EINVAL;
-  const void* ptrs[] = {q, k, wq, wk, bq, bk, rot, d_qhat, d_khat, d_q, d_k, d_wq, d_wk, d_bq, d_bk, d_rot, workspace};
+  if (!at_element(q, P.bf) || !at_element(k, P.bf)) return MOMENTS_EINVAL;
+  const void* ptrs[] = {wq, wk, bq, bk, rot, d_qhat, d_khat, d_q, d_k, d_wq, d_wk, d_bq, d_bk, d_rot, workspace};
   for (const void* p : ptrs)
     if (p != nullptr && !aligned16(p)) return MOMENTS_EINVAL;
   if (workspace == nullptr || workspace_bytes < P.ws) return MOMENTS_EWORKSPACE;

@@ -132,3 +132,19 @@ def test_bias_gradients_of_very_many_heads():
     n = x.double() / (x.double().square().mean(-1, keepdim=True) + 1e-5).sqrt()
     ref = (n * d_q.double().view(1, 1, 1, g, h // g, r).sum(4)).sum((0, 1, 2, 3))
     _check("d_wq", got["d_wq"], _np(ref), TOL[F32])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("r,at", [(45, (0, 45)), (24, (3, 29)), (128, (1, 130)), (16, (8, 25))])
+def test_columns_that_start_at_any_element(dtype, r, at):
+    """Queries and keys cut out of one projection: the base need not be aligned either."""
+    t = _make(2, 9, 1, 2, 1, r, M.ROT_PAIRWISE, 4, dtype, seed=r)
+    wide = torch.randn(2, 9, at[1] + r + 3, device=DEV).to(dtype)
+    for n, lo in zip(("q", "k"), at):
+        t[n] = wide[:, :, lo:lo + r].view(2, 9, 1, 1, r)
+    print(f"[case] r={r} at={at} {dtype}: {t['q'].data_ptr() % 16} {t['k'].data_ptr() % 16}", flush=True)
+    hats, got = _against_oracle(t, 2, M.ROT_PAIRWISE, 1e-5)
+    own = dict(t, q=t["q"].contiguous(), k=t["k"].contiguous())      # aligned rows of their own
+    hats2, got2 = _run(own, 2, M.ROT_PAIRWISE, 1e-5)
+    for a, b in zip(hats, hats2):
+        _check("hat", a, _np(b), TOL[dtype])

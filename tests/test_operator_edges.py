@@ -63,3 +63,15 @@ def test_sizes_that_a_launch_cannot_hold(p, chains, fwd, bwd):
     if fwd != 0:
         assert lib.moments_attn_fwd(d, *[FAKE] * 7, FAKE, BIG, NULL) == fwd
         assert lib.moments_attn_step(d, *[FAKE] * 5, chains, FAKE, FAKE, NULL) == fwd
+
+
+def test_queries_between_elements_are_refused():
+    lib, d = _lib.load(), ctypes.byref(_qk())
+    for at, code in ((2, -1), (1, -1)):
+        args = [ctypes.c_void_p((1 << 20) + at)] + [FAKE] * 8
+        assert lib.moments_qk_fwd(d, *args, NULL) == code
+        assert lib.moments_qk_fwd(d, FAKE, args[0], *[FAKE] * 7, NULL) == code
+    for i in range(2, 9):      # all the others start at 16 bytes
+        args = [FAKE] * 9
+        args[i] = ctypes.c_void_p((1 << 20) + 8)
+        assert lib.moments_qk_fwd(d, *args, NULL) == -1
