@@ -50,7 +50,8 @@
  * wait for the stream, and return MOMENTS_ENONFINITE if one holds a NaN or an
  * infinity (the pages sanitise m2 and m1 at the end of moments_phys_fwd,
  * "recalculated.rs" source page; the sanitiser's body is not on the pages and
- * is read as this check). The flag lives in the last 256 bytes of the workspace.
+ * is read as this check). The flag lives in the last 256 bytes of the workspace, or
+ * with the library where the call has none.
  */
 #ifndef MOMENTS_H
 #define MOMENTS_H

@@ -25,7 +25,7 @@ struct AttnPlan {
   bool wide;    // 128 rows of p a workgroup (bf16, p > 64), else 64
   int items;    // chains times p tiles
   size_t seg_dec, save, seg_loc_b, seg_dec_b, part_q, part_k, part_da;  // workspace offsets (seg_loc at 0)
-  size_t ws_fwd, ws_bwd, flag_fwd, flag_bwd, saved;
+  size_t ws_fwd, ws_bwd, flag_bwd, saved;
 };
 
 // Segments a chain's walk is split into: one when the chains alone nearly fill the `want`
@@ -93,9 +93,7 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   if (g.nseg > 1) o = align256(o + (size_t)P->items * g.nseg * tiles * 4);
   P->seg_dec = o;
   if (g.nseg > 1) o = align256(o + (size_t)P->items * g.nseg * 8);
-  // the finiteness check's flag: only calls with one segment and no check need no workspace
-  P->flag_fwd = o;
-  P->ws_fwd = o > 0 || check_finite_on() ? o + 256 : 0;
+  P->ws_fwd = o;   // nothing with one segment
   P->saved = (size_t)P->items * g.NK * tiles * tsz;
   P->save = o;
   o = align256(o + P->saved);
@@ -193,7 +191,7 @@ int attn_fwd(const moments_attn_desc* desc, const void* x, const void* k, const 
   if (check_finite_on()) {
     const OutSpan outs[] = {{y, (size_t)P.g.b * P.g.s * P.g.c * P.g.h * P.g.p, !P.bf},
                             {h_last, (size_t)P.g.b * P.g.h * P.g.p * P.g.r, true}};
-    return check_finite(outs, 2, ws + P.flag_fwd, st);
+    return check_finite(outs, 2, nullptr, st);
   }
   return 0;
 }

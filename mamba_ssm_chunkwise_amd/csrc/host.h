@@ -75,7 +75,8 @@ template <typename T> struct TT { using type = T; };
 
 // Debug finiteness check, on when the environment variable MOMENTS_CHECK_FINITE
 // is set to anything but "" or "0". It waits for the stream and returns
-// MOMENTS_ENONFINITE if any listed output holds a NaN or an infinity.
+// MOMENTS_ENONFINITE if any listed output holds a NaN or an infinity. flag_mem: 4 bytes of the
+// call's workspace, or nullptr where it has none (a flag of the library's own, under a lock).
 struct OutSpan {
   const void* p;
   size_t n;

@@ -690,8 +690,20 @@ bool check_finite_on() {
   return e != nullptr && e[0] != 0 && !(e[0] == '0' && e[1] == 0);
 }
 
+// Calls that have no workspace share one flag of the library's own per device: one at a time.
+static __device__ int own_flag;
+static std::mutex own_flag_mu;
+
 int check_finite(const OutSpan* outs, int nout, unsigned char* flag_mem, hipStream_t st) {
+  std::unique_lock<std::mutex> one(own_flag_mu, std::defer_lock);
   int* flag = (int*)flag_mem;
+  if (flag == nullptr) {
+    one.lock();
+    void* p = nullptr;
+    const hipError_t e = hipGetSymbolAddress(&p, HIP_SYMBOL(own_flag));
+    if (e != hipSuccess) return hip_fail(e);
+    flag = (int*)p;
+  }
   hipLaunchKernelGGL(k_flag_clear, dim3(1), dim3(NTH), 0, st, flag);
   MOM_TRY(check_launch());
   for (int i = 0; i < nout; i++) {

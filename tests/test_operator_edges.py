@@ -75,3 +75,14 @@ def test_queries_between_elements_are_refused():
         args = [FAKE] * 9
         args[i] = ctypes.c_void_p((1 << 20) + 8)
         assert lib.moments_qk_fwd(d, *args, NULL) == -1
+
+
+@pytest.mark.parametrize("s", [5, 64, 5000])
+def test_the_finite_check_does_not_change_the_workspace(monkeypatch, s):
+    """A workspace sized before MOMENTS_CHECK_FINITE is set holds for the calls after it."""
+    lib, d = _lib.load(), ctypes.byref(_attn(b=1, h=1, g=1, s=s, valid_len=s))
+    sizes = lambda: [lib.moments_attn_workspace_size(d, i) for i in (0, 1)]  # noqa: E731
+    monkeypatch.delenv("MOMENTS_CHECK_FINITE", raising=False)
+    before = sizes()
+    monkeypatch.setenv("MOMENTS_CHECK_FINITE", "1")
+    assert sizes() == before
