@@ -292,7 +292,7 @@ int moments_attn_step(const moments_attn_desc* desc, const void* xhat, const voi
  * bias[h,r] (NULL: none) are float32. rot is [b,s,rot_h,a] or [b,s,rot_h,J,4] in
  * desc->dtype with rot_h = h, or 1 (all heads turn alike). All but q and k start at 16
  * bytes. qhat and khat are [b,s,c,h,r]: head hi takes group hi / (h/g), with its own
- * bias and rotation.
+ * bias and rotation. Ownership, errors and MOMENTS_CHECK_FINITE are those stated above.
  *
  * moments_qk_bwd is the vector-Jacobian product at d_qhat, d_khat: d_q, d_k
  * [b,s,c,g,r] and d_rot in desc->dtype (dense), d_wq, d_wk[r] and d_bq, d_bk[h,r] in

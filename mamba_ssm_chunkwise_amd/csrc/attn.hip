@@ -371,7 +371,13 @@ int moments_attn_step(const moments_attn_desc* desc, const void* xhat, const voi
     if (g.r <= 64) return go(tt, IC<16>{}, IC<4>{});
     return go(tt, IC<32>{}, IC<8>{});
   };
-  return P.bf ? by_r(TT<bf16>{}) : by_r(TT<float>{});
+  MOM_TRY(P.bf ? by_r(TT<bf16>{}) : by_r(TT<float>{}));
+  if (check_finite_on()) {
+    // y tells of the states too: a value that is not finite spoils its row's sum
+    const OutSpan outs[] = {{y, (size_t)g.b * g.c * g.h * g.p, !P.bf}};
+    return check_finite(outs, 1, nullptr, st);
+  }
+  return 0;
 }
 
 }  // extern "C"

@@ -206,7 +206,7 @@ int moments_qk_fwd(const moments_qk_desc* desc, const void* q, const void* k, co
   for (const void* p : ptrs)
     if (p != nullptr && !aligned16(p)) return MOMENTS_EINVAL;
   hipStream_t st = (hipStream_t)stream;
-  return with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto hpp, auto vec) -> int {
+  MOM_TRY(with_qk(P, desc->rot_kind, [&](auto tt, auto lpr, auto rk, auto cc, auto hb, auto hpp, auto vec) -> int {
     using T = typename decltype(tt)::type;
     constexpr int LPR = decltype(lpr)::value, ROT = decltype(rk)::value, C = decltype(cc)::value;
     ProfScope ps(KID_QK_FWD, st);
@@ -214,7 +214,13 @@ int moments_qk_fwd(const moments_qk_desc* desc, const void* q, const void* k, co
                        dim3((unsigned)P.nfwd, (unsigned)g.g), dim3(QKT), 0, st, g, (const T*)q, (const T*)k, wq, wk,
                        bq, bk, (const T*)rot, (T*)qhat, (T*)khat);
     return check_launch();
-  });
+  }));
+  if (check_finite_on()) {
+    const size_t n = (size_t)g.b * g.s * g.c * g.h * g.r;
+    const OutSpan outs[] = {{qhat, n, !P.bf}, {khat, n, !P.bf}};
+    return check_finite(outs, 2, nullptr, st);
+  }
+  return 0;
 }
 
 int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, const float* wq, const float* wk,

@@ -6,10 +6,11 @@ import pytest
 import torch
 
 import mamba_ssm_chunkwise_amd as M
+from mamba_ssm_chunkwise_amd import _lib
 from test_gpu_attn import BF16, DEV, F32, _make
 
 pytestmark = pytest.mark.gpu
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 INPUTS = ("xhat", "bhat", "qhat", "da")
 
 
@@ -73,3 +74,18 @@ def test_the_largest_launches():
     x, k, da, h0 = x[:n, :0], k[:n, :0], da[:n, :0], h0[:n].contiguous()
     got = M.moments_attn_bwd(M.attn_desc(x, k), x, k, k, da, h0, x, h0)
     assert torch.equal(got["d_h0"], h0)
+
+
+def test_finite_check_of_single_tokens(monkeypatch):
+    t = _make(3, 1, 1, 2, 2, 16, 16, BF16, seed=2)
+    a = _args(t)
+    d = M.attn_desc(a[0], a[1])
+    pool = torch.full((4, 2, 16, 16), NAN, device=DEV)      # a slot that no sequence has is not looked at
+    pool[:2] = 0.0
+    slots = torch.tensor([1, -1, 0], dtype=torch.int32, device=DEV)
+    monkeypatch.setenv("MOMENTS_CHECK_FINITE", "1")
+    M.moments_attn_step(d, *a, pool, slots)
+    pool[0, 1, 3, 5] = INF
+    with pytest.raises(M.MomentsError) as e:
+        M.moments_attn_step(d, *a, pool, slots)
+    assert e.value.code == _lib.ENONFINITE

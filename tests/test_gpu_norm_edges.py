@@ -148,3 +148,15 @@ def test_columns_that_start_at_any_element(dtype, r, at):
     hats2, got2 = _run(own, 2, M.ROT_PAIRWISE, 1e-5)
     for a, b in zip(hats, hats2):
         _check("hat", a, _np(b), TOL[dtype])
+
+
+def test_finite_check_of_the_forward(monkeypatch):
+    t = _make(1, 7, 1, 2, 2, 24, M.ROT_PAIRWISE, 4, F32, seed=2)
+    d = M.qk_desc(t["q"], t["k"], 2, M.ROT_PAIRWISE, rot=t["rot"])
+    args = [t[n] for n in NAMES]
+    monkeypatch.setenv("MOMENTS_CHECK_FINITE", "1")
+    M.moments_qk_fwd(d, *args)
+    t["k"][0, 3, 0, 1, 5] = float("inf")
+    with pytest.raises(M.MomentsError) as e:
+        M.moments_qk_fwd(d, *args)
+    assert e.value.code == _lib.ENONFINITE
