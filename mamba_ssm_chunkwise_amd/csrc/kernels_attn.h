@@ -68,7 +68,8 @@ struct Segment {
 // difference. A decay below e^-110 is zero in fp32; da is clamped there (also
 // -inf, a cleared state) so that later differences stay finite. NaN stays NaN.
 constexpr double kLog2e = 1.4426950408889634;
-__device__ __forceinline__ double log2_decay(float da) { return (double)(da < -110.0f ? -110.0f : da) * kLog2e; }
+constexpr float kCleared = -110.0f;
+__device__ __forceinline__ double log2_decay(float da) { return (double)(da < kCleared ? kCleared : da) * kLog2e; }
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ---- types ------------------------------------------------------------------
@@ -875,9 +876,13 @@ __global__ __launch_bounds__(256) void k_attn_step(AttnGeo g, int nslots, const 
   f4 S[NB];
 #pragma unroll
   for (int i = 0; i < NB; i++) S[i] = ld_state4(st, g.p, g.r, row0 + i * RPW, r0);
-  const float dec = ex2((float)log2_decay(to_f(da[chain])));
+  // a decay of zero clears the state whatever the slot holds (0 * NaN would not)
+  const float log_dec = to_f(da[chain]), dec = ex2((float)log2_decay(log_dec));
+  const bool cleared = log_dec < kCleared;
 #pragma unroll
-  for (int i = 0; i < NB; i++) S[i] *= dec;
+  for (int i = 0; i < NB; i++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) S[i][e] = cleared ? 0.0f : S[i][e] * dec;
   for (int c = 0; c < g.c; c++) {
     const T* kr = k + (((size_t)bi * g.c + c) * g.g + gi) * g.r;
     const T* xr = x + (((size_t)bi * g.c + c) * g.h + hi) * g.p;

@@ -2,12 +2,14 @@
 that a caller uses twice, empty inputs, the finite check of single tokens.
 
 Tolerances are those of test_gpu_attn.py."""
+import numpy as np
 import pytest
 import torch
 
 import mamba_ssm_chunkwise_amd as M
 from mamba_ssm_chunkwise_amd import _lib
-from test_gpu_attn import BF16, DEV, F32, _make
+from oracle import attn_seq
+from test_gpu_attn import BF16, DEV, F32, TOL, _check, _make, _np
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -89,3 +91,23 @@ def test_finite_check_of_single_tokens(monkeypatch):
     with pytest.raises(M.MomentsError) as e:
         M.moments_attn_step(d, *a, pool, slots)
     assert e.value.code == _lib.ENONFINITE
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("c,h,g,p,r", [(1, 2, 1, 16, 24), (3, 2, 2, 70, 45), (2, 1, 1, 130, 128)])
+def test_single_tokens_start_anew_on_a_slot_that_holds_anything(dtype, c, h, g, p, r):
+    """da = -inf (or the type's lowest value): the slot's NaN and infinities are gone."""
+    t = _make(3, 1, c, h, g, p, r, dtype, seed=p)
+    t["da"][0], t["da"][1], t["da"][2] = -INF, torch.finfo(dtype).min, -0.5
+    a = _args(t)
+    pool = torch.full((3, h, p, r), NAN, device=DEV)
+    pool[1] = INF
+    pool[2] = 0.25
+    ref = pool.clone()
+    ref[:2] = 0.0
+    y = M.moments_attn_step(M.attn_desc(a[0], a[1]), *a, pool)
+    o = [_np(v) for v in a]
+    o[3] = np.maximum(o[3], -1e4)
+    ry, rs = attn_seq.attn_fwd(*o, _np(ref))
+    _check("y", y, ry, TOL[dtype])
+    _check("state", pool, rs, TOL[F32])
