@@ -65,11 +65,13 @@ struct Segment {
 
 // Decays. Sums of da are kept in units of log2 as a float and its remainder
 // (from a sum in double), so that differences of long sums keep 24 bits of the
-// difference. A decay below e^-110 is zero in fp32; da is clamped there (also
-// -inf, a cleared state) so that later differences stay finite. NaN stays NaN.
+// difference. A decay below e^-110 is zero in fp32: a cleared state (da = -inf among it).
+// Its place in the sums is taken by kReset, so that later differences stay finite and no
+// growth that fp32 can hold makes up for it. NaN stays NaN.
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kCleared = -110.0f;
-__device__ __forceinline__ double log2_decay(float da) { return (double)(da < kCleared ? kCleared : da) * kLog2e; }
+constexpr double kReset = -150000.0;   // in log2 units; a chunk of other decays sums to -1.1e4 at least
+__device__ __forceinline__ double log2_decay(float da) { return da < kCleared ? kReset : (double)da * kLog2e; }
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ---- types ------------------------------------------------------------------

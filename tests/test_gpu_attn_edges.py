@@ -111,3 +111,18 @@ def test_single_tokens_start_anew_on_a_slot_that_holds_anything(dtype, c, h, g, 
     ry, rs = attn_seq.attn_fwd(*o, _np(ref))
     _check("y", y, ry, TOL[dtype])
     _check("state", pool, rs, TOL[F32])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_cleared_state_is_gone_however_much_later_decays_grow(dtype):
+    """A state of 1e30, cleared, then log-decays of +1 on zero values: nothing comes back."""
+    t = _make(1, 2200, 1, 1, 1, 16, 24, dtype, seed=8)
+    t["xhat"].zero_()
+    t["h0"][:] = 1e30
+    t["da"].zero_()
+    t["da"][:, 3:70] = 1.0
+    t["da"][:, 1] = -INF
+    a = _args(t)
+    y, last = M.moments_attn_fwd(M.attn_desc(a[0], a[1]), *a, t["h0"])
+    assert torch.count_nonzero(y[:, 1:]) == 0 and torch.count_nonzero(last) == 0
+    assert torch.count_nonzero(y[:, 0]) > 0
