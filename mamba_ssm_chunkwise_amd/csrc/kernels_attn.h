@@ -71,6 +71,7 @@ struct Segment {
 constexpr double kLog2e = 1.4426950408889634;
 constexpr float kCleared = -110.0f;
 constexpr double kReset = -150000.0;   // in log2 units; a chunk of other decays sums to -1.1e4 at least
+constexpr float kGone = -1e5f;         // sums below hold a cleared state
 __device__ __forceinline__ double log2_decay(float da) { return da < kCleared ? kReset : (double)da * kLog2e; }
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -322,6 +323,7 @@ struct DecayTab {
   float hi[64], lo[64];   // a_u in log2 units: hi + lo
   float start[64];        // e^{a_u}
   float end[64];          // e^{a_end - a_u}
+  float own[64];          // log2 decay of the token that the row opens (kReset: cleared); 0 elsewhere
   double total;           // a_end in log2 units
   double pad;             // tiles behind it start at 16 bytes
 };
@@ -355,6 +357,7 @@ __device__ __forceinline__ void decay_table(DecayTab* t, double v, int lane) {
   t->lo[lane] = (float)(a - hi);
   t->start[lane] = ex2(hi);
   t->end[lane] = ex2((float)(e - a));
+  t->own[lane] = (float)v;
   if (lane == 0) t->total = e;
 }
 
@@ -484,6 +487,70 @@ __device__ __forceinline__ void state_update(f4 (&H)[PW][RT], const T* ks, const
         for (int rt = 0; rt < RT; rt++)
 #pragma unroll
           for (int pw = 0; pw < PW; pw++) H[pw][rt] = mma32(kf[m][rt], xf[m][pw].piece(i), H[pw][rt]);
+  }
+}
+
+// A chunk token by token, for a wave whose values are not all finite: the matrix products
+// give every row of a chunk its share of every other one, and a share of zero (a later
+// token's, or one from before a cleared state) is NaN where the other holds a NaN or an
+// infinity. Here a value meets only what reads it. Leaves y in `a` and the chunk's last state
+// in H. Finite values never come here; 128 chains of 4096 rows from states of NaN, every chunk
+// of them: 1180 us instead of 104.
+template <typename T, int RT, int PW>
+__device__ __forceinline__ void walk_tokens(f4 (&H)[PW][RT], f4 (&a)[AV<T>::L / 16][PW], const T* ks, const T* xs,
+                                            const T* qs, const float* own, int c, int nrows, int wave, int lane) {
+  using LD = LdsA<T, RT, PW>;
+  const int ln = lane & 15, lq = lane >> 4;
+#pragma unroll 1
+  for (int u0 = 0; u0 < nrows; u0 += c) {
+    const float log_dec = own[u0], dec = ex2(log_dec);
+    const bool cleared = log_dec < kGone;
+#pragma unroll
+    for (int pw = 0; pw < PW; pw++)
+#pragma unroll
+      for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) H[pw][rt][e] = cleared ? 0.0f : H[pw][rt][e] * dec;
+#pragma unroll 1
+    for (int u = u0; u < u0 + c; u++) {
+      float x[PW];
+#pragma unroll
+      for (int pw = 0; pw < PW; pw++) {
+        const int col = 16 * (wave * PW + pw) + ln;
+        x[pw] = to_f(xs[u * LD::PP + 4 * ((col >> 2) ^ swz<T, LD::PC>(u)) + (col & 3)]);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; rt++) {
+        const f4 kv = quad_f(ld_quad<LD::RC>(ks, u, 4 * rt + lq));
+#pragma unroll
+        for (int pw = 0; pw < PW; pw++) H[pw][rt] += x[pw] * kv;
+      }
+    }
+#pragma unroll 1
+    for (int u = u0; u < u0 + c; u++) {
+      float v[PW];
+#pragma unroll
+      for (int pw = 0; pw < PW; pw++) v[pw] = 0.0f;
+#pragma unroll
+      for (int rt = 0; rt < RT; rt++) {
+        const f4 qv = quad_f(ld_quad<LD::RC>(qs, u, 4 * rt + lq));
+#pragma unroll
+        for (int pw = 0; pw < PW; pw++)
+          v[pw] += H[pw][rt][0] * qv[0] + H[pw][rt][1] * qv[1] + H[pw][rt][2] * qv[2] + H[pw][rt][3] * qv[3];
+      }
+      // the sums of state rows n stand in lanes n; they go to lane (q, u % 16) for rows 4q + e
+#pragma unroll
+      for (int pw = 0; pw < PW; pw++) {
+        v[pw] = col4_sum(v[pw]);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const float y = __shfl(v[pw], 4 * lq + e);
+#pragma unroll
+          for (int ut = 0; ut < AV<T>::L / 16; ut++)
+            if (ut == (u >> 4) && ln == (u & 15)) a[ut][pw][e] = y;
+        }
+      }
+    }
   }
 }
 
@@ -669,6 +736,7 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
     }
     const double total = tab->total;
     acc_dec += total;
+    bool apart = false;   // this wave's values are not all finite: token by token
 
     if constexpr (MODE == 0) {
       // scores s[u][j] = (q[u].k[j]) e^{a_u - a_j} in 16x16 tiles (columns u)
@@ -775,13 +843,24 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
 #pragma unroll
             for (int pw = 0; pw < PW; pw++) a[ut][pw] = mma32(xf[m][pw], sf[m][ut], a[ut][pw]);
       }
+      // Where the state that entered, a row of x or a row of k is not finite, no column of the
+      // chunk's last row is (it reads them all, if only with weights of zero): the check of 4 PW
+      // values finds them.
+      float nan = 0.0f;
+#pragma unroll
+      for (int pw = 0; pw < PW; pw++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) nan = fmaf(a[NT - 1][pw][e], 0.0f, nan);
+      apart = __any(nan != 0.0f);
+      if (__builtin_expect(apart, 0)) walk_tokens<T, RT, PW>(H, a, ks, xs, qs, tab->own, g.c, nrows, wave, lane);
       const RowOut<T, VEC> yo(y + (row0 + u0) * xst + (size_t)hi * g.p + p0, xst, nrows, pn);
 #pragma unroll
       for (int ut = 0; ut < NT; ut++)
 #pragma unroll
         for (int pw = 0; pw < PW; pw++) yo.put(16 * ut + ln, 16 * (wave * PW + pw) + 4 * lq, a[ut][pw]);
     }
-    state_update<T, RT, PW>(H, ks, xs, MODE == 2 ? tab->start : tab->end, ex2((float)total), wave, fresh(lane));
+    if (!apart)
+      state_update<T, RT, PW>(H, ks, xs, MODE == 2 ? tab->start : tab->end, ex2((float)total), wave, fresh(lane));
   }
 
   if constexpr (MODE == 0) {

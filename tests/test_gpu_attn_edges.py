@@ -126,3 +126,47 @@ def test_a_cleared_state_is_gone_however_much_later_decays_grow(dtype):
     y, last = M.moments_attn_fwd(M.attn_desc(a[0], a[1]), *a, t["h0"])
     assert torch.count_nonzero(y[:, 1:]) == 0 and torch.count_nonzero(last) == 0
     assert torch.count_nonzero(y[:, 0]) > 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("c,p,r,at", [(1, 32, 40, 40), (3, 24, 32, 15), (1, 37, 45, 10), (2, 128, 128, 29),
+                                      (4, 70, 64, 3)])
+@pytest.mark.parametrize("name", ["xhat", "bhat", "qhat", "da"])
+@pytest.mark.parametrize("v", [NAN, INF, -INF])
+def test_later_tokens_do_not_reach_earlier_ones(dtype, c, p, r, at, name, v):
+    """A NaN or an infinity at a token: the outputs before it are what they are without it."""
+    if name == "da" and v == -INF:
+        pytest.skip("a cleared state")
+    print(f"[case] {name} {v} c={c} p={p} r={r} at={at} {dtype}", flush=True)
+    t = _make(1, at + 50, c, 2, 2, p, r, dtype, seed=at)
+    a = _args(t)
+    d = M.attn_desc(a[0], a[1])
+    clean = [v_.clone() for v_ in a]
+    t[name][:, at] = v
+    y, _ = M.moments_attn_fwd(d, *a, t["h0"])
+    o = [_np(x[:, :at]) for x in clean]
+    ry, _ = attn_seq.attn_fwd(*o, _np(t["h0"]))
+    _check("y", y[:, :at], ry, TOL[dtype])
+    # and from there on it is seen: no output that reads the value is finite (a NaN or an infinite
+    # query is seen by its own token alone)
+    seen = y[:, at] if name == "qhat" else y[:, at:]
+    assert not torch.isfinite(seen).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_bad_value_stays_in_its_state_row(dtype):
+    """x[t, 0, 0, 7] = NaN reaches y[t:, :, 0, 7] and the state's row 7, nothing else."""
+    t = _make(1, 100, 1, 2, 1, 72, 64, dtype, seed=7)
+    a = _args(t)
+    d = M.attn_desc(a[0], a[1])
+    clean, last0 = M.moments_attn_fwd(d, *a, t["h0"])
+    a[0][0, 50, 0, 0, 7] = NAN
+    y, last = M.moments_attn_fwd(d, *a, t["h0"])
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[:, 50:, :, 0, 7] = True
+    assert torch.isnan(y[hit]).all() and torch.isfinite(y[~hit]).all()
+    _check("y", torch.where(hit, 0.0, y.float()), _np(torch.where(hit, 0.0, clean.float())), 2 * TOL[dtype])
+    hit = torch.zeros_like(last, dtype=torch.bool)
+    hit[:, 0, 7] = True
+    assert torch.isnan(last[hit]).all()
+    _check("h_last", torch.where(hit, 0.0, last), _np(torch.where(hit, 0.0, last0)), 2 * TOL[F32])
