@@ -227,7 +227,7 @@ int moments_rot_bwd(const moments_desc* desc, const void* inc, const void* d_rot
  * desc->valid_len and valid_lens are those of moments_desc: rows of y, and of every
  * gradient, past a sequence's length are zero, whatever the inputs hold there; a
  * sequence of length 0 leaves h_last = h0. da below -110 (-inf among it) is a decay
- * of exactly zero: a token with da = -inf starts its sequence anew.
+ * of exactly zero: a token with da = -inf starts its sequence anew, whatever stood before.
  * Values that are not finite: a NaN or an infinity at a valid token reaches only the y and the
  * states that read it (later tokens, of its state row where it stands in xhat). The gradients
  * do not keep rows apart: it may reach those of its whole chunk and sequence.

@@ -268,14 +268,20 @@ struct Stage {
       v[i] = make_uint4(x[0], x[1], x[2], x[3]);
     }
   }
-  __device__ __forceinline__ void store(T* t) const {
+  // `drop`: the rows that become zeros, whatever they hold.
+  struct NoRow {
+    __device__ __forceinline__ bool operator()(int) const { return false; }
+  };
+  template <typename F = NoRow>
+  __device__ __forceinline__ void store(T* t, F drop = F{}) const {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int e = i * NT + (int)threadIdx.x;
-      st_piece<COLS>(t, e / PR, e % PR, v[i]);
+      st_piece<COLS>(t, e / PR, e % PR, drop(e / PR) ? make_uint4(0, 0, 0, 0) : v[i]);
     }
   }
-  __device__ __forceinline__ void direct(T* t, Rsrc r, int n) const {
+  template <typename F = NoRow>
+  __device__ __forceinline__ void direct(T* t, Rsrc r, int n, F drop = F{}) const {
     static_assert(sizeof(T) == 2, "bf16 elements");
     const int c0 = (int)threadIdx.x % PR * PE;
     unsigned short x[N][PE];
@@ -287,9 +293,9 @@ struct Stage {
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int e = i * NT + (int)threadIdx.x;
-      st_piece<COLS>(t, e / PR, e % PR,
-                     make_uint4(x[i][0] | (unsigned)x[i][1] << 16, x[i][2] | (unsigned)x[i][3] << 16,
-                                x[i][4] | (unsigned)x[i][5] << 16, x[i][6] | (unsigned)x[i][7] << 16));
+      const uint4 v8 = make_uint4(x[i][0] | (unsigned)x[i][1] << 16, x[i][2] | (unsigned)x[i][3] << 16,
+                                  x[i][4] | (unsigned)x[i][5] << 16, x[i][6] | (unsigned)x[i][7] << 16);
+      st_piece<COLS>(t, e / PR, e % PR, drop(e / PR) ? make_uint4(0, 0, 0, 0) : v8);
     }
   }
 };
@@ -349,8 +355,15 @@ __device__ __forceinline__ double lane63(double v) {
   const unsigned lo = __builtin_amdgcn_readlane((int)b, 63), hi = __builtin_amdgcn_readlane((int)(b >> 32), 63);
   return __builtin_bit_cast(double, ((long long)hi << 32) | lo);
 }
-// v: log2 decay of row u = lane (zero where the row does not open a token).
+// v: log2 decay of row u = lane (zero where the row does not open a token). FORGET: for what the
+// chunk leaves behind it alone: log-decays that are not finite and stand before its last
+// cleared state are left out.
+template <bool FORGET = false>
 __device__ __forceinline__ void decay_table(DecayTab* t, double v, int lane) {
+  if constexpr (FORGET) {
+    const unsigned long long resets = __ballot(v == kReset);
+    if (resets != 0 && lane < 63 - __builtin_clzll(resets) && !(fabs(v) < 1e30)) v = 0.0;
+  }
   const double a = wave_sum_incl(v), e = lane63(a);
   const float hi = (float)a;
   t->hi[lane] = hi;
@@ -687,7 +700,7 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
   if (nlive > n0) {
     if (wave == TWAVE) {
       fetch_da(chunk(n0));
-      decay_table(tabs, log2_decay(to_f(dnext)), lane);
+      decay_table<MODE == 1>(tabs, log2_decay(to_f(dnext)), lane);
       if (n0 + 1 < nlive) fetch_da(chunk(n0 + 1));
     }
     fetch(chunk(n0));
@@ -702,15 +715,23 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
     const size_t u0 = (size_t)t0 * g.c;
     const DecayTab* tab = tabs + ((i - n0) & 1);
     __syncthreads();   // the last chunk's tiles have been read
-    if constexpr (VEC || sizeof(T) == 4) {
-      sk.store(ks);
-      sx.store(xs);
-      if constexpr (MODE == 0) sq.store(qs);
-    } else {
-      sk.direct(ks, row_rsrc(kb + u0 * kst, kst, nrows, g.r), g.r);
-      sx.direct(xs, row_rsrc(xb + u0 * xst, xst, nrows, pn), pn);
-      if constexpr (MODE == 0) sq.direct(qs, row_rsrc(qb + u0 * kst, kst, nrows, g.r), g.r);
-    }
+    auto to_lds = [&](auto... drop) {
+      if constexpr (VEC || sizeof(T) == 4) {
+        sk.store(ks, drop...);
+        sx.store(xs, drop...);
+        if constexpr (MODE == 0) sq.store(qs);
+      } else {
+        sk.direct(ks, row_rsrc(kb + u0 * kst, kst, nrows, g.r), g.r, drop...);
+        sx.direct(xs, row_rsrc(xb + u0 * xst, xst, nrows, pn), pn, drop...);
+        if constexpr (MODE == 0) sq.direct(qs, row_rsrc(qb + u0 * kst, kst, nrows, g.r), g.r);
+      }
+    };
+    // In a chunk that clears the state, what stood before is dropped: weights of zero would not
+    // do where it is not finite (MODE 0 sees that in y).
+    const float end = (float)tab->total;
+    const bool clears = MODE == 1 && end < kGone;
+    if (clears) to_lds([&](int u) { return end - tab->hi[u] < kGone; });
+    else to_lds();
     __syncthreads();
     if constexpr (MODE != 2) {
       if (save != nullptr) {
@@ -730,12 +751,12 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
     if (i + 1 < nlive) {
       fetch(chunk(i + 1));
       if (wave == TWAVE) {
-        decay_table(tabs + ((i + 1 - n0) & 1), log2_decay(to_f(dnext)), lane);
+        decay_table<MODE == 1>(tabs + ((i + 1 - n0) & 1), log2_decay(to_f(dnext)), lane);
         if (i + 2 < nlive) fetch_da(chunk(i + 2));
       }
     }
     const double total = tab->total;
-    acc_dec += total;
+    acc_dec = clears ? -INFINITY : acc_dec + total;
     bool apart = false;   // this wave's values are not all finite: token by token
 
     if constexpr (MODE == 0) {
@@ -859,6 +880,12 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
 #pragma unroll
         for (int pw = 0; pw < PW; pw++) yo.put(16 * ut + ln, 16 * (wave * PW + pw) + 4 * lq, a[ut][pw]);
     }
+    if (clears) {
+#pragma unroll
+      for (int pw = 0; pw < PW; pw++)
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) H[pw][rt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
     if (!apart)
       state_update<T, RT, PW>(H, ks, xs, MODE == 2 ? tab->start : tab->end, ex2((float)total), wave, fresh(lane));
   }
@@ -905,14 +932,14 @@ __global__ __launch_bounds__(256) void k_attn_scan(AttnGeo g, int RT, int tiles,
   constexpr int U = 8;   // segments whose loads are in flight together
   for (int s0 = 0; s0 < g.nseg; s0 += U) {
     f4 loc[U];
-    float dec[U];
+    float dec[U];   // log2; -inf: the segment clears the state
 #pragma unroll
     for (int i = 0; i < U; i++) {
       if (s0 + i < g.nseg - 1) {   // the last one's own state is not needed
         const int s = BACK ? g.nseg - 1 - s0 - i : s0 + i;
         const size_t at = ((size_t)chain * g.nseg + s) * g.npt + pt;
         loc[i] = *reinterpret_cast<const f4*>(seg_loc + at * tiles + 4 * e);
-        dec[i] = ex2((float)seg_dec[at]);
+        dec[i] = (float)seg_dec[at];
       }
     }
 #pragma unroll
@@ -920,7 +947,11 @@ __global__ __launch_bounds__(256) void k_attn_scan(AttnGeo g, int RT, int tiles,
       if (s0 + i < g.nseg) {
         const int s = BACK ? g.nseg - 1 - s0 - i : s0 + i;
         *reinterpret_cast<f4*>(seg_loc + (((size_t)chain * g.nseg + s) * g.npt + pt) * tiles + 4 * e) = v;
-        if (s0 + i < g.nseg - 1) v = v * dec[i] + loc[i];
+        if (s0 + i < g.nseg - 1) {
+          const float w = ex2(dec[i]);
+#pragma unroll
+          for (int c = 0; c < 4; c++) v[c] = (dec[i] == -INFINITY ? 0.0f : v[c] * w) + loc[i][c];
+        }
       }
     }
   }

@@ -128,6 +128,37 @@ def test_a_cleared_state_is_gone_however_much_later_decays_grow(dtype):
     assert torch.count_nonzero(y[:, 0]) > 0
 
 
+def _cleared(t, cut, dtype):
+    """The oracle's outputs of what follows token `cut`, where the state is cleared."""
+    tail = [v[:, cut:].contiguous() for v in _args(t)]
+    o = [_np(v) for v in tail]
+    o[3] = np.maximum(o[3], -1e4)
+    return attn_seq.attn_fwd(*o, None)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("c,p,r,s,cut", [(1, 32, 40, 150, 0), (1, 32, 40, 150, 77), (3, 24, 32, 60, 25),
+                                         (1, 37, 45, 90, 64), (2, 128, 128, 70, 33), (1, 64, 128, 2300, 1111)])
+@pytest.mark.parametrize("bad", ["h0", "xhat", "bhat", "qhat", "da", "inf xhat", "inf bhat"])
+def test_a_cleared_state_forgets_what_is_not_finite(dtype, c, p, r, s, cut, bad):
+    """da = -inf starts the sequence anew, also behind a NaN or an infinity, in its chunk or an earlier one."""
+    print(f"[case] {bad} c={c} p={p} r={r} s={s} cut={cut} {dtype}", flush=True)
+    t = _make(1, s, c, 2, 1, p, r, dtype, seed=s + cut)
+    name, v = bad.split()[-1], INF if " " in bad else NAN
+    if name != "h0" and cut == 0:
+        pytest.skip("nothing is before the first token")
+    if name == "h0":
+        t["h0"][:] = NAN
+    else:
+        t[name][:, max(0, cut - 5)] = v
+    t["da"][:, cut] = -INF
+    a = _args(t)
+    y, last, saved = M.moments_attn_fwd_save(M.attn_desc(a[0], a[1]), *a, t["h0"])
+    ry, rl = _cleared(t, cut, dtype)
+    _check("y", y[:, cut:], ry, TOL[dtype])
+    _check("h_last", last, rl, TOL[F32])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("c,p,r,at", [(1, 32, 40, 40), (3, 24, 32, 15), (1, 37, 45, 10), (2, 128, 128, 29),
                                       (4, 70, 64, 3)])
