@@ -383,6 +383,11 @@ def _scratch(t):
     return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
 
 
+def _wrote(*tensors):
+    """Tells autograd that the library wrote to these tensors of the caller's."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def _size(n):
     if n < 0:
         _lib.check(int(n))
@@ -446,6 +451,7 @@ def _attn_forward(desc, xhat, bhat, qhat, da, h0, y, h_last, saved, want_saved, 
         _tensors_ok(dev, (("y", y, xhat.shape, xhat.dtype, True), ("h_last", h_last, state, torch.float32, True)))
     lib = _gpu(dev)
     ws = _buffer("workspace", moments_attn_workspace_size(desc, False), dev, workspace)
+    _wrote(y, h_last, saved)
     if y is None:
         y = torch.empty_like(xhat)
     if h_last is None:
@@ -480,6 +486,7 @@ def _gradients(dev, want, out, like):
     _tensors_ok(dev, [("d_" + k, out.get("d_" + k), t.shape, t.dtype, True) for k, t in like.items()
                       if k in want and t is not None])
     _gpu(dev)
+    _wrote(*[out.get("d_" + k) for k, t in like.items() if k in want and t is not None])
     for k, t in like.items():
         if k not in want or t is None:
             out["d_" + k] = None
@@ -528,6 +535,7 @@ def moments_attn_step(desc: AttnDesc, xhat, bhat, qhat, da, state, slots=None, y
                                     ("slots", slots, (desc.b,), torch.int32, True),
                                     ("y", y, xhat.shape, xhat.dtype, True)))
     lib = _gpu(dev)
+    _wrote(state, y)
     if y is None:
         y = torch.empty_like(xhat)
         out = y.data_ptr()
@@ -615,6 +623,7 @@ def moments_qk_fwd(desc: QkDesc, q, k, wq, wk, bq=None, bk=None, rot=None, qhat=
     if qhat is not None or khat is not None:
         _tensors_ok(dev, (("qhat", qhat, shape, dt, True), ("khat", khat, shape, dt, True)))
     lib = _gpu(dev)
+    _wrote(qhat, khat)
     if qhat is None:
         qhat = torch.empty(shape, dtype=dt, device=dev)
     if khat is None:

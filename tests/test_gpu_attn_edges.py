@@ -201,3 +201,25 @@ def test_one_bad_value_stays_in_its_state_row(dtype):
     hit[:, 0, 7] = True
     assert torch.isnan(last[hit]).all()
     _check("h_last", torch.where(hit, 0.0, last), _np(torch.where(hit, 0.0, last0)), 2 * TOL[F32])
+
+
+def test_autograd_sees_what_is_written_in_place():
+    """A tensor that a graph holds for its backward, then given as the state or as an output."""
+    t = _make(2, 1, 1, 2, 2, 16, 24, F32, seed=9)
+    a = _args(t)
+    d = M.attn_desc(a[0], a[1])
+
+    def held(v):
+        leaf = torch.randn_like(v).requires_grad_()
+        return leaf.exp()            # its backward reads the result
+
+    for write in (lambda v: M.moments_attn_step(d, *a, v), lambda v: M.moments_attn_fwd(d, *a, t["h0"], h_last=v),
+                  lambda v: M.moments_attn_fwd(d, *a, v, h_last=v),
+                  lambda v: M.moments_attn_bwd(d, *a, t["h0"], t["d_y"], out={"d_h0": v})):
+        v = held(t["h0"])
+        write(v.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            v.sum().backward()
+    v = held(t["h0"])
+    M.moments_attn_fwd(d, *a, v.detach())          # read only
+    v.sum().backward()
