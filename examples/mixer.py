@@ -55,15 +55,14 @@ class Attention(torch.autograd.Function):
     def forward(ctx, x, khat, qhat, da, h0, lens):
         desc = M.attn_desc(x, khat, valid_lens=lens)
         y, last, saved = M.moments_attn_fwd_save(desc, x, khat, qhat, da, h0)
-        ctx.desc, ctx.saved, ctx.h0 = desc, saved, h0
-        ctx.save_for_backward(x, khat, qhat, da)
+        ctx.desc = desc
+        ctx.save_for_backward(x, khat, qhat, da, h0, saved)
         return y, last
 
     @staticmethod
     def backward(ctx, d_y, d_last):
-        x, khat, qhat, da = ctx.saved_tensors
-        g = M.moments_attn_bwd_saved(ctx.desc, x, khat, qhat, da, ctx.h0, ctx.saved, d_y.contiguous(),
-                                     d_last.contiguous())
+        x, khat, qhat, da, h0, saved = ctx.saved_tensors
+        g = M.moments_attn_bwd_saved(ctx.desc, x, khat, qhat, da, h0, saved, d_y.contiguous(), d_last.contiguous())
         return g["d_xhat"], g["d_bhat"], g["d_qhat"], g["d_da"], g["d_h0"], None
 
 
@@ -74,13 +73,14 @@ class Moments(torch.autograd.Function):
     def forward(ctx, x, khat, da, rot):
         ctx.desc = M.make_desc(x, khat, 1, x.shape[1], M.ROT_PAIRWISE, rope_dim=2 * rot.shape[3])
         ctx.save_for_backward(x, khat, da, rot)
-        m2, ctx.m1 = M.moments_fwd(ctx.desc, x, khat, da, rot, None)
+        m2, m1 = M.moments_fwd(ctx.desc, x, khat, da, rot, None)
+        ctx.m1_shape = m1.shape
         return m2
 
     @staticmethod
     def backward(ctx, d_m2):
         x, khat, da, rot = ctx.saved_tensors
-        g = M.moments_bwd(ctx.desc, x, khat, da, rot, None, d_m2.contiguous(), torch.zeros_like(ctx.m1),
+        g = M.moments_bwd(ctx.desc, x, khat, da, rot, None, d_m2.contiguous(), d_m2.new_zeros(ctx.m1_shape),
                           want=("xhat", "bhat", "da", "rot"))
         return g["d_xhat"], g["d_bhat"], g["d_da"], g["d_rot"]
 
