@@ -13,6 +13,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
@@ -28,6 +29,7 @@ class Rotation(torch.autograd.Function):
         return M.moments_rot_fwd(M.rot_desc(inc, M.ROT_PAIRWISE), inc)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_rot):
         (inc,) = ctx.saved_tensors
         return M.moments_rot_bwd(M.rot_desc(inc, M.ROT_PAIRWISE), inc, d_rot.contiguous())
@@ -43,6 +45,7 @@ class QueryKey(torch.autograd.Function):
         return M.moments_qk_fwd(ctx.desc, q, k, wq, wk, bq, bk, rot)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_qhat, d_khat):
         g = M.moments_qk_bwd(ctx.desc, *ctx.saved_tensors, d_qhat.contiguous(), d_khat.contiguous())
         return g["d_q"], g["d_k"], g["d_wq"], g["d_wk"], g["d_bq"], g["d_bk"], g["d_rot"], None
@@ -60,6 +63,7 @@ class Attention(torch.autograd.Function):
         return y, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_y, d_last):
         x, khat, qhat, da, h0, saved = ctx.saved_tensors
         g = M.moments_attn_bwd_saved(ctx.desc, x, khat, qhat, da, h0, saved, d_y.contiguous(), d_last.contiguous())
@@ -78,6 +82,7 @@ class Moments(torch.autograd.Function):
         return m2
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_m2):
         x, khat, da, rot = ctx.saved_tensors
         g = M.moments_bwd(ctx.desc, x, khat, da, rot, None, d_m2.contiguous(), d_m2.new_zeros(ctx.m1_shape),
