@@ -10,11 +10,15 @@
 // each other). A workgroup walks the chunks of one chain with H in fp32
 // accumulator registers, so q, k, x are read once and y is written once.
 //
-// Rounding. Products of bf16 values are exact in fp32. The two operands that the
-// walk itself makes are rounded to bf16 for the matrix instructions: the scores
-// (q.k) e^{a_u - a_j}, and a copy of H where y reads it. The running H never is:
-// the decayed writes e^{a_end - a_j} x[j] enter as the sum of three bf16 pieces
-// (24 bits), so the state, which is handed on to later calls, keeps fp32 accuracy.
+// Rounding. Products of bf16 values are exact in fp32. What the walk itself makes for the
+// matrix instructions is split into bf16 pieces, each the rounded rest of those before: the
+// decayed writes e^{a_end - a_j} x[j] into three (24 bits), so that the state, which is handed
+// on to later calls, keeps fp32 accuracy, and the scores (q.k) e^{a_u - a_j} into two (17 bits),
+// so that y is right to its own rounding. With scores of one piece y had 1.4 times that error,
+// and up to 1.7 times in sequences of a few tokens, where single scores stand out. The second
+// piece costs 8 of 105 us in 128 ragged chains of up to 4096 rows, 2 % in 32 of 240000, nothing
+// where the chains fill the card (memory bounds them). Only the copy of H that y reads is
+// rounded to one piece: e^{a_u} weights it, and two would cost another 7 us and 9 %.
 //
 // MFMA fragments here span 32 slots of the contracted index in the order in which
 // a pair of accumulator tiles holds its rows: lane group q (= lane / 16) has
@@ -449,7 +453,8 @@ struct LdsA {
   static constexpr int RP = AV<T>::pitch(RC), PP = AV<T>::pitch(PC), SP = AV<T>::pitch(L);
   static constexpr size_t tab = 0, k = 2 * sizeof(DecayTab), x = k + (size_t)L * RP * sizeof(T),
                           state_total = x + (size_t)L * PP * sizeof(T), q = state_total,
-                          s = q + (size_t)L * RP * sizeof(T), total = s + (size_t)L * SP * sizeof(T);
+                          s = q + (size_t)L * RP * sizeof(T), sl = s + (size_t)L * SP * sizeof(T),
+                          total = sl + (sizeof(T) == 2 ? (size_t)L * SP * sizeof(T) : 0);
   static_assert(sizeof(DecayTab) % 16 == 0, "tiles start at 16 bytes");
 };
 
@@ -622,6 +627,8 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
   T* xs = reinterpret_cast<T*>(lds + LD::x);
   T* qs = reinterpret_cast<T*>(lds + LD::q);
   T* ss = reinterpret_cast<T*>(lds + LD::s);
+  constexpr int SP = sizeof(T) == 2 ? 2 : 1;   // pieces of a score, a tile for each
+  constexpr int STILE = L * LD::SP;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ln = lane & 15, lq = lane >> 4;
 
@@ -707,7 +714,7 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
     if constexpr (VEC && MODE == 0) dropped_stores<T, NT * PW>();
   }
   if constexpr (MODE == 0) {
-    for (int e = threadIdx.x; e < L * LD::SP / 4; e += ATT)
+    for (int e = threadIdx.x; e < SP * STILE / 4; e += ATT)
       reinterpret_cast<typename V::quad*>(ss)[e] = typename V::quad{};
   }
   for (int i = n0; i < nlive; i++) {
@@ -808,7 +815,12 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
 #pragma unroll
           for (int e = 0; e < 4; e++)
             a[k2][e] = keep_if(e <= last, a[k2][e] * ex2((uh[k2] - jh[k2][e]) + (ul[k2] - jl[k2][e])));
-          st_quad<LD::L>(ss, u, jt[k2] / 4 + lq, to_quad<T>(a[k2]));
+#pragma unroll
+          for (int i = 0; i < SP; i++) {
+            const typename V::quad piece = to_quad<T>(a[k2]);
+            st_quad<LD::L>(ss + i * STILE, u, jt[k2] / 4 + lq, piece);
+            if (i + 1 < SP) a[k2] -= quad_f(piece);
+          }
         }
       }
       typename V::frag hf[PW][RT / 2];
@@ -843,26 +855,36 @@ __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __rest
       {
         typename V::frag xf[NJ][PW], sf[NJ][NT];
         float st[NT];
+        // scores of the 32 rows j from 32m on that some u of tile ut reads (a token has up to four rows)
+        auto reads = [](int ut, int m) { return 32 * m <= 16 * ut + 15 + 3; };
 #pragma unroll
         for (int ut = 0; ut < NT; ut++) st[ut] = tab->start[16 * ut + (lb & 15)];
 #pragma unroll
-        for (int m = 0; m < NJ; m++) {
+        for (int m = 0; m < NJ; m++)
 #pragma unroll
           for (int pw = 0; pw < PW; pw++) xf[m][pw] = col_frag<LD::PC>(xs, m, 16 * (wave * PW + pw), lb);
 #pragma unroll
-          for (int ut = 0; ut < NT; ut++) sf[m][ut] = row_frag<LD::L>(ss, 16 * ut, m, lb);
+        for (int i = SP - 1; i >= 0; i--) {   // the smaller pieces first
+#pragma unroll
+          for (int m = 0; m < NJ; m++)
+#pragma unroll
+            for (int ut = 0; ut < NT; ut++)
+              if (reads(ut, m)) sf[m][ut] = row_frag<LD::L>(ss + i * STILE, 16 * ut, m, lb);
+          issue_fence();
+          if (i == SP - 1) {
+#pragma unroll
+            for (int ut = 0; ut < NT; ut++)
+#pragma unroll
+              for (int pw = 0; pw < PW; pw++) a[ut][pw] *= st[ut];
+          }
+#pragma unroll
+          for (int m = 0; m < NJ; m++)
+#pragma unroll
+            for (int ut = 0; ut < NT; ut++)
+#pragma unroll
+              for (int pw = 0; pw < PW; pw++)
+                if (reads(ut, m)) a[ut][pw] = mma32(xf[m][pw], sf[m][ut], a[ut][pw]);
         }
-        issue_fence();
-#pragma unroll
-        for (int ut = 0; ut < NT; ut++)
-#pragma unroll
-          for (int pw = 0; pw < PW; pw++) a[ut][pw] *= st[ut];
-#pragma unroll
-        for (int m = 0; m < NJ; m++)
-#pragma unroll
-          for (int ut = 0; ut < NT; ut++)
-#pragma unroll
-            for (int pw = 0; pw < PW; pw++) a[ut][pw] = mma32(xf[m][pw], sf[m][ut], a[ut][pw]);
       }
       // Where the state that entered, a row of x or a row of k is not finite, no column of the
       // chunk's last row is (it reads them all, if only with weights of zero): the check of 4 PW

@@ -223,3 +223,22 @@ def test_autograd_sees_what_is_written_in_place():
     v = held(t["h0"])
     M.moments_attn_fwd(d, *a, v.detach())          # read only
     v.sum().backward()
+
+
+def _beside_rounding(name, got, ref):
+    """The error of a bf16 result, at most 1.1 times that of rounding the exact one: scores of 17 bits add
+    2^-17 of their terms to its 2^-9."""
+    alone = torch.from_numpy(ref).to(BF16).double().numpy()
+    e, e0 = np.linalg.norm(_np(got) - ref), np.linalg.norm(alone - ref)
+    print(f"[compare] {name}: {e / e0:.3f} times the rounding's error", flush=True)
+    assert e <= 1.1 * e0, (name, e / e0)
+
+
+@pytest.mark.parametrize("s,c,h,g,p,r", [(1, 1, 8, 8, 64, 128), (2, 2, 4, 2, 37, 45), (7, 3, 4, 4, 64, 64), (16, 4, 2, 1, 128, 128),
+                                         (64, 1, 2, 2, 64, 128), (21, 3, 2, 1, 96, 24)])
+def test_bf16_outputs_are_right_to_their_rounding(s, c, h, g, p, r):
+    """Within one chunk from a state of zeros, where nothing but the scores is rounded on the way."""
+    t = _make(3, s, c, h, g, p, r, BF16, seed=s + p, h0=False)
+    a = _args(t)
+    y, _ = M.moments_attn_fwd(M.attn_desc(a[0], a[1]), *a)
+    _beside_rounding("y", y, attn_seq.attn_fwd(*[_np(v) for v in a])[0])
