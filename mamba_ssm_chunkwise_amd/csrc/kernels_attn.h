@@ -215,6 +215,11 @@ struct Scaled<1> {
   __device__ __forceinline__ const AV<float>::frag& piece(int) const { return p; }
 };
 
+// Nothing is scheduled across: the loads before it are all issued before the matrix
+// instructions behind it, which then wait for them one by one. (Left to itself the compiler
+// saves registers by loading one operand pair, waiting out its latency, and so on.)
+__device__ __forceinline__ void issue_fence() { __builtin_amdgcn_sched_barrier(0); }
+
 // ---- staging ----------------------------------------------------------------
 // Rows of a chunk in global memory through a buffer descriptor that ends with the last
 // valid row: loads past it return zeros and stores past it are dropped by the hardware, so
@@ -294,6 +299,7 @@ struct Stage {
 #pragma unroll
       for (int e = 0; e < PE; e++)
         x[i][e] = __builtin_amdgcn_raw_buffer_load_b16(r, c0 + e < n ? off0 + (unsigned)i * step + 2u * e : kPast, 0, 0);
+    issue_fence();
 #pragma unroll
     for (int i = 0; i < N; i++) {
       const int e = i * NT + (int)threadIdx.x;
@@ -387,10 +393,6 @@ __device__ __forceinline__ int fresh(int lane) {
   return lane;
 }
 
-// Nothing is scheduled across: the loads before it are all issued before the matrix
-// instructions behind it, which then wait for them one by one. (Left to itself the compiler
-// saves registers by loading one operand pair, waiting out its latency, and so on.)
-__device__ __forceinline__ void issue_fence() { __builtin_amdgcn_sched_barrier(0); }
 // v where keep, else zero, whatever v is; without a branch.
 __device__ __forceinline__ float keep_if(bool keep, float v) {
   return __uint_as_float(__float_as_uint(v) & (keep ? 0xFFFFFFFFu : 0u));
