@@ -16,6 +16,13 @@
 // A workgroup walks one chain's chunks in reverse with G in fp32 registers; H
 // comes from the copies that the forward (or a walk over k and x) left per chunk.
 //
+// Rounding. s and t enter the products as two bf16 pieces each (17 bits; s as one where p and r
+// are both above 64, for which LDS is too small), so that d_q, d_k and d_x are right to their own
+// rounding: with one piece they had 1.4 times its error, 1.65 in sequences of a few tokens. The
+// second pieces cost 6 to 8 % of the kernel. The copies of H and G that the outputs and d_da read
+// are rounded once: pieces of them would double the 25 % of the forward's bytes that the copies
+// of H are, and do not fit LDS.
+//
 // Eight waves and one workgroup per CU: the operand tiles, both score tiles and the copies
 // of G and H take most of the LDS, and with eight waves a wave's share of G is half of what
 // it would be with the walk's four.
@@ -41,12 +48,15 @@ struct LdsB {
   static constexpr int RC = 16 * RT, PC = 16 * PT;
   static constexpr int RP = AV<T>::pitch(RC), PP = AV<T>::pitch(PC), SP = AV<T>::pitch(L);
   static constexpr size_t E = sizeof(T);
+  // pieces of s and of t, a tile for each: bf16 two, but with both widths at their largest, where
+  // LDS ends, s has one
+  static constexpr int NTP = sizeof(T) == 2 ? 2 : 1, NS = RT == 8 && PT == 8 ? 1 : NTP;
   static constexpr size_t tab = 0;
   static constexpr size_t sums = sizeof(DecayTab);   // rsum, csum, up, vp [4][64], th[8]
   static constexpr size_t k = sums + 16 * 64 * 4 + 32;
   static constexpr size_t q = k + (size_t)L * RP * E, x = q + (size_t)L * RP * E, dy = x + (size_t)L * PP * E,
-                          s = dy + (size_t)L * PP * E, t = s + (size_t)L * SP * E,
-                          hs = t + (size_t)L * SP * E, gs = hs + (size_t)16 * PT * RP * E,
+                          s = dy + (size_t)L * PP * E, t = s + (size_t)NS * L * SP * E,
+                          hs = t + (size_t)NTP * L * SP * E, gs = hs + (size_t)16 * PT * RP * E,
                           total = gs + (size_t)16 * PT * RP * E;
 };
 
@@ -174,10 +184,9 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     if (wave == 0 && lane < nrows && ltok * g.c == lane) dnext = dab[(size_t)(t0 + ltok) * g.h];
   };
   // tiles of the scores without pairs j <= u are never written: zeros throughout
-  for (int e = threadIdx.x; e < L * LD::SP / 4; e += ABT) {
+  constexpr int STILE = L * LD::SP;
+  for (int e = threadIdx.x; e < (LD::NS + LD::NTP) * STILE / 4; e += ABT)   // s, and t behind it
     reinterpret_cast<typename V::quad*>(ss)[e] = typename V::quad{};
-    reinterpret_cast<typename V::quad*>(ts)[e] = typename V::quad{};
-  }
   rsum[threadIdx.x] = 0.0f;   // and csum behind it
   const ScoreTiles<NT> tl(g.c);
   if (nlive > n0) fetch(nlive - 1);
@@ -218,7 +227,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
       if (lane == 0) th[wave] = v;
     }
     // s, t (stored [u][j]) and the sums of (q.k) t over pairs of different tokens
-    const int la = fresh<PT == 8>(lane);
+    const int la = fresh<PT == 8 || !VEC>(lane);
 #pragma unroll 1
     for (int at = wave; at < tl.pairs; at += ABW) {
       const int code = (int)(tl.lower >> (4 * at)) & 15, ut = 16 * (code >> 2), jt = 16 * (code & 3);
@@ -256,8 +265,18 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
         cs[e] = keep_if(e < first, qk * b[e]);
         rs += cs[e];
       }
-      st_quad<LD::L>(ss, u, jt / 4 + lq, to_quad<T>(a));
-      st_quad<LD::L>(ts, u, jt / 4 + lq, to_quad<T>(b));
+#pragma unroll
+      for (int i = 0; i < LD::NS; i++) {
+        const typename V::quad piece = to_quad<T>(a);
+        st_quad<LD::L>(ss + i * STILE, u, jt / 4 + lq, piece);
+        a -= quad_f(piece);
+      }
+#pragma unroll
+      for (int i = 0; i < LD::NTP; i++) {
+        const typename V::quad piece = to_quad<T>(b);
+        st_quad<LD::L>(ts + i * STILE, u, jt / 4 + lq, piece);
+        b -= quad_f(piece);
+      }
       rs = col4_sum(rs);
       if (lq == 0) rsum[4 * jt + u] = rs;
 #pragma unroll
@@ -296,7 +315,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
         }
 #pragma unroll
         for (int j0 = 0; j0 < UB; j0 += JB) {
-          typename V::frag ff[JB][PT / 2], gf[JB][NJ];
+          typename V::frag ff[JB][PT / 2], gf[JB][NJ], ge[JB][NJ];   // ge: the larger pieces
           typename V::quad ow[JB][RB];
           float wu[JB];
 #pragma unroll
@@ -305,7 +324,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
             for (int m = 0; m < PT / 2; m++) ff[j][m] = first(ut, m);
 #pragma unroll
-            for (int m = 0; m < NJ; m++) gf[j][m] = second(ut, m);
+            for (int m = 0; m < NJ; m++) gf[j][m] = second(ut, m, ts + (LD::NTP - 1) * STILE);
             wu[j] = w[16 * ut + ln];
 #pragma unroll
             for (int i = 0; i < RB; i++) ow[j][i] = ld_quad<LD::RC>(own + 16 * ut * LD::RP, l & 15, 4 * (rt0 + i) + lq);
@@ -322,6 +341,13 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
             for (int j = 0; j < JB; j++)
 #pragma unroll
               for (int i = 0; i < RB; i++) a[j][i] = mma32(sf[i][m], ff[j][m], a[j][i]);
+          if constexpr (LD::NTP > 1) {
+            issue_fence();
+#pragma unroll
+            for (int j = 0; j < JB; j++)
+#pragma unroll
+              for (int m = 0; m < NJ; m++) ge[j][m] = second(ut0 + j0 + j, m, ts);
+          }
 #pragma unroll
           for (int j = 0; j < JB; j++) {
             float us = 0.0f;
@@ -340,6 +366,14 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
             for (int j = 0; j < JB; j++)
 #pragma unroll
               for (int i = 0; i < RB; i++) a[j][i] = mma32(cf[i][m], gf[j][m], a[j][i]);
+          if constexpr (LD::NTP > 1) {
+#pragma unroll
+            for (int m = 0; m < NJ; m++)
+#pragma unroll
+              for (int j = 0; j < JB; j++)
+#pragma unroll
+                for (int i = 0; i < RB; i++) a[j][i] = mma32(cf[i][m], ge[j][m], a[j][i]);
+          }
 #pragma unroll
           for (int j = 0; j < JB; j++)
 #pragma unroll
@@ -347,15 +381,15 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
         }
       };
       {
-        const int lb = fresh<PT == 8>(lane);
+        const int lb = fresh<PT == 8 || !VEC>(lane);
         rows_grad(hs, ks, [&](int ut, int m) { return row_frag<LD::PC>(ys, 16 * ut, m, lb); },
-                  [&](int ut, int m) { return row_frag<LD::L>(ts, 16 * ut, m, lb); }, tab->start, qs, up, oq, lb);
+                  [&](int ut, int m, const T* t) { return row_frag<LD::L>(t, 16 * ut, m, lb); }, tab->start, qs, up, oq, lb);
       }
       __builtin_amdgcn_sched_barrier(0);
       {
-        const int lc = fresh<PT == 8>(lane);
+        const int lc = fresh<PT == 8 || !VEC>(lane);
         rows_grad(gs, qs, [&](int ut, int m) { return row_frag<LD::PC>(xs, 16 * ut, m, lc); },
-                  [&](int ut, int m) { return col_frag<LD::L>(ts, m, 16 * ut, lc); }, tab->end, ks, vp, ok, lc);
+                  [&](int ut, int m, const T* t) { return col_frag<LD::L>(t, m, 16 * ut, lc); }, tab->end, ks, vp, ok, lc);
       }
     }
     // d_x, likewise over PB tiles of rows p
@@ -363,12 +397,12 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     {
       constexpr int PB = PT * NT >= 16 ? 2 : 1, WP = PT / PB, WU = ABW / WP, UB = NT / WU > 0 ? NT / WU : 1;
       static_assert(WP * WU == ABW && UB * WU == NT, "tiles and waves");
-      const int ld = fresh<PT == 8>(lane);
+      const int ld = fresh<PT == 8 || !VEC>(lane);
       const int pj0 = wave % WP * PB, ut0 = wave / WP * UB;
 #pragma unroll
       for (int j = 0; j < UB; j++) {
         const int ut = ut0 + j, u = 16 * ut + ln;
-        typename V::frag kf[RT / 2], gf[PB][RT / 2], sf[NJ], yf[PB][NJ];
+        typename V::frag kf[RT / 2], gf[PB][RT / 2], sf[LD::NS][NJ], yf[PB][NJ];
 #pragma unroll
         for (int m = 0; m < RT / 2; m++) {
           kf[m] = row_frag<LD::RC>(ks, 16 * ut, m, ld);
@@ -377,7 +411,8 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
         }
 #pragma unroll
         for (int m = 0; m < NJ; m++) {
-          sf[m] = col_frag<LD::L>(ss, m, 16 * ut, ld);
+#pragma unroll
+          for (int i = 0; i < LD::NS; i++) sf[i][m] = col_frag<LD::L>(ss + i * STILE, m, 16 * ut, ld);
 #pragma unroll
           for (int i = 0; i < PB; i++) yf[i][m] = col_frag<LD::PC>(ys, m, 16 * (pj0 + i), ld);
         }
@@ -393,9 +428,11 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
 #pragma unroll
         for (int i = 0; i < PB; i++) a[i] *= en;
 #pragma unroll
-        for (int m = 0; m < NJ; m++)
+        for (int k2 = LD::NS - 1; k2 >= 0; k2--)
 #pragma unroll
-          for (int i = 0; i < PB; i++) a[i] = mma32(yf[i][m], sf[m], a[i]);
+          for (int m = 0; m < NJ; m++)
+#pragma unroll
+            for (int i = 0; i < PB; i++) a[i] = mma32(yf[i][m], sf[k2][m], a[i]);
 #pragma unroll
         for (int i = 0; i < PB; i++) ox.put(u, 16 * (pj0 + i) + 4 * lq, a[i]);
       }
@@ -403,7 +440,7 @@ __global__ __launch_bounds__(ABT, 1) void k_attn_bwd(
     // G'
     __builtin_amdgcn_sched_barrier(0);
     {
-      const int le = fresh<PT == 8>(lane);
+      const int le = fresh<PT == 8 || !VEC>(lane);
       typename V::frag qf[NJ][RW], yr[NJ];
       f4 w0[NJ], w1[NJ];
 #pragma unroll
