@@ -136,7 +136,8 @@ class Mixer(torch.nn.Module):
 
     @torch.no_grad()
     def token(self, u, state, theta, slots=None):
-        """One token of each sequence u [b,1,width]; state and theta are updated in place."""
+        """One token of each sequence u [b,1,width]; state and theta are updated in place: theta [b,heads,angles]
+        row by row, state, a pool, at the rows' slots (without slots row by row too)."""
         q, k, x, da, inc = self.project(u)
         theta += inc[:, 0].float()
         rot = theta[:, None].to(u.dtype)

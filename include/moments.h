@@ -222,8 +222,9 @@ int moments_rot_bwd(const moments_desc* desc, const void* inc, const void* d_rot
  *
  * States are float32 whatever desc->dtype is, [b,h,p,r]: h0 (NULL: zeros), h_last
  * (the state after the last valid token; NULL: not wanted). They are kept to fp32
- * accuracy (the scores, and the copy of the state that y reads, are rounded to bf16
- * for bf16 inputs), so a sequence may be cut into calls that hand them on.
+ * accuracy, so a sequence may be cut into calls that hand them on. For bf16 inputs the
+ * scores enter with 17 bits and the copy of the state that y reads with 8; the gradients
+ * likewise (d_xhat with scores of 8 where p and r are both above 64).
  * desc->valid_len and valid_lens are those of moments_desc: rows of y, and of every
  * gradient, past a sequence's length are zero, whatever the inputs hold there; a
  * sequence of length 0 leaves h_last = h0. da below -110 (-inf among it) is a decay
@@ -295,7 +296,8 @@ int moments_attn_step(const moments_attn_desc* desc, const void* xhat, const voi
  * bias[h,r] (NULL: none) are float32. rot is [b,s,rot_h,a] or [b,s,rot_h,J,4] in
  * desc->dtype with rot_h = h, or 1 (all heads turn alike). All but q and k start at 16
  * bytes. qhat and khat are [b,s,c,h,r]: head hi takes group hi / (h/g), with its own
- * bias and rotation. Ownership, errors and MOMENTS_CHECK_FINITE are those stated above.
+ * bias and rotation. Ownership, errors and MOMENTS_CHECK_FINITE are those stated above; no
+ * output may overlap an input or another output.
  *
  * moments_qk_bwd is the vector-Jacobian product at d_qhat, d_khat: d_q, d_k
  * [b,s,c,g,r] and d_rot in desc->dtype (dense), d_wq, d_wk[r] and d_bq, d_bk[h,r] in

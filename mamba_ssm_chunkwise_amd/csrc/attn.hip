@@ -30,8 +30,9 @@ struct AttnPlan {
 
 // Segments a chain's walk is split into: one when the chains alone nearly fill the `want`
 // places that the chip has for workgroups of the walk, else as many as fill them, of four
-// chunks or more (two, up to eight segments). Measured on 32 chains of 8192 tokens: one
-// segment 415 us, 4: 157, 8: 90, 16 (taken): 87, 32: 101; on 8 chains: 32 (taken) 35, 64: 40.
+// chunks or more (two, up to eight segments). Measured on 32 chains of 8192 tokens, the launches'
+// times together: one segment 465 us, 4: 189, 8: 114, 16 (taken): 102, 32: 116; on 8 chains:
+// 16: 61, 32 (taken): 46, 64: 51.
 void split(AttnGeo& g, int items, long want) {
   long n = 1;
   if ((long)items * 4 < want * 3)
@@ -62,16 +63,16 @@ int make_attn_plan(const moments_attn_desc* d, AttnPlan* P) {
   g.NK = (g.V + g.CT - 1) / g.CT;
   g.cinv = (65536 + g.c - 1) / g.c;
   // Rows of whole 16-byte pieces are fetched a chunk ahead; others, which such loads cannot
-  // address, element by element. Aligned shapes, either way (forward, backward): float, 32
-  // chains of 3800 rows, 44 and 56 us; bf16, 512 of 16384, 1.87 and 3.94 ms, 3.3 and 10.6 ms.
+  // address, element by element. Aligned shapes, either way: float, 32 chains of 3800 rows,
+  // forward 49 and 63 us, gradients 97 and 113; bf16, 512 of 16384, 1.87 and 3.99 ms, 3.5 and 8.7 ms.
   P->vec = (g.r * tsz) % 16 == 0 && (g.p * tsz) % 16 == 0;
   g.lens = (const int*)d->valid_lens;
-  // Half the columns where they do: r = 64, float, 32 chains of 3800 rows, 4 tiles 21 us for
-  // the segments' states and 44 for the walk, 8 tiles 31 and 68.
+  // Half the columns where they do: r = 64, float, 32 chains of 3800 rows, 4 tiles 45 us for the
+  // segments' states both ways, 49 for the walk and 97 for the gradients, 8 tiles 66, 77 and 159.
   P->RT = g.r <= 64 ? 4 : 8;
   // All of up to 128 state rows to a workgroup, so that keys and scores are made once:
-  // 32 chains of 240000 rows, p = 128, 0.84 ms for the segments' states and 2.05 for the walk;
-  // two workgroups of 64 each 0.96 and 2.62. Float, whose LDS tiles are
+  // 32 chains of 240000 rows, p = 128, 0.88 ms for the segments' states and 2.20 for the walk;
+  // two workgroups of 64 each 1.04 and 2.87. Float, whose LDS tiles are
   // twice as large, stays at 64.
   P->wide = P->bf && g.p > 64;
   g.PT = P->wide ? 128 : 64;

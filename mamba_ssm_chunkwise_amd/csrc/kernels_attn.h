@@ -126,8 +126,10 @@ template <typename T> __device__ __forceinline__ typename AV<T>::frag acc_frag(f
 // COLS is 64 or 128 (32 for the float scores). bf16 rows are not padded: quad v (four
 // columns, 8 bytes) of a row sits at v ^ swz(row). What 32 lanes read together, one quad
 // and its neighbour of 16 rows, or (transposing reads) four quads of eight rows, then
-// touches each of the 64 banks once (measured: no conflicts), and the pairs of quads that
-// 16-byte pieces are stay together. Float rows are padded by one quad instead.
+// touches each of the 64 banks once, and the pairs of quads that 16-byte pieces are stay
+// together. Measured: no conflicts in the walk over k and x, whose reads transpose; 28 to 30 %
+// of the LDS cycles in the forward and 13 % in the gradients, which read row fragments and
+// tables too (which of these, and why, is open). Float rows are padded by one quad instead.
 template <typename T, int COLS> __device__ __forceinline__ int swz(int row) {
   if constexpr (sizeof(T) != 2) return 0;
   else if constexpr (COLS >= 128) return ((row & 7) << 2) | (((row >> 3) & 1) << 1);
@@ -609,11 +611,12 @@ template <> struct ScoreTiles<2> {
 // bf16; 32 in float, whose tiles are twice as large). Two workgroups share a CU, one's loads
 // under the other's barriers; three measured no faster.
 // Bound: memory where the chains fill the card. bf16, r = 128: 512 chains of 16384 rows,
-// p = 64, with the saved copies, 8.6 GB in 1.87 ms (4.6 TB/s; a large copy reaches 4.75);
-// 32 chains of 240000 rows, p = 128, 8.0 GB in 2.05 ms (3.9 TB/s) behind a MODE 1 pass of
-// 3.9 GB in 0.85 ms (4.6 TB/s), matrix pipes 31 % and vector pipes 51 % busy. Else the
-// latency of a chunk: its phases depend on one another through LDS and three barriers (128
-// chains of 4096 rows, p = 64: 109 us; of ragged rows, the longest deciding: 96 us).
+// p = 64, with the saved copies, 8.6 GB in 1.89 ms (4.6 TB/s; a large copy reaches 4.75);
+// 32 chains of 240000 rows, p = 128, 8.0 GB in 2.1 to 2.3 ms (3.5 to 3.8 TB/s) behind a MODE 1
+// pass of 3.9 GB in 0.83 to 0.91 ms (4.3 to 4.7 TB/s), matrix pipes 32 % and vector pipes 52 %
+// busy. Else the latency of a chunk: its phases depend on one another through LDS and three
+// barriers (128 chains of 4096 rows, p = 64: 114 to 127 us; of ragged rows, the longest deciding:
+// 103 us).
 template <typename T, int RT, int PW, int MODE, bool VEC>
 __global__ __launch_bounds__(ATT, 2) void k_attn_walk(AttnGeo g, const T* __restrict__ x, const T* __restrict__ k,
                                                       const T* __restrict__ q, const T* __restrict__ da,
@@ -987,7 +990,7 @@ __global__ __launch_bounds__(256) void k_attn_scan(AttnGeo g, int RT, int tiles,
 // 64 / LPR rows at a time and NB such batches, with all their loads in flight first:
 // the state is read and written once and is all that counts (2 * 4 p r bytes against
 // 2 (2 r + 2 p) for the rest). Bound by memory: 256 sequences of 64 heads, p = 64, r = 128
-// (1.08 GB): 226 us, 4.8 TB/s, as a large copy. One sequence: the launch's own time (4 us
+// (1.08 GB): 227 to 233 us, 4.6 to 4.75 TB/s, a large copy's rate. One sequence: the launch's own time (4 us
 // of the 11 that the call takes on the host).
 template <typename T, int LPR, int NB>
 __global__ __launch_bounds__(256) void k_attn_step(AttnGeo g, int nslots, const T* __restrict__ x,

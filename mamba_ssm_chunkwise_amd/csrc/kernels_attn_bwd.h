@@ -26,11 +26,11 @@
 // Eight waves and one workgroup per CU: the operand tiles, both score tiles and the copies
 // of G and H take most of the LDS, and with eight waves a wave's share of G is half of what
 // it would be with the walk's four.
-// Measured, bf16, p = 64, r = 128, 512 chains of 16384 rows: 3.2 to 3.4 ms for 14.0 GB (8.6
-// read, the copies of H among them, 5.4 written: 4.1 to 4.4 TB/s; a large copy reaches 4.75),
-// vector pipes 42 %, matrix pipes 18 % busy. When it took 3.36 ms, it took 3.07 without its
-// stores and 3.32 without the copies' loads, so what bounds it is the chunk's chain of
-// phases (three barriers, LDS round trips between products), not bytes.
+// Measured, bf16, p = 64, r = 128, 512 chains of 16384 rows: 3.5 to 3.7 ms for 14.0 GB (8.6
+// read, the copies of H among them, 5.4 written: 3.8 to 4.0 TB/s; a large copy reaches 4.75),
+// vector pipes 41 %, matrix pipes 22 % busy. When it took 3.36 ms, with scores of one piece, it
+// took 3.07 without its stores and 3.32 without the copies' loads, so what bounds it is the
+// chunk's chain of phases (three barriers, LDS round trips between products), not bytes.
 #pragma once
 
 #include <type_traits>

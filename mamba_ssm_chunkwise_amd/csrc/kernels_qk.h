@@ -329,8 +329,8 @@ __device__ __forceinline__ float recip_sqrt(float v) {
 // angles are whole 16-byte pieces (8 bytes, bf16 angles); others go one element at a time.
 // A wave takes tokens a grid apart, with the next one's rows already in flight.
 // Bound by memory, most of it what it writes: bf16, 8 x 8192 tokens of two channels, 64 heads
-// in 8 groups, r = 128: 5.1 GB in 1.07 to 1.26 ms (4.0 to 4.8 TB/s; a large copy 4.75).
-// float32, 2 x 2048 tokens, 16 heads, r = 64: 23 us.
+// in 8 groups, r = 128: 5.1 GB in 1.15 to 1.31 ms, 1.24 on average (4.1 TB/s; a large copy 4.75).
+// float32, 2 x 2048 tokens, 16 heads, r = 64: 24 us.
 template <typename T, int LPR, int ROT, int C, int HB, bool VEC>
 __global__ __launch_bounds__(QKT) void k_qk_fwd(QkGeo g, const T* __restrict__ q, const T* __restrict__ k,
                                                 const float* __restrict__ wq, const float* __restrict__ wk,
@@ -475,10 +475,11 @@ __device__ __forceinline__ void qk_row_grad(const QkRot<ROT>& R, const float (&n
 // stand in LDS, one place per thread and head. part_b [2][nblk][h][r], part_w
 // [2][nblk][g][r]; part_rot [b,s,g][RW] where all heads share a rotation (d_rot is then
 // their sum over g). HPP: head slots of a token (all a wave has, with HB = 0 or 2).
-// Bound by the vector pipes (63 % busy) and by registers: about 230, two waves per SIMD, so
-// that loads in flight are few. Sizes as at k_qk_fwd: 5.9 GB in 1.63 to 1.69 ms (3.6 TB/s), and
-// 46 us in float32. Queries and keys one after the other need fewer registers but more
-// passes: 1.71 ms; a launch bound of three or four waves spills.
+// Registers decide: about 230, so two waves per SIMD, whose loads are issued when their token
+// starts; neither the vector pipes (64 % busy) nor memory (3.5 TB/s) is at its end. Sizes as at
+// k_qk_fwd: 5.9 GB in 1.65 to 1.81 ms, 1.69 on average, and 48 us in float32. Queries and keys
+// one after the other need fewer registers but more passes (1.71 ms where this took 1.63); a
+// launch bound of three or four waves spills.
 template <typename T, int LPR, int ROT, int C, int HB, int HPP, bool VEC>
 __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q, const T* __restrict__ k,
                                                 const float* __restrict__ wq, const float* __restrict__ wk,
@@ -763,7 +764,7 @@ __global__ __launch_bounds__(QKT) void k_qk_bwd(QkGeo g, const T* __restrict__ q
 
 // The sums of the blocks' partials, in double and in a fixed order: d_w over the n_w
 // rows of part_w [2][n_w][r], d_b over the n_b rows of part_b [2][n_b][hr]. A workgroup
-// takes 16 columns of one of them, 64 threads each. 12 us beside 1.63 ms of k_qk_bwd.
+// takes 16 columns of one of them, 64 threads each. 12 us beside 1.69 ms of k_qk_bwd.
 __global__ __launch_bounds__(1024) void k_qk_sum(const float* __restrict__ part_w, int n_w, int r,
                                                  float* __restrict__ d_wq, float* __restrict__ d_wk,
                                                  const float* __restrict__ part_b, int n_b, int hr,

@@ -66,8 +66,8 @@ int make_qk_plan(const moments_qk_desc* d, QkPlan* P, bool bases) {
   g.rinv = 1.0f / (float)d->r;
   // The rules below on 8 x 8192 tokens of two channels, 64 heads in 8 groups, r = 128, bf16
   // ("large"), and 2 x 2048 of two, 16 heads, r = 64, float ("small"), forward and backward.
-  // Whole pieces, or, where alignment does not allow them, element by element: large 1.26 and
-  // 1.66 ms against 4.4 and 10.1, small 25 and 48 us against 148 and 543.
+  // Whole pieces, or, where alignment does not allow them, element by element: large 1.24 and
+  // 1.69 ms against 4.4 and 10.1, small 24 and 48 us against 148 and 543.
   P->vec = bases && g.r % 8 == 0 && qs * tsz % 16 == 0 && ks * tsz % 16 == 0 && A % 4 == 0;
   // 16 lanes for rows that 8 would do: small 29 and 58 us.
   P->LPR = g.r <= 64 && P->vec ? 8 : 16;
