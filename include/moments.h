@@ -324,6 +324,130 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
                    void* d_q, void* d_k, float* d_wq, float* d_wk, float* d_bq, float* d_bk, void* d_rot,
                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gated linear recurrence: a state and a decay for each channel.
+ *   h[t] = a[t] h[t-1] + u[t],  h[-1] = h0;   y[t] = h[t] silu(z[t])   (without z: y[t] = h[t])
+ * where the gate g gives, desc->gate,
+ *   MOMENTS_GATE_LOG : a = exp(g),    u = x                    (g a log-decay, as da above)
+ *   MOMENTS_GATE_MIX : a = sigma(g),  u = (1 - a) x            (a mean of the state and x)
+ *   MOMENTS_GATE_UNIT: a = sigma(g),  u = sqrt(1 - a^2) x      (x of unit variance keeps it so)
+ * with sigma the logistic function. x, g and z are [b,s,w] in desc->dtype, each token's w values
+ * together and tokens x_stride, g_stride and z_stride elements apart (0: w), so they may be columns
+ * of one projection; they may start at any element (two channels are read as one piece where bases,
+ * strides and w allow it, else one at a time). All else starts at 16 bytes; y is [b,s,w], dense.
+ * States are float32 [b,w]: h0 (NULL: zeros), h_last (the state after the last valid token; NULL: not
+ * wanted). valid_len and valid_lens are those of moments_desc: rows of y, and of every gradient, past
+ * a sequence's length are zero, whatever the inputs hold there; a sequence of length 0 leaves
+ * h_last = h0. A decay below 2^-126 (g below -87.3, -inf among it) is exactly zero: such a token
+ * starts its sequence anew, whatever stood before, infinities and NaN too (1 - a below 2^-126 may be
+ * zero likewise). Otherwise a value that is
+ * not finite reaches its channel's later tokens (in the gradients its earlier ones too) and no other.
+ *
+ * moments_rec_bwd is the vector-Jacobian product: d_y[b,s,w] (desc->dtype) and d_h_last[b,w] (float32,
+ * NULL: zeros) to d_x, d_g, d_z in desc->dtype, [b,s,w] dense, and d_h0 (float32); any of them may be
+ * NULL (not wanted), d_z has to be without z. moments_rec_fwd_save also leaves, in the caller's
+ * buffer `saved` of moments_rec_saved_size() bytes, states along the sequences, as
+ * moments_rec_bwd_saved reads them (opaque; same descriptor and inputs); moments_rec_bwd makes these
+ * itself from one more pass over x and g. h_last may be the buffer h0, and d_h0 the buffer d_h_last;
+ * no other output may overlap an input or another output.
+ *
+ * moments_rec_step is one token of each sequence (desc->s = 1) on a pool of states state[nslots,w],
+ * slots as in moments_attn_step.
+ *
+ * Supported: s <= 2^28, w <= 2^24, b * w / 64 (each rounded up) below 2^22, strides up to 2^40;
+ * b or s may be 0 (with s = 0 h_last is h0 and d_h0 is d_h_last). Ownership, errors and
+ * MOMENTS_CHECK_FINITE are those stated above; moments_rec_fwd may need no workspace. */
+typedef enum { MOMENTS_GATE_LOG = 0, MOMENTS_GATE_MIX = 1, MOMENTS_GATE_UNIT = 2 } moments_gate_kind;
+
+typedef struct {
+  int64_t b, s, w;                       /* batch, sequence, channels */
+  int64_t valid_len;                     /* positions >= valid_len are padding; >= s acts as s */
+  int64_t x_stride, g_stride, z_stride;  /* elements between tokens, or 0: w */
+  int32_t dtype;                         /* moments_dtype */
+  int32_t gate;                          /* moments_gate_kind */
+  int32_t has_z;                         /* 1: y is gated by z; 0: z and d_z are NULL */
+  int32_t reserved;                      /* 0 */
+  const int32_t* valid_lens;             /* per-sequence lengths [b] on the device, or NULL */
+} moments_rec_desc;
+
+int moments_rec_validate(const moments_rec_desc* desc);
+int64_t moments_rec_workspace_size(const moments_rec_desc* desc, int is_bwd);
+int64_t moments_rec_saved_size(const moments_rec_desc* desc);
+int moments_rec_fwd(const moments_rec_desc* desc, const void* x, const void* g, const void* z, const float* h0,
+                    void* y, float* h_last, void* workspace, size_t workspace_bytes, void* stream);
+int moments_rec_fwd_save(const moments_rec_desc* desc, const void* x, const void* g, const void* z, const float* h0,
+                         void* y, float* h_last, void* saved, size_t saved_bytes, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int moments_rec_bwd(const moments_rec_desc* desc, const void* x, const void* g, const void* z, const float* h0,
+                    const void* d_y, const float* d_h_last, void* d_x, void* d_g, void* d_z, float* d_h0,
+                    void* workspace, size_t workspace_bytes, void* stream);
+int moments_rec_bwd_saved(const moments_rec_desc* desc, const void* x, const void* g, const void* z, const float* h0,
+                          const void* saved, size_t saved_bytes, const void* d_y, const float* d_h_last, void* d_x,
+                          void* d_g, void* d_z, float* d_h0, void* workspace, size_t workspace_bytes, void* stream);
+int moments_rec_step(const moments_rec_desc* desc, const void* x, const void* g, const void* z, const int32_t* slots,
+                     int64_t nslots, float* state, void* y, void* stream);
+
+/* Layer norm of rows, with the residual stream added before it where there is one:
+ *   sum = x + res,   y = (sum - mean) / sqrt(var + eps) * weight + bias
+ * with the mean and the variance (the mean square about the mean) of each row. x is [n,w] in
+ * desc->dtype, rows x_stride elements apart (0: w) from any element on (rows of whole 16-byte pieces,
+ * with base and stride alike, are read as such, others one element at a time). The residual stream is
+ * float32 whatever desc->dtype is, so that a stack's many additions do not round to 8 bits: res[n,w]
+ * and sum[n,w] are there if desc->residual is 1 and NULL if it is 0 (then x itself is normed). weight
+ * [w] and bias [w] (NULL: none) are float32; y is [n,w] in desc->dtype. All but x start at 16 bytes.
+ *
+ * moments_ln_bwd is the vector-Jacobian product at d_y (desc->dtype) and, with a residual, d_sum
+ * (float32: the cotangent of sum from whatever else reads it; NULL: zeros). Its x is what was normed:
+ * with a residual the forward's sum (float32, dense), else x. It gives d_x in desc->dtype, dense, with a
+ * residual d_res too (the same values in float32), d_weight and d_bias (float32, summed over the rows in
+ * a fixed order); any of them may be NULL. sum may be the buffer res, and d_res the buffer d_sum; no
+ * other output may overlap an input or another output.
+ *
+ * Supported: w <= 16384, eps from 1e-30, n <= 2^40; n may be 0 (d_weight and d_bias are then
+ * zeros). A row that holds an infinity or a NaN is NaN. Ownership, errors and MOMENTS_CHECK_FINITE are
+ * those stated above. */
+typedef struct {
+  int64_t n, w;      /* rows, columns */
+  int64_t x_stride;  /* elements between rows of x, or 0: w */
+  int32_t dtype;     /* moments_dtype */
+  int32_t residual;  /* 1: with res and sum */
+  float eps;
+  int32_t reserved;  /* 0 */
+} moments_ln_desc;
+
+int64_t moments_ln_workspace_size(const moments_ln_desc* desc);
+int moments_ln_fwd(const moments_ln_desc* desc, const void* x, const float* res, const float* weight,
+                   const float* bias, void* y, float* sum, void* stream);
+int moments_ln_bwd(const moments_ln_desc* desc, const void* x, const float* weight, const void* d_y,
+                   const float* d_sum, void* d_x, float* d_res, float* d_weight, float* d_bias, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Global norm of many gradients, and their clipping:
+ *   norm = sqrt(sum over the spans' values of v^2),   out = v * min(1, max_norm / (norm + 1e-6))
+ * A span is n values of either dtype from any element on; `out` NULL (or p) writes in place. The
+ * array of spans is the host's and is read during the call only; the norm is one float32 on the
+ * device, so that a program may join it with other ranks' before it clips (a sum of squares). A norm that is
+ * not finite leaves the values as they are (out of place: copies them). Squares are summed in double, in a
+ * fixed order. max_norm is a finite or infinite number from 0 on.
+ *
+ * moments_grad_validate checks the spans, also that no span's output overlaps another span or output
+ * (a tensor listed twice would be scaled twice): EINVAL. The other calls do not repeat that last
+ * check. Supported: up to 2^20 spans of up to 2^40 values; spans may be empty, and there may be
+ * none. Neither call waits. Errors are those stated above; with MOMENTS_CHECK_FINITE moments_grad_norm
+ * checks the norm. */
+typedef struct {
+  const void* p;     /* values, device memory */
+  void* out;         /* where the clipped values go, or NULL: in place */
+  int64_t n;
+  int32_t dtype;     /* moments_dtype */
+  int32_t reserved;  /* 0 */
+} moments_span;
+
+int moments_grad_validate(const moments_span* spans, int64_t count);
+int64_t moments_grad_workspace_size(const moments_span* spans, int64_t count);
+int moments_grad_norm(const moments_span* spans, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                      void* stream);
+int moments_grad_clip(const moments_span* spans, int64_t count, const float* norm, float max_norm, void* stream);
+
 const char* moments_strerror(int code);
 int moments_last_hip_error(void);
 

@@ -11,8 +11,8 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import (BF16, F32, ROT_HALF, ROT_NONE, ROT_PAIRWISE, ROT_QUAT, AttnDesc, Desc,  # noqa: F401
-                   MomentsError, QkDesc)
+from ._lib import (BF16, F32, GATE_LOG, GATE_MIX, GATE_UNIT, ROT_HALF, ROT_NONE, ROT_PAIRWISE,  # noqa: F401
+                   ROT_QUAT, AttnDesc, Desc, LnDesc, MomentsError, QkDesc, RecDesc)
 
 __all__ = ["make_desc", "set_valid_lens", "moments_validate", "moments_workspace_size", "moments_fwd", "moments_fwd_static",
            "moments_bwd", "moments_saved_size", "moments_fwd_save", "moments_bwd_saved", "rot_desc", "moments_rot_workspace_size", "moments_rot_fwd", "moments_rot_bwd",
@@ -20,7 +20,11 @@ __all__ = ["make_desc", "set_valid_lens", "moments_validate", "moments_workspace
            "attn_desc", "moments_attn_validate", "moments_attn_workspace_size", "moments_attn_saved_size",
            "moments_attn_fwd", "moments_attn_fwd_save", "moments_attn_bwd", "moments_attn_bwd_saved",
            "moments_attn_step", "qk_desc", "moments_qk_workspace_size", "moments_qk_fwd", "moments_qk_bwd",
-           "AttnDesc", "QkDesc",
+           "rec_desc", "moments_rec_validate", "moments_rec_workspace_size", "moments_rec_saved_size",
+           "moments_rec_fwd", "moments_rec_fwd_save", "moments_rec_bwd", "moments_rec_bwd_saved", "moments_rec_step",
+           "ln_desc", "moments_ln_workspace_size", "moments_ln_fwd", "moments_ln_bwd",
+           "grad_desc", "moments_grad_workspace_size", "moments_grad_norm", "moments_grad_clip",
+           "AttnDesc", "QkDesc", "RecDesc", "LnDesc", "GradDesc", "GATE_LOG", "GATE_MIX", "GATE_UNIT",
            "Desc", "MomentsError", "ROT_NONE", "ROT_PAIRWISE", "ROT_HALF", "ROT_QUAT"]
 
 
@@ -643,6 +647,334 @@ def moments_qk_bwd(desc: QkDesc, q, k, wq, wk, bq, bk, rot, d_qhat, d_khat,
     ws = _buffer("workspace", moments_qk_workspace_size(desc), dev, workspace)
     _lib.check(_lib.load().moments_qk_bwd(ctypes.byref(desc), *ins, *cot, *grads, *_scratch(ws), _stream_of(dev)))
     return out
+
+
+# ---------------------------------------------------------------- gated linear recurrence
+def _row_stride(name, t, w):
+    """Elements between tokens of t [b,s,w] (0 where any would do)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a torch.Tensor of three dimensions")
+    if t.is_contiguous():
+        return w if t.shape[0] * t.shape[1] > 1 else 0
+    b, s, n = t.shape
+    if t.numel() == 0:
+        return 0
+    sb, ss, sw = t.stride()
+    step = ss if s > 1 else (sb if b > 1 else n)
+    if (n > 1 and sw != 1) or step < n or (b > 1 and s > 1 and sb != s * step):
+        raise ValueError(f"{name} must hold each token's values together, tokens a fixed stride apart")
+    return step
+
+
+def rec_desc(x, g, z=None, gate=GATE_LOG, valid_len=None, valid_lens=None) -> RecDesc:
+    """Descriptor of the gated linear recurrence for x, g and (or None) z [b,s,w]; they
+    may be columns of one projection: each token's values together, tokens a fixed stride
+    apart. ``valid_len`` defaults to s; ``valid_lens`` as in make_desc."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a torch.Tensor [b,s,w]")
+    b, s, w = x.shape
+    d = RecDesc(b, s, w, s if valid_len is None else int(valid_len), _row_stride("x", x, w), _row_stride("g", g, w),
+                0 if z is None else _row_stride("z", z, w), BF16 if x.dtype is torch.bfloat16 else F32, int(gate),
+                0 if z is None else 1)
+    return set_valid_lens(d, valid_lens) if valid_lens is not None else d
+
+
+def moments_rec_validate(desc: RecDesc) -> int:
+    return _lib.load().moments_rec_validate(ctypes.byref(desc))
+
+
+def moments_rec_workspace_size(desc: RecDesc, is_bwd: bool) -> int:
+    return _size(_lib.load().moments_rec_workspace_size(ctypes.byref(desc), int(bool(is_bwd))))
+
+
+def moments_rec_saved_size(desc: RecDesc) -> int:
+    """Bytes of the buffer of moments_rec_fwd_save / moments_rec_bwd_saved."""
+    return _size(_lib.load().moments_rec_saved_size(ctypes.byref(desc)))
+
+
+def _rec_inputs(desc: RecDesc, x, g, z, h0):
+    """Checks the inputs against the descriptor (all on x's device). Returns the device
+    and their addresses."""
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a torch.Tensor")
+    dev, dt = x.device, _DTYPES.get(desc.dtype)
+    if desc.valid_lens:
+        ref = getattr(desc, "_valid_lens_ref", None)
+        if ref is None or ref.data_ptr() != desc.valid_lens:
+            raise ValueError("set per-sequence lengths with set_valid_lens (the descriptor keeps the tensor)")
+        if ref.device != dev:
+            raise ValueError(f"valid_lens is on {ref.device}, the inputs on {dev}")
+    b, s, w = desc.b, desc.s, desc.w
+    if (z is not None) != bool(desc.has_z):
+        raise ValueError("z must be None when the descriptor has no z" if z is not None else "z is required")
+    ptrs = []
+    for name, t, stride in (("x", x, desc.x_stride), ("g", g, desc.g_stride), ("z", z, desc.z_stride)):
+        if t is None and name == "z":
+            ptrs.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a torch.Tensor")
+        if t.shape != (b, s, w) or t.dtype is not dt or t.device != dev:
+            raise ValueError(f"{name} must be {dt} of shape {(b, s, w)} on {dev}, got {t.dtype} {tuple(t.shape)} "
+                             f"on {t.device}")
+        step = _row_stride(name, t, w) or w   # also one token's values have to lie together
+        if b * s > 1 and step != (stride or w):
+            raise ValueError(f"{name} has another token stride than the descriptor ({stride or w})")
+        ptrs.append(t.data_ptr())
+    return dev, dt, [*ptrs, *_tensors_ok(dev, (("h0", h0, (b, w), torch.float32, True),))]
+
+
+def _rec_forward(desc, x, g, z, h0, y, h_last, saved, want_saved, workspace):
+    dev, dt, ins = _rec_inputs(desc, x, g, z, h0)
+    shape, state = (desc.b, desc.s, desc.w), (desc.b, desc.w)
+    if y is not None or h_last is not None:
+        _tensors_ok(dev, (("y", y, shape, dt, True), ("h_last", h_last, state, torch.float32, True)))
+    lib = _gpu(dev)
+    ws = _buffer("workspace", moments_rec_workspace_size(desc, False), dev, workspace)
+    if want_saved:
+        saved = _buffer("saved", moments_rec_saved_size(desc), dev, saved)
+    _wrote(y, h_last, saved)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dev)
+    if h_last is None:
+        h_last = torch.empty(state, dtype=torch.float32, device=dev)
+    head = (ctypes.byref(desc), *ins, y.data_ptr(), h_last.data_ptr())
+    tail = (*_scratch(ws), _stream_of(dev))
+    if want_saved:
+        _lib.check(lib.moments_rec_fwd_save(*head, *_scratch(saved), *tail))
+        return y, h_last, torch.empty(0, dtype=torch.uint8, device=dev) if saved is None else saved
+    _lib.check(lib.moments_rec_fwd(*head, *tail))
+    return y, h_last
+
+
+def moments_rec_fwd(desc: RecDesc, x, g, z=None, h0=None, y=None, h_last=None, workspace=None):
+    """The gated recurrence over a whole sequence: returns (y [b,s,w] in the input dtype,
+    h_last [b,w] float32)."""
+    return _rec_forward(desc, x, g, z, h0, y, h_last, None, False, workspace)
+
+
+def moments_rec_fwd_save(desc: RecDesc, x, g, z=None, h0=None, y=None, h_last=None, saved=None, workspace=None):
+    """moments_rec_fwd that also keeps states along the sequences. Returns (y, h_last,
+    saved); saved is opaque, for moments_rec_bwd_saved."""
+    return _rec_forward(desc, x, g, z, h0, y, h_last, saved, True, workspace)
+
+
+def moments_rec_bwd(desc: RecDesc, x, g, z, h0, d_y, d_h_last=None, want=("x", "g", "z", "h0"), out=None,
+                    workspace=None, _saved=None):
+    """Returns dict d_x, d_g, d_z (input dtype, dense), d_h0 (float32); None when not
+    wanted (d_z, d_h0: or when there is no z, no h0)."""
+    dev, dt, ins = _rec_inputs(desc, x, g, z, h0)
+    cot = _tensors_ok(dev, (("d_y", d_y, (desc.b, desc.s, desc.w), dt, False),
+                            ("d_h_last", d_h_last, (desc.b, desc.w), torch.float32, True)))
+    out, grads = _gradients(dev, want, out, {"x": x, "g": g, "z": z, "h0": h0})
+    lib = _lib.load()
+    ws = _buffer("workspace", moments_rec_workspace_size(desc, True), dev, workspace)
+    tail = (*cot, *grads, *_scratch(ws), _stream_of(dev))
+    if _saved is None:
+        _lib.check(lib.moments_rec_bwd(ctypes.byref(desc), *ins, *tail))
+    else:
+        sv = _buffer("saved", moments_rec_saved_size(desc), dev, _saved)
+        _lib.check(lib.moments_rec_bwd_saved(ctypes.byref(desc), *ins, *_scratch(sv), *tail))
+    return out
+
+
+def moments_rec_bwd_saved(desc: RecDesc, x, g, z, h0, saved, d_y, d_h_last=None, want=("x", "g", "z", "h0"),
+                          out=None, workspace=None):
+    """moments_rec_bwd reading what moments_rec_fwd_save kept. Same returns."""
+    if saved is None:
+        raise ValueError("saved is required")
+    return moments_rec_bwd(desc, x, g, z, h0, d_y, d_h_last, want=want, out=out, workspace=workspace, _saved=saved)
+
+
+def moments_rec_step(desc: RecDesc, x, g, z, state, slots=None, y=None):
+    """One token of each sequence (s = 1) on a pool of states, state [nslots,w] float32,
+    updated in place; ``slots`` as in moments_attn_step. Returns y [b,1,w]."""
+    dev, dt, ins = _rec_inputs(desc, x, g, z, None)
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise ValueError("state must be a torch.Tensor [nslots,w]")
+    n = state.shape[0]
+    st, sl, out = _tensors_ok(dev, (("state", state, (n, desc.w), torch.float32, False),
+                                    ("slots", slots, (desc.b,), torch.int32, True),
+                                    ("y", y, (desc.b, desc.s, desc.w), dt, True)))
+    lib = _gpu(dev)
+    _wrote(state, y)
+    if y is None:
+        y = torch.empty((desc.b, desc.s, desc.w), dtype=dt, device=dev)
+        out = y.data_ptr()
+    _lib.check(lib.moments_rec_step(ctypes.byref(desc), *ins[:3], sl, n, st, out, _stream_of(dev)))
+    return y
+
+
+# ---------------------------------------------------------------- layer norm
+def _flat_rows(name, t, w):
+    """Rows of t [..., w] and the elements between them (0: dense)."""
+    if not isinstance(t, torch.Tensor) or t.dim() < 1 or t.shape[-1] != w:
+        raise ValueError(f"{name} must be a torch.Tensor of rows of {w}")
+    n = t.numel() // w if w else 0
+    if t.is_contiguous() or n == 0:
+        return n, 0
+    dims = [(size, step) for size, step in zip(t.shape[:-1], t.stride()[:-1]) if size > 1]
+    step = dims[-1][1] if dims else w
+    want = step
+    for size, st in reversed(dims):
+        if st != want:
+            raise ValueError(f"{name} must have its rows a fixed stride apart")
+        want = st * size
+    if (w > 1 and t.stride(-1) != 1) or step < w:
+        raise ValueError(f"{name} must hold each row's values together")
+    return n, step if dims else 0
+
+
+def ln_desc(x, eps=1e-5, residual=False) -> LnDesc:
+    """Descriptor of layer norm for x [..., w], whose rows may be columns of a wider tensor
+    (a fixed stride apart); ``residual``: with a float32 residual stream added before it."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a torch.Tensor of rows")
+    n, step = _flat_rows("x", x, x.shape[-1])
+    return LnDesc(n, x.shape[-1], step, BF16 if x.dtype is torch.bfloat16 else F32, int(bool(residual)), float(eps))
+
+
+def moments_ln_workspace_size(desc: LnDesc) -> int:
+    """Bytes of the backward's workspace (the forward needs none)."""
+    return _size(_lib.load().moments_ln_workspace_size(ctypes.byref(desc)))
+
+
+def _ln_x(desc, name, x, dt, stride):
+    if not isinstance(x, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    n, step = _flat_rows(name, x, desc.w)
+    if n != desc.n or x.dtype is not dt:
+        raise ValueError(f"{name} must be {desc.n} rows of {dt}, got {n} of {x.dtype}")
+    if n > 1 and (step or desc.w) != (stride or desc.w):
+        raise ValueError(f"{name} has another row stride than the descriptor ({stride or desc.w})")
+    return x.device
+
+
+def moments_ln_fwd(desc: LnDesc, x, weight, bias=None, res=None, y=None, sum=None):
+    """Returns (y, sum): the normed rows in the input dtype and, with a residual, x + res in
+    float32 (else None), both of x's shape. ``sum`` may be ``res``."""
+    dt = _DTYPES.get(desc.dtype)
+    dev = _ln_x(desc, "x", x, dt, desc.x_stride)
+    if not desc.residual and (res is not None or sum is not None):
+        raise ValueError("res and sum must be None when the descriptor has no residual")
+    f32 = torch.float32
+    wp, bp, rp, yp, sp = _tensors_ok(dev, (
+        ("weight", weight, (desc.w,), f32, False), ("bias", bias, (desc.w,), f32, True),
+        ("res", res, x.shape, f32, not desc.residual), ("y", y, x.shape, dt, True), ("sum", sum, x.shape, f32, True)))
+    lib = _gpu(dev)
+    _wrote(y, sum)
+    if y is None:
+        y = torch.empty(x.shape, dtype=dt, device=dev)
+    if sum is None and desc.residual:
+        sum = torch.empty(x.shape, dtype=f32, device=dev)
+    _lib.check(lib.moments_ln_fwd(ctypes.byref(desc), x.data_ptr(), rp, wp, bp, y.data_ptr(),
+                                  None if sum is None else sum.data_ptr(), _stream_of(dev)))
+    return y, sum
+
+
+def moments_ln_bwd(desc: LnDesc, x, weight, bias, d_y, d_sum=None, want=("x", "res", "weight", "bias"), out=None,
+                   workspace=None):
+    """x is what was normed: the forward's sum with a residual, else its x. Returns dict
+    d_x (input dtype, dense), d_res (float32, with a residual), d_weight, d_bias (float32);
+    None when not wanted or not defined. d_res may be ``d_sum``."""
+    dt, f32 = _DTYPES.get(desc.dtype), torch.float32
+    dev = _ln_x(desc, "x", x, f32 if desc.residual else dt, 0 if desc.residual else desc.x_stride)
+    if not desc.residual and d_sum is not None:
+        raise ValueError("d_sum must be None when the descriptor has no residual")
+    wp, _, yp, sp = _tensors_ok(dev, (("weight", weight, (desc.w,), f32, False), ("bias", bias, (desc.w,), f32, True),
+                                      ("d_y", d_y, x.shape, dt, False), ("d_sum", d_sum, x.shape, f32, True)))
+    like = {"x": _like(x.shape, dt), "res": _like(x.shape, f32) if desc.residual else None, "weight": weight,
+            "bias": bias}
+    out, grads = _gradients(dev, want, out, like)
+    lib = _lib.load()
+    ws = _buffer("workspace", moments_ln_workspace_size(desc), dev, workspace)
+    _lib.check(lib.moments_ln_bwd(ctypes.byref(desc), x.data_ptr(), wp, yp, sp, *grads, *_scratch(ws),
+                                  _stream_of(dev)))
+    return out
+
+
+class _like:
+    """Shape and dtype of a gradient, as _gradients reads them of an input."""
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype = shape, dtype
+
+
+# ---------------------------------------------------------------- gradients' norm and clipping
+class GradDesc:
+    """Gradients and where their clipped values go; keeps the tensors. See grad_desc."""
+
+    def __init__(self, grads, out):
+        self.grads, self.out = list(grads), list(grads if out is None else out)
+        self.in_place = out is None
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"out holds {len(self.out)} tensors, grads {len(self.grads)}")
+        self.device = None
+        spans = (_lib.Span * max(len(self.grads), 1))()
+        for i, (t, o) in enumerate(zip(self.grads, self.out)):
+            if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError(f"grads[{i}] must be a float32 or bfloat16 torch.Tensor")
+            if self.device is None:
+                self.device = t.device
+            if t.device != self.device:
+                raise ValueError(f"grads[{i}] is on {t.device}, the others on {self.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"grads[{i}] must be contiguous")
+            if o is not t:
+                _expect(f"out[{i}]", o, t.shape, t.dtype, t.device)
+            spans[i] = _lib.Span(t.data_ptr(), o.data_ptr(), t.numel(), BF16 if t.dtype is torch.bfloat16 else F32)
+        self.spans, self.count = spans, len(self.grads)
+
+
+def grad_desc(grads, out=None) -> GradDesc:
+    """Descriptor of many gradients (contiguous float32 or bfloat16 tensors on one device),
+    for moments_grad_norm and moments_grad_clip; it keeps the tensors, which may be refilled
+    between calls. ``out``: tensors like them that take the clipped values (None: in place).
+    Raises if a tensor that is written overlaps another."""
+    d = GradDesc(grads, out)
+    rc = _lib.load().moments_grad_validate(d.spans, d.count)
+    if rc == _lib.EINVAL:
+        raise ValueError("two of the tensors overlap (a gradient listed twice?)")
+    _lib.check(rc)
+    d.workspace_bytes = _size(_lib.load().moments_grad_workspace_size(d.spans, d.count))
+    return d
+
+
+def moments_grad_workspace_size(desc: GradDesc) -> int:
+    return desc.workspace_bytes
+
+
+def _grad_device(desc, norm):
+    dev = desc.device if desc.device is not None else (norm.device if isinstance(norm, torch.Tensor) else None)
+    if dev is None:
+        raise ValueError("norm is required when there are no gradients")
+    return dev
+
+
+def moments_grad_norm(desc: GradDesc, norm=None, workspace=None):
+    """The root of the sum of all values' squares: a float32 scalar on the device. Ranks that
+    hold shares of the gradients join their norms' squares before clipping."""
+    dev = _grad_device(desc, norm)
+    _tensors_ok(dev, (("norm", norm, (), torch.float32, True),))
+    lib = _gpu(dev)
+    ws = _buffer("workspace", desc.workspace_bytes, dev, workspace)
+    _wrote(norm)
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    _lib.check(lib.moments_grad_norm(desc.spans, desc.count, norm.data_ptr(), *_scratch(ws), _stream_of(dev)))
+    return norm
+
+
+def moments_grad_clip(desc: GradDesc, norm, max_norm):
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or into the
+    descriptor's ``out``; a norm that is not finite leaves them as they are. Returns the
+    tensors that hold the result."""
+    dev = _grad_device(desc, norm)
+    (at,) = _tensors_ok(dev, (("norm", norm, (), torch.float32, False),))
+    lib = _gpu(dev)
+    _wrote(*desc.out)
+    _lib.check(lib.moments_grad_clip(desc.spans, desc.count, at, float(max_norm), _stream_of(dev)))
+    return desc.out
 
 
 def kernel_chunk_len() -> int:

@@ -1,11 +1,12 @@
 """Build the HIP library libmoments.so for gfx950 (in-tree, under _build/).
 
-Five translation units: moments.hip (the moments' C ABI, the dispatcher and
+Eight translation units: moments.hip (the moments' C ABI, the dispatcher and
 every kernel of theirs but the lane-pair forward), fwd4.hip twice, for the
 lane-pair forward's instances that do not save carries (with the ILP
 machine-scheduling strategy) and for those that do (default strategy), attn.hip
-(linear attention with a decay for each head) and qk.hip (norms of queries and
-keys with the rotation). They are compiled in parallel and linked with no
+(linear attention with a decay for each head), qk.hip (norms of queries and
+keys with the rotation), rec.hip (the gated linear recurrence), ln.hip (layer norm
+with the residual stream) and grad.hip (gradients' norm and clipping). They are compiled in parallel and linked with no
 undefined symbols allowed."""
 from __future__ import annotations
 
@@ -32,6 +33,9 @@ UNITS = {
     "fwd4_save.o": ("fwd4.hip", ["-DMOM_FWD4_SAVE=1"]),
     "attn.o": ("attn.hip", []),
     "qk.o": ("qk.hip", []),
+    "rec.o": ("rec.hip", []),
+    "ln.o": ("ln.hip", []),
+    "grad.o": ("grad.hip", []),
 }
 
 

@@ -1,0 +1,287 @@
+// Layer norm of rows, with the residual stream added before it, and its gradients: kernels.
+//
+//   s = x (+ res),  d = s - mean(s),  y = d rstd weight (+ bias),  rstd = 1 / sqrt(mean(d^2) + eps)
+//   gy = d_y weight,  d_s = rstd (gy - mean(gy) - xhat mean(gy xhat)) (+ d_sum),  xhat = d rstd
+//   d_weight = sum of d_y xhat over the rows,  d_bias = sum of d_y
+//
+// A row lies in the registers of NT threads, E elements each, and is read once. The mean is taken
+// twice: the first, of s, may be off by the rounding of a sum of large values, so the second
+// reduction carries sum(d) beside sum(d^2) and what is left of the mean leaves d and the variance.
+// The gradients make the statistics again, with their own two sums in that same reduction, so
+// nothing is kept from the forward.
+#pragma once
+
+#include "common.h"
+
+namespace mom {
+
+struct LnGeo {
+  int64_t n;
+  int w;
+  size_t xs;    // elements between rows of x
+  float eps, winv;
+};
+
+constexpr float kLnScale = 8.271806125530277e-25f;   // 2^-80
+
+// Columns of a thread: whole 8-element pieces NT pieces apart, or (VEC false) elements NT apart.
+template <int NT, bool VEC> __device__ __forceinline__ int ln_col(int i, int tid) {
+  return VEC ? ((i >> 3) * NT + tid) * 8 + (i & 7) : i * NT + tid;
+}
+
+template <typename T, int NT, int E, bool VEC>
+__device__ __forceinline__ void ln_load(float (&v)[E], const T* p, int w, int tid) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int k = 0; k < E / 8; k++) {
+      const int c = (k * NT + tid) * 8;
+      if (c < w) {
+        if constexpr (sizeof(T) == 2) {
+          const u4 r = *reinterpret_cast<const u4*>(p + c);
+#pragma unroll
+          for (int j = 0; j < 4; j++) v[8 * k + 2 * j] = bf16_lo(r[j]), v[8 * k + 2 * j + 1] = bf16_hi(r[j]);
+        } else {
+          const f4 r0 = *reinterpret_cast<const f4*>(p + c), r1 = *reinterpret_cast<const f4*>(p + c + 4);
+#pragma unroll
+          for (int j = 0; j < 4; j++) v[8 * k + j] = r0[j], v[8 * k + 4 + j] = r1[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[8 * k + j] = 0.0f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; i++) v[i] = i * NT + tid < w ? to_f(p[i * NT + tid]) : 0.0f;
+  }
+}
+
+template <typename T, int NT, int E, bool VEC>
+__device__ __forceinline__ void ln_store(T* p, const float (&v)[E], int w, int tid) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int k = 0; k < E / 8; k++) {
+      const int c = (k * NT + tid) * 8;
+      if (c < w) {
+        if constexpr (sizeof(T) == 2) {
+          u4 r;
+#pragma unroll
+          for (int j = 0; j < 4; j++) r[j] = pk_bf16(v[8 * k + 2 * j], v[8 * k + 2 * j + 1]);
+          *reinterpret_cast<u4*>(p + c) = r;
+        } else {
+          f4 r0, r1;
+#pragma unroll
+          for (int j = 0; j < 4; j++) r0[j] = v[8 * k + j], r1[j] = v[8 * k + 4 + j];
+          *reinterpret_cast<f4*>(p + c) = r0;
+          *reinterpret_cast<f4*>(p + c + 4) = r1;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; i++)
+      if (i * NT + tid < w) p[i * NT + tid] = to_t<T>(v[i]);
+  }
+}
+
+// Sums over the NT threads of a row, in a fixed order; every thread gets them. Consecutive
+// calls alternate between two places in LDS, so one barrier each is enough.
+template <int NT> struct LnSum {
+  float* lds;   // [2][NT / 64][4]
+  int buf = 0;
+  template <int M> __device__ __forceinline__ void operator()(float (&v)[M]) {
+#pragma unroll
+    for (int i = 0; i < M; i++) v[i] = col4_sum(row16_sum(v[i]));
+    if constexpr (NT > 64) {
+      float* at = lds + buf * (NT / 64) * 4;
+      buf ^= 1;
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < M; i++) at[(threadIdx.x >> 6) * 4 + i] = v[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < M; i++) v[i] = at[i];
+#pragma unroll
+      for (int k = 1; k < NT / 64; k++)
+#pragma unroll
+        for (int i = 0; i < M; i++) v[i] += at[k * 4 + i];
+    }
+  }
+};
+
+// d = scale (s - mean), zero past the row's end, and the row's sums: m[0] of what is left of the
+// mean, m[1] of d^2, with GY also m[2] of gy = dy wt and m[3] of gy d. d and the sums are of the
+// centred row. The first mean is taken about s0, the row's first value, so that a row of one value
+// is centred to exact zeros, however large it is.
+template <int NT, int E, bool VEC, bool GY, class Sum>
+__device__ __forceinline__ void ln_center(const LnGeo& g, const float (&s)[E], const float (&dy)[E],
+                                          const float (&wt)[E], float s0, float scale, float (&d)[E],
+                                          float (&m)[GY ? 4 : 2], int tid, Sum& sum) {
+  float one[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < E; i++)
+    if (ln_col<NT, VEC>(i, tid) < g.w) one[0] = fmaf(fmaf(s[i], scale, -s0 * scale), g.winv, one[0]);
+  sum(one);
+  const float mean = fmaf(s0, scale, one[0]);
+#pragma unroll
+  for (int i = 0; i < (GY ? 4 : 2); i++) m[i] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E; i++) {
+    d[i] = ln_col<NT, VEC>(i, tid) < g.w ? fmaf(s[i], scale, -mean) : 0.0f;
+    m[0] += d[i];
+    m[1] = fmaf(d[i], d[i], m[1]);
+    if constexpr (GY) {
+      const float gy = dy[i] * wt[i];
+      m[2] += gy;
+      m[3] = fmaf(gy, d[i], m[3]);
+    }
+  }
+  sum(m);
+  const float off = m[0] * g.winv;
+#pragma unroll
+  for (int i = 0; i < E; i++) d[i] = ln_col<NT, VEC>(i, tid) < g.w ? d[i] - off : 0.0f;
+  m[1] = fmaf(-off, m[0], m[1]);
+  if (m[1] < 0.0f) m[1] = 0.0f;   // NaN stays
+  if constexpr (GY) m[3] = fmaf(-off, m[2], m[3]);
+}
+
+// The row's d and the rstd that goes with it. A row whose squares (or differences) overflow is
+// centred again at 2^-80 of its size, where eps is nothing beside them; one that holds an infinity
+// or a NaN stays NaN.
+template <int NT, int E, bool VEC, bool GY, class Sum>
+__device__ __forceinline__ float ln_stats(const LnGeo& g, const float (&s)[E], const float (&dy)[E],
+                                          const float (&wt)[E], float s0, float (&d)[E], float (&m)[GY ? 4 : 2],
+                                          float& scale, int tid, Sum& sum) {
+  scale = 1.0f;
+  float eps = g.eps;
+  ln_center<NT, E, VEC, GY>(g, s, dy, wt, s0, scale, d, m, tid, sum);
+  if (!(m[1] < __builtin_inff())) {   // the same for all threads of the row
+    scale = kLnScale;
+    eps = 0.0f;
+    ln_center<NT, E, VEC, GY>(g, s, dy, wt, s0, scale, d, m, tid, sum);
+  }
+  return 1.0f / sqrtf(fmaf(m[1], g.winv, eps));
+}
+
+// Rows are dealt to the workgroups (to their waves, where a wave has a row) one after the other.
+template <typename T, int NT, int E, bool VEC, bool RES>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_fwd(LnGeo g, const T* __restrict__ x, const float* res,
+                                                                const float* __restrict__ weight,
+                                                                const float* __restrict__ bias, T* __restrict__ y,
+                                                                float* total) {
+  constexpr int NB = NT == 64 ? 256 : NT, RPB = NB / NT;
+  __shared__ float lds[NT > 64 ? NT / 64 * 8 : 1];
+  const int tid = NT == 64 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  LnSum<NT> sum{lds};
+  float wt[E], bs[E];
+  ln_load<float, NT, E, VEC>(wt, weight, g.w, tid);
+  if (bias != nullptr) {
+    ln_load<float, NT, E, VEC>(bs, bias, g.w, tid);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; i++) bs[i] = 0.0f;
+  }
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + (NT == 64 ? threadIdx.x >> 6 : 0); row < g.n; row += step) {
+    float s[E], d[E], m[2], scale, s0 = to_f(x[(size_t)row * g.xs]);
+    ln_load<T, NT, E, VEC>(s, x + (size_t)row * g.xs, g.w, tid);
+    if constexpr (RES) {
+      float r[E];
+      s0 += res[(size_t)row * g.w];
+      ln_load<float, NT, E, VEC>(r, res + (size_t)row * g.w, g.w, tid);
+#pragma unroll
+      for (int i = 0; i < E; i++) s[i] += r[i];
+      ln_store<float, NT, E, VEC>(total + (size_t)row * g.w, s, g.w, tid);
+    }
+    const float rstd = ln_stats<NT, E, VEC, false>(g, s, s, s, s0, d, m, scale, tid, sum);
+#pragma unroll
+    for (int i = 0; i < E; i++) d[i] = fmaf(d[i] * rstd, wt[i], bs[i]);
+    ln_store<T, NT, E, VEC>(y + (size_t)row * g.w, d, g.w, tid);
+  }
+}
+
+// part: a row of w sums for each workgroup, of d_weight, then of d_bias (NULL: neither is wanted).
+// TS: of the normed rows (float where a residual was added).
+template <typename T, typename TS, int NT, int E, bool VEC>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_bwd(LnGeo g, const TS* __restrict__ x,
+                                                                const float* __restrict__ weight,
+                                                                const T* __restrict__ dy, const float* d_sum,
+                                                                T* __restrict__ d_x, float* d_res,
+                                                                float* __restrict__ part) {
+  constexpr int RPB = NT == 64 ? 4 : 1;
+  __shared__ float lds[NT > 64 ? NT / 64 * 8 : RPB * 64 * E];
+  const int tid = NT == 64 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  const int wave = NT == 64 ? (int)(threadIdx.x >> 6) : 0;
+  LnSum<NT> sum{lds};
+  float wt[E], dw[E], db[E];
+  ln_load<float, NT, E, VEC>(wt, weight, g.w, tid);
+#pragma unroll
+  for (int i = 0; i < E; i++) dw[i] = db[i] = 0.0f;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + wave; row < g.n; row += step) {
+    float s[E], v[E], d[E], m[4], scale;
+    const float s0 = to_f(x[(size_t)row * g.xs]);
+    ln_load<TS, NT, E, VEC>(s, x + (size_t)row * g.xs, g.w, tid);
+    ln_load<T, NT, E, VEC>(v, dy + (size_t)row * g.w, g.w, tid);
+    const float rstd = ln_stats<NT, E, VEC, true>(g, s, v, wt, s0, d, m, scale, tid, sum);
+    const float m1 = m[2] * g.winv, m2 = m[3] * g.winv * rstd, rs = rstd * scale;
+#pragma unroll
+    for (int i = 0; i < E; i++) {
+      const float xhat = d[i] * rstd;
+      db[i] += v[i];
+      dw[i] = fmaf(v[i], xhat, dw[i]);
+      d[i] = rs * (fmaf(v[i], wt[i], -m1) - xhat * m2);
+    }
+    if (d_sum != nullptr) {
+      ln_load<float, NT, E, VEC>(s, d_sum + (size_t)row * g.w, g.w, tid);
+#pragma unroll
+      for (int i = 0; i < E; i++) d[i] += s[i];
+    }
+    if (d_x != nullptr) ln_store<T, NT, E, VEC>(d_x + (size_t)row * g.w, d, g.w, tid);
+    if (d_res != nullptr) ln_store<float, NT, E, VEC>(d_res + (size_t)row * g.w, d, g.w, tid);
+  }
+  if (part == nullptr) return;
+  float* pw = part + (size_t)blockIdx.x * g.w;
+  float* pb = pw + (size_t)gridDim.x * g.w;
+  if constexpr (NT == 64) {   // the four waves' sums first
+    for (int k = 0; k < 2; k++) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < E; i++) lds[(wave * E + i) * 64 + tid] = k == 0 ? dw[i] : db[i];
+      __syncthreads();
+      if (wave == 0) {
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < E; i++)
+          v[i] = (lds[i * 64 + tid] + lds[(E + i) * 64 + tid]) + (lds[(2 * E + i) * 64 + tid] + lds[(3 * E + i) * 64 + tid]);
+        ln_store<float, NT, E, VEC>(k == 0 ? pw : pb, v, g.w, tid);
+      }
+    }
+  } else {
+    ln_store<float, NT, E, VEC>(pw, dw, g.w, tid);
+    ln_store<float, NT, E, VEC>(pb, db, g.w, tid);
+  }
+}
+
+// The parameters' gradients from np partial rows each (zeros for none), summed in double: 64
+// columns a workgroup, its 16 waves take every 16th row. blockIdx.y: 0 d_weight, 1 d_bias.
+__global__ __launch_bounds__(1024) void k_ln_sum(const float* __restrict__ part, int np, int w, float* d_weight,
+                                                 float* d_bias) {
+  __shared__ double lds[16][64];
+  float* out = blockIdx.y == 0 ? d_weight : d_bias;
+  if (out == nullptr) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = (int)blockIdx.x * 64 + lane;
+  double s = 0.0;
+  if (c < w) {
+    const float* p = part + (size_t)blockIdx.y * np * w + c;
+#pragma unroll 4
+    for (int k = wave; k < np; k += 16) s += (double)p[(size_t)k * w];
+  }
+  lds[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || c >= w) return;
+  for (int k = 1; k < 16; k++) s += lds[k][lane];
+  out[c] = (float)s;
+}
+
+}  // namespace mom

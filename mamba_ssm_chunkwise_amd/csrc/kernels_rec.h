@@ -1,0 +1,524 @@
+// Gated linear recurrence with a decay for each channel: kernels.
+//
+//   h[t] = a[t] h[t-1] + u[t],  y[t] = h[t] silu(z[t])     (no z: y = h)
+//   LOG : a = exp(g), u = x;   MIX : a = s(g), u = (1-a) x;   UNIT: a = s(g), u = sqrt(1-a^2) x
+//
+// A lane has V neighbouring channels and REC_R tokens that follow each other; the waves of a
+// workgroup have the same channels and one run of tokens after the other, so a wave reads whole
+// pieces of rows and nothing crosses lanes. A run is the map h -> P h + H of its entering state;
+// the waves exchange (P, H) through LDS, once for a tile of all their runs, and every wave
+// applies those before its own. What enters the next tile stays in registers. The next tile's
+// rows are in flight meanwhile.
+//
+// A decay of exactly zero (below 2^-126) clears: what stood before, infinities and NaN too, is
+// gone. In a run's map that is a sign bit on P, which no product of decays has by itself, so a
+// product that only underflows is told apart from it.
+#pragma once
+
+#include "common.h"
+
+namespace mom {
+
+constexpr int REC_W = 16;              // waves of a workgroup
+constexpr int REC_T = REC_W * 64;      // its threads
+constexpr int REC_R = 8;               // tokens of a lane in the forward walks
+constexpr int REC_RB = 4;              // in the gradients' walk
+constexpr int REC_TILE = REC_W * REC_R;
+constexpr int REC_SAVE = REC_W * REC_RB;   // tokens between saved states: a tile of the gradients' walk
+
+struct RecGeo {
+  int b, s, w;
+  int V;               // min(valid_len, s)
+  int ncg;             // channel groups (64 * channels of a lane)
+  int nseg;            // segments of a sequence
+  int seg;             // tokens of a segment, whole tiles
+  size_t xs, gs, zs;   // elements between tokens
+  const int* lens;
+};
+
+__device__ __forceinline__ int rec_len(const RecGeo& g, int bi) {
+  if (g.lens == nullptr) return g.V;
+  const int v = g.lens[bi];
+  return v < 0 ? 0 : (v < g.V ? v : g.V);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kExpMin = -87.336544f;   // exp of less is below 2^-126
+
+template <typename T, int V> struct RecVec { typedef T type __attribute__((ext_vector_type(V))); };
+template <typename T> struct RecVec<T, 1> { typedef T type; };
+template <typename T, int V> using rvec = typename RecVec<T, V>::type;
+
+template <typename T, int V> __device__ __forceinline__ float rec_get(const rvec<T, V>& v, int i) {
+  if constexpr (V == 1) return to_f(v); else return to_f((T)v[i]);
+}
+template <typename T, int V> __device__ __forceinline__ void rec_put(T* p, const float (&f)[V]) {
+  rvec<T, V> v;
+  if constexpr (V == 1) v = to_t<T>(f[0]);
+  else {
+#pragma unroll
+    for (int i = 0; i < V; i++) v[i] = to_t<T>(f[i]);
+  }
+  *reinterpret_cast<rvec<T, V>*>(p) = v;
+}
+template <typename T, int V> __device__ __forceinline__ rvec<T, V> rec_ld(const T* p) {
+  return *reinterpret_cast<const rvec<T, V>*>(p);
+}
+
+// The decay a, and for the logistic gates b = 1 - a and the input's factor f (else 1). The
+// logistic of the smaller side is q = e / (1 + e) with e = exp(-|g|); the larger is 1 - q, whose one
+// rounding is half that of a reciprocal near 1 and without its bias, which a long memory would
+// add up (against 64 bits, gates from 4 to 9: mean 0.065 units of 2^-24 and rms 0.65 by the
+// reciprocal). sqrt(1 - a^2) = sqrt(b (1 + a)) takes the root of e as an exponential, exp(-|g| / 2),
+// so that it does not vanish where b leaves the range (the instruction has no subnormal results).
+template <int GATE> __device__ __forceinline__ void rec_gate(float g, float& a, float& b, float& f) {
+  if constexpr (GATE == 0) {
+    a = g < kExpMin ? 0.0f : __builtin_amdgcn_exp2f(g * kLog2e);
+    b = 0.0f;
+    f = 1.0f;
+  } else {
+    const float h = __builtin_amdgcn_exp2f(-fabsf(g) * (GATE == 1 ? kLog2e : 0.5f * kLog2e));
+    const float e = GATE == 1 ? h : h * h;
+    const float r = __builtin_amdgcn_rcpf(1.0f + e), q = e * r;
+    const float p = 1.0f - q;
+    a = g < 0.0f ? (g < kExpMin ? 0.0f : q) : p;
+    b = g < 0.0f ? p : q;
+    f = GATE == 1 ? b : __builtin_amdgcn_sqrtf(r * (1.0f + a)) * (g < 0.0f ? 1.0f : h);
+  }
+}
+
+__device__ __forceinline__ float rec_sigma(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
+}
+
+// h after a token; the run's map after a token more; a map applied; a map after another.
+__device__ __forceinline__ float rec_next(float a, float h, float u) { return a == 0.0f ? u : fmaf(a, h, u); }
+__device__ __forceinline__ float rec_prod(float P, float a) { return a == 0.0f ? -1.0f : P * a; }
+__device__ __forceinline__ float rec_apply(float P, float H, float h) {
+  return __float_as_int(P) < 0 ? H : fmaf(P, h, H);
+}
+__device__ __forceinline__ float rec_chain(float P, float next) { return __float_as_int(next) < 0 ? next : P * next; }
+
+// Rows of a tensor at a lane's channels: token t of the sequence whose first token is at p.
+template <typename T, int V, int R>
+__device__ __forceinline__ void rec_rows(rvec<T, V> (&r)[R], const T* p, size_t stride, int t0, int last) {
+#pragma unroll
+  for (int i = 0; i < R; i++) r[i] = rec_ld<T, V>(p + (size_t)min(t0 + i, last) * stride);
+}
+
+// Where a workgroup stands: its sequence, its lanes' channels and its segment's tokens.
+struct RecAt {
+  int bi, seg, ch, Vb, t0, t1;
+  bool on;   // the lane has channels
+  __device__ RecAt(const RecGeo& g, int V) {
+    const int items = g.b * g.ncg;
+    seg = (int)blockIdx.x / items;
+    const int it = (int)blockIdx.x % items;
+    bi = it / g.ncg;
+    const int c = (it % g.ncg) * 64 * V + (int)(threadIdx.x & 63) * V;
+    on = c < g.w;
+    ch = on ? c : 0;
+    Vb = rec_len(g, bi);
+    t0 = min(seg * g.seg, Vb);
+    t1 = seg == g.nseg - 1 ? Vb : min(t0 + g.seg, Vb);
+  }
+};
+
+// Zeros in the rows of a segment's share that hold no token: past the sequence's length, and
+// past the batch's.
+template <typename T, int V>
+__device__ __forceinline__ void rec_zero_rows(const RecGeo& g, const RecAt& at, T* out, int wave) {
+  if (!at.on || out == nullptr) return;
+  const float zero[V] = {};
+  T* p = out + ((size_t)at.bi * g.s) * g.w + at.ch;
+  const int per = (g.s - g.V + g.nseg - 1) / g.nseg;
+  const int a0 = max(at.Vb, min(at.seg * g.seg, g.V)), a1 = at.seg == g.nseg - 1 ? g.V : min((at.seg + 1) * g.seg, g.V);
+  for (int t = a0 + wave; t < a1; t += REC_W) rec_put<T, V>(p + (size_t)t * g.w, zero);
+  const int b0 = g.V + min(at.seg * per, g.s - g.V), b1 = g.V + min((at.seg + 1) * per, g.s - g.V);
+  for (int t = b0 + wave; t < b1; t += REC_W) rec_put<T, V>(p + (size_t)t * g.w, zero);
+}
+
+// The maps of the segments before a workgroup's own, in order, on the state that enters the
+// first. part: [segment][b][w] of P, then of H; first: [b][w].
+template <int V>
+__device__ __forceinline__ void rec_enter(const RecGeo& g, const RecAt& at, const float* part, const float* first,
+                                          bool back, float (&h)[V]) {
+  const size_t n = (size_t)g.b * g.w, o = (size_t)at.bi * g.w + at.ch;
+  const float* H = part + (size_t)g.nseg * n;
+#pragma unroll
+  for (int i = 0; i < V; i++) h[i] = first[o + i];
+  const int from = back ? g.nseg - 1 : 0, step = back ? -1 : 1;
+  for (int k = from; k != at.seg; k += step)
+#pragma unroll
+    for (int i = 0; i < V; i++) h[i] = rec_apply(part[k * n + o + i], H[k * n + o + i], h[i]);
+}
+
+// The map of a segment: every wave walks a run of its own and the waves' maps are joined at the
+// end. BACK: of the cotangent c[t] = a[t] (d_y[t] silu(z[t]) + c[t+1]), from the last token.
+// The outermost segment also copies the state that enters it, which the caller's output may
+// overwrite before another workgroup has read it.
+template <typename T, int GATE, bool Z, int V, bool BACK>
+__global__ __launch_bounds__(REC_T) void k_rec_seg(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
+                                                   const T* __restrict__ z, const float* __restrict__ h0,
+                                                   float* __restrict__ part, float* __restrict__ first) {
+  __shared__ float sp[REC_W][64][V], sh[REC_W][64][V];
+  const RecAt at(g, V);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const size_t n = (size_t)g.b * g.w, o = (size_t)at.bi * g.w + at.ch;
+  if (at.seg == (BACK ? g.nseg - 1 : 0) && wave == 0 && at.on)
+#pragma unroll
+    for (int i = 0; i < V; i++) first[o + i] = h0 ? h0[o + i] : 0.0f;
+  const int per = (at.t1 - at.t0 + REC_W - 1) / REC_W;
+  const int r0 = min(at.t0 + wave * per, at.t1), r1 = min(r0 + per, at.t1);
+  const size_t row = (size_t)at.bi * g.s;
+  const T* xp = x + row * (BACK ? (size_t)g.w : g.xs) + at.ch;   // BACK: d_y
+  const T* gp = gg + row * g.gs + at.ch;
+  const T* zp = Z ? z + row * g.zs + at.ch : nullptr;
+  const size_t xst = BACK ? (size_t)g.w : g.xs;
+  float P[V], H[V];
+#pragma unroll
+  for (int i = 0; i < V; i++) P[i] = 1.0f, H[i] = 0.0f;
+  constexpr int R = REC_R;
+  rvec<T, V> rx[R], rg[R], rz[R];
+  auto fetch = [&](int k) {   // run k of the wave's tokens, from its end where BACK
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+      const int t = BACK ? max(r1 - 1 - (k * R + i), r0) : min(r0 + k * R + i, r1 - 1);
+      rx[i] = rec_ld<T, V>(xp + (size_t)t * xst);
+      rg[i] = rec_ld<T, V>(gp + (size_t)t * g.gs);
+      if constexpr (Z && BACK) rz[i] = rec_ld<T, V>(zp + (size_t)t * g.zs);
+    }
+  };
+  const int nr = (r1 - r0 + R - 1) / R;
+  if (nr > 0) fetch(0);
+  for (int k = 0; k < nr; k++) {
+    rvec<T, V> cx[R], cg[R], cz[R];
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+      cx[i] = rx[i];
+      cg[i] = rg[i];
+      if constexpr (Z && BACK) cz[i] = rz[i];
+    }
+    if (k + 1 < nr) fetch(k + 1);
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+      if (k * R + i < r1 - r0) {
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+          float a, b, f;
+          rec_gate<GATE>(rec_get<T, V>(cg[i], j), a, b, f);
+          float v = rec_get<T, V>(cx[i], j);
+          if constexpr (BACK) {
+            if constexpr (Z) {
+              const float zz = rec_get<T, V>(cz[i], j);
+              v *= zz * rec_sigma(zz);
+            }
+            H[j] = a == 0.0f ? 0.0f : a * (v + H[j]);
+          } else {
+            H[j] = rec_next(a, H[j], GATE == 0 ? v : f * v);
+          }
+          P[j] = rec_prod(P[j], a);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; j++) sp[wave][lane][j] = P[j], sh[wave][lane][j] = H[j];
+  __syncthreads();
+  if (wave != 0 || !at.on) return;
+  for (int k = 1; k < REC_W; k++) {
+    const int from = BACK ? REC_W - 1 - k : k;
+    if (k == 1 && BACK)
+#pragma unroll
+      for (int j = 0; j < V; j++) P[j] = sp[REC_W - 1][lane][j], H[j] = sh[REC_W - 1][lane][j];
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+      H[j] = rec_apply(sp[from][lane][j], sh[from][lane][j], H[j]);
+      P[j] = rec_chain(P[j], sp[from][lane][j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; j++) {
+    part[(size_t)at.seg * n + o + j] = P[j];
+    part[(size_t)(g.nseg + at.seg) * n + o + j] = H[j];
+  }
+}
+
+// The forward walk of a segment. OUT: with y; else only the states that `save` keeps, the one
+// entering every REC_SAVE tokens, [b][ceil(V / REC_SAVE)][w].
+template <typename T, int GATE, bool Z, int V, bool OUT>
+__global__ __launch_bounds__(REC_T) void k_rec_fwd(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
+                                                   const T* __restrict__ z, const float* h0,
+                                                   const float* __restrict__ part, const float* __restrict__ first,
+                                                   T* __restrict__ y, float* h_last, float* __restrict__ save) {
+  constexpr int R = REC_R, W = REC_W;
+  __shared__ float sp[2][W][64][V], sh[2][W][64][V];
+  const RecAt at(g, V);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const size_t row = (size_t)at.bi * g.s, o = (size_t)at.bi * g.w + at.ch;
+  const T* xp = x + row * g.xs + at.ch;
+  const T* gp = gg + row * g.gs + at.ch;
+  const T* zp = Z ? z + row * g.zs + at.ch : nullptr;
+  T* yp = OUT ? y + row * g.w + at.ch : nullptr;
+  const int nsv = (g.V + REC_SAVE - 1) / REC_SAVE;
+  float h[V];
+  if (g.nseg > 1) {
+    rec_enter<V>(g, at, part, first, false, h);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j++) h[j] = h0 ? h0[o + j] : 0.0f;
+  }
+  const int last = at.Vb - 1;
+  rvec<T, V> rx[R], rg[R], rz[R];
+  auto fetch = [&](int t) {
+    rec_rows<T, V, R>(rx, xp, g.xs, t, last);
+    rec_rows<T, V, R>(rg, gp, g.gs, t, last);
+    if constexpr (Z && OUT) rec_rows<T, V, R>(rz, zp, g.zs, t, last);
+  };
+  if (at.t0 < at.t1) fetch(at.t0 + wave * R);
+  int buf = 0;
+  for (int t = at.t0; t < at.t1; t += REC_TILE, buf ^= 1) {
+    const int tw = t + wave * R, cnt = min(at.Vb - tw, R);   // this wave's tokens
+    float a[R][V], u[R][V], P[V], H[V];
+    rvec<T, V> cz[R];
+#pragma unroll
+    for (int j = 0; j < V; j++) P[j] = 1.0f, H[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+      if constexpr (Z && OUT) cz[i] = rz[i];
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        float b, f;
+        rec_gate<GATE>(rec_get<T, V>(rg[i], j), a[i][j], b, f);
+        const float v = rec_get<T, V>(rx[i], j);
+        u[i][j] = i < cnt ? (GATE == 0 ? v : f * v) : 0.0f;
+        a[i][j] = i < cnt ? a[i][j] : 1.0f;
+        P[j] = rec_prod(P[j], a[i][j]);
+        H[j] = rec_next(a[i][j], H[j], u[i][j]);
+      }
+    }
+    if (t + REC_TILE < at.t1) fetch(tw + REC_TILE);
+#pragma unroll
+    for (int j = 0; j < V; j++) sp[buf][wave][lane][j] = P[j], sh[buf][wave][lane][j] = H[j];
+    __syncthreads();   // the other buffer is written again only past the next one
+    float in[V];
+#pragma unroll
+    for (int k = 0; k < W; k++) {
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        if (k == wave) in[j] = h[j];
+        h[j] = rec_apply(sp[buf][k][lane][j], sh[buf][k][lane][j], h[j]);
+      }
+    }
+    if (save != nullptr && (wave * R) % REC_SAVE == 0 && tw < at.Vb && at.on) {
+      float* sv = save + ((size_t)at.bi * nsv + tw / REC_SAVE) * g.w + at.ch;
+#pragma unroll
+      for (int j = 0; j < V; j++) sv[j] = in[j];
+    }
+    if constexpr (OUT) {
+#pragma unroll
+      for (int i = 0; i < R; i++) {
+        float out[V];
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+          in[j] = rec_next(a[i][j], in[j], u[i][j]);
+          out[j] = in[j];
+          if constexpr (Z) {
+            const float zz = rec_get<T, V>(cz[i], j);
+            out[j] *= zz * rec_sigma(zz);
+          }
+        }
+        if (i < cnt && at.on) rec_put<T, V>(yp + (size_t)(tw + i) * g.w, out);
+      }
+    }
+  }
+  if constexpr (OUT) {
+    if (h_last != nullptr && at.seg == g.nseg - 1) {
+      __syncthreads();   // h_last may be h0: every wave has read it
+      if (wave == 0 && at.on)
+#pragma unroll
+        for (int j = 0; j < V; j++) h_last[o + j] = h[j];
+    }
+    rec_zero_rows<T, V>(g, at, y, wave);
+  }
+}
+
+// The gradients' walk of a segment, from its last tile to its first: the states of a tile again
+// from the saved one that enters it, and the cotangent c[t] = a[t] delta[t] that the tokens hand
+// to the left, the waves' maps of both exchanged at once.
+template <typename T, int GATE, bool Z, int V>
+__global__ __launch_bounds__(REC_T) void k_rec_bwd(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
+                                                   const T* __restrict__ z, const float* __restrict__ save,
+                                                   const T* __restrict__ dy, const float* d_last,
+                                                   const float* __restrict__ part, const float* __restrict__ first,
+                                                   T* __restrict__ d_x, T* __restrict__ d_g, T* __restrict__ d_z,
+                                                   float* d_h0) {
+  constexpr int R = REC_RB, W = REC_W, TL = REC_SAVE;
+  __shared__ float sp[2][W][64][V], sh[2][W][64][V], sc[2][W][64][V];
+  const RecAt at(g, V);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const size_t row = (size_t)at.bi * g.s, o = (size_t)at.bi * g.w + at.ch;
+  const T* xp = x + row * g.xs + at.ch;
+  const T* gp = gg + row * g.gs + at.ch;
+  const T* zp = Z ? z + row * g.zs + at.ch : nullptr;
+  const T* dp = dy + row * g.w + at.ch;
+  const int nsv = (g.V + TL - 1) / TL, last = at.Vb - 1;
+  const float* sv = save + (size_t)at.bi * nsv * g.w + at.ch;
+  float c[V];   // from the right
+  if (g.nseg > 1) {
+    rec_enter<V>(g, at, part, first, true, c);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j++) c[j] = d_last ? d_last[o + j] : 0.0f;
+  }
+  rvec<T, V> rx[R], rg[R], rz[R], rd[R];
+  float hs[V];
+  auto fetch = [&](int n) {
+    const int t = at.t0 + n * TL + wave * R;
+    rec_rows<T, V, R>(rx, xp, g.xs, t, last);
+    rec_rows<T, V, R>(rg, gp, g.gs, t, last);
+    if constexpr (Z) rec_rows<T, V, R>(rz, zp, g.zs, t, last);
+    rec_rows<T, V, R>(rd, dp, (size_t)g.w, t, last);
+#pragma unroll
+    for (int j = 0; j < V; j++) hs[j] = sv[(size_t)(at.t0 / TL + n) * g.w + j];
+  };
+  const int nt = (at.t1 - at.t0 + TL - 1) / TL;
+  if (nt > 0) fetch(nt - 1);
+  int buf = 0;
+  for (int n = nt - 1; n >= 0; n--, buf ^= 1) {
+    const int tw = at.t0 + n * TL + wave * R, cnt = min(at.Vb - tw, R);
+    float a[R][V], b[R][V], f[R][V], xx[R][V], s[R][V], P[V], H[V], C[V], h[V];
+    rvec<T, V> cz[R], cd[R];
+#pragma unroll
+    for (int j = 0; j < V; j++) P[j] = 1.0f, H[j] = 0.0f, C[j] = 0.0f, h[j] = hs[j];
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+      cd[i] = rd[i];
+      if constexpr (Z) cz[i] = rz[i];
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        rec_gate<GATE>(rec_get<T, V>(rg[i], j), a[i][j], b[i][j], f[i][j]);
+        xx[i][j] = i < cnt ? rec_get<T, V>(rx[i], j) : 0.0f;
+        float v = rec_get<T, V>(cd[i], j);
+        if constexpr (Z) {
+          const float zz = rec_get<T, V>(cz[i], j);
+          v *= zz * rec_sigma(zz);
+        }
+        s[i][j] = i < cnt ? v : 0.0f;
+        a[i][j] = i < cnt ? a[i][j] : 1.0f;
+        f[i][j] = i < cnt ? f[i][j] : 0.0f;
+        P[j] = rec_prod(P[j], a[i][j]);
+        H[j] = rec_next(a[i][j], H[j], GATE == 0 ? xx[i][j] : f[i][j] * xx[i][j]);
+      }
+    }
+#pragma unroll
+    for (int i = R - 1; i >= 0; i--)
+#pragma unroll
+      for (int j = 0; j < V; j++) C[j] = a[i][j] == 0.0f ? 0.0f : a[i][j] * (s[i][j] + C[j]);
+    if (n > 0) fetch(n - 1);
+#pragma unroll
+    for (int j = 0; j < V; j++)
+      sp[buf][wave][lane][j] = P[j], sh[buf][wave][lane][j] = H[j], sc[buf][wave][lane][j] = C[j];
+    __syncthreads();
+    float cin[V];
+#pragma unroll
+    for (int k = 0; k < W - 1; k++)
+      if (k < wave)
+#pragma unroll
+        for (int j = 0; j < V; j++) h[j] = rec_apply(sp[buf][k][lane][j], sh[buf][k][lane][j], h[j]);
+#pragma unroll
+    for (int k = W - 1; k >= 0; k--)
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        if (k == wave) cin[j] = c[j];
+        c[j] = rec_apply(sp[buf][k][lane][j], sc[buf][k][lane][j], c[j]);
+      }
+    float before[R][V];
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+      float out[V];
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        before[i][j] = h[j];
+        h[j] = rec_next(a[i][j], h[j], GATE == 0 ? xx[i][j] : f[i][j] * xx[i][j]);
+        if constexpr (Z) {
+          const float zz = rec_get<T, V>(cz[i], j), sg = rec_sigma(zz);
+          out[j] = rec_get<T, V>(cd[i], j) * h[j] * (sg * fmaf(zz, 1.0f - sg, 1.0f));
+        }
+      }
+      if constexpr (Z)
+        if (d_z != nullptr && i < cnt && at.on) rec_put<T, V>(d_z + (row + tw + i) * g.w + at.ch, out);
+    }
+#pragma unroll
+    for (int i = R - 1; i >= 0; i--) {
+      float ox[V], og[V];
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        const float d = s[i][j] + cin[j], aa = a[i][j];
+        float q;
+        if constexpr (GATE == 0) {
+          ox[j] = d;
+          q = before[i][j];
+        } else {
+          ox[j] = f[i][j] * d;
+          if constexpr (GATE == 1) q = b[i][j] * (before[i][j] - xx[i][j]);
+          else q = b[i][j] * before[i][j] - aa * xx[i][j] * (f[i][j] * __builtin_amdgcn_rcpf(1.0f + aa));
+        }
+        og[j] = aa == 0.0f ? 0.0f : aa * q * d;
+        cin[j] = aa == 0.0f ? 0.0f : aa * d;
+      }
+      if (i < cnt && at.on) {
+        const size_t e = (row + tw + i) * g.w + at.ch;
+        if (d_x != nullptr) rec_put<T, V>(d_x + e, ox);
+        if (d_g != nullptr) rec_put<T, V>(d_g + e, og);
+      }
+    }
+  }
+  if (d_h0 != nullptr && at.seg == 0) {
+    __syncthreads();   // d_h0 may be d_h_last: every wave has read it
+    if (wave == 0 && at.on)
+#pragma unroll
+      for (int j = 0; j < V; j++) d_h0[o + j] = c[j];
+  }
+  rec_zero_rows<T, V>(g, at, d_x, wave);
+  rec_zero_rows<T, V>(g, at, d_g, wave);
+  if constexpr (Z) rec_zero_rows<T, V>(g, at, d_z, wave);
+}
+
+// One token of each sequence on a pool of states.
+template <typename T, int GATE, bool Z, int V>
+__global__ __launch_bounds__(256) void k_rec_step(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
+                                                  const T* __restrict__ z, const int* __restrict__ slots, int64_t nslots,
+                                                  float* __restrict__ state, T* __restrict__ y) {
+  const int ch = ((int)blockIdx.x * 256 + (int)threadIdx.x) * V;
+  if (ch >= g.w) return;
+  for (int bi = blockIdx.y; bi < g.b; bi += gridDim.y) {
+    const int64_t slot = slots ? (int64_t)slots[bi] : (int64_t)bi;
+    T* yp = y + (size_t)bi * g.w + ch;
+    float out[V] = {};
+    if (slot >= 0 && slot < nslots && rec_len(g, bi) > 0) {
+      float* sp = state + (size_t)slot * g.w + ch;
+      const rvec<T, V> vx = rec_ld<T, V>(x + (size_t)bi * g.xs + ch), vg = rec_ld<T, V>(gg + (size_t)bi * g.gs + ch);
+      rvec<T, V> vz;
+      if constexpr (Z) vz = rec_ld<T, V>(z + (size_t)bi * g.zs + ch);
+      rvec<float, V> st = rec_ld<float, V>(sp);
+      float h[V];
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        float a, b, f;
+        rec_gate<GATE>(rec_get<T, V>(vg, j), a, b, f);
+        const float v = rec_get<T, V>(vx, j);
+        h[j] = rec_next(a, rec_get<float, V>(st, j), GATE == 0 ? v : f * v);
+        out[j] = h[j];
+        if constexpr (Z) {
+          const float zz = rec_get<T, V>(vz, j);
+          out[j] *= zz * rec_sigma(zz);
+        }
+      }
+      rec_put<float, V>(sp, h);
+    }
+    rec_put<T, V>(yp, out);
+  }
+}
+
+}  // namespace mom

@@ -39,7 +39,9 @@ const char* const kKernelNames[KID_N] = {"k_carry", "k_scan",      "k_fwd",     
                                          "k_cscan", "k_rot_seg",   "k_rot_carry", "k_rot_apply",
                                          "k_pair",  "k_gentry",    "k_cscan_sum", "k_cscan_grp",
                                          "k_attn_state", "k_attn_scan", "k_attn_fwd", "k_attn_bwd", "k_attn_sum", "k_attn_step",
-                                         "k_qk_fwd", "k_qk_bwd", "k_qk_sum"};
+                                         "k_qk_fwd", "k_qk_bwd", "k_qk_sum",
+                                         "k_rec_seg", "k_rec_fwd", "k_rec_bwd", "k_rec_step", "k_ln_fwd", "k_ln_bwd",
+                                         "k_ln_sum", "k_grad_norm", "k_grad_total", "k_grad_clip"};
 struct Prof {
   std::mutex mu;
   bool on = false;
