@@ -15,16 +15,20 @@
 // product that only underflows is told apart from it.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace mom {
 
-constexpr int REC_W = 16;              // waves of a workgroup
-constexpr int REC_T = REC_W * 64;      // its threads
-constexpr int REC_R = 8;               // tokens of a lane in the forward walks
-constexpr int REC_RB = 4;              // in the gradients' walk
-constexpr int REC_TILE = REC_W * REC_R;
-constexpr int REC_SAVE = REC_W * REC_RB;   // tokens between saved states: a tile of the gradients' walk
+constexpr int REC_W = 16;              // waves of a workgroup of the forward walk
+template <typename T> constexpr int REC_R = 16 / sizeof(T);   // tokens of a lane there
+constexpr int REC_WB = 8;              // waves of a workgroup of the gradients' walk
+constexpr int REC_RB = 8;              // tokens of a lane there
+constexpr int REC_TILE = REC_W * REC_R<__bf16>;   // segments are whole multiples of any tile
+constexpr int REC_SAVE = REC_WB * REC_RB;   // tokens between saved states: a tile of the gradients' walk
+constexpr int REC_SW = 16;             // waves of a workgroup that makes a segment's map
+constexpr int REC_SR = 8;              // its lanes' tokens in flight
 
 struct RecGeo {
   int b, s, w;
@@ -52,17 +56,58 @@ template <typename T, int V> using rvec = typename RecVec<T, V>::type;
 template <typename T, int V> __device__ __forceinline__ float rec_get(const rvec<T, V>& v, int i) {
   if constexpr (V == 1) return to_f(v); else return to_f((T)v[i]);
 }
-template <typename T, int V> __device__ __forceinline__ void rec_put(T* p, const float (&f)[V]) {
+template <typename T, int V> __device__ __forceinline__ rvec<T, V> rec_vec(const float (&f)[V]) {
   rvec<T, V> v;
-  if constexpr (V == 1) v = to_t<T>(f[0]);
-  else {
+  if constexpr (V == 1) {
+    v = to_t<T>(f[0]);
+  } else {
 #pragma unroll
     for (int i = 0; i < V; i++) v[i] = to_t<T>(f[i]);
   }
-  *reinterpret_cast<rvec<T, V>*>(p) = v;
+  return v;
+}
+template <typename T, int V> __device__ __forceinline__ void rec_put(T* p, const float (&f)[V]) {
+  *reinterpret_cast<rvec<T, V>*>(p) = rec_vec<T, V>(f);
 }
 template <typename T, int V> __device__ __forceinline__ rvec<T, V> rec_ld(const T* p) {
   return *reinterpret_cast<const rvec<T, V>*>(p);
+}
+
+// A wave's rows of a tensor as a buffer that ends with them: rows past the sequence's end read as
+// zeros and are not written, without a branch. `n` rows from p on, `cols` columns from p's to the
+// tensor's last. A lane without channels stores at kRecPast, which is past every buffer's end.
+using RecBuf = __amdgpu_buffer_rsrc_t;
+constexpr unsigned kRecPast = 0xfffffff0u;
+template <typename T>
+__device__ __forceinline__ RecBuf rec_buf(const T* p, size_t stride, int n, int cols) {
+  const unsigned bytes = n <= 0 ? 0u : (unsigned)((n - 1) * stride + cols) * (unsigned)sizeof(T);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, bytes, 0x00027000);
+}
+template <typename T, int V> __device__ __forceinline__ rvec<T, V> rec_bld(RecBuf r, unsigned off) {
+  typedef unsigned u2 __attribute__((ext_vector_type(2)));
+  if constexpr (sizeof(T) * V == 2) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+  else if constexpr (sizeof(T) * V == 4)
+    return __builtin_bit_cast(rvec<T, V>, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+  else return __builtin_bit_cast(rvec<T, V>, (u2)__builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+}
+template <typename T, int V> __device__ __forceinline__ void rec_bst(RecBuf r, unsigned off, const float (&f)[V]) {
+  typedef unsigned u2 __attribute__((ext_vector_type(2)));
+  const rvec<T, V> v = rec_vec<T, V>(f);
+  if constexpr (sizeof(T) * V == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, off, 0, 0);
+  else if constexpr (sizeof(T) * V == 4)
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, off, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), r, off, 0, 0);
+}
+
+// Rows t0, t0 + 1, ... of a tensor at a lane's channels (p: the sequence's first row at the
+// workgroup's first channel), in flight together.
+template <typename T, int V, int R>
+__device__ __forceinline__ void rec_rows(rvec<T, V> (&r)[R], const T* p, size_t stride, int t0, int n, int cols,
+                                         unsigned lane_off) {
+  const RecBuf buf = rec_buf(p + (size_t)t0 * stride, stride, min(n, R), cols);
+  const unsigned step = (unsigned)stride * (unsigned)sizeof(T);
+#pragma unroll
+  for (int i = 0; i < R; i++) r[i] = rec_bld<T, V>(buf, lane_off + (unsigned)i * step);
 }
 
 // The decay a, and for the logistic gates b = 1 - a and the input's factor f (else 1). The
@@ -91,31 +136,59 @@ __device__ __forceinline__ float rec_sigma(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
 }
 
-// h after a token; the run's map after a token more; a map applied; a map after another.
-__device__ __forceinline__ float rec_next(float a, float h, float u) { return a == 0.0f ? u : fmaf(a, h, u); }
-__device__ __forceinline__ float rec_prod(float P, float a) { return a == 0.0f ? -1.0f : P * a; }
+// A map applied to a state; a map after another.
 __device__ __forceinline__ float rec_apply(float P, float H, float h) {
   return __float_as_int(P) < 0 ? H : fmaf(P, h, H);
 }
 __device__ __forceinline__ float rec_chain(float P, float next) { return __float_as_int(next) < 0 ? next : P * next; }
 
-// Rows of a tensor at a lane's channels: token t of the sequence whose first token is at p.
-template <typename T, int V, int R>
-__device__ __forceinline__ void rec_rows(rvec<T, V> (&r)[R], const T* p, size_t stride, int t0, int last) {
+// One token. A decay of zero (CLEAR: there may be some) forgets what it meets, NaN too; where a
+// wave's tokens hold none, as almost everywhere, nothing has to be compared.
+template <bool CLEAR> __device__ __forceinline__ float rec_next(float a, float h, float u) {
+  return CLEAR && a == 0.0f ? u : fmaf(a, h, u);
+}
+template <bool CLEAR> __device__ __forceinline__ float rec_prod(float P, float a) {
+  return CLEAR && a == 0.0f ? -1.0f : P * a;
+}
+template <bool CLEAR> __device__ __forceinline__ float rec_back(float a, float d) {
+  return CLEAR && a == 0.0f ? 0.0f : a * d;
+}
+template <int R, int V> __device__ __forceinline__ bool rec_clears(const float (&a)[R][V]) {
+  float m = a[0][0];
 #pragma unroll
-  for (int i = 0; i < R; i++) r[i] = rec_ld<T, V>(p + (size_t)min(t0 + i, last) * stride);
+  for (int i = 0; i < R; i++)
+#pragma unroll
+    for (int j = 0; j < V; j++) m = fminf(m, a[i][j]);
+  return __any(m == 0.0f);
+}
+// Keeps what is computed of v behind this point: the compiler would move what both of rec_either's
+// branches share before them, where all tokens' values are live at once.
+template <typename R> __device__ __forceinline__ void rec_pin(R& v) {
+  if constexpr (sizeof(R) == 2) {
+    unsigned w = __builtin_bit_cast(unsigned short, v);
+    asm volatile("" : "+v"(w));
+    v = __builtin_bit_cast(R, (unsigned short)w);
+  } else {
+    asm volatile("" : "+v"(v));
+  }
+}
+// Calls f(CLEAR) once.
+template <class F> __device__ __forceinline__ void rec_either(bool clears, F&& f) {
+  if (clears) f(std::integral_constant<bool, true>{});
+  else f(std::integral_constant<bool, false>{});
 }
 
 // Where a workgroup stands: its sequence, its lanes' channels and its segment's tokens.
 struct RecAt {
-  int bi, seg, ch, Vb, t0, t1;
-  bool on;   // the lane has channels
+  int bi, seg, c0, ch, Vb, t0, t1;   // c0: the workgroup's first channel, ch: the lane's (0 without one)
+  bool on;                           // the lane has channels
   __device__ RecAt(const RecGeo& g, int V) {
     const int items = g.b * g.ncg;
     seg = (int)blockIdx.x / items;
     const int it = (int)blockIdx.x % items;
     bi = it / g.ncg;
-    const int c = (it % g.ncg) * 64 * V + (int)(threadIdx.x & 63) * V;
+    c0 = (it % g.ncg) * 64 * V;
+    const int c = c0 + (int)(threadIdx.x & 63) * V;
     on = c < g.w;
     ch = on ? c : 0;
     Vb = rec_len(g, bi);
@@ -127,15 +200,15 @@ struct RecAt {
 // Zeros in the rows of a segment's share that hold no token: past the sequence's length, and
 // past the batch's.
 template <typename T, int V>
-__device__ __forceinline__ void rec_zero_rows(const RecGeo& g, const RecAt& at, T* out, int wave) {
+__device__ __forceinline__ void rec_zero_rows(const RecGeo& g, const RecAt& at, T* out, int wave, int waves) {
   if (!at.on || out == nullptr) return;
   const float zero[V] = {};
   T* p = out + ((size_t)at.bi * g.s) * g.w + at.ch;
   const int per = (g.s - g.V + g.nseg - 1) / g.nseg;
   const int a0 = max(at.Vb, min(at.seg * g.seg, g.V)), a1 = at.seg == g.nseg - 1 ? g.V : min((at.seg + 1) * g.seg, g.V);
-  for (int t = a0 + wave; t < a1; t += REC_W) rec_put<T, V>(p + (size_t)t * g.w, zero);
+  for (int t = a0 + wave; t < a1; t += waves) rec_put<T, V>(p + (size_t)t * g.w, zero);
   const int b0 = g.V + min(at.seg * per, g.s - g.V), b1 = g.V + min((at.seg + 1) * per, g.s - g.V);
-  for (int t = b0 + wave; t < b1; t += REC_W) rec_put<T, V>(p + (size_t)t * g.w, zero);
+  for (int t = b0 + wave; t < b1; t += waves) rec_put<T, V>(p + (size_t)t * g.w, zero);
 }
 
 // The maps of the segments before a workgroup's own, in order, on the state that enters the
@@ -158,17 +231,17 @@ __device__ __forceinline__ void rec_enter(const RecGeo& g, const RecAt& at, cons
 // The outermost segment also copies the state that enters it, which the caller's output may
 // overwrite before another workgroup has read it.
 template <typename T, int GATE, bool Z, int V, bool BACK>
-__global__ __launch_bounds__(REC_T) void k_rec_seg(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
+__global__ __launch_bounds__(REC_SW * 64) void k_rec_seg(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
                                                    const T* __restrict__ z, const float* __restrict__ h0,
                                                    float* __restrict__ part, float* __restrict__ first) {
-  __shared__ float sp[REC_W][64][V], sh[REC_W][64][V];
+  __shared__ float sp[REC_SW][64][V], sh[REC_SW][64][V];
   const RecAt at(g, V);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const size_t n = (size_t)g.b * g.w, o = (size_t)at.bi * g.w + at.ch;
   if (at.seg == (BACK ? g.nseg - 1 : 0) && wave == 0 && at.on)
 #pragma unroll
     for (int i = 0; i < V; i++) first[o + i] = h0 ? h0[o + i] : 0.0f;
-  const int per = (at.t1 - at.t0 + REC_W - 1) / REC_W;
+  const int per = (at.t1 - at.t0 + REC_SW - 1) / REC_SW;
   const int r0 = min(at.t0 + wave * per, at.t1), r1 = min(r0 + per, at.t1);
   const size_t row = (size_t)at.bi * g.s;
   const T* xp = x + row * (BACK ? (size_t)g.w : g.xs) + at.ch;   // BACK: d_y
@@ -178,7 +251,7 @@ __global__ __launch_bounds__(REC_T) void k_rec_seg(RecGeo g, const T* __restrict
   float P[V], H[V];
 #pragma unroll
   for (int i = 0; i < V; i++) P[i] = 1.0f, H[i] = 0.0f;
-  constexpr int R = REC_R;
+  constexpr int R = REC_SR;
   rvec<T, V> rx[R], rg[R], rz[R];
   auto fetch = [&](int k) {   // run k of the wave's tokens, from its end where BACK
 #pragma unroll
@@ -213,11 +286,11 @@ __global__ __launch_bounds__(REC_T) void k_rec_seg(RecGeo g, const T* __restrict
               const float zz = rec_get<T, V>(cz[i], j);
               v *= zz * rec_sigma(zz);
             }
-            H[j] = a == 0.0f ? 0.0f : a * (v + H[j]);
+            H[j] = rec_back<true>(a, v + H[j]);
           } else {
-            H[j] = rec_next(a, H[j], GATE == 0 ? v : f * v);
+            H[j] = rec_next<true>(a, H[j], GATE == 0 ? v : f * v);
           }
-          P[j] = rec_prod(P[j], a);
+          P[j] = rec_prod<true>(P[j], a);
         }
       }
     }
@@ -226,11 +299,11 @@ __global__ __launch_bounds__(REC_T) void k_rec_seg(RecGeo g, const T* __restrict
   for (int j = 0; j < V; j++) sp[wave][lane][j] = P[j], sh[wave][lane][j] = H[j];
   __syncthreads();
   if (wave != 0 || !at.on) return;
-  for (int k = 1; k < REC_W; k++) {
-    const int from = BACK ? REC_W - 1 - k : k;
+  for (int k = 1; k < REC_SW; k++) {
+    const int from = BACK ? REC_SW - 1 - k : k;
     if (k == 1 && BACK)
 #pragma unroll
-      for (int j = 0; j < V; j++) P[j] = sp[REC_W - 1][lane][j], H[j] = sh[REC_W - 1][lane][j];
+      for (int j = 0; j < V; j++) P[j] = sp[REC_SW - 1][lane][j], H[j] = sh[REC_SW - 1][lane][j];
 #pragma unroll
     for (int j = 0; j < V; j++) {
       H[j] = rec_apply(sp[from][lane][j], sh[from][lane][j], H[j]);
@@ -247,42 +320,42 @@ __global__ __launch_bounds__(REC_T) void k_rec_seg(RecGeo g, const T* __restrict
 // The forward walk of a segment. OUT: with y; else only the states that `save` keeps, the one
 // entering every REC_SAVE tokens, [b][ceil(V / REC_SAVE)][w].
 template <typename T, int GATE, bool Z, int V, bool OUT>
-__global__ __launch_bounds__(REC_T) void k_rec_fwd(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
+__global__ __launch_bounds__(REC_W * 64) void k_rec_fwd(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
                                                    const T* __restrict__ z, const float* h0,
                                                    const float* __restrict__ part, const float* __restrict__ first,
                                                    T* __restrict__ y, float* h_last, float* __restrict__ save) {
-  constexpr int R = REC_R, W = REC_W;
-  __shared__ float sp[2][W][64][V], sh[2][W][64][V];
+  constexpr int R = REC_R<T>, W = REC_W, TL = W * R;
+  __shared__ float sp[2][W][64][V], sh[2][W][64][V], se[2][64][V];
   const RecAt at(g, V);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const size_t row = (size_t)at.bi * g.s, o = (size_t)at.bi * g.w + at.ch;
-  const T* xp = x + row * g.xs + at.ch;
-  const T* gp = gg + row * g.gs + at.ch;
-  const T* zp = Z ? z + row * g.zs + at.ch : nullptr;
-  T* yp = OUT ? y + row * g.w + at.ch : nullptr;
-  const int nsv = (g.V + REC_SAVE - 1) / REC_SAVE;
-  float h[V];
+  const T* xp = x + row * g.xs + at.c0;
+  const T* gp = gg + row * g.gs + at.c0;
+  const T* zp = Z ? z + row * g.zs + at.c0 : nullptr;
+  T* yp = OUT ? y + row * g.w + at.c0 : nullptr;
+  const int cols = g.w - at.c0, nsv = (g.V + REC_SAVE - 1) / REC_SAVE;
+  const unsigned lo = (unsigned)(lane * V * (int)sizeof(T)), step = (unsigned)g.w * (unsigned)sizeof(T);
+  float h[V], last[V];   // last: past the tile so far, in the last wave
   if (g.nseg > 1) {
     rec_enter<V>(g, at, part, first, false, h);
   } else {
 #pragma unroll
     for (int j = 0; j < V; j++) h[j] = h0 ? h0[o + j] : 0.0f;
   }
-  const int last = at.Vb - 1;
+#pragma unroll
+  for (int j = 0; j < V; j++) last[j] = h[j];
   rvec<T, V> rx[R], rg[R], rz[R];
   auto fetch = [&](int t) {
-    rec_rows<T, V, R>(rx, xp, g.xs, t, last);
-    rec_rows<T, V, R>(rg, gp, g.gs, t, last);
-    if constexpr (Z && OUT) rec_rows<T, V, R>(rz, zp, g.zs, t, last);
+    rec_rows<T, V, R>(rx, xp, g.xs, t, at.Vb - t, cols, lo);
+    rec_rows<T, V, R>(rg, gp, g.gs, t, at.Vb - t, cols, lo);
+    if constexpr (Z && OUT) rec_rows<T, V, R>(rz, zp, g.zs, t, at.Vb - t, cols, lo);
   };
   if (at.t0 < at.t1) fetch(at.t0 + wave * R);
   int buf = 0;
-  for (int t = at.t0; t < at.t1; t += REC_TILE, buf ^= 1) {
-    const int tw = t + wave * R, cnt = min(at.Vb - tw, R);   // this wave's tokens
+  for (int t = at.t0; t < at.t1; t += TL, buf ^= 1) {
+    const int tw = t + wave * R, cnt = at.Vb - tw;   // this wave's tokens
     float a[R][V], u[R][V], P[V], H[V];
     rvec<T, V> cz[R];
-#pragma unroll
-    for (int j = 0; j < V; j++) P[j] = 1.0f, H[j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; i++) {
       if constexpr (Z && OUT) cz[i] = rz[i];
@@ -291,55 +364,77 @@ __global__ __launch_bounds__(REC_T) void k_rec_fwd(RecGeo g, const T* __restrict
         float b, f;
         rec_gate<GATE>(rec_get<T, V>(rg[i], j), a[i][j], b, f);
         const float v = rec_get<T, V>(rx[i], j);
-        u[i][j] = i < cnt ? (GATE == 0 ? v : f * v) : 0.0f;
-        a[i][j] = i < cnt ? a[i][j] : 1.0f;
-        P[j] = rec_prod(P[j], a[i][j]);
-        H[j] = rec_next(a[i][j], H[j], u[i][j]);
+        u[i][j] = GATE == 0 ? v : f * v;
+        rec_pin(a[i][j]);
+        rec_pin(u[i][j]);
       }
     }
-    if (t + REC_TILE < at.t1) fetch(tw + REC_TILE);
+    if (t + TL < at.t1) fetch(tw + TL);
+    if (cnt < R)   // padding hands the state on
+#pragma unroll
+      for (int i = 0; i < R; i++)
+#pragma unroll
+        for (int j = 0; j < V; j++) a[i][j] = i < cnt ? a[i][j] : 1.0f;
+    const bool clears = rec_clears<R, V>(a);
+    rec_either(clears, [&](auto cl) {
+#pragma unroll
+      for (int j = 0; j < V; j++) P[j] = 1.0f, H[j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < R; i++)
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+          P[j] = rec_prod<cl.value>(P[j], a[i][j]);
+          H[j] = rec_next<cl.value>(a[i][j], H[j], u[i][j]);
+        }
+    });
 #pragma unroll
     for (int j = 0; j < V; j++) sp[buf][wave][lane][j] = P[j], sh[buf][wave][lane][j] = H[j];
-    __syncthreads();   // the other buffer is written again only past the next one
-    float in[V];
+    __syncthreads();   // each buffer is written again only past the next one
+    if (t > at.t0)
 #pragma unroll
-    for (int k = 0; k < W; k++) {
+      for (int j = 0; j < V; j++) h[j] = se[buf ^ 1][lane][j];
 #pragma unroll
-      for (int j = 0; j < V; j++) {
-        if (k == wave) in[j] = h[j];
-        h[j] = rec_apply(sp[buf][k][lane][j], sh[buf][k][lane][j], h[j]);
-      }
-    }
+    for (int k = 0; k < W - 1; k++)
+      if (k < wave)
+#pragma unroll
+        for (int j = 0; j < V; j++) h[j] = rec_apply(sp[buf][k][lane][j], sh[buf][k][lane][j], h[j]);
     if (save != nullptr && (wave * R) % REC_SAVE == 0 && tw < at.Vb && at.on) {
       float* sv = save + ((size_t)at.bi * nsv + tw / REC_SAVE) * g.w + at.ch;
 #pragma unroll
-      for (int j = 0; j < V; j++) sv[j] = in[j];
+      for (int j = 0; j < V; j++) sv[j] = h[j];
     }
+    if (wave == W - 1)
+#pragma unroll
+      for (int j = 0; j < V; j++) se[buf][lane][j] = last[j] = rec_apply(P[j], H[j], h[j]);
     if constexpr (OUT) {
+      const RecBuf yb = rec_buf(yp + (size_t)tw * g.w, (size_t)g.w, min(cnt, R), cols);
+      rec_either(clears, [&](auto cl) {
 #pragma unroll
-      for (int i = 0; i < R; i++) {
-        float out[V];
+        for (int i = 0; i < R; i++) {
+          float out[V];
+          if constexpr (Z) rec_pin(cz[i]);
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-          in[j] = rec_next(a[i][j], in[j], u[i][j]);
-          out[j] = in[j];
-          if constexpr (Z) {
-            const float zz = rec_get<T, V>(cz[i], j);
-            out[j] *= zz * rec_sigma(zz);
+          for (int j = 0; j < V; j++) {
+            h[j] = rec_next<cl.value>(a[i][j], h[j], u[i][j]);
+            out[j] = h[j];
+            if constexpr (Z) {
+              const float zz = rec_get<T, V>(cz[i], j);
+              out[j] *= zz * rec_sigma(zz);
+            }
           }
+          rec_bst<T, V>(yb, at.on ? lo + (unsigned)i * step : kRecPast, out);
         }
-        if (i < cnt && at.on) rec_put<T, V>(yp + (size_t)(tw + i) * g.w, out);
-      }
+      });
     }
   }
   if constexpr (OUT) {
     if (h_last != nullptr && at.seg == g.nseg - 1) {
       __syncthreads();   // h_last may be h0: every wave has read it
-      if (wave == 0 && at.on)
+      if (wave == W - 1 && at.on)
 #pragma unroll
-        for (int j = 0; j < V; j++) h_last[o + j] = h[j];
+        for (int j = 0; j < V; j++) h_last[o + j] = last[j];
     }
-    rec_zero_rows<T, V>(g, at, y, wave);
+    rec_zero_rows<T, V>(g, at, y, wave, W);
   }
 }
 
@@ -347,38 +442,42 @@ __global__ __launch_bounds__(REC_T) void k_rec_fwd(RecGeo g, const T* __restrict
 // from the saved one that enters it, and the cotangent c[t] = a[t] delta[t] that the tokens hand
 // to the left, the waves' maps of both exchanged at once.
 template <typename T, int GATE, bool Z, int V>
-__global__ __launch_bounds__(REC_T) void k_rec_bwd(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
+__global__ __launch_bounds__(REC_WB * 64) void k_rec_bwd(RecGeo g, const T* __restrict__ x, const T* __restrict__ gg,
                                                    const T* __restrict__ z, const float* __restrict__ save,
                                                    const T* __restrict__ dy, const float* d_last,
                                                    const float* __restrict__ part, const float* __restrict__ first,
                                                    T* __restrict__ d_x, T* __restrict__ d_g, T* __restrict__ d_z,
                                                    float* d_h0) {
-  constexpr int R = REC_RB, W = REC_W, TL = REC_SAVE;
-  __shared__ float sp[2][W][64][V], sh[2][W][64][V], sc[2][W][64][V];
+  constexpr int R = REC_RB, W = REC_WB, TL = REC_SAVE;
+  __shared__ float sp[2][W][64][V], sh[2][W][64][V], sc[2][W][64][V], se[2][64][V];
   const RecAt at(g, V);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const size_t row = (size_t)at.bi * g.s, o = (size_t)at.bi * g.w + at.ch;
-  const T* xp = x + row * g.xs + at.ch;
-  const T* gp = gg + row * g.gs + at.ch;
-  const T* zp = Z ? z + row * g.zs + at.ch : nullptr;
-  const T* dp = dy + row * g.w + at.ch;
-  const int nsv = (g.V + TL - 1) / TL, last = at.Vb - 1;
+  const T* xp = x + row * g.xs + at.c0;
+  const T* gp = gg + row * g.gs + at.c0;
+  const T* zp = Z ? z + row * g.zs + at.c0 : nullptr;
+  const T* dp = dy + row * g.w + at.c0;
+  const size_t out0 = row * g.w + at.c0;
+  const int cols = g.w - at.c0, nsv = (g.V + TL - 1) / TL;
+  const unsigned lo = (unsigned)(lane * V * (int)sizeof(T)), step = (unsigned)g.w * (unsigned)sizeof(T);
   const float* sv = save + (size_t)at.bi * nsv * g.w + at.ch;
-  float c[V];   // from the right
+  float c[V], last[V];   // from the right; last: before the tile so far, in the first wave
   if (g.nseg > 1) {
     rec_enter<V>(g, at, part, first, true, c);
   } else {
 #pragma unroll
     for (int j = 0; j < V; j++) c[j] = d_last ? d_last[o + j] : 0.0f;
   }
+#pragma unroll
+  for (int j = 0; j < V; j++) last[j] = c[j];
   rvec<T, V> rx[R], rg[R], rz[R], rd[R];
   float hs[V];
   auto fetch = [&](int n) {
     const int t = at.t0 + n * TL + wave * R;
-    rec_rows<T, V, R>(rx, xp, g.xs, t, last);
-    rec_rows<T, V, R>(rg, gp, g.gs, t, last);
-    if constexpr (Z) rec_rows<T, V, R>(rz, zp, g.zs, t, last);
-    rec_rows<T, V, R>(rd, dp, (size_t)g.w, t, last);
+    rec_rows<T, V, R>(rx, xp, g.xs, t, at.Vb - t, cols, lo);
+    rec_rows<T, V, R>(rg, gp, g.gs, t, at.Vb - t, cols, lo);
+    if constexpr (Z) rec_rows<T, V, R>(rz, zp, g.zs, t, at.Vb - t, cols, lo);
+    rec_rows<T, V, R>(rd, dp, (size_t)g.w, t, at.Vb - t, cols, lo);
 #pragma unroll
     for (int j = 0; j < V; j++) hs[j] = sv[(size_t)(at.t0 / TL + n) * g.w + j];
   };
@@ -386,103 +485,116 @@ __global__ __launch_bounds__(REC_T) void k_rec_bwd(RecGeo g, const T* __restrict
   if (nt > 0) fetch(nt - 1);
   int buf = 0;
   for (int n = nt - 1; n >= 0; n--, buf ^= 1) {
-    const int tw = at.t0 + n * TL + wave * R, cnt = min(at.Vb - tw, R);
-    float a[R][V], b[R][V], f[R][V], xx[R][V], s[R][V], P[V], H[V], C[V], h[V];
-    rvec<T, V> cz[R], cd[R];
+    const int tw = at.t0 + n * TL + wave * R, cnt = at.Vb - tw;
+    float a[R][V], b[R][V], f[R][V], xx[R][V], s[R][V], dz[R][V], P[V], H[V], C[V], h[V];
 #pragma unroll
-    for (int j = 0; j < V; j++) P[j] = 1.0f, H[j] = 0.0f, C[j] = 0.0f, h[j] = hs[j];
+    for (int j = 0; j < V; j++) h[j] = hs[j];
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-      cd[i] = rd[i];
-      if constexpr (Z) cz[i] = rz[i];
+    for (int i = 0; i < R; i++)
 #pragma unroll
       for (int j = 0; j < V; j++) {
         rec_gate<GATE>(rec_get<T, V>(rg[i], j), a[i][j], b[i][j], f[i][j]);
-        xx[i][j] = i < cnt ? rec_get<T, V>(rx[i], j) : 0.0f;
-        float v = rec_get<T, V>(cd[i], j);
-        if constexpr (Z) {
-          const float zz = rec_get<T, V>(cz[i], j);
-          v *= zz * rec_sigma(zz);
+        xx[i][j] = rec_get<T, V>(rx[i], j);
+        s[i][j] = rec_get<T, V>(rd[i], j);
+        if constexpr (Z) {   // d_y silu'(z), for the state, and d_y silu(z)
+          const float zz = rec_get<T, V>(rz[i], j), sg = rec_sigma(zz), ds = s[i][j] * sg;
+          dz[i][j] = ds * fmaf(zz, 1.0f - sg, 1.0f);
+          s[i][j] = ds * zz;
+          rec_pin(dz[i][j]);
         }
-        s[i][j] = i < cnt ? v : 0.0f;
-        a[i][j] = i < cnt ? a[i][j] : 1.0f;
-        f[i][j] = i < cnt ? f[i][j] : 0.0f;
-        P[j] = rec_prod(P[j], a[i][j]);
-        H[j] = rec_next(a[i][j], H[j], GATE == 0 ? xx[i][j] : f[i][j] * xx[i][j]);
+        rec_pin(a[i][j]);
+        rec_pin(f[i][j]);
+        rec_pin(s[i][j]);
       }
-    }
-#pragma unroll
-    for (int i = R - 1; i >= 0; i--)
-#pragma unroll
-      for (int j = 0; j < V; j++) C[j] = a[i][j] == 0.0f ? 0.0f : a[i][j] * (s[i][j] + C[j]);
     if (n > 0) fetch(n - 1);
+    if (cnt < R)
+#pragma unroll
+      for (int i = 0; i < R; i++)
+#pragma unroll
+        for (int j = 0; j < V; j++) a[i][j] = i < cnt ? a[i][j] : 1.0f;
+    const bool clears = rec_clears<R, V>(a);
+    rec_either(clears, [&](auto cl) {
+#pragma unroll
+      for (int j = 0; j < V; j++) P[j] = 1.0f, H[j] = 0.0f, C[j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < R; i++)
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+          P[j] = rec_prod<cl.value>(P[j], a[i][j]);
+          H[j] = rec_next<cl.value>(a[i][j], H[j], GATE == 0 ? xx[i][j] : f[i][j] * xx[i][j]);
+          C[j] = rec_back<cl.value>(a[R - 1 - i][j], s[R - 1 - i][j] + C[j]);
+        }
+    });
 #pragma unroll
     for (int j = 0; j < V; j++)
       sp[buf][wave][lane][j] = P[j], sh[buf][wave][lane][j] = H[j], sc[buf][wave][lane][j] = C[j];
     __syncthreads();
-    float cin[V];
+    if (n < nt - 1)
+#pragma unroll
+      for (int j = 0; j < V; j++) c[j] = se[buf ^ 1][lane][j];
 #pragma unroll
     for (int k = 0; k < W - 1; k++)
       if (k < wave)
 #pragma unroll
         for (int j = 0; j < V; j++) h[j] = rec_apply(sp[buf][k][lane][j], sh[buf][k][lane][j], h[j]);
 #pragma unroll
-    for (int k = W - 1; k >= 0; k--)
+    for (int k = W - 1; k > 0; k--)
+      if (k > wave)
 #pragma unroll
-      for (int j = 0; j < V; j++) {
-        if (k == wave) cin[j] = c[j];
-        c[j] = rec_apply(sp[buf][k][lane][j], sc[buf][k][lane][j], c[j]);
-      }
-    float before[R][V];
+        for (int j = 0; j < V; j++) c[j] = rec_apply(sp[buf][k][lane][j], sc[buf][k][lane][j], c[j]);
+    if (wave == 0)
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-      float out[V];
+      for (int j = 0; j < V; j++) se[buf][lane][j] = last[j] = rec_apply(P[j], C[j], c[j]);
+    const size_t e = out0 + (size_t)tw * g.w;
+    const RecBuf zb = rec_buf(d_z + e, (size_t)g.w, Z && d_z ? min(cnt, R) : 0, cols);
+    const RecBuf xb = rec_buf(d_x + e, (size_t)g.w, d_x ? min(cnt, R) : 0, cols);
+    const RecBuf gb = rec_buf(d_g + e, (size_t)g.w, d_g ? min(cnt, R) : 0, cols);
+    rec_either(clears, [&](auto cl) {
 #pragma unroll
-      for (int j = 0; j < V; j++) {
-        before[i][j] = h[j];
-        h[j] = rec_next(a[i][j], h[j], GATE == 0 ? xx[i][j] : f[i][j] * xx[i][j]);
-        if constexpr (Z) {
-          const float zz = rec_get<T, V>(cz[i], j), sg = rec_sigma(zz);
-          out[j] = rec_get<T, V>(cd[i], j) * h[j] * (sg * fmaf(zz, 1.0f - sg, 1.0f));
+      for (int i = 0; i < R; i++) {
+        float out[V];
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+          const float before = h[j];
+          h[j] = rec_next<cl.value>(a[i][j], h[j], GATE == 0 ? xx[i][j] : f[i][j] * xx[i][j]);
+          out[j] = dz[i][j] * h[j];
+          dz[i][j] = before;   // for d_g
         }
+        if constexpr (Z) rec_bst<T, V>(zb, at.on ? lo + (unsigned)i * step : kRecPast, out);
       }
-      if constexpr (Z)
-        if (d_z != nullptr && i < cnt && at.on) rec_put<T, V>(d_z + (row + tw + i) * g.w + at.ch, out);
-    }
 #pragma unroll
-    for (int i = R - 1; i >= 0; i--) {
-      float ox[V], og[V];
+      for (int i = R - 1; i >= 0; i--) {
+        float ox[V], og[V];
 #pragma unroll
-      for (int j = 0; j < V; j++) {
-        const float d = s[i][j] + cin[j], aa = a[i][j];
-        float q;
-        if constexpr (GATE == 0) {
-          ox[j] = d;
-          q = before[i][j];
-        } else {
-          ox[j] = f[i][j] * d;
-          if constexpr (GATE == 1) q = b[i][j] * (before[i][j] - xx[i][j]);
-          else q = b[i][j] * before[i][j] - aa * xx[i][j] * (f[i][j] * __builtin_amdgcn_rcpf(1.0f + aa));
+        for (int j = 0; j < V; j++) {
+          const float d = s[i][j] + c[j], aa = a[i][j], before = dz[i][j];
+          float q;
+          if constexpr (GATE == 0) {
+            ox[j] = d;
+            q = before;
+          } else {
+            ox[j] = f[i][j] * d;
+            if constexpr (GATE == 1) q = b[i][j] * (before - xx[i][j]);
+            else q = b[i][j] * before - aa * xx[i][j] * (f[i][j] * __builtin_amdgcn_rcpf(1.0f + aa));
+          }
+          c[j] = rec_back<cl.value>(aa, d);
+          og[j] = rec_back<cl.value>(aa, q * d);
         }
-        og[j] = aa == 0.0f ? 0.0f : aa * q * d;
-        cin[j] = aa == 0.0f ? 0.0f : aa * d;
+        const unsigned off = at.on ? lo + (unsigned)i * step : kRecPast;
+        rec_bst<T, V>(xb, off, ox);
+        rec_bst<T, V>(gb, off, og);
       }
-      if (i < cnt && at.on) {
-        const size_t e = (row + tw + i) * g.w + at.ch;
-        if (d_x != nullptr) rec_put<T, V>(d_x + e, ox);
-        if (d_g != nullptr) rec_put<T, V>(d_g + e, og);
-      }
-    }
+    });
   }
   if (d_h0 != nullptr && at.seg == 0) {
     __syncthreads();   // d_h0 may be d_h_last: every wave has read it
     if (wave == 0 && at.on)
 #pragma unroll
-      for (int j = 0; j < V; j++) d_h0[o + j] = c[j];
+      for (int j = 0; j < V; j++) d_h0[o + j] = last[j];
   }
-  rec_zero_rows<T, V>(g, at, d_x, wave);
-  rec_zero_rows<T, V>(g, at, d_g, wave);
-  if constexpr (Z) rec_zero_rows<T, V>(g, at, d_z, wave);
+  rec_zero_rows<T, V>(g, at, d_x, wave, W);
+  rec_zero_rows<T, V>(g, at, d_g, wave, W);
+  if constexpr (Z) rec_zero_rows<T, V>(g, at, d_z, wave, W);
 }
 
 // One token of each sequence on a pool of states.
@@ -508,7 +620,7 @@ __global__ __launch_bounds__(256) void k_rec_step(RecGeo g, const T* __restrict_
         float a, b, f;
         rec_gate<GATE>(rec_get<T, V>(vg, j), a, b, f);
         const float v = rec_get<T, V>(vx, j);
-        h[j] = rec_next(a, rec_get<float, V>(st, j), GATE == 0 ? v : f * v);
+        h[j] = rec_next<true>(a, rec_get<float, V>(st, j), GATE == 0 ? v : f * v);
         out[j] = h[j];
         if constexpr (Z) {
           const float zz = rec_get<T, V>(vz, j);

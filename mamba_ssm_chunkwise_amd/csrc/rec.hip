@@ -22,8 +22,8 @@ struct RecPlan {
   size_t ws_fwd, ws_bwd, saved;
 };
 
-// A launch holds fewer than 2^32 threads.
-constexpr int64_t kMostItems = ((int64_t)1 << 32) / REC_T - 1;
+// A launch holds fewer than 2^32 threads, up to 1024 of them to a workgroup.
+constexpr int64_t kMostItems = ((int64_t)1 << 22) - 1;
 
 // lanes: x, g and z start where a lane's two channels can be read as one piece.
 int make_rec_plan(const moments_rec_desc* d, RecPlan* P, bool bases) {
@@ -36,7 +36,7 @@ int make_rec_plan(const moments_rec_desc* d, RecPlan* P, bool bases) {
   const int64_t xs = d->x_stride == 0 ? d->w : d->x_stride, gs = d->g_stride == 0 ? d->w : d->g_stride;
   const int64_t zs = d->z_stride == 0 ? d->w : d->z_stride;
   if (xs < d->w || gs < d->w || (d->has_z && zs < d->w)) return MOMENTS_EINVAL;
-  const int64_t far = (int64_t)1 << 40;   // elements between tokens
+  const int64_t far = (int64_t)1 << 25;   // a lane's tokens are addressed with 32-bit offsets
   if (xs > far || gs > far || (d->has_z && zs > far)) return MOMENTS_ENOTSUP;
   P->empty = d->b == 0;
   P->bf = d->dtype == MOMENTS_BF16;
@@ -118,17 +118,17 @@ int launch_rec_fwd(const RecPlan& P, int gate, const void* x, const void* gg, co
     const unsigned items = (unsigned)g.b * g.ncg;
     if (g.nseg > 1) {
       ProfScope ps(KID_REC_SEG, st);
-      hipLaunchKernelGGL((k_rec_seg<T, G, Z, V, false>), dim3(items * (g.nseg - 1)), dim3(REC_T), 0, st, g,
+      hipLaunchKernelGGL((k_rec_seg<T, G, Z, V, false>), dim3(items * (g.nseg - 1)), dim3(REC_SW * 64), 0, st, g,
                          (const T*)x, (const T*)gg, (const T*)z, h0, part, first);
       MOM_TRY(check_launch());
     }
     if (y != nullptr) {
       ProfScope ps(KID_REC_FWD, st);
-      hipLaunchKernelGGL((k_rec_fwd<T, G, Z, V, true>), dim3(items * g.nseg), dim3(REC_T), 0, st, g, (const T*)x,
+      hipLaunchKernelGGL((k_rec_fwd<T, G, Z, V, true>), dim3(items * g.nseg), dim3(REC_W * 64), 0, st, g, (const T*)x,
                          (const T*)gg, (const T*)z, h0, part, first, (T*)y, h_last, save);
     } else {
       ProfScope ps(KID_REC_FWD, st);
-      hipLaunchKernelGGL((k_rec_fwd<T, G, Z, V, false>), dim3(items * g.nseg), dim3(REC_T), 0, st, g, (const T*)x,
+      hipLaunchKernelGGL((k_rec_fwd<T, G, Z, V, false>), dim3(items * g.nseg), dim3(REC_W * 64), 0, st, g, (const T*)x,
                          (const T*)gg, (const T*)z, h0, part, first, (T*)nullptr, (float*)nullptr, save);
     }
     return check_launch();
@@ -194,12 +194,12 @@ int rec_backward(const moments_rec_desc* desc, const void* x, const void* gg, co
     const unsigned items = (unsigned)g.b * g.ncg;
     if (g.nseg > 1) {
       ProfScope ps(KID_REC_SEG, st);
-      hipLaunchKernelGGL((k_rec_seg<T, G, Z, V, true>), dim3(items * g.nseg), dim3(REC_T), 0, st, g, (const T*)d_y,
+      hipLaunchKernelGGL((k_rec_seg<T, G, Z, V, true>), dim3(items * g.nseg), dim3(REC_SW * 64), 0, st, g, (const T*)d_y,
                          (const T*)gg, (const T*)z, d_h_last, part, first);
       MOM_TRY(check_launch());
     }
     ProfScope ps(KID_REC_BWD, st);
-    hipLaunchKernelGGL((k_rec_bwd<T, G, Z, V>), dim3(items * g.nseg), dim3(REC_T), 0, st, g, (const T*)x,
+    hipLaunchKernelGGL((k_rec_bwd<T, G, Z, V>), dim3(items * g.nseg), dim3(REC_WB * 64), 0, st, g, (const T*)x,
                        (const T*)gg, (const T*)z, save, (const T*)d_y, d_h_last, part, first, (T*)d_x, (T*)d_g,
                        (T*)d_z, d_h0);
     return check_launch();
