@@ -337,10 +337,10 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
  * States are float32 [b,w]: h0 (NULL: zeros), h_last (the state after the last valid token; NULL: not
  * wanted). valid_len and valid_lens are those of moments_desc: rows of y, and of every gradient, past
  * a sequence's length are zero, whatever the inputs hold there; a sequence of length 0 leaves
- * h_last = h0. A decay below 2^-126 (g below -87.3, -inf among it) is exactly zero: such a token
- * starts its sequence anew, whatever stood before, infinities and NaN too (1 - a below 2^-126 may be
- * zero likewise). Otherwise a value that is
- * not finite reaches its channel's later tokens (in the gradients its earlier ones too) and no other.
+ * h_last = h0. A decay that underflows (g = -inf, every g below -104; below -87.3 it may) is exactly
+ * zero: such a token starts its sequence anew, whatever stood before, infinities and NaN too.
+ * Otherwise a value that is not finite reaches its channel's later tokens (in the gradients its earlier
+ * ones too) and no other.
  *
  * moments_rec_bwd is the vector-Jacobian product: d_y[b,s,w] (desc->dtype) and d_h_last[b,w] (float32,
  * NULL: zeros) to d_x, d_g, d_z in desc->dtype, [b,s,w] dense, and d_h0 (float32); any of them may be

@@ -10,8 +10,8 @@
 // applies those before its own. What enters the next tile stays in registers. The next tile's
 // rows are in flight meanwhile.
 //
-// A decay of exactly zero (below 2^-126) clears: what stood before, infinities and NaN too, is
-// gone. In a run's map that is a sign bit on P, which no product of decays has by itself, so a
+// A decay of exactly zero (one that underflows) clears: what stood before, infinities and NaN too,
+// is gone. In a run's map that is a sign bit on P, which no product of decays has by itself, so a
 // product that only underflows is told apart from it.
 #pragma once
 
@@ -47,7 +47,6 @@ __device__ __forceinline__ int rec_len(const RecGeo& g, int bi) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kExpMin = -87.336544f;   // exp of less is below 2^-126
 
 template <typename T, int V> struct RecVec { typedef T type __attribute__((ext_vector_type(V))); };
 template <typename T> struct RecVec<T, 1> { typedef T type; };
@@ -75,20 +74,19 @@ template <typename T, int V> __device__ __forceinline__ rvec<T, V> rec_ld(const 
 
 // A wave's rows of a tensor as a buffer that ends with them: rows past the sequence's end read as
 // zeros and are not written, without a branch. `n` rows from p on, `cols` columns from p's to the
-// tensor's last. A lane without channels stores at kRecPast, which is past every buffer's end.
+// tensor's last.
 using RecBuf = __amdgpu_buffer_rsrc_t;
-constexpr unsigned kRecPast = 0xfffffff0u;
 template <typename T>
 __device__ __forceinline__ RecBuf rec_buf(const T* p, size_t stride, int n, int cols) {
   const unsigned bytes = n <= 0 ? 0u : (unsigned)((n - 1) * stride + cols) * (unsigned)sizeof(T);
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, bytes, 0x00027000);
 }
-template <typename T, int V> __device__ __forceinline__ rvec<T, V> rec_bld(RecBuf r, unsigned off) {
+template <typename T, int V> __device__ __forceinline__ rvec<T, V> rec_bld(RecBuf r, unsigned off, unsigned row) {
   typedef unsigned u2 __attribute__((ext_vector_type(2)));
-  if constexpr (sizeof(T) * V == 2) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+  if constexpr (sizeof(T) * V == 2) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0));
   else if constexpr (sizeof(T) * V == 4)
-    return __builtin_bit_cast(rvec<T, V>, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-  else return __builtin_bit_cast(rvec<T, V>, (u2)__builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    return __builtin_bit_cast(rvec<T, V>, __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0));
+  else return __builtin_bit_cast(rvec<T, V>, (u2)__builtin_amdgcn_raw_buffer_load_b64(r, off, row, 0));
 }
 template <typename T, int V> __device__ __forceinline__ void rec_bst(RecBuf r, unsigned off, const float (&f)[V]) {
   typedef unsigned u2 __attribute__((ext_vector_type(2)));
@@ -100,14 +98,21 @@ template <typename T, int V> __device__ __forceinline__ void rec_bst(RecBuf r, u
 }
 
 // Rows t0, t0 + 1, ... of a tensor at a lane's channels (p: the sequence's first row at the
-// workgroup's first channel), in flight together.
+// workgroup's first channel), in flight together; n rows are left. Where all R are there the rows'
+// offsets are scalars (no lane is past the buffer's end: `lane_off` of one without channels is 0);
+// else they stand in the lanes' own offsets, which is what the buffer's end is compared with.
 template <typename T, int V, int R>
 __device__ __forceinline__ void rec_rows(rvec<T, V> (&r)[R], const T* p, size_t stride, int t0, int n, int cols,
                                          unsigned lane_off) {
   const RecBuf buf = rec_buf(p + (size_t)t0 * stride, stride, min(n, R), cols);
   const unsigned step = (unsigned)stride * (unsigned)sizeof(T);
+  if (n >= R) {
 #pragma unroll
-  for (int i = 0; i < R; i++) r[i] = rec_bld<T, V>(buf, lane_off + (unsigned)i * step);
+    for (int i = 0; i < R; i++) r[i] = rec_bld<T, V>(buf, lane_off, (unsigned)i * step);
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; i++) r[i] = rec_bld<T, V>(buf, lane_off + (unsigned)i * step, 0);
+  }
 }
 
 // The decay a, and for the logistic gates b = 1 - a and the input's factor f (else 1). The
@@ -118,7 +123,7 @@ __device__ __forceinline__ void rec_rows(rvec<T, V> (&r)[R], const T* p, size_t 
 // so that it does not vanish where b leaves the range (the instruction has no subnormal results).
 template <int GATE> __device__ __forceinline__ void rec_gate(float g, float& a, float& b, float& f) {
   if constexpr (GATE == 0) {
-    a = g < kExpMin ? 0.0f : __builtin_amdgcn_exp2f(g * kLog2e);
+    a = __builtin_amdgcn_exp2f(g * kLog2e);
     b = 0.0f;
     f = 1.0f;
   } else {
@@ -126,7 +131,7 @@ template <int GATE> __device__ __forceinline__ void rec_gate(float g, float& a, 
     const float e = GATE == 1 ? h : h * h;
     const float r = __builtin_amdgcn_rcpf(1.0f + e), q = e * r;
     const float p = 1.0f - q;
-    a = g < 0.0f ? (g < kExpMin ? 0.0f : q) : p;
+    a = g < 0.0f ? q : p;
     b = g < 0.0f ? p : q;
     f = GATE == 1 ? b : __builtin_amdgcn_sqrtf(r * (1.0f + a)) * (g < 0.0f ? 1.0f : h);
   }
@@ -243,57 +248,60 @@ __global__ __launch_bounds__(REC_SW * 64) void k_rec_seg(RecGeo g, const T* __re
     for (int i = 0; i < V; i++) first[o + i] = h0 ? h0[o + i] : 0.0f;
   const int per = (at.t1 - at.t0 + REC_SW - 1) / REC_SW;
   const int r0 = min(at.t0 + wave * per, at.t1), r1 = min(r0 + per, at.t1);
-  const size_t row = (size_t)at.bi * g.s;
-  const T* xp = x + row * (BACK ? (size_t)g.w : g.xs) + at.ch;   // BACK: d_y
-  const T* gp = gg + row * g.gs + at.ch;
-  const T* zp = Z ? z + row * g.zs + at.ch : nullptr;
-  const size_t xst = BACK ? (size_t)g.w : g.xs;
+  const size_t row = (size_t)at.bi * g.s, xst = BACK ? (size_t)g.w : g.xs;
+  const T* xp = x + row * xst + at.c0;   // BACK: d_y
+  const T* gp = gg + row * g.gs + at.c0;
+  const T* zp = Z ? z + row * g.zs + at.c0 : nullptr;
+  const int cols = g.w - at.c0;
+  const unsigned lo = at.on ? (unsigned)(lane * V * (int)sizeof(T)) : 0u;
   float P[V], H[V];
 #pragma unroll
   for (int i = 0; i < V; i++) P[i] = 1.0f, H[i] = 0.0f;
   constexpr int R = REC_SR;
   rvec<T, V> rx[R], rg[R], rz[R];
-  auto fetch = [&](int k) {   // run k of the wave's tokens, from its end where BACK
-#pragma unroll
-    for (int i = 0; i < R; i++) {
-      const int t = BACK ? max(r1 - 1 - (k * R + i), r0) : min(r0 + k * R + i, r1 - 1);
-      rx[i] = rec_ld<T, V>(xp + (size_t)t * xst);
-      rg[i] = rec_ld<T, V>(gp + (size_t)t * g.gs);
-      if constexpr (Z && BACK) rz[i] = rec_ld<T, V>(zp + (size_t)t * g.zs);
-    }
-  };
   const int nr = (r1 - r0 + R - 1) / R;
+  auto fetch = [&](int k) {
+    const int t = r0 + (BACK ? nr - 1 - k : k) * R;
+    rec_rows<T, V, R>(rx, xp, xst, t, r1 - t, cols, lo);
+    rec_rows<T, V, R>(rg, gp, g.gs, t, r1 - t, cols, lo);
+    if constexpr (Z) rec_rows<T, V, R>(rz, zp, g.zs, t, r1 - t, cols, lo);
+  };
   if (nr > 0) fetch(0);
   for (int k = 0; k < nr; k++) {
-    rvec<T, V> cx[R], cg[R], cz[R];
+    const int cnt = r1 - r0 - (BACK ? nr - 1 - k : k) * R;
+    float a[R][V], u[R][V];
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-      cx[i] = rx[i];
-      cg[i] = rg[i];
-      if constexpr (Z && BACK) cz[i] = rz[i];
-    }
+    for (int i = 0; i < R; i++)
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        float b, f;
+        rec_gate<GATE>(rec_get<T, V>(rg[i], j), a[i][j], b, f);
+        u[i][j] = rec_get<T, V>(rx[i], j);
+        if constexpr (!BACK && GATE != 0) u[i][j] *= f;
+        if constexpr (Z) {
+          const float zz = rec_get<T, V>(rz[i], j);
+          u[i][j] *= zz * rec_sigma(zz);
+        }
+        rec_pin(a[i][j]);
+        rec_pin(u[i][j]);
+      }
     if (k + 1 < nr) fetch(k + 1);
+    if (cnt < R)
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-      if (k * R + i < r1 - r0) {
+      for (int i = 0; i < R; i++)
+#pragma unroll
+        for (int j = 0; j < V; j++) a[i][j] = i < cnt ? a[i][j] : 1.0f;
+    rec_either(rec_clears<R, V>(a), [&](auto cl) {
+#pragma unroll
+      for (int i = 0; i < R; i++)
 #pragma unroll
         for (int j = 0; j < V; j++) {
-          float a, b, f;
-          rec_gate<GATE>(rec_get<T, V>(cg[i], j), a, b, f);
-          float v = rec_get<T, V>(cx[i], j);
-          if constexpr (BACK) {
-            if constexpr (Z) {
-              const float zz = rec_get<T, V>(cz[i], j);
-              v *= zz * rec_sigma(zz);
-            }
-            H[j] = rec_back<true>(a, v + H[j]);
-          } else {
-            H[j] = rec_next<true>(a, H[j], GATE == 0 ? v : f * v);
-          }
-          P[j] = rec_prod<true>(P[j], a);
+          const int q = BACK ? R - 1 - i : i;
+          if constexpr (BACK) H[j] = rec_back<cl.value>(a[q][j], u[q][j] + H[j]);
+          else H[j] = rec_next<cl.value>(a[q][j], H[j], u[q][j]);
+          P[j] = rec_prod<cl.value>(P[j], a[q][j]);
         }
-      }
-    }
+    });
   }
 #pragma unroll
   for (int j = 0; j < V; j++) sp[wave][lane][j] = P[j], sh[wave][lane][j] = H[j];
@@ -334,7 +342,7 @@ __global__ __launch_bounds__(REC_W * 64) void k_rec_fwd(RecGeo g, const T* __res
   const T* zp = Z ? z + row * g.zs + at.c0 : nullptr;
   T* yp = OUT ? y + row * g.w + at.c0 : nullptr;
   const int cols = g.w - at.c0, nsv = (g.V + REC_SAVE - 1) / REC_SAVE;
-  const unsigned lo = (unsigned)(lane * V * (int)sizeof(T)), step = (unsigned)g.w * (unsigned)sizeof(T);
+  const unsigned lo = at.on ? (unsigned)(lane * V * (int)sizeof(T)) : 0u, step = (unsigned)g.w * (unsigned)sizeof(T);
   float h[V], last[V];   // last: past the tile so far, in the last wave
   if (g.nseg > 1) {
     rec_enter<V>(g, at, part, first, false, h);
@@ -408,7 +416,7 @@ __global__ __launch_bounds__(REC_W * 64) void k_rec_fwd(RecGeo g, const T* __res
       for (int j = 0; j < V; j++) se[buf][lane][j] = last[j] = rec_apply(P[j], H[j], h[j]);
     if constexpr (OUT) {
       const RecBuf yb = rec_buf(yp + (size_t)tw * g.w, (size_t)g.w, min(cnt, R), cols);
-      rec_either(clears, [&](auto cl) {
+      if (at.on) rec_either(clears, [&](auto cl) {
 #pragma unroll
         for (int i = 0; i < R; i++) {
           float out[V];
@@ -422,7 +430,7 @@ __global__ __launch_bounds__(REC_W * 64) void k_rec_fwd(RecGeo g, const T* __res
               out[j] *= zz * rec_sigma(zz);
             }
           }
-          rec_bst<T, V>(yb, at.on ? lo + (unsigned)i * step : kRecPast, out);
+          rec_bst<T, V>(yb, lo + (unsigned)i * step, out);
         }
       });
     }
@@ -459,7 +467,7 @@ __global__ __launch_bounds__(REC_WB * 64) void k_rec_bwd(RecGeo g, const T* __re
   const T* dp = dy + row * g.w + at.c0;
   const size_t out0 = row * g.w + at.c0;
   const int cols = g.w - at.c0, nsv = (g.V + TL - 1) / TL;
-  const unsigned lo = (unsigned)(lane * V * (int)sizeof(T)), step = (unsigned)g.w * (unsigned)sizeof(T);
+  const unsigned lo = at.on ? (unsigned)(lane * V * (int)sizeof(T)) : 0u, step = (unsigned)g.w * (unsigned)sizeof(T);
   const float* sv = save + (size_t)at.bi * nsv * g.w + at.ch;
   float c[V], last[V];   // from the right; last: before the tile so far, in the first wave
   if (g.nseg > 1) {
@@ -549,7 +557,7 @@ __global__ __launch_bounds__(REC_WB * 64) void k_rec_bwd(RecGeo g, const T* __re
     const RecBuf zb = rec_buf(d_z + e, (size_t)g.w, Z && d_z ? min(cnt, R) : 0, cols);
     const RecBuf xb = rec_buf(d_x + e, (size_t)g.w, d_x ? min(cnt, R) : 0, cols);
     const RecBuf gb = rec_buf(d_g + e, (size_t)g.w, d_g ? min(cnt, R) : 0, cols);
-    rec_either(clears, [&](auto cl) {
+    if (at.on) rec_either(clears, [&](auto cl) {
 #pragma unroll
       for (int i = 0; i < R; i++) {
         float out[V];
@@ -560,7 +568,7 @@ __global__ __launch_bounds__(REC_WB * 64) void k_rec_bwd(RecGeo g, const T* __re
           out[j] = dz[i][j] * h[j];
           dz[i][j] = before;   // for d_g
         }
-        if constexpr (Z) rec_bst<T, V>(zb, at.on ? lo + (unsigned)i * step : kRecPast, out);
+        if constexpr (Z) rec_bst<T, V>(zb, lo + (unsigned)i * step, out);
       }
 #pragma unroll
       for (int i = R - 1; i >= 0; i--) {
@@ -580,7 +588,7 @@ __global__ __launch_bounds__(REC_WB * 64) void k_rec_bwd(RecGeo g, const T* __re
           c[j] = rec_back<cl.value>(aa, d);
           og[j] = rec_back<cl.value>(aa, q * d);
         }
-        const unsigned off = at.on ? lo + (unsigned)i * step : kRecPast;
+        const unsigned off = lo + (unsigned)i * step;
         rec_bst<T, V>(xb, off, ox);
         rec_bst<T, V>(gb, off, og);
       }

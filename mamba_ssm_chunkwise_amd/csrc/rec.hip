@@ -118,7 +118,7 @@ int launch_rec_fwd(const RecPlan& P, int gate, const void* x, const void* gg, co
     const unsigned items = (unsigned)g.b * g.ncg;
     if (g.nseg > 1) {
       ProfScope ps(KID_REC_SEG, st);
-      hipLaunchKernelGGL((k_rec_seg<T, G, Z, V, false>), dim3(items * (g.nseg - 1)), dim3(REC_SW * 64), 0, st, g,
+      hipLaunchKernelGGL((k_rec_seg<T, G, false, V, false>), dim3(items * (g.nseg - 1)), dim3(REC_SW * 64), 0, st, g,
                          (const T*)x, (const T*)gg, (const T*)z, h0, part, first);
       MOM_TRY(check_launch());
     }
@@ -128,8 +128,8 @@ int launch_rec_fwd(const RecPlan& P, int gate, const void* x, const void* gg, co
                          (const T*)gg, (const T*)z, h0, part, first, (T*)y, h_last, save);
     } else {
       ProfScope ps(KID_REC_FWD, st);
-      hipLaunchKernelGGL((k_rec_fwd<T, G, Z, V, false>), dim3(items * g.nseg), dim3(REC_W * 64), 0, st, g, (const T*)x,
-                         (const T*)gg, (const T*)z, h0, part, first, (T*)nullptr, (float*)nullptr, save);
+      hipLaunchKernelGGL((k_rec_fwd<T, G, false, V, false>), dim3(items * g.nseg), dim3(REC_W * 64), 0, st, g, (const T*)x,
+                         (const T*)gg, (const T*)nullptr, h0, part, first, (T*)nullptr, (float*)nullptr, save);
     }
     return check_launch();
   });
