@@ -650,14 +650,17 @@ def moments_qk_bwd(desc: QkDesc, q, k, wq, wk, bq, bk, rot, d_qhat, d_khat,
 
 
 # ---------------------------------------------------------------- gated linear recurrence
-def _row_stride(name, t, w):
+def _dense_like(t):
+    """An uninitialised dense tensor of t's shape and dtype."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _row_stride(name, t):
     """Elements between tokens of t [b,s,w] (0 where any would do)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a torch.Tensor of three dimensions")
-    if t.is_contiguous():
-        return w if t.shape[0] * t.shape[1] > 1 else 0
     b, s, n = t.shape
-    if t.numel() == 0:
+    if t.numel() == 0 or (b * s == 1 and t.is_contiguous()):
         return 0
     sb, ss, sw = t.stride()
     step = ss if s > 1 else (sb if b > 1 else n)
@@ -673,8 +676,8 @@ def rec_desc(x, g, z=None, gate=GATE_LOG, valid_len=None, valid_lens=None) -> Re
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be a torch.Tensor [b,s,w]")
     b, s, w = x.shape
-    d = RecDesc(b, s, w, s if valid_len is None else int(valid_len), _row_stride("x", x, w), _row_stride("g", g, w),
-                0 if z is None else _row_stride("z", z, w), BF16 if x.dtype is torch.bfloat16 else F32, int(gate),
+    d = RecDesc(b, s, w, s if valid_len is None else int(valid_len), _row_stride("x", x), _row_stride("g", g),
+                0 if z is None else _row_stride("z", z), BF16 if x.dtype is torch.bfloat16 else F32, int(gate),
                 0 if z is None else 1)
     return set_valid_lens(d, valid_lens) if valid_lens is not None else d
 
@@ -704,9 +707,10 @@ def _rec_inputs(desc: RecDesc, x, g, z, h0):
             raise ValueError("set per-sequence lengths with set_valid_lens (the descriptor keeps the tensor)")
         if ref.device != dev:
             raise ValueError(f"valid_lens is on {ref.device}, the inputs on {dev}")
-    b, s, w = desc.b, desc.s, desc.w
     if (z is not None) != bool(desc.has_z):
         raise ValueError("z must be None when the descriptor has no z" if z is not None else "z is required")
+    b, s, w = shape = (desc.b, desc.s, desc.w)
+    at = -1 if dev.index is None else dev.index
     ptrs = []
     for name, t, stride in (("x", x, desc.x_stride), ("g", g, desc.g_stride), ("z", z, desc.z_stride)):
         if t is None and name == "z":
@@ -714,14 +718,19 @@ def _rec_inputs(desc: RecDesc, x, g, z, h0):
             continue
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a torch.Tensor")
-        if t.shape != (b, s, w) or t.dtype is not dt or t.device != dev:
-            raise ValueError(f"{name} must be {dt} of shape {(b, s, w)} on {dev}, got {t.dtype} {tuple(t.shape)} "
+        if t.shape != shape or t.dtype is not dt or t.get_device() != at or (at < 0 and t.device != dev):
+            raise ValueError(f"{name} must be {dt} of shape {shape} on {dev}, got {t.dtype} {tuple(t.shape)} "
                              f"on {t.device}")
-        step = _row_stride(name, t, w) or w   # also one token's values have to lie together
-        if b * s > 1 and step != (stride or w):
-            raise ValueError(f"{name} has another token stride than the descriptor ({stride or w})")
+        step = stride or w
+        # also one token's values have to lie together
+        if t.stride() != (s * step, step, 1) and (_row_stride(name, t) or step) != step:
+            raise ValueError(f"{name} has another token stride than the descriptor ({step})")
         ptrs.append(t.data_ptr())
-    return dev, dt, [*ptrs, *_tensors_ok(dev, (("h0", h0, (b, w), torch.float32, True),))]
+    if h0 is None:
+        ptrs.append(None)
+    else:
+        ptrs += _tensors_ok(dev, (("h0", h0, (b, w), torch.float32, True),))
+    return dev, dt, ptrs
 
 
 def _rec_forward(desc, x, g, z, h0, y, h_last, saved, want_saved, workspace):
@@ -735,7 +744,7 @@ def _rec_forward(desc, x, g, z, h0, y, h_last, saved, want_saved, workspace):
         saved = _buffer("saved", moments_rec_saved_size(desc), dev, saved)
     _wrote(y, h_last, saved)
     if y is None:
-        y = torch.empty(shape, dtype=dt, device=dev)
+        y = _dense_like(x)
     if h_last is None:
         h_last = torch.empty(state, dtype=torch.float32, device=dev)
     head = (ctypes.byref(desc), *ins, y.data_ptr(), h_last.data_ptr())
@@ -799,7 +808,7 @@ def moments_rec_step(desc: RecDesc, x, g, z, state, slots=None, y=None):
     lib = _gpu(dev)
     _wrote(state, y)
     if y is None:
-        y = torch.empty((desc.b, desc.s, desc.w), dtype=dt, device=dev)
+        y = _dense_like(x)
         out = y.data_ptr()
     _lib.check(lib.moments_rec_step(ctypes.byref(desc), *ins[:3], sl, n, st, out, _stream_of(dev)))
     return y
@@ -864,9 +873,9 @@ def moments_ln_fwd(desc: LnDesc, x, weight, bias=None, res=None, y=None, sum=Non
     lib = _gpu(dev)
     _wrote(y, sum)
     if y is None:
-        y = torch.empty(x.shape, dtype=dt, device=dev)
+        y = _dense_like(x)
     if sum is None and desc.residual:
-        sum = torch.empty(x.shape, dtype=f32, device=dev)
+        sum = torch.empty_like(res)
     _lib.check(lib.moments_ln_fwd(ctypes.byref(desc), x.data_ptr(), rp, wp, bp, y.data_ptr(),
                                   None if sum is None else sum.data_ptr(), _stream_of(dev)))
     return y, sum
