@@ -274,7 +274,7 @@ __global__ __launch_bounds__(1024) void k_ln_sum(const float* __restrict__ part,
   double s = 0.0;
   if (c < w) {
     const float* p = part + (size_t)blockIdx.y * np * w + c;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = wave; k < np; k += 16) s += (double)p[(size_t)k * w];
   }
   lds[wave][lane] = s;

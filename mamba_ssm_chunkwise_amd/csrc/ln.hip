@@ -48,7 +48,7 @@ int make_ln_plan(const moments_ln_desc* d, LnPlan* P, bool bases) {
   const int rows = P->NT == 64 ? 4 : 1, nb = std::max(P->NT, P->NT == 64 ? 256 : 128);
   const int64_t all = (d->n + rows - 1) / rows;
   P->nfwd = (int)std::min<int64_t>(all, kCUs * 4096 / nb);
-  P->nblk = (int)std::min<int64_t>(all, kCUs * 2048 / nb);
+  P->nblk = (int)std::min<int64_t>(all, kCUs * std::max(768 / nb, 1));
   P->part = 0;
   P->flag = align256((size_t)2 * P->nblk * g.w * 4);
   P->ws = P->flag + 256;
