@@ -216,19 +216,37 @@ __device__ __forceinline__ void rec_zero_rows(const RecGeo& g, const RecAt& at, 
   for (int t = b0 + wave; t < b1; t += waves) rec_put<T, V>(p + (size_t)t * g.w, zero);
 }
 
-// The maps of the segments before a workgroup's own, in order, on the state that enters the
-// first. part: [segment][b][w] of P, then of H; first: [b][w].
-template <int V>
+// The maps of the segments before a workgroup's own (BACK: behind it), in order, on the state that
+// enters the first: every wave joins a share of them, then all apply the waves' maps. part:
+// [segment][b][w] of P, then of H; first: [b][w]; sp, sh: [waves][64][V] in LDS.
+template <int V, int W, bool BACK>
 __device__ __forceinline__ void rec_enter(const RecGeo& g, const RecAt& at, const float* part, const float* first,
-                                          bool back, float (&h)[V]) {
+                                          float (&sp)[W][64][V], float (&sh)[W][64][V], float (&h)[V]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const size_t n = (size_t)g.b * g.w, o = (size_t)at.bi * g.w + at.ch;
-  const float* H = part + (size_t)g.nseg * n;
+  const float* hpart = part + (size_t)g.nseg * n;
+  const int many = BACK ? g.nseg - 1 - at.seg : at.seg, per = (many + W - 1) / W;
+  float P[V], H[V];
 #pragma unroll
-  for (int i = 0; i < V; i++) h[i] = first[o + i];
-  const int from = back ? g.nseg - 1 : 0, step = back ? -1 : 1;
-  for (int k = from; k != at.seg; k += step)
+  for (int j = 0; j < V; j++) P[j] = 1.0f, H[j] = 0.0f, h[j] = first[o + j];
+#pragma unroll 4
+  for (int i = wave * per; i < min((wave + 1) * per, many); i++) {
+    const size_t k = (size_t)(BACK ? g.nseg - 1 - i : i) * n + o;
 #pragma unroll
-    for (int i = 0; i < V; i++) h[i] = rec_apply(part[k * n + o + i], H[k * n + o + i], h[i]);
+    for (int j = 0; j < V; j++) {
+      const float p = part[k + j];
+      H[j] = rec_apply(p, hpart[k + j], H[j]);
+      P[j] = rec_chain(P[j], p);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; j++) sp[wave][lane][j] = P[j], sh[wave][lane][j] = H[j];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < W; k++)
+#pragma unroll
+    for (int j = 0; j < V; j++) h[j] = rec_apply(sp[k][lane][j], sh[k][lane][j], h[j]);
+  __syncthreads();
 }
 
 // The map of a segment: every wave walks a run of its own and the waves' maps are joined at the
@@ -345,7 +363,7 @@ __global__ __launch_bounds__(REC_W * 64) void k_rec_fwd(RecGeo g, const T* __res
   const unsigned lo = at.on ? (unsigned)(lane * V * (int)sizeof(T)) : 0u, step = (unsigned)g.w * (unsigned)sizeof(T);
   float h[V], last[V];   // last: past the tile so far, in the last wave
   if (g.nseg > 1) {
-    rec_enter<V>(g, at, part, first, false, h);
+    rec_enter<V, W, false>(g, at, part, first, sp[0], sh[0], h);
   } else {
 #pragma unroll
     for (int j = 0; j < V; j++) h[j] = h0 ? h0[o + j] : 0.0f;
@@ -471,7 +489,7 @@ __global__ __launch_bounds__(REC_WB * 64) void k_rec_bwd(RecGeo g, const T* __re
   const float* sv = save + (size_t)at.bi * nsv * g.w + at.ch;
   float c[V], last[V];   // from the right; last: before the tile so far, in the first wave
   if (g.nseg > 1) {
-    rec_enter<V>(g, at, part, first, true, c);
+    rec_enter<V, W, true>(g, at, part, first, sp[0], sh[0], c);
   } else {
 #pragma unroll
     for (int j = 0; j < V; j++) c[j] = d_last ? d_last[o + j] : 0.0f;

@@ -52,8 +52,8 @@ int make_rec_plan(const moments_rec_desc* d, RecPlan* P, bool bases) {
   if (d->b * ncg > kMostItems) return MOMENTS_ENOTSUP;
   g.ncg = (int)ncg;
   const int64_t items = d->b * ncg, tiles = (g.V + REC_TILE - 1) / REC_TILE;
-  int64_t n = 1;
-  if (items > 0 && items * 4 < kCUs * 3) n = std::min((kCUs + items - 1) / items, std::max<int64_t>(tiles / 2, 1));
+  // One workgroup to a CU, and no more of them than CUs.
+  const int64_t n = std::max<int64_t>(1, std::min(kCUs / std::max<int64_t>(items, 1), tiles / 2));
   const int64_t per = std::max<int64_t>((tiles + n - 1) / n, 1);
   g.seg = (int)(per * REC_TILE);
   g.nseg = (int)std::max<int64_t>((tiles + per - 1) / per, 1);
