@@ -389,8 +389,7 @@ int moments_rec_step(const moments_rec_desc* desc, const void* x, const void* g,
 /* Layer norm of rows, with the residual stream added before it where there is one:
  *   sum = x + res,   y = (sum - mean) / sqrt(var + eps) * weight + bias
  * with the mean and the variance (the mean square about the mean) of each row. x is [n,w] in
- * desc->dtype, rows x_stride elements apart (0: w) from any element on (rows of whole 16-byte pieces,
- * with base and stride alike, are read as such, others one element at a time). The residual stream is
+ * desc->dtype, rows x_stride elements apart (0: w) from any element on. The residual stream is
  * float32 whatever desc->dtype is, so that a stack's many additions do not round to 8 bits: res[n,w]
  * and sum[n,w] are there if desc->residual is 1 and NULL if it is 0 (then x itself is normed). weight
  * [w] and bias [w] (NULL: none) are float32; y is [n,w] in desc->dtype. All but x start at 16 bytes.

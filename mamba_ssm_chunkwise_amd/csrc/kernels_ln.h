@@ -4,7 +4,10 @@
 //   gy = d_y weight,  d_s = rstd (gy - mean(gy) - xhat mean(gy xhat)) (+ d_sum),  xhat = d rstd
 //   d_weight = sum of d_y xhat over the rows,  d_bias = sum of d_y
 //
-// A row lies in the registers of NT threads, E elements each, and is read once. The mean is taken
+// A row lies in the registers of NT threads, E elements each, and is read once. Threads take pieces of
+// eight neighbouring elements wherever they stand in memory: loads and stores of 16 bytes need no
+// alignment here (the compiler is told that there is none), only the last piece of a row whose width
+// is not a multiple of eight goes element by element. The mean is taken
 // twice: the first, of s, may be off by the rounding of a sum of large values, so the second
 // reduction carries sum(d) beside sum(d^2) and what is left of the mean leaves d and the variance.
 // The gradients make the statistics again, with their own two sums in that same reduction, so
@@ -24,74 +27,96 @@ struct LnGeo {
 
 constexpr float kLnScale = 8.271806125530277e-25f;   // 2^-80
 
-// Columns of a thread: whole 8-element pieces NT pieces apart, or (VEC false) elements NT apart.
-template <int NT, bool VEC> __device__ __forceinline__ int ln_col(int i, int tid) {
-  return VEC ? ((i >> 3) * NT + tid) * 8 + (i & 7) : i * NT + tid;
+// Columns of a thread: 8-element pieces, NT pieces apart.
+template <int NT> __device__ __forceinline__ int ln_col(int i, int tid) { return ((i >> 3) * NT + tid) * 8 + (i & 7); }
+
+// Eight elements from an address of theirs on.
+struct __attribute__((packed, aligned(2))) LnWord2 { u4 v; };
+struct __attribute__((packed, aligned(4))) LnWord4 { f4 v; };
+__device__ __forceinline__ void ln_get8(float* v, const bf16* p) {
+  const u4 r = reinterpret_cast<const LnWord2*>(p)->v;
+#pragma unroll
+  for (int j = 0; j < 4; j++) v[2 * j] = bf16_lo(r[j]), v[2 * j + 1] = bf16_hi(r[j]);
+}
+__device__ __forceinline__ void ln_get8(float* v, const float* p) {
+  const f4 r0 = reinterpret_cast<const LnWord4*>(p)->v, r1 = reinterpret_cast<const LnWord4*>(p + 4)->v;
+#pragma unroll
+  for (int j = 0; j < 4; j++) v[j] = r0[j], v[4 + j] = r1[j];
+}
+__device__ __forceinline__ void ln_put8(bf16* p, const float* v) {
+  u4 r;
+#pragma unroll
+  for (int j = 0; j < 4; j++) r[j] = pk_bf16(v[2 * j], v[2 * j + 1]);
+  reinterpret_cast<LnWord2*>(p)->v = r;
+}
+__device__ __forceinline__ void ln_put8(float* p, const float* v) {
+  f4 r0, r1;
+#pragma unroll
+  for (int j = 0; j < 4; j++) r0[j] = v[j], r1[j] = v[4 + j];
+  reinterpret_cast<LnWord4*>(p)->v = r0;
+  reinterpret_cast<LnWord4*>(p + 4)->v = r1;
 }
 
-template <typename T, int NT, int E, bool VEC>
-__device__ __forceinline__ void ln_load(float (&v)[E], const T* p, int w, int tid) {
-  if constexpr (VEC) {
+// A thread's elements of a row. `past`: the memory goes on far enough behind the row that its last
+// piece can be read whole; what stands there is in v then, past the row's end.
+template <typename T, int NT, int E>
+__device__ __forceinline__ void ln_load(float (&v)[E], const T* p, int w, int tid, bool past) {
 #pragma unroll
-    for (int k = 0; k < E / 8; k++) {
-      const int c = (k * NT + tid) * 8;
-      if (c < w) {
-        if constexpr (sizeof(T) == 2) {
-          const u4 r = *reinterpret_cast<const u4*>(p + c);
+  for (int k = 0; k < E / 8; k++) {
+    const int c = (k * NT + tid) * 8;
+    if (past ? c < w : c + 8 <= w) {
+      ln_get8(v + 8 * k, p + c);
+    } else {
 #pragma unroll
-          for (int j = 0; j < 4; j++) v[8 * k + 2 * j] = bf16_lo(r[j]), v[8 * k + 2 * j + 1] = bf16_hi(r[j]);
-        } else {
-          const f4 r0 = *reinterpret_cast<const f4*>(p + c), r1 = *reinterpret_cast<const f4*>(p + c + 4);
+      for (int j = 0; j < 8; j++) v[8 * k + j] = 0.0f;
+      if (!past)
 #pragma unroll
-          for (int j = 0; j < 4; j++) v[8 * k + j] = r0[j], v[8 * k + 4 + j] = r1[j];
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[8 * k + j] = 0.0f;
-      }
+        for (int j = 0; j < 8; j++)
+          if (c + j < w) v[8 * k + j] = to_f(p[c + j]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; i++) v[i] = i * NT + tid < w ? to_f(p[i * NT + tid]) : 0.0f;
   }
 }
+// Whether that is so of a row of a tensor whose rows are `stride` elements apart.
+__device__ __forceinline__ bool ln_past(const LnGeo& g, int64_t row, size_t stride) {
+  return (size_t)(g.n - 1 - row) * stride + (size_t)g.w >= (size_t)((g.w + 7) & ~7);
+}
 
-template <typename T, int NT, int E, bool VEC>
+template <typename T, int NT, int E>
 __device__ __forceinline__ void ln_store(T* p, const float (&v)[E], int w, int tid) {
-  if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < E / 8; k++) {
-      const int c = (k * NT + tid) * 8;
-      if (c < w) {
-        if constexpr (sizeof(T) == 2) {
-          u4 r;
+  for (int k = 0; k < E / 8; k++) {
+    const int c = (k * NT + tid) * 8;
+    if (c + 8 <= w) {
+      ln_put8(p + c, v + 8 * k);
+    } else {
 #pragma unroll
-          for (int j = 0; j < 4; j++) r[j] = pk_bf16(v[8 * k + 2 * j], v[8 * k + 2 * j + 1]);
-          *reinterpret_cast<u4*>(p + c) = r;
-        } else {
-          f4 r0, r1;
-#pragma unroll
-          for (int j = 0; j < 4; j++) r0[j] = v[8 * k + j], r1[j] = v[8 * k + 4 + j];
-          *reinterpret_cast<f4*>(p + c) = r0;
-          *reinterpret_cast<f4*>(p + c + 4) = r1;
-        }
-      }
+      for (int j = 0; j < 8; j++)
+        if (c + j < w) p[c + j] = to_t<T>(v[8 * k + j]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; i++)
-      if (i * NT + tid < w) p[i * NT + tid] = to_t<T>(v[i]);
   }
 }
 
-// Sums over the NT threads of a row, in a fixed order; every thread gets them. Consecutive
-// calls alternate between two places in LDS, so one barrier each is enough.
+// Sums over the NT threads of a row, in a fixed order; every thread gets them. Up to 64 threads are
+// neighbours in a wave. Consecutive calls of more alternate between two places in LDS, so one
+// barrier each is enough.
 template <int NT> struct LnSum {
   float* lds;   // [2][NT / 64][4]
   int buf = 0;
+  static __device__ __forceinline__ float lanes(float v) {
+    v += dpp<QP_SWAP1>(v);
+    v += dpp<QP_X2>(v);
+    v += dpp<DPP_ROW_HALF_MIRROR>(v);
+    if constexpr (NT >= 16) v += dpp<DPP_ROW_MIRROR>(v);
+    if constexpr (NT == 32) {
+      const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+      v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    }
+    if constexpr (NT >= 64) v = col4_sum(v);
+    return v;
+  }
   template <int M> __device__ __forceinline__ void operator()(float (&v)[M]) {
 #pragma unroll
-    for (int i = 0; i < M; i++) v[i] = col4_sum(row16_sum(v[i]));
+    for (int i = 0; i < M; i++) v[i] = lanes(v[i]);
     if constexpr (NT > 64) {
       float* at = lds + buf * (NT / 64) * 4;
       buf ^= 1;
@@ -113,25 +138,25 @@ template <int NT> struct LnSum {
 // mean, m[1] of d^2, with GY also m[2] of gy = dy wt and m[3] of gy d. d and the sums are of the
 // centred row. The first mean is taken about s0, the row's first value, so that a row of one value
 // is centred to exact zeros, however large it is.
-template <int NT, int E, bool VEC, bool GY, class Sum>
+template <int NT, int E, bool GY, class Sum>
 __device__ __forceinline__ void ln_center(const LnGeo& g, const float (&s)[E], const float (&dy)[E],
                                           const float (&wt)[E], float s0, float scale, float (&d)[E],
                                           float (&m)[GY ? 4 : 2], int tid, Sum& sum) {
   float one[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < E; i++)
-    if (ln_col<NT, VEC>(i, tid) < g.w) one[0] = fmaf(fmaf(s[i], scale, -s0 * scale), g.winv, one[0]);
+    if (ln_col<NT>(i, tid) < g.w) one[0] = fmaf(fmaf(s[i], scale, -s0 * scale), g.winv, one[0]);
   sum(one);
   const float mean = fmaf(s0, scale, one[0]);
 #pragma unroll
   for (int i = 0; i < (GY ? 4 : 2); i++) m[i] = 0.0f;
 #pragma unroll
   for (int i = 0; i < E; i++) {
-    d[i] = ln_col<NT, VEC>(i, tid) < g.w ? fmaf(s[i], scale, -mean) : 0.0f;
+    d[i] = ln_col<NT>(i, tid) < g.w ? fmaf(s[i], scale, -mean) : 0.0f;
     m[0] += d[i];
     m[1] = fmaf(d[i], d[i], m[1]);
     if constexpr (GY) {
-      const float gy = dy[i] * wt[i];
+      const float gy = ln_col<NT>(i, tid) < g.w ? dy[i] * wt[i] : 0.0f;
       m[2] += gy;
       m[3] = fmaf(gy, d[i], m[3]);
     }
@@ -139,7 +164,7 @@ __device__ __forceinline__ void ln_center(const LnGeo& g, const float (&s)[E], c
   sum(m);
   const float off = m[0] * g.winv;
 #pragma unroll
-  for (int i = 0; i < E; i++) d[i] = ln_col<NT, VEC>(i, tid) < g.w ? d[i] - off : 0.0f;
+  for (int i = 0; i < E; i++) d[i] = ln_col<NT>(i, tid) < g.w ? d[i] - off : 0.0f;
   m[1] = fmaf(-off, m[0], m[1]);
   if (m[1] < 0.0f) m[1] = 0.0f;   // NaN stays
   if constexpr (GY) m[3] = fmaf(-off, m[2], m[3]);
@@ -148,118 +173,144 @@ __device__ __forceinline__ void ln_center(const LnGeo& g, const float (&s)[E], c
 // The row's d and the rstd that goes with it. A row whose squares (or differences) overflow is
 // centred again at 2^-80 of its size, where eps is nothing beside them; one that holds an infinity
 // or a NaN stays NaN.
-template <int NT, int E, bool VEC, bool GY, class Sum>
+template <int NT, int E, bool GY, class Sum>
 __device__ __forceinline__ float ln_stats(const LnGeo& g, const float (&s)[E], const float (&dy)[E],
                                           const float (&wt)[E], float s0, float (&d)[E], float (&m)[GY ? 4 : 2],
                                           float& scale, int tid, Sum& sum) {
   scale = 1.0f;
   float eps = g.eps;
-  ln_center<NT, E, VEC, GY>(g, s, dy, wt, s0, scale, d, m, tid, sum);
+  ln_center<NT, E, GY>(g, s, dy, wt, s0, scale, d, m, tid, sum);
   if (!(m[1] < __builtin_inff())) {   // the same for all threads of the row
     scale = kLnScale;
     eps = 0.0f;
-    ln_center<NT, E, VEC, GY>(g, s, dy, wt, s0, scale, d, m, tid, sum);
+    ln_center<NT, E, GY>(g, s, dy, wt, s0, scale, d, m, tid, sum);
   }
   return 1.0f / sqrtf(fmaf(m[1], g.winv, eps));
 }
 
-// Rows are dealt to the workgroups (to their waves, where a wave has a row) one after the other.
-template <typename T, int NT, int E, bool VEC, bool RES>
+// Rows are dealt to the workgroups, 256 / NT at a time where NT is less, one after the other.
+template <typename T, int NT, int E, bool RES>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_fwd(LnGeo g, const T* __restrict__ x, const float* res,
                                                                 const float* __restrict__ weight,
                                                                 const float* __restrict__ bias, T* __restrict__ y,
                                                                 float* total) {
-  constexpr int NB = NT == 64 ? 256 : NT, RPB = NB / NT;
+  constexpr int RPB = NT <= 64 ? 256 / NT : 1;
   __shared__ float lds[NT > 64 ? NT / 64 * 8 : 1];
-  const int tid = NT == 64 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  const int tid = NT <= 64 ? (int)threadIdx.x % NT : (int)threadIdx.x, at = NT <= 64 ? (int)threadIdx.x / NT : 0;
   LnSum<NT> sum{lds};
   float wt[E], bs[E];
-  ln_load<float, NT, E, VEC>(wt, weight, g.w, tid);
+  ln_load<float, NT, E>(wt, weight, g.w, tid, false);
   if (bias != nullptr) {
-    ln_load<float, NT, E, VEC>(bs, bias, g.w, tid);
+    ln_load<float, NT, E>(bs, bias, g.w, tid, false);
   } else {
 #pragma unroll
     for (int i = 0; i < E; i++) bs[i] = 0.0f;
   }
   const int64_t step = (int64_t)gridDim.x * RPB;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + (NT == 64 ? threadIdx.x >> 6 : 0); row < g.n; row += step) {
+  for (int64_t row = (int64_t)blockIdx.x * RPB + at; row < g.n; row += step) {
     float s[E], d[E], m[2], scale, s0 = to_f(x[(size_t)row * g.xs]);
-    ln_load<T, NT, E, VEC>(s, x + (size_t)row * g.xs, g.w, tid);
+    const bool past = ln_past(g, row, (size_t)g.w);
+    ln_load<T, NT, E>(s, x + (size_t)row * g.xs, g.w, tid, ln_past(g, row, g.xs));
     if constexpr (RES) {
       float r[E];
       s0 += res[(size_t)row * g.w];
-      ln_load<float, NT, E, VEC>(r, res + (size_t)row * g.w, g.w, tid);
+      ln_load<float, NT, E>(r, res + (size_t)row * g.w, g.w, tid, past);
 #pragma unroll
       for (int i = 0; i < E; i++) s[i] += r[i];
-      ln_store<float, NT, E, VEC>(total + (size_t)row * g.w, s, g.w, tid);
     }
-    const float rstd = ln_stats<NT, E, VEC, false>(g, s, s, s, s0, d, m, scale, tid, sum);
+    const float rstd = ln_stats<NT, E, false>(g, s, s, s, s0, d, m, scale, tid, sum);
+    // behind the row's sums, which need every thread's s0: `total` may be `res`
+    if constexpr (RES) ln_store<float, NT, E>(total + (size_t)row * g.w, s, g.w, tid);
 #pragma unroll
     for (int i = 0; i < E; i++) d[i] = fmaf(d[i] * rstd, wt[i], bs[i]);
-    ln_store<T, NT, E, VEC>(y + (size_t)row * g.w, d, g.w, tid);
+    ln_store<T, NT, E>(y + (size_t)row * g.w, d, g.w, tid);
   }
 }
 
 // part: a row of w sums for each workgroup, of d_weight, then of d_bias (NULL: neither is wanted).
-// TS: of the normed rows (float where a residual was added).
-template <typename T, typename TS, int NT, int E, bool VEC>
+// TS: of the normed rows (float where a residual was added). With E = 32 elements a thread's 2 E
+// sums stand in LDS (ln_wide_lds bytes) and the weights are loaded for each row: 16384 x 16384 bf16
+// with residual 947 us at 1024 threads of 16 elements, whose 128 registers do not hold them.
+template <int NT, int E> constexpr size_t ln_wide_lds = E == 32 ? (size_t)2 * E * NT * 4 : 0;
+template <typename T, typename TS, int NT, int E>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_bwd(LnGeo g, const TS* __restrict__ x,
                                                                 const float* __restrict__ weight,
                                                                 const T* __restrict__ dy, const float* d_sum,
                                                                 T* __restrict__ d_x, float* d_res,
                                                                 float* __restrict__ part) {
-  constexpr int RPB = NT == 64 ? 4 : 1;
-  __shared__ float lds[NT > 64 ? NT / 64 * 8 : RPB * 64 * E];
-  const int tid = NT == 64 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
-  const int wave = NT == 64 ? (int)(threadIdx.x >> 6) : 0;
+  constexpr int RPB = NT <= 64 ? 256 / NT : 1;
+  constexpr bool HOLD = E < 32;
+  extern __shared__ float acc[];   // [2][E][NT]
+  __shared__ float lds[NT > 64 ? NT / 64 * 8 : 256 * E];
+  const int tid = NT <= 64 ? (int)threadIdx.x % NT : (int)threadIdx.x, at = NT <= 64 ? (int)threadIdx.x / NT : 0;
   LnSum<NT> sum{lds};
-  float wt[E], dw[E], db[E];
-  ln_load<float, NT, E, VEC>(wt, weight, g.w, tid);
+  float held[HOLD ? E : 1], dw[E], db[E];
+  if constexpr (HOLD) ln_load<float, NT, E>(held, weight, g.w, tid, false);
 #pragma unroll
-  for (int i = 0; i < E; i++) dw[i] = db[i] = 0.0f;
+  for (int i = 0; i < E; i++) {
+    dw[i] = db[i] = 0.0f;
+    if constexpr (!HOLD) acc[i * NT + tid] = acc[(E + i) * NT + tid] = 0.0f;
+  }
   const int64_t step = (int64_t)gridDim.x * RPB;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + wave; row < g.n; row += step) {
-    float s[E], v[E], d[E], m[4], scale;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + at; row < g.n; row += step) {
+    float s[E], v[E], d[E], wt[E], m[4], scale;
+    const bool past = ln_past(g, row, (size_t)g.w);
     const float s0 = to_f(x[(size_t)row * g.xs]);
-    ln_load<TS, NT, E, VEC>(s, x + (size_t)row * g.xs, g.w, tid);
-    ln_load<T, NT, E, VEC>(v, dy + (size_t)row * g.w, g.w, tid);
-    const float rstd = ln_stats<NT, E, VEC, true>(g, s, v, wt, s0, d, m, scale, tid, sum);
+    ln_load<TS, NT, E>(s, x + (size_t)row * g.xs, g.w, tid, ln_past(g, row, g.xs));
+    ln_load<T, NT, E>(v, dy + (size_t)row * g.w, g.w, tid, past);
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int i = 0; i < E; i++) wt[i] = held[i];
+    } else {
+      ln_load<float, NT, E>(wt, weight, g.w, tid, false);
+    }
+    const float rstd = ln_stats<NT, E, true>(g, s, v, wt, s0, d, m, scale, tid, sum);
     const float m1 = m[2] * g.winv, m2 = m[3] * g.winv * rstd, rs = rstd * scale;
 #pragma unroll
     for (int i = 0; i < E; i++) {
       const float xhat = d[i] * rstd;
-      db[i] += v[i];
-      dw[i] = fmaf(v[i], xhat, dw[i]);
+      if constexpr (HOLD) {
+        db[i] += v[i];
+        dw[i] = fmaf(v[i], xhat, dw[i]);
+      } else {   // the thread's own places
+        acc[(E + i) * NT + tid] += v[i];
+        acc[i * NT + tid] = fmaf(v[i], xhat, acc[i * NT + tid]);
+      }
       d[i] = rs * (fmaf(v[i], wt[i], -m1) - xhat * m2);
     }
     if (d_sum != nullptr) {
-      ln_load<float, NT, E, VEC>(s, d_sum + (size_t)row * g.w, g.w, tid);
+      ln_load<float, NT, E>(s, d_sum + (size_t)row * g.w, g.w, tid, past);
 #pragma unroll
       for (int i = 0; i < E; i++) d[i] += s[i];
     }
-    if (d_x != nullptr) ln_store<T, NT, E, VEC>(d_x + (size_t)row * g.w, d, g.w, tid);
-    if (d_res != nullptr) ln_store<float, NT, E, VEC>(d_res + (size_t)row * g.w, d, g.w, tid);
+    if (d_x != nullptr) ln_store<T, NT, E>(d_x + (size_t)row * g.w, d, g.w, tid);
+    if (d_res != nullptr) ln_store<float, NT, E>(d_res + (size_t)row * g.w, d, g.w, tid);
   }
   if (part == nullptr) return;
+  if constexpr (!HOLD)
+#pragma unroll
+    for (int i = 0; i < E; i++) dw[i] = acc[i * NT + tid], db[i] = acc[(E + i) * NT + tid];
   float* pw = part + (size_t)blockIdx.x * g.w;
   float* pb = pw + (size_t)gridDim.x * g.w;
-  if constexpr (NT == 64) {   // the four waves' sums first
+  if constexpr (RPB > 1) {   // the rows' places first
     for (int k = 0; k < 2; k++) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < E; i++) lds[(wave * E + i) * 64 + tid] = k == 0 ? dw[i] : db[i];
+      for (int i = 0; i < E; i++) lds[(at * E + i) * NT + tid] = k == 0 ? dw[i] : db[i];
       __syncthreads();
-      if (wave == 0) {
+      if (at == 0) {
         float v[E];
 #pragma unroll
-        for (int i = 0; i < E; i++)
-          v[i] = (lds[i * 64 + tid] + lds[(E + i) * 64 + tid]) + (lds[(2 * E + i) * 64 + tid] + lds[(3 * E + i) * 64 + tid]);
-        ln_store<float, NT, E, VEC>(k == 0 ? pw : pb, v, g.w, tid);
+        for (int i = 0; i < E; i++) {
+          v[i] = lds[i * NT + tid];
+          for (int q = 1; q < RPB; q++) v[i] += lds[(q * E + i) * NT + tid];
+        }
+        ln_store<float, NT, E>(k == 0 ? pw : pb, v, g.w, tid);
       }
     }
   } else {
-    ln_store<float, NT, E, VEC>(pw, dw, g.w, tid);
-    ln_store<float, NT, E, VEC>(pb, db, g.w, tid);
+    ln_store<float, NT, E>(pw, dw, g.w, tid);
+    ln_store<float, NT, E>(pb, db, g.w, tid);
   }
 }
 

@@ -17,14 +17,13 @@ namespace {
 
 struct LnPlan {
   LnGeo g;
-  bool bf, res, empty, vec;
+  bool bf, res, empty;
   int NT, E;          // threads of a row, elements of a thread
   int nblk, nfwd;     // workgroups of the gradients and of the forward
   size_t part, flag, ws;
 };
 
-// bases: x starts at 16 bytes (the gradients read a sum, which always does).
-int make_ln_plan(const moments_ln_desc* d, LnPlan* P, bool bases) {
+int make_ln_plan(const moments_ln_desc* d, LnPlan* P) {
   if (d == nullptr) return MOMENTS_EINVAL;
   if (d->n < 0 || d->w < 1 || (d->residual != 0 && d->residual != 1) || d->reserved != 0) return MOMENTS_EINVAL;
   if (d->dtype != MOMENTS_F32 && d->dtype != MOMENTS_BF16) return MOMENTS_EINVAL;
@@ -41,11 +40,10 @@ int make_ln_plan(const moments_ln_desc* d, LnPlan* P, bool bases) {
   g.n = d->n; g.w = (int)d->w; g.xs = (size_t)xs;
   g.eps = d->eps;
   g.winv = 1.0f / (float)d->w;
-  P->vec = bases && g.w % 8 == 0 && xs % 8 == 0;
   P->E = g.w <= 512 ? 8 : 16;
-  P->NT = 64;
+  P->NT = 8;
   while (P->NT * P->E < g.w) P->NT *= 2;
-  const int rows = P->NT == 64 ? 4 : 1, nb = std::max(P->NT, P->NT == 64 ? 256 : 128);
+  const int rows = P->NT <= 64 ? 256 / P->NT : 1, nb = std::max(P->NT, P->NT <= 64 ? 256 : 128);
   const int64_t all = (d->n + rows - 1) / rows;
   P->nfwd = (int)std::min<int64_t>(all, kCUs * 4096 / nb);
   P->nblk = (int)std::min<int64_t>(all, kCUs * std::max(768 / nb, 1));
@@ -55,18 +53,20 @@ int make_ln_plan(const moments_ln_desc* d, LnPlan* P, bool bases) {
   return MOMENTS_OK;
 }
 
-// Calls f(TT<T>, IC<NT>, IC<E>, IC<VEC>) for the compiled variant of the plan.
+// Calls f(TT<T>, IC<NT>, IC<E>) for the compiled variant of the plan.
 template <class F>
 int with_ln(const LnPlan& P, F&& f) {
-  auto by_vec = [&](auto tt, auto nt, auto e) -> int { return P.vec ? f(tt, nt, e, IC<1>{}) : f(tt, nt, e, IC<0>{}); };
   auto by_w = [&](auto tt) -> int {
     switch (P.NT) {
-      case 64: return P.E == 8 ? by_vec(tt, IC<64>{}, IC<8>{}) : by_vec(tt, IC<64>{}, IC<16>{});
-      case 128: return by_vec(tt, IC<128>{}, IC<16>{});
-      case 256: return by_vec(tt, IC<256>{}, IC<16>{});
-      case 512: return by_vec(tt, IC<512>{}, IC<16>{});
+      case 8: return f(tt, IC<8>{}, IC<8>{});
+      case 16: return f(tt, IC<16>{}, IC<8>{});
+      case 32: return f(tt, IC<32>{}, IC<8>{});
+      case 64: return P.E == 8 ? f(tt, IC<64>{}, IC<8>{}) : f(tt, IC<64>{}, IC<16>{});
+      case 128: return f(tt, IC<128>{}, IC<16>{});
+      case 256: return f(tt, IC<256>{}, IC<16>{});
+      case 512: return f(tt, IC<512>{}, IC<16>{});
     }
-    return by_vec(tt, IC<1024>{}, IC<16>{});
+    return f(tt, IC<1024>{}, IC<16>{});
   };
   return P.bf ? by_w(TT<bf16>{}) : by_w(TT<float>{});
 }
@@ -92,31 +92,30 @@ extern "C" {
 
 int64_t moments_ln_workspace_size(const moments_ln_desc* desc) {
   LnPlan P;
-  MOM_TRY(make_ln_plan(desc, &P, true));
+  MOM_TRY(make_ln_plan(desc, &P));
   return P.empty ? 0 : (int64_t)P.ws;
 }
 
 int moments_ln_fwd(const moments_ln_desc* desc, const void* x, const float* res, const float* weight,
                    const float* bias, void* y, float* sum, void* stream) {
   LnPlan P;
-  MOM_TRY(make_ln_plan(desc, &P, aligned16(x)));
+  MOM_TRY(make_ln_plan(desc, &P));
   if (P.empty) return 0;
   if (!x || !weight || !y) return MOMENTS_EINVAL;
   if (P.res ? !res || !sum : res != nullptr || sum != nullptr) return MOMENTS_EINVAL;
   if (!at_element(x, P.bf)) return MOMENTS_EINVAL;
   MOM_TRY(all_aligned({res, weight, bias, y, sum}));
   hipStream_t st = (hipStream_t)stream;
-  MOM_TRY(with_ln(P, [&](auto tt, auto nt, auto ee, auto vec) -> int {
+  MOM_TRY(with_ln(P, [&](auto tt, auto nt, auto ee) -> int {
     using T = typename decltype(tt)::type;
     constexpr int NT = decltype(nt)::value, E = decltype(ee)::value;
-    constexpr bool VEC = decltype(vec)::value != 0;
     ProfScope ps(KID_LN_FWD, st);
-    const dim3 grid((unsigned)P.nfwd), block(NT == 64 ? 256 : NT);
+    const dim3 grid((unsigned)P.nfwd), block(NT <= 64 ? 256 : NT);
     if (P.res)
-      hipLaunchKernelGGL((k_ln_fwd<T, NT, E, VEC, true>), grid, block, 0, st, P.g, (const T*)x, res, weight, bias,
+      hipLaunchKernelGGL((k_ln_fwd<T, NT, E, true>), grid, block, 0, st, P.g, (const T*)x, res, weight, bias,
                          (T*)y, sum);
     else
-      hipLaunchKernelGGL((k_ln_fwd<T, NT, E, VEC, false>), grid, block, 0, st, P.g, (const T*)x, res, weight, bias,
+      hipLaunchKernelGGL((k_ln_fwd<T, NT, E, false>), grid, block, 0, st, P.g, (const T*)x, res, weight, bias,
                          (T*)y, sum);
     return check_launch();
   }));
@@ -132,14 +131,8 @@ int moments_ln_bwd(const moments_ln_desc* desc, const void* x, const float* weig
                    const float* d_sum, void* d_x, float* d_res, float* d_weight, float* d_bias, void* workspace,
                    size_t workspace_bytes, void* stream) {
   LnPlan P;
-  moments_ln_desc of;   // with a residual x is the sum: float32 rows, one after the other
-  if (desc != nullptr && desc->residual == 1) {
-    MOM_TRY(make_ln_plan(desc, &P, true));
-    of = *desc;
-    of.x_stride = 0;
-    desc = &of;
-  }
-  MOM_TRY(make_ln_plan(desc, &P, aligned16(x)));
+  MOM_TRY(make_ln_plan(desc, &P));
+  if (P.res) P.g.xs = (size_t)P.g.w;   // x is the sum: float32 rows, one after the other
   hipStream_t st = (hipStream_t)stream;
   if (!P.res && (d_sum != nullptr || d_res != nullptr)) return MOMENTS_EINVAL;
   MOM_TRY(all_aligned({weight, d_y, d_sum, d_x, d_res, d_weight, d_bias, workspace}));
@@ -149,19 +142,24 @@ int moments_ln_bwd(const moments_ln_desc* desc, const void* x, const float* weig
   if (workspace == nullptr || workspace_bytes < P.ws) return MOMENTS_EWORKSPACE;
   unsigned char* ws = (unsigned char*)workspace;
   float* part = d_weight || d_bias ? (float*)(ws + P.part) : nullptr;
-  MOM_TRY(with_ln(P, [&](auto tt, auto nt, auto ee, auto vec) -> int {
+  MOM_TRY(with_ln(P, [&](auto tt, auto nt, auto ee) -> int {
     using T = typename decltype(tt)::type;
-    constexpr int NT = decltype(nt)::value, E = decltype(ee)::value;
-    constexpr bool VEC = decltype(vec)::value != 0;
-    ProfScope ps(KID_LN_BWD, st);
-    const dim3 grid((unsigned)P.nblk), block(NT == 64 ? 256 : NT);
-    if (P.res)
-      hipLaunchKernelGGL((k_ln_bwd<T, float, NT, E, VEC>), grid, block, 0, st, P.g, (const float*)x, weight,
-                         (const T*)d_y, d_sum, (T*)d_x, d_res, part);
-    else
-      hipLaunchKernelGGL((k_ln_bwd<T, T, NT, E, VEC>), grid, block, 0, st, P.g, (const T*)x, weight, (const T*)d_y,
-                         d_sum, (T*)d_x, d_res, part);
-    return check_launch();
+    // as many threads as a row of the plan has, or half of 1024 with twice the elements
+    constexpr bool WIDE = decltype(nt)::value == 1024;
+    constexpr int NT = WIDE ? 512 : decltype(nt)::value, E = WIDE ? 32 : decltype(ee)::value;
+    const auto go = [&](auto ts) -> int {
+      using TS = typename decltype(ts)::type;
+      constexpr size_t lds = ln_wide_lds<NT, E>;
+      if constexpr (lds > 0) {
+        static std::atomic<uint64_t> done{0};
+        MOM_TRY(set_lds_once(done, k_ln_bwd<T, TS, NT, E>, lds));
+      }
+      ProfScope ps(KID_LN_BWD, st);
+      hipLaunchKernelGGL((k_ln_bwd<T, TS, NT, E>), dim3((unsigned)P.nblk), dim3(NT <= 64 ? 256 : NT), lds, st, P.g,
+                         (const TS*)x, weight, (const T*)d_y, d_sum, (T*)d_x, d_res, part);
+      return check_launch();
+    };
+    return P.res ? go(TT<float>{}) : go(TT<T>{});
   }));
   MOM_TRY(launch_ln_sum(part, P.nblk, P.g.w, d_weight, d_bias, st));
   if (check_finite_on()) {

@@ -52,8 +52,12 @@ int make_rec_plan(const moments_rec_desc* d, RecPlan* P, bool bases) {
   if (d->b * ncg > kMostItems) return MOMENTS_ENOTSUP;
   g.ncg = (int)ncg;
   const int64_t items = d->b * ncg, tiles = (g.V + REC_TILE - 1) / REC_TILE;
-  // One workgroup to a CU, and no more of them than CUs.
-  const int64_t n = std::max<int64_t>(1, std::min(kCUs / std::max<int64_t>(items, 1), tiles / 2));
+  // Segments where the chain groups alone leave half the CUs without one: as many as fill them once
+  // (a second round of workgroups costs as much as the first: 8 x 8192 x 2050 bf16, 136 groups, one
+  // segment 982 us for forward and gradients, two 1514), of a tile or more, from four tiles on
+  // (600 x 512: a tile each 54 us, two 69, one segment 75; 2 x 300 x 4096, three tiles: one segment
+  // 47 us, three 53).
+  const int64_t n = tiles < 4 ? 1 : std::max<int64_t>(1, std::min(kCUs / std::max<int64_t>(items, 1), tiles));
   const int64_t per = std::max<int64_t>((tiles + n - 1) / n, 1);
   g.seg = (int)(per * REC_TILE);
   g.nseg = (int)std::max<int64_t>((tiles + per - 1) / per, 1);
