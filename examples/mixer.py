@@ -157,6 +157,8 @@ def main():
         loss = (out.float() - target).square().mean() + 1e-9 * m2.square().mean()
         opt.zero_grad()
         loss.backward()
+        grads = M.grad_desc([p.grad for p in mixer.parameters()])
+        M.moments_grad_clip(grads, M.moments_grad_norm(grads), 1.0)
         opt.step()
         print(f"step {step}: loss {loss.item():.5f}", flush=True)
     whole, _ = mixer(u[:, :200])
