@@ -118,7 +118,7 @@ __global__ __launch_bounds__(1024) void k_grad_total(const double* __restrict__ 
 __global__ __launch_bounds__(GRAD_T) void k_grad_clip(GradArgs A, const float* __restrict__ norm, float max_norm) {
   const float n = *norm;
   float f = max_norm / (n + 1e-6f);
-  if (!(n < __builtin_inff()) || !(f < 1.0f)) f = 1.0f;
+  if (!(n >= 0.0f && n < __builtin_inff()) || !(f < 1.0f)) f = 1.0f;
   for (unsigned i0 = blockIdx.x; i0 < A.pieces; i0 += gridDim.x) {
     const unsigned piece = A.pieces - 1 - i0;
     const GradSpan sp = A.span[grad_find(A, piece)];

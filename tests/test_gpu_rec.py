@@ -361,6 +361,33 @@ def test_captured(s, w):
             assert torch.equal(a, b)
 
 
+def test_more_chains_than_the_card_holds_at_once():
+    """Several rounds of workgroups, and a count of them that is no multiple of the card's."""
+    for b, s, w, dtype in ((300, 40, 130, BF16), (37, 260, 1100, F32)):
+        both(make(b, s, w, M.GATE_MIX, dtype, seed=b), M.GATE_MIX)
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace, in segments."""
+    t = [make(2, 2100, 70, M.GATE_UNIT, BF16, seed=k) for k in (1, 2)]
+    want = [run_all(v, M.GATE_UNIT) for v in t]
+    streams = [torch.cuda.Stream() for _ in t]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for v, st in zip(t, streams):
+            with torch.cuda.stream(st):
+                d = desc(v, M.GATE_UNIT)
+                y, last, saved = M.moments_rec_fwd_save(d, v["x"], v["g"], v["z"], v["h0"])
+                g = M.moments_rec_bwd_saved(d, v["x"], v["g"], v["z"], v["h0"], saved, v["d_y"], v["d_h_last"])
+                got.append({**g, "y": y, "h_last": last})
+        for st in streams:
+            st.synchronize()
+        for a, b in zip(want, got):
+            for k in a:
+                assert torch.equal(a[k], b[k]), k
+
+
 def test_offsets_past_32_bits():
     """Rows cut out of a projection of more than 2^31 values."""
     s, width = 70_000, 32_768

@@ -93,3 +93,58 @@ def test_prompt_and_single_tokens():
 def test_the_example_runs():
     _example().main()
     _example("mixer").main()
+
+
+def test_second_order_gradients_are_refused():
+    """The gradients have no graph of their own: asking for theirs is an error, not a silent zero."""
+    ex = _example()
+    f = lambda *shape: torch.randn(*shape, device="cuda").requires_grad_()  # noqa: E731
+    x, g, z = f(1, 6, 8), f(1, 6, 8), f(1, 6, 8)
+    weight, bias = f(8), f(8)
+    for leaf, out in ((x, ex.Recurrence.apply(x, g, z, None, M.GATE_MIX, None)[0]),
+                      (weight, ex.AddNorm.apply(x, z, weight, bias)[0])):
+        (d,) = torch.autograd.grad(out.square().sum(), leaf, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (d.square().sum() + leaf.sum()).backward()
+
+
+def test_a_state_changed_before_the_backward_is_noticed():
+    """The initial state, a cached one, is updated in place by single tokens between forward and backward."""
+    ex = _example()
+    f = lambda *shape: torch.randn(*shape, device="cuda").requires_grad_()  # noqa: E731
+    x, g, z, h0 = f(1, 6, 8), f(1, 6, 8), f(1, 6, 8), f(1, 8)
+    y, _ = ex.Recurrence.apply(x, g, z, h0, M.GATE_MIX, None)
+    one = [v[:, :1].detach().contiguous() for v in (x, g, z)]
+    M.moments_rec_step(M.rec_desc(*one, M.GATE_MIX), *one, h0.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_training_step_captured():
+    """Forward and backward of the stack in a graph, replayed on new inputs, against the eager step."""
+    torch.manual_seed(8)
+    stack = _example().Stack(32, blocks=2, inner=24, dtype=torch.float32)
+    u = torch.randn(2, 140, 32, device="cuda")
+    params = list(stack.parameters())
+
+    def step():
+        x, res = stack(u)
+        return torch.autograd.grad(x.square().sum() + res.square().sum(), params)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for seed in (1, 2, 3):
+        torch.manual_seed(seed)
+        u.copy_(torch.randn(2, 140, 32, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for a, b in zip(got, step()):
+            assert torch.allclose(a, b, rtol=1e-5, atol=1e-5 * b.abs().max().item())
