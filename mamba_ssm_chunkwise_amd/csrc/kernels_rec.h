@@ -90,12 +90,13 @@ template <typename T, int V> __device__ __forceinline__ rvec<T, V> rec_bld(RecBu
 }
 // Stores are streamed past the caches' other lines: 8 x 8192 x 4096 bf16, forward 448 us without that,
 // 407 with it, gradients 743 and 731; with a kernel that reads y at once behind it 616 and 604 us, of
-// 8 x 1024 x 4096 82 and 79. (Loads likewise slow down where x and g are read twice.)
+// 8 x 1024 x 4096 82 and 79. (Loads likewise slow down where x and g are read twice; single 16-bit
+// stores, 8 x 8192 x 4095 gradients, 1198 us without and 1750 with it, so those go without.)
 constexpr int kRecStream = 2;   // the instruction's nt bit
 template <typename T, int V> __device__ __forceinline__ void rec_bst(RecBuf r, unsigned off, const float (&f)[V]) {
   typedef unsigned u2 __attribute__((ext_vector_type(2)));
   const rvec<T, V> v = rec_vec<T, V>(f);
-  if constexpr (sizeof(T) * V == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, off, 0, kRecStream);
+  if constexpr (sizeof(T) * V == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, off, 0, 0);
   else if constexpr (sizeof(T) * V == 4)
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, off, 0, kRecStream);
   else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, v), r, off, 0, kRecStream);
