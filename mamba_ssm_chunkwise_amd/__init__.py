@@ -676,9 +676,14 @@ def rec_desc(x, g, z=None, gate=GATE_LOG, valid_len=None, valid_lens=None) -> Re
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be a torch.Tensor [b,s,w]")
     b, s, w = x.shape
-    d = RecDesc(b, s, w, s if valid_len is None else int(valid_len), _row_stride("x", x), _row_stride("g", g),
-                0 if z is None else _row_stride("z", z), BF16 if x.dtype is torch.bfloat16 else F32, int(gate),
-                0 if z is None else 1)
+    dense, steps = (s * w, w, 1), []
+    for name, t in (("x", x), ("g", g), ("z", z)):
+        if t is None and name == "z":
+            steps.append(0)
+        else:   # dense rows are what most calls have
+            steps.append(w if isinstance(t, torch.Tensor) and t.stride() == dense else _row_stride(name, t))
+    d = RecDesc(b, s, w, s if valid_len is None else int(valid_len), *steps,
+                BF16 if x.dtype is torch.bfloat16 else F32, int(gate), 0 if z is None else 1)
     return set_valid_lens(d, valid_lens) if valid_lens is not None else d
 
 
@@ -819,9 +824,9 @@ def _flat_rows(name, t, w):
     """Rows of t [..., w] and the elements between them (0: dense)."""
     if not isinstance(t, torch.Tensor) or t.dim() < 1 or t.shape[-1] != w:
         raise ValueError(f"{name} must be a torch.Tensor of rows of {w}")
-    n = t.numel() // w if w else 0
-    if t.is_contiguous() or n == 0:
-        return n, 0
+    if t.is_contiguous() or t.numel() == 0:
+        return (t.numel() // w if w else 0), 0
+    n = t.numel() // w
     dims = [(size, step) for size, step in zip(t.shape[:-1], t.stride()[:-1]) if size > 1]
     step = dims[-1][1] if dims else w
     want = step
