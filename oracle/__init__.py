@@ -22,6 +22,11 @@ Two independent CPU implementations live here:
   a coaxial closed form, finite differences, scale invariance, and the moments
   gradient with respect to the increments).
 
+* ``gated_rec.py`` and ``layer_norm.py`` (numpy fp64): the gated recurrence over
+  channels and layer norm with a residual, each with its derivative and with the
+  error that float32 arithmetic may leave in each element, pinned in
+  ``tests/test_block_oracles.py``.
+
 Parity pins (see ``tests/test_oracle_pins.py``): finite differences, torch
 float64 autograd, chunk-length invariance, the rotation-orthogonality trace
 identity, closed forms, zero gradients past valid_len, d_m2 antisymmetric
