@@ -41,7 +41,6 @@ struct RecGeo {
   int V;               // min(valid_len, s)
   int ncg;             // channel groups (64 * channels of a lane)
   int nseg;            // segments of a sequence
-  int seg;             // tokens of a segment, whole tiles
   size_t xs, gs, zs;   // elements between tokens
   const int* lens;
 };
@@ -208,23 +207,21 @@ struct RecAt {
     on = c < g.w;
     ch = on ? c : 0;
     Vb = rec_len(g, bi);
-    t0 = min(seg * g.seg, Vb);
-    t1 = seg == g.nseg - 1 ? Vb : min(t0 + g.seg, Vb);
+    // each sequence has segments of its own length, whole tiles
+    const int per = ((Vb + REC_TILE - 1) / REC_TILE + g.nseg - 1) / g.nseg * REC_TILE;
+    t0 = min(seg * per, Vb);
+    t1 = min(t0 + per, Vb);
   }
 };
 
-// Zeros in the rows of a segment's share that hold no token: past the sequence's length, and
-// past the batch's.
+// Zeros in a segment's share of the rows past the sequence's length.
 template <typename T, int V>
 __device__ __forceinline__ void rec_zero_rows(const RecGeo& g, const RecAt& at, T* out, int wave, int waves) {
   if (!at.on || out == nullptr) return;
   const float zero[V] = {};
   T* p = out + ((size_t)at.bi * g.s) * g.w + at.ch;
-  const int per = (g.s - g.V + g.nseg - 1) / g.nseg;
-  const int a0 = max(at.Vb, min(at.seg * g.seg, g.V)), a1 = at.seg == g.nseg - 1 ? g.V : min((at.seg + 1) * g.seg, g.V);
-  for (int t = a0 + wave; t < a1; t += waves) rec_put<T, V>(p + (size_t)t * g.w, zero);
-  const int b0 = g.V + min(at.seg * per, g.s - g.V), b1 = g.V + min((at.seg + 1) * per, g.s - g.V);
-  for (int t = b0 + wave; t < b1; t += waves) rec_put<T, V>(p + (size_t)t * g.w, zero);
+  const int per = (g.s - at.Vb + g.nseg - 1) / g.nseg, t0 = at.Vb + at.seg * per;
+  for (int t = t0 + wave; t < min(t0 + per, g.s); t += waves) rec_put<T, V>(p + (size_t)t * g.w, zero);
 }
 
 // The maps of the segments before a workgroup's own (BACK: behind it), in order, on the state that

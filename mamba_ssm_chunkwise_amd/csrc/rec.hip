@@ -59,7 +59,6 @@ int make_rec_plan(const moments_rec_desc* d, RecPlan* P, bool bases) {
   // 47 us, three 53).
   const int64_t n = tiles < 4 ? 1 : std::max<int64_t>(1, std::min(kCUs / std::max<int64_t>(items, 1), tiles));
   const int64_t per = std::max<int64_t>((tiles + n - 1) / n, 1);
-  g.seg = (int)(per * REC_TILE);
   g.nseg = (int)std::max<int64_t>((tiles + per - 1) / per, 1);
   const size_t states = (size_t)g.b * g.w * 4, nsv = (size_t)((g.V + REC_SAVE - 1) / REC_SAVE);
   size_t o = 0;
