@@ -340,7 +340,8 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
  * h_last = h0. A decay that underflows (g = -inf, every g below -104; below -87.3 it may) is exactly
  * zero: such a token starts its sequence anew, whatever stood before, infinities and NaN too.
  * Otherwise a value that is not finite reaches its channel's later tokens (in the gradients its earlier
- * ones too) and no other.
+ * ones too) and no other. Log-decays above zero let a state grow; runs of them whose product passes
+ * 2^127 (88 in all) may give infinities or NaN where a state that is not zero meets them.
  *
  * moments_rec_bwd is the vector-Jacobian product: d_y[b,s,w] (desc->dtype) and d_h_last[b,w] (float32,
  * NULL: zeros) to d_x, d_g, d_z in desc->dtype, [b,s,w] dense, and d_h0 (float32); any of them may be

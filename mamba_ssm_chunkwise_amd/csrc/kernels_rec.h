@@ -7,7 +7,7 @@
 // workgroup have the same channels and one run of tokens after the other, so a wave reads whole
 // pieces of rows and nothing crosses lanes. A run is the map h -> P h + H of its entering state;
 // the waves exchange (P, H) through LDS, once for a tile of all their runs, and every wave
-// applies those before its own. What enters the next tile stays in registers. The next tile's
+// applies those before its own. The last wave hands on what enters the next tile. The next tile's
 // rows are in flight meanwhile.
 //
 // A decay of exactly zero (one that underflows) clears: what stood before, infinities and NaN too,
@@ -151,9 +151,10 @@ __device__ __forceinline__ float rec_sigma(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e));
 }
 
-// A map applied to a state; a map after another.
+// A map applied to a state; a map after another. A state of zero stays out of it however far the
+// product of a growing run's decays went (infinity times zero would be NaN).
 __device__ __forceinline__ float rec_apply(float P, float H, float h) {
-  return __float_as_int(P) < 0 ? H : fmaf(P, h, H);
+  return __float_as_int(P) < 0 || h == 0.0f ? H : fmaf(P, h, H);
 }
 __device__ __forceinline__ float rec_chain(float P, float next) { return __float_as_int(next) < 0 ? next : P * next; }
 

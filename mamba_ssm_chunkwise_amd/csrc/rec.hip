@@ -25,7 +25,7 @@ struct RecPlan {
 // A launch holds fewer than 2^32 threads, up to 1024 of them to a workgroup.
 constexpr int64_t kMostItems = ((int64_t)1 << 22) - 1;
 
-// lanes: x, g and z start where a lane's two channels can be read as one piece.
+// bases: x, g and z start where a lane's two channels can be read as one piece.
 int make_rec_plan(const moments_rec_desc* d, RecPlan* P, bool bases) {
   if (d == nullptr) return MOMENTS_EINVAL;
   if (d->b < 0 || d->s < 0 || d->w < 1 || d->valid_len < 0 || d->reserved != 0) return MOMENTS_EINVAL;
@@ -281,7 +281,8 @@ int moments_rec_step(const moments_rec_desc* desc, const void* x, const void* g,
     ProfScope ps(KID_REC_STEP, st);
     const int cols = (q.w + 256 * V - 1) / (256 * V);   // a launch holds fewer than 2^32 threads
     hipLaunchKernelGGL((k_rec_step<T, decltype(gk)::value, decltype(zk)::value != 0, V>),
-                       dim3((unsigned)cols, (unsigned)std::min(q.b, std::min(65535, (1 << 23) / cols))), dim3(256), 0, st, q, (const T*)x, (const T*)g, (const T*)z, slots, nslots, state, (T*)y);
+                       dim3((unsigned)cols, (unsigned)std::min(q.b, std::min(65535, (1 << 23) / cols))), dim3(256), 0,
+                       st, q, (const T*)x, (const T*)g, (const T*)z, slots, nslots, state, (T*)y);
     return check_launch();
   }));
   if (check_finite_on()) {

@@ -9,7 +9,8 @@ With ``bounds`` every result comes with what float32 arithmetic may be off by, i
 walk. One rounding is U = 2^-24 of its result; the exponential, reciprocal and root
 instructions are good to one unit in the last place, 2 U. M is the sum of magnitudes that
 a state is made of; each token may add the roundings of its decay, of the product that
-hands the state on (through runs, waves and segments: 4) and of its input.
+hands the state on (through runs, waves and segments: 4) and of its input. 2^-125 is for what
+underflows on the way; a state of zero that meets an input of zero stays exactly that.
 """
 import numpy as np
 
@@ -77,7 +78,8 @@ def rec(x, g, z, h0, kind, lens=None, d_y=None, d_h_last=None, bounds=False):
             H[t + 1] = _times(a[t], H[t]) + u[t]
             if bounds:
                 M[t + 1] = a[t] * M[t] + np.abs(u[t])
-                E[t + 1] = a[t] * E[t] + U * ((ra[t] + 4) * a[t] * M[t] + (ru[t] + 4) * np.abs(u[t])) + 2.0 ** -125
+                E[t + 1] = a[t] * E[t] + U * ((ra[t] + 4) * a[t] * M[t] + (ru[t] + 4) * np.abs(u[t]))
+                E[t + 1] += np.where((M[t] > 0) | (u[t] != 0), 2.0 ** -125, 0.0)
         o["h_last"][i], o["e_h_last"][i] = H[n], E[n]
         if z is None:
             o["y"][i, :n], o["e_y"][i, :n] = H[1:], E[1:]
@@ -119,7 +121,8 @@ def rec(x, g, z, h0, kind, lens=None, d_y=None, d_h_last=None, bounds=False):
                 o["d_z"][i, t] = dy[t] * H[t + 1] * sp
                 o["e_d_z"][i, t] = np.abs(dy[t]) * (E[t + 1] * np.abs(sp) + np.abs(H[t + 1]) * esp) + 3 * U * np.abs(
                     dy[t] * H[t + 1] * sp)
-            ec = at * (ec + U * rsrc[t] * np.abs(src[t])) + U * (ra[t] + 4) * at * (np.abs(src[t]) + mc) + 2.0 ** -125
+            ec = at * (ec + U * rsrc[t] * np.abs(src[t])) + U * (ra[t] + 4) * at * (np.abs(src[t]) + mc)
+            ec += np.where((mc > 0) | (src[t] != 0), 2.0 ** -125, 0.0)
             c, mc = _times(at, d), at * (np.abs(src[t]) + mc)
         o["d_h0"][i], o["e_d_h0"][i] = c, ec
     return o

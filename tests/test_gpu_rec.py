@@ -201,6 +201,18 @@ def test_growth(dtype):
     both(t, M.GATE_LOG)
 
 
+@pytest.mark.parametrize("s", [120, 4000])
+def test_growth_of_a_zero_state(s):
+    """Log-decays above zero over tokens of zeros, whose product leaves the range, before the first value."""
+    t = make(1, s, 6, M.GATE_LOG, F32, state=False)
+    t["g"][:, :s - 40] = 1.0
+    t["x"][:, :s - 40] = 0.0
+    t["d_y"][:] = 0.0
+    got = run_all(t, M.GATE_LOG)
+    compare(t, M.GATE_LOG, got)
+    assert torch.isfinite(got["y"]).all()
+
+
 def test_last_state_may_be_the_first_and_pieces():
     """h_last in h0's buffer, d_h0 in d_h_last's, split into segments and not; a sequence in pieces."""
     for s in (60, 3000):
