@@ -938,13 +938,18 @@ class GradDesc:
                 _expect(f"out[{i}]", o, t.shape, t.dtype, t.device)
             spans[i] = _lib.Span(t.data_ptr(), o.data_ptr(), t.numel(), BF16 if t.dtype is torch.bfloat16 else F32)
         self.spans, self.count = spans, len(self.grads)
+        self._at = self._addresses()
+
+    def _addresses(self):
+        tensors = self.grads if self.in_place else self.grads + self.out
+        return [*map(torch.Tensor.data_ptr, tensors)]
 
 
 def grad_desc(grads, out=None) -> GradDesc:
     """Descriptor of many gradients (contiguous float32 or bfloat16 tensors on one device),
     for moments_grad_norm and moments_grad_clip; it keeps the tensors, which may be refilled
-    between calls. ``out``: tensors like them that take the clipped values (None: in place).
-    Raises if a tensor that is written overlaps another."""
+    between calls but not given other memory. ``out``: tensors like them that take the
+    clipped values (None: in place). Raises if a tensor that is written overlaps another."""
     d = GradDesc(grads, out)
     rc = _lib.load().moments_grad_validate(d.spans, d.count)
     if rc == _lib.EINVAL:
@@ -959,6 +964,9 @@ def moments_grad_workspace_size(desc: GradDesc) -> int:
 
 
 def _grad_device(desc, norm):
+    if desc._addresses() != desc._at:
+        raise ValueError("a tensor of the descriptor has got other memory since (resize_, set_, .data): "
+                         "make the descriptor again")
     dev = desc.device if desc.device is not None else (norm.device if isinstance(norm, torch.Tensor) else None)
     if dev is None:
         raise ValueError("norm is required when there are no gradients")

@@ -226,3 +226,16 @@ def test_binding_checks():
         M.moments_grad_norm(M.grad_desc([]))
     with pytest.raises(M.MomentsError):
         M._size(_lib.load().moments_ln_workspace_size(ctypes.byref(M.ln_desc(x, eps=0.0))))
+
+
+def test_gradients_that_moved():
+    """A descriptor holds addresses: tensors that got other memory since are refused."""
+    for move in (lambda t: t.resize_(4096), lambda t: t.untyped_storage().resize_(0),
+                 lambda t: setattr(t, "data", torch.zeros(40))):
+        for moved in (0, 1):
+            g, o = torch.zeros(40), torch.zeros(40)
+            d = M.grad_desc([g], out=[o])
+            move((g, o)[moved])
+            for call in (lambda: M.moments_grad_norm(d), lambda: M.moments_grad_clip(d, torch.zeros(()), 1.0)):
+                with pytest.raises(ValueError, match="other memory"):
+                    call()
