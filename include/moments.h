@@ -341,7 +341,8 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
  * zero: such a token starts its sequence anew, whatever stood before, infinities and NaN too.
  * Otherwise a value that is not finite reaches its channel's later tokens (in the gradients its earlier
  * ones too) and no other. Log-decays above zero let a state grow; runs of them whose product passes
- * 2^127 (88 in all) may give infinities or NaN where a state that is not zero meets them.
+ * 2^127 (88 in all) may give infinities or NaN where a state that is not zero meets them, and a single
+ * one above 88 is an infinite decay: NaN where it meets a state of zero.
  *
  * moments_rec_bwd is the vector-Jacobian product: d_y[b,s,w] (desc->dtype) and d_h_last[b,w] (float32,
  * NULL: zeros) to d_x, d_g, d_z in desc->dtype, [b,s,w] dense, and d_h0 (float32); any of them may be
