@@ -340,7 +340,7 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
  * h_last = h0. A decay that underflows (g = -inf, every g below -104; below -87.3 it may) is exactly
  * zero: such a token starts its sequence anew, whatever stood before, infinities and NaN too.
  * Otherwise a value that is not finite reaches its channel's later tokens (in the gradients its earlier
- * ones too) and no other. Log-decays above zero let a state grow; runs of them whose product passes
+ * ones too, back to a token whose decay is zero) and no other. Log-decays above zero let a state grow; runs of them whose product passes
  * 2^127 (88 in all) may give infinities or NaN where a state that is not zero meets them, and a single
  * one above 88 is an infinite decay: NaN where it meets a state of zero.
  *

@@ -163,8 +163,11 @@ __device__ __forceinline__ float rec_chain(float P, float next) { return __float
 template <bool CLEAR> __device__ __forceinline__ float rec_next(float a, float h, float u) {
   return CLEAR && a == 0.0f ? u : fmaf(a, h, u);
 }
+// The sign of a cleared map outlasts decays of the same run that are not numbers: the gradients'
+// map of the run, which starts behind them, still forgets at the clearing token.
 template <bool CLEAR> __device__ __forceinline__ float rec_prod(float P, float a) {
-  return CLEAR && a == 0.0f ? -1.0f : P * a;
+  if constexpr (CLEAR) return a == 0.0f ? -1.0f : __builtin_copysignf(P * a, P);
+  else return P * a;
 }
 template <bool CLEAR> __device__ __forceinline__ float rec_back(float a, float d) {
   return CLEAR && a == 0.0f ? 0.0f : a * d;

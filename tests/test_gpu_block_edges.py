@@ -1,0 +1,43 @@
+"""Edges of the gated recurrence, layer norm and the gradients' norm and clipping on the GPU."""
+import pytest
+import torch
+
+import mamba_ssm_chunkwise_amd as M
+from bounds_util import same
+from test_gpu_rec import make as make_rec, run_all
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", [M.GATE_LOG, M.GATE_MIX, M.GATE_UNIT])
+@pytest.mark.parametrize("s", [60, 2200])
+@pytest.mark.parametrize("clear,bad", [(18, 21), (18, 30), (50, 51), (8, 15)])
+def test_a_cleared_state_keeps_later_nan_decays_out_of_earlier_gradients(dtype, gate, s, clear, bad):
+    """A decay that is not a number behind a clearing one: in the same run of tokens, and in another."""
+    t = make_rec(2, s, 12, gate, dtype, seed=s + clear)
+    t["g"][:, clear] = -float("inf")
+    clean = run_all(t, gate)
+    t["g"][0, bad, 3] = float("nan")
+    t["g"][1, bad, ::5] = float("nan")
+    got = run_all(t, gate)
+    for k in ("d_x", "d_g", "d_z"):      # what the clearing token hands to the left is zero
+        assert same(got[k][:, :clear].contiguous(), clean[k][:, :clear].contiguous()), k
+    assert same(got["d_h0"], clean["d_h0"])
+    assert same(got["y"][:, :bad].contiguous(), clean["y"][:, :bad].contiguous())
+    assert torch.isnan(got["y"][0, bad:, 3]).all() and torch.isnan(got["h_last"][0, 3])
+    assert torch.isnan(got["d_x"][0, clear:bad, 3]).all()
+
+
+def test_a_cleared_state_keeps_later_infinite_decays_out_of_earlier_gradients():
+    """A clearing decay, two whose product underflows, an infinite one, all in one run of tokens."""
+    t = make_rec(1, 60, 6, M.GATE_LOG, F32, z=False, seed=8)
+    t["g"][:, 18] = -float("inf")
+    clean = run_all(t, M.GATE_LOG)
+    t["g"][0, 19:21, 2], t["g"][0, 21, 2] = -60.0, 95.0
+    got = run_all(t, M.GATE_LOG)
+    for k in ("d_x", "d_g"):
+        assert same(got[k][:, :18].contiguous(), clean[k][:, :18].contiguous()), k
+    assert same(got["d_h0"], clean["d_h0"])
