@@ -45,13 +45,13 @@ class Recurrence(torch.autograd.Function):
     def forward(ctx, x, g, z, h0, gate, lens):
         ctx.desc = M.rec_desc(x, g, z, gate, valid_lens=lens)
         y, last, saved = M.moments_rec_fwd_save(ctx.desc, x, g, z, h0)
-        ctx.save_for_backward(x, g, z, h0, saved)
+        ctx.save_for_backward(x, g, z, h0, lens, saved)   # lens too: the descriptor reads the buffer again
         return y, last
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_y, d_last):
-        x, g, z, h0, saved = ctx.saved_tensors
+        x, g, z, h0, _, saved = ctx.saved_tensors
         d = M.moments_rec_bwd_saved(ctx.desc, x, g, z, h0, saved, d_y.contiguous(), d_last.contiguous())
         return d["d_x"], d["d_g"], d["d_z"], d["d_h0"], None, None
 

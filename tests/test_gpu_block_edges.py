@@ -5,6 +5,7 @@ import torch
 import mamba_ssm_chunkwise_amd as M
 from bounds_util import same
 from test_gpu_rec import make as make_rec, run_all
+from test_gpu_recurrent import _example
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -41,3 +42,15 @@ def test_a_cleared_state_keeps_later_infinite_decays_out_of_earlier_gradients():
     for k in ("d_x", "d_g"):
         assert same(got[k][:, :18].contiguous(), clean[k][:, :18].contiguous()), k
     assert same(got["d_h0"], clean["d_h0"])
+
+
+@pytest.mark.parametrize("n", [3, 60])
+def test_lengths_changed_before_the_backward_are_noticed(n):
+    """A buffer of lengths that the next batch fills between a forward and its backward."""
+    ex = _example()
+    f = lambda *shape: torch.randn(*shape, device=DEV).requires_grad_()  # noqa: E731
+    lens = torch.tensor([40, 7], dtype=torch.int32, device=DEV)
+    y, _ = ex.Recurrence.apply(f(2, 80, 8), f(2, 80, 8), f(2, 80, 8), None, M.GATE_MIX, lens)
+    lens.fill_(n)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
