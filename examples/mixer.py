@@ -59,13 +59,13 @@ class Attention(torch.autograd.Function):
         desc = M.attn_desc(x, khat, valid_lens=lens)
         y, last, saved = M.moments_attn_fwd_save(desc, x, khat, qhat, da, h0)
         ctx.desc = desc
-        ctx.save_for_backward(x, khat, qhat, da, h0, saved)
+        ctx.save_for_backward(x, khat, qhat, da, h0, lens, saved)   # lens too: the descriptor reads the buffer again
         return y, last
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_y, d_last):
-        x, khat, qhat, da, h0, saved = ctx.saved_tensors
+        x, khat, qhat, da, h0, _, saved = ctx.saved_tensors
         g = M.moments_attn_bwd_saved(ctx.desc, x, khat, qhat, da, h0, saved, d_y.contiguous(), d_last.contiguous())
         return g["d_xhat"], g["d_bhat"], g["d_qhat"], g["d_da"], g["d_h0"], None
 

@@ -54,3 +54,13 @@ def test_lengths_changed_before_the_backward_are_noticed(n):
     lens.fill_(n)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+def test_lengths_of_the_mixer_changed_before_the_backward_are_noticed():
+    ex = _example("mixer")
+    f = lambda *shape: torch.randn(*shape, device=DEV).requires_grad_()  # noqa: E731
+    lens = torch.tensor([40, 7], dtype=torch.int32, device=DEV)
+    y, _ = ex.Attention.apply(f(2, 80, 1, 2, 8), f(2, 80, 1, 2, 16), f(2, 80, 1, 2, 16), f(2, 80, 2), None, lens)
+    lens.fill_(3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
