@@ -39,6 +39,8 @@
  * keeps them alive until the work queued on `stream` (a hipStream_t, NULL = the
  * default stream) has finished. The library allocates no device memory, keeps
  * no state between calls, and fully overwrites every output it is given.
+ * Kernels are launched on the current HIP device, which has to be the one that
+ * the buffers and the stream belong to.
  *
  * Errors: functions return 0 on success or a negative MOMENTS_E* code; nothing
  * is launched when a call fails validation. moments_strerror() names a code;

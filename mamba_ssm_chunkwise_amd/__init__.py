@@ -1,8 +1,8 @@
 """MI355X-native physical-frame state moments (Mamba-3): fwd + recompute bwd.
 
 Python entry points with the C ABI's names. They marshal torch tensors into the
-HIP library (libmoments.so) and run on torch's current HIP stream; no
-computation happens in Python. See include/moments.h for the operation.
+HIP library (libmoments.so) and run on torch's current HIP stream of the tensors'
+device, whichever device is current; no computation happens in Python. See include/moments.h for the operation.
 """
 from __future__ import annotations
 
@@ -141,8 +141,26 @@ def _require_gpu(dev):
     _lib.load()
 
 
-def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream_of(dev):
+    """torch's current stream on dev as an integer handle."""
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _launch(dev, call, *args):
+    """Calls the library with torch's current stream on dev as the last argument and raises on
+    an error. HIP launches on the current device, so dev is made that for the call."""
+    if dev.index is None or dev.index == _current_device():
+        rc = call(*args, _stream_of(dev))
+    else:
+        with torch.cuda.device(dev.index):
+            rc = call(*args, _stream_of(dev))
+    _lib.check(rc)
 
 
 def _workspace(desc, is_bwd, device, workspace):
@@ -168,10 +186,8 @@ def moments_fwd(desc: Desc, xhat, bhat, da, rot, h0, m2=None, m1=None, workspace
     if m1 is None:
         m1 = torch.empty(desc.b, desc.h, desc.p, desc.r, dtype=torch.float32, device=dev)
     ws = _workspace(desc, False, dev, workspace)
-    rc = _lib.load().moments_fwd(ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(da), _ptr(rot),
-                                 _ptr(h0), _ptr(m2), _ptr(m1), _ptr(ws), ws.numel() * ws.element_size(),
-                                 _stream(dev))
-    _lib.check(rc)
+    _launch(dev, _lib.load().moments_fwd, ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(da), _ptr(rot), _ptr(h0),
+            _ptr(m2), _ptr(m1), _ptr(ws), ws.numel() * ws.element_size())
     return m2, m1
 
 
@@ -183,9 +199,8 @@ def moments_fwd_static(desc: Desc, xhat, bhat, da, rot, h0, m2, m1):
     _expect("m2", m2, (desc.b, desc.h, desc.r, desc.r), torch.float32, dev)
     _expect("m1", m1, (desc.b, desc.h, desc.p, desc.r), torch.float32, dev)
     _require_gpu(dev)
-    rc = _lib.load().moments_fwd_static(ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(da), _ptr(rot),
-                                        _ptr(h0), _ptr(m2), _ptr(m1), _stream(dev))
-    _lib.check(rc)
+    _launch(dev, _lib.load().moments_fwd_static, ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(da), _ptr(rot),
+            _ptr(h0), _ptr(m2), _ptr(m1))
     return m2, m1
 
 
@@ -222,10 +237,8 @@ def moments_fwd_save(desc: Desc, xhat, bhat, da, rot, h0, m2=None, m1=None, save
         m1 = torch.empty(desc.b, desc.h, desc.p, desc.r, dtype=torch.float32, device=dev)
     sv = _saved_buffer(desc, dev, saved)
     ws = _workspace(desc, False, dev, workspace)
-    rc = _lib.load().moments_fwd_save(ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(da), _ptr(rot),
-                                      _ptr(h0), _ptr(m2), _ptr(m1), _ptr(sv), sv.numel(), _ptr(ws),
-                                      ws.numel() * ws.element_size(), _stream(dev))
-    _lib.check(rc)
+    _launch(dev, _lib.load().moments_fwd_save, ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(da), _ptr(rot),
+            _ptr(h0), _ptr(m2), _ptr(m1), _ptr(sv), sv.numel(), _ptr(ws), ws.numel() * ws.element_size())
     return m2, m1, sv
 
 
@@ -258,15 +271,13 @@ def moments_bwd(desc: Desc, xhat, bhat, da, rot, h0, d_m2, d_m1, want=("xhat", "
             out[key] = torch.empty(specs[k], dtype=dt, device=dev)
     ws = _workspace(desc, True, dev, workspace)
     grads = (_ptr(d_m2), _ptr(d_m1), _ptr(out["d_xhat"]), _ptr(out["d_bhat"]), _ptr(out["d_da"]),
-             _ptr(out["d_rot"]), _ptr(out["d_h0"]), _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
+             _ptr(out["d_rot"]), _ptr(out["d_h0"]), _ptr(ws), ws.numel() * ws.element_size())
+    ins = (ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(da), _ptr(rot), _ptr(h0))
     if _saved is None:
-        rc = _lib.load().moments_bwd(ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(da), _ptr(rot),
-                                     _ptr(h0), *grads)
+        _launch(dev, _lib.load().moments_bwd, *ins, *grads)
     else:
         sv = _saved_buffer(desc, dev, _saved)
-        rc = _lib.load().moments_bwd_saved(ctypes.byref(desc), _ptr(xhat), _ptr(bhat), _ptr(da), _ptr(rot),
-                                           _ptr(h0), _ptr(sv), sv.numel() * sv.element_size(), *grads)
-    _lib.check(rc)
+        _launch(dev, _lib.load().moments_bwd_saved, *ins, _ptr(sv), sv.numel() * sv.element_size(), *grads)
     return out
 
 
@@ -317,10 +328,9 @@ def _rot_call(desc, is_bwd, inc, d_rot, out):
     ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
     lib = _lib.load()
     if is_bwd:
-        rc = lib.moments_rot_bwd(ctypes.byref(desc), _ptr(inc), _ptr(d_rot), _ptr(out), _ptr(ws), n, _stream(dev))
+        _launch(dev, lib.moments_rot_bwd, ctypes.byref(desc), _ptr(inc), _ptr(d_rot), _ptr(out), _ptr(ws), n)
     else:
-        rc = lib.moments_rot_fwd(ctypes.byref(desc), _ptr(inc), _ptr(out), _ptr(ws), n, _stream(dev))
-    _lib.check(rc)
+        _launch(dev, lib.moments_rot_fwd, ctypes.byref(desc), _ptr(inc), _ptr(out), _ptr(ws), n)
     return out
 
 
@@ -338,14 +348,6 @@ def moments_rot_bwd(desc: Desc, inc, d_rot, d_inc=None):
 # These entry points also serve single tokens, where the host's time counts: tensors are
 # checked in one pass and pointers go to the library as plain integers.
 _DTYPES = {F32: torch.float32, BF16: torch.bfloat16}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_of(dev):
-    """torch's current stream on dev as an integer handle."""
-    if _raw_stream is not None and dev.index is not None:
-        return _raw_stream(dev.index)
-    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _tensors_ok(dev, specs):
@@ -461,12 +463,12 @@ def _attn_forward(desc, xhat, bhat, qhat, da, h0, y, h_last, saved, want_saved, 
     if h_last is None:
         h_last = torch.empty(state, dtype=torch.float32, device=dev)
     head = (ctypes.byref(desc), *ins, y.data_ptr(), h_last.data_ptr())
-    tail = (*_scratch(ws), _stream_of(dev))
+    tail = _scratch(ws)
     if want_saved:
         saved = _buffer("saved", moments_attn_saved_size(desc), dev, saved)
-        _lib.check(lib.moments_attn_fwd_save(*head, *_scratch(saved), *tail))
+        _launch(dev, lib.moments_attn_fwd_save, *head, *_scratch(saved), *tail)
         return y, h_last, torch.empty(0, dtype=torch.uint8, device=dev) if saved is None else saved
-    _lib.check(lib.moments_attn_fwd(*head, *tail))
+    _launch(dev, lib.moments_attn_fwd, *head, *tail)
     return y, h_last
 
 
@@ -509,12 +511,12 @@ def moments_attn_bwd(desc: AttnDesc, xhat, bhat, qhat, da, h0, d_y, d_h_last=Non
     out, grads = _gradients(dev, want, out, {"xhat": xhat, "bhat": bhat, "qhat": qhat, "da": da, "h0": h0})
     lib = _lib.load()
     ws = _buffer("workspace", moments_attn_workspace_size(desc, True), dev, workspace)
-    tail = (*cot, *grads, *_scratch(ws), _stream_of(dev))
+    tail = (*cot, *grads, *_scratch(ws))
     if _saved is None:
-        _lib.check(lib.moments_attn_bwd(ctypes.byref(desc), *ins, *tail))
+        _launch(dev, lib.moments_attn_bwd, ctypes.byref(desc), *ins, *tail)
     else:
         sv = _buffer("saved", moments_attn_saved_size(desc), dev, _saved)
-        _lib.check(lib.moments_attn_bwd_saved(ctypes.byref(desc), *ins, *_scratch(sv), *tail))
+        _launch(dev, lib.moments_attn_bwd_saved, ctypes.byref(desc), *ins, *_scratch(sv), *tail)
     return out
 
 
@@ -543,7 +545,7 @@ def moments_attn_step(desc: AttnDesc, xhat, bhat, qhat, da, state, slots=None, y
     if y is None:
         y = torch.empty_like(xhat)
         out = y.data_ptr()
-    _lib.check(lib.moments_attn_step(ctypes.byref(desc), *ins[:4], sl, n, st, out, _stream_of(dev)))
+    _launch(dev, lib.moments_attn_step, ctypes.byref(desc), *ins[:4], sl, n, st, out)
     return y
 
 
@@ -632,7 +634,7 @@ def moments_qk_fwd(desc: QkDesc, q, k, wq, wk, bq=None, bk=None, rot=None, qhat=
         qhat = torch.empty(shape, dtype=dt, device=dev)
     if khat is None:
         khat = torch.empty_like(qhat)
-    _lib.check(lib.moments_qk_fwd(ctypes.byref(desc), *ins, qhat.data_ptr(), khat.data_ptr(), _stream_of(dev)))
+    _launch(dev, lib.moments_qk_fwd, ctypes.byref(desc), *ins, qhat.data_ptr(), khat.data_ptr())
     return qhat, khat
 
 
@@ -645,7 +647,7 @@ def moments_qk_bwd(desc: QkDesc, q, k, wq, wk, bq, bk, rot, d_qhat, d_khat,
     cot = _tensors_ok(dev, (("d_qhat", d_qhat, shape, dt, False), ("d_khat", d_khat, shape, dt, False)))
     out, grads = _gradients(dev, want, out, {"q": q, "k": k, "wq": wq, "wk": wk, "bq": bq, "bk": bk, "rot": rot})
     ws = _buffer("workspace", moments_qk_workspace_size(desc), dev, workspace)
-    _lib.check(_lib.load().moments_qk_bwd(ctypes.byref(desc), *ins, *cot, *grads, *_scratch(ws), _stream_of(dev)))
+    _launch(dev, _lib.load().moments_qk_bwd, ctypes.byref(desc), *ins, *cot, *grads, *_scratch(ws))
     return out
 
 
@@ -753,11 +755,11 @@ def _rec_forward(desc, x, g, z, h0, y, h_last, saved, want_saved, workspace):
     if h_last is None:
         h_last = torch.empty(state, dtype=torch.float32, device=dev)
     head = (ctypes.byref(desc), *ins, y.data_ptr(), h_last.data_ptr())
-    tail = (*_scratch(ws), _stream_of(dev))
+    tail = _scratch(ws)
     if want_saved:
-        _lib.check(lib.moments_rec_fwd_save(*head, *_scratch(saved), *tail))
+        _launch(dev, lib.moments_rec_fwd_save, *head, *_scratch(saved), *tail)
         return y, h_last, torch.empty(0, dtype=torch.uint8, device=dev) if saved is None else saved
-    _lib.check(lib.moments_rec_fwd(*head, *tail))
+    _launch(dev, lib.moments_rec_fwd, *head, *tail)
     return y, h_last
 
 
@@ -783,12 +785,12 @@ def moments_rec_bwd(desc: RecDesc, x, g, z, h0, d_y, d_h_last=None, want=("x", "
     out, grads = _gradients(dev, want, out, {"x": x, "g": g, "z": z, "h0": h0})
     lib = _lib.load()
     ws = _buffer("workspace", moments_rec_workspace_size(desc, True), dev, workspace)
-    tail = (*cot, *grads, *_scratch(ws), _stream_of(dev))
+    tail = (*cot, *grads, *_scratch(ws))
     if _saved is None:
-        _lib.check(lib.moments_rec_bwd(ctypes.byref(desc), *ins, *tail))
+        _launch(dev, lib.moments_rec_bwd, ctypes.byref(desc), *ins, *tail)
     else:
         sv = _buffer("saved", moments_rec_saved_size(desc), dev, _saved)
-        _lib.check(lib.moments_rec_bwd_saved(ctypes.byref(desc), *ins, *_scratch(sv), *tail))
+        _launch(dev, lib.moments_rec_bwd_saved, ctypes.byref(desc), *ins, *_scratch(sv), *tail)
     return out
 
 
@@ -815,7 +817,7 @@ def moments_rec_step(desc: RecDesc, x, g, z, state, slots=None, y=None):
     if y is None:
         y = _dense_like(x)
         out = y.data_ptr()
-    _lib.check(lib.moments_rec_step(ctypes.byref(desc), *ins[:3], sl, n, st, out, _stream_of(dev)))
+    _launch(dev, lib.moments_rec_step, ctypes.byref(desc), *ins[:3], sl, n, st, out)
     return y
 
 
@@ -881,8 +883,8 @@ def moments_ln_fwd(desc: LnDesc, x, weight, bias=None, res=None, y=None, sum=Non
         y = _dense_like(x)
     if sum is None and desc.residual:
         sum = torch.empty_like(res)
-    _lib.check(lib.moments_ln_fwd(ctypes.byref(desc), x.data_ptr(), rp, wp, bp, y.data_ptr(),
-                                  None if sum is None else sum.data_ptr(), _stream_of(dev)))
+    _launch(dev, lib.moments_ln_fwd, ctypes.byref(desc), x.data_ptr(), rp, wp, bp, y.data_ptr(),
+            None if sum is None else sum.data_ptr())
     return y, sum
 
 
@@ -902,8 +904,7 @@ def moments_ln_bwd(desc: LnDesc, x, weight, bias, d_y, d_sum=None, want=("x", "r
     out, grads = _gradients(dev, want, out, like)
     lib = _lib.load()
     ws = _buffer("workspace", moments_ln_workspace_size(desc), dev, workspace)
-    _lib.check(lib.moments_ln_bwd(ctypes.byref(desc), x.data_ptr(), wp, yp, sp, *grads, *_scratch(ws),
-                                  _stream_of(dev)))
+    _launch(dev, lib.moments_ln_bwd, ctypes.byref(desc), x.data_ptr(), wp, yp, sp, *grads, *_scratch(ws))
     return out
 
 
@@ -983,7 +984,7 @@ def moments_grad_norm(desc: GradDesc, norm=None, workspace=None):
     _wrote(norm)
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=dev)
-    _lib.check(lib.moments_grad_norm(desc.spans, desc.count, norm.data_ptr(), *_scratch(ws), _stream_of(dev)))
+    _launch(dev, lib.moments_grad_norm, desc.spans, desc.count, norm.data_ptr(), *_scratch(ws))
     return norm
 
 
@@ -995,7 +996,7 @@ def moments_grad_clip(desc: GradDesc, norm, max_norm):
     (at,) = _tensors_ok(dev, (("norm", norm, (), torch.float32, False),))
     lib = _gpu(dev)
     _wrote(*desc.out)
-    _lib.check(lib.moments_grad_clip(desc.spans, desc.count, at, float(max_norm), _stream_of(dev)))
+    _launch(dev, lib.moments_grad_clip, desc.spans, desc.count, at, float(max_norm))
     return desc.out
 
 

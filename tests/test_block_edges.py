@@ -1,0 +1,51 @@
+"""Edges of the binding and of the C entry points of the gated recurrence, layer norm and the
+gradients' norm and clipping, on the host. No GPU is touched."""
+import contextlib
+import inspect
+import re
+
+import pytest
+import torch
+
+import mamba_ssm_chunkwise_amd as M
+from mamba_ssm_chunkwise_amd import _lib
+
+
+def test_a_call_runs_on_its_tensors_device(monkeypatch):
+    """HIP launches on the current device: tensors of another make theirs current for the call, on
+    their own stream, and the one before is current again, after an error too."""
+    now = [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        before, now[0] = now[0], index
+        try:
+            yield
+        finally:
+            now[0] = before
+
+    monkeypatch.setattr(M, "_current_device", lambda: now[0])
+    monkeypatch.setattr(M, "_stream_of", lambda dev: 100 + dev.index)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    seen = []
+
+    def call(*args):
+        seen.append((now[0], args))
+        return args[0]
+
+    for index in (0, 1, 3):
+        M._launch(torch.device("cuda", index), call, 0, "a")
+        assert seen[-1] == (index, (0, "a", 100 + index)) and now[0] == 0
+        with pytest.raises(M.MomentsError):
+            M._launch(torch.device("cuda", index), call, _lib.EINVAL)
+        assert now[0] == 0
+
+
+def test_every_launch_names_its_device():
+    """No entry point that takes a stream is called in another way."""
+    src = inspect.getsource(M)
+    direct = set(re.findall(r"(?:lib|load\(\))\.(moments_\w+)\(", src))
+    assert direct and all(re.search(r"_(size|validate|len|enable|reset|read)$", n) for n in direct), direct
+    launched = set(re.findall(r"_launch\(dev, (?:lib|_lib\.load\(\))\.(moments_\w+),", src))
+    takes_stream = {n for n in _lib.EXPORTS if re.search(r"_(fwd|bwd|step|norm|clip|static|save|saved)$", n)}
+    assert launched == takes_stream
