@@ -357,9 +357,10 @@ int moments_qk_bwd(const moments_qk_desc* desc, const void* q, const void* k, co
  * moments_rec_step is one token of each sequence (desc->s = 1) on a pool of states state[nslots,w],
  * slots as in moments_attn_step.
  *
- * Supported: s <= 2^28, w <= 2^24, b * w / 64 (each rounded up) below 2^22, strides up to 2^25;
- * b or s may be 0 (with s = 0 h_last is h0 and d_h0 is d_h_last). Ownership, errors and
- * MOMENTS_CHECK_FINITE are those stated above; moments_rec_fwd may need no workspace. */
+ * Supported: s <= 2^28, w <= 2^24, b * w / 64 (each rounded up) below 2^22, strides up to 2^25
+ * (2^37 where s is below 2: the last token of each sequence of a long projection); b or s may be 0
+ * (with s = 0 h_last is h0 and d_h0 is d_h_last). Ownership, errors and MOMENTS_CHECK_FINITE are
+ * those stated above; moments_rec_fwd may need no workspace. */
 typedef enum { MOMENTS_GATE_LOG = 0, MOMENTS_GATE_MIX = 1, MOMENTS_GATE_UNIT = 2 } moments_gate_kind;
 
 typedef struct {

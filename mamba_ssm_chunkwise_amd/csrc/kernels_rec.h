@@ -42,6 +42,7 @@ struct RecGeo {
   int ncg;             // channel groups (64 * channels of a lane)
   int nseg;            // segments of a sequence
   size_t xs, gs, zs;   // elements between tokens
+  size_t xr, gr, zr;   // the same within a sequence: w where it has one token, as the next may be farther than 32 bits
   const int* lens;
 };
 
@@ -384,9 +385,9 @@ __global__ __launch_bounds__(REC_W * 64) void k_rec_fwd(RecGeo g, const T* __res
   for (int j = 0; j < V; j++) last[j] = h[j];
   rvec<T, V> rx[R], rg[R], rz[R];
   auto fetch = [&](int t) {
-    rec_rows<T, V, R>(rx, xp, g.xs, t, at.Vb - t, cols, lo);
-    rec_rows<T, V, R>(rg, gp, g.gs, t, at.Vb - t, cols, lo);
-    if constexpr (Z && OUT) rec_rows<T, V, R>(rz, zp, g.zs, t, at.Vb - t, cols, lo);
+    rec_rows<T, V, R>(rx, xp, g.xr, t, at.Vb - t, cols, lo);
+    rec_rows<T, V, R>(rg, gp, g.gr, t, at.Vb - t, cols, lo);
+    if constexpr (Z && OUT) rec_rows<T, V, R>(rz, zp, g.zr, t, at.Vb - t, cols, lo);
   };
   if (at.t0 < at.t1) fetch(at.t0 + wave * R);
   int buf = 0;
@@ -512,9 +513,9 @@ __global__ __launch_bounds__(REC_WB * 64) void k_rec_bwd(RecGeo g, const T* __re
   float hs[V];
   auto fetch = [&](int n) {
     const int t = at.t0 + n * TL + wave * R;
-    rec_rows<T, V, R>(rx, xp, g.xs, t, at.Vb - t, cols, lo);
-    rec_rows<T, V, R>(rg, gp, g.gs, t, at.Vb - t, cols, lo);
-    if constexpr (Z) rec_rows<T, V, R>(rz, zp, g.zs, t, at.Vb - t, cols, lo);
+    rec_rows<T, V, R>(rx, xp, g.xr, t, at.Vb - t, cols, lo);
+    rec_rows<T, V, R>(rg, gp, g.gr, t, at.Vb - t, cols, lo);
+    if constexpr (Z) rec_rows<T, V, R>(rz, zp, g.zr, t, at.Vb - t, cols, lo);
     rec_rows<T, V, R>(rd, dp, (size_t)g.w, t, at.Vb - t, cols, lo);
 #pragma unroll
     for (int j = 0; j < V; j++) hs[j] = sv[(size_t)(at.t0 / TL + n) * g.w + j];

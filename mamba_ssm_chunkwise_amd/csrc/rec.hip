@@ -36,7 +36,9 @@ int make_rec_plan(const moments_rec_desc* d, RecPlan* P, bool bases) {
   const int64_t xs = d->x_stride == 0 ? d->w : d->x_stride, gs = d->g_stride == 0 ? d->w : d->g_stride;
   const int64_t zs = d->z_stride == 0 ? d->w : d->z_stride;
   if (xs < d->w || gs < d->w || (d->has_z && zs < d->w)) return MOMENTS_EINVAL;
-  const int64_t far = (int64_t)1 << 25;   // a lane's tokens are addressed with 32-bit offsets
+  // A lane's tokens are addressed with 32-bit offsets; where a sequence has one token, the next
+  // sequence's may be as far as the card's memory goes.
+  const int64_t far = (int64_t)1 << (d->s > 1 ? 25 : 37);
   if (xs > far || gs > far || (d->has_z && zs > far)) return MOMENTS_ENOTSUP;
   P->empty = d->b == 0;
   P->bf = d->dtype == MOMENTS_BF16;
@@ -46,6 +48,7 @@ int make_rec_plan(const moments_rec_desc* d, RecPlan* P, bool bases) {
   g.b = (int)d->b; g.s = (int)d->s; g.w = (int)d->w;
   g.V = (int)std::min(d->valid_len, d->s);
   g.xs = (size_t)xs; g.gs = (size_t)gs; g.zs = (size_t)zs;
+  g.xr = d->s > 1 ? g.xs : (size_t)d->w; g.gr = d->s > 1 ? g.gs : (size_t)d->w; g.zr = d->s > 1 ? g.zs : (size_t)d->w;
   g.lens = (const int*)d->valid_lens;
   P->VC = bases && d->w % 2 == 0 && xs % 2 == 0 && gs % 2 == 0 && (!P->z || zs % 2 == 0) ? 2 : 1;
   const int64_t ncg = (d->w + 64 * P->VC - 1) / (64 * P->VC);

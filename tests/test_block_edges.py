@@ -49,3 +49,14 @@ def test_every_launch_names_its_device():
     launched = set(re.findall(r"_launch\(dev, (?:lib|_lib\.load\(\))\.(moments_\w+),", src))
     takes_stream = {n for n in _lib.EXPORTS if re.search(r"_(fwd|bwd|step|norm|clip|static|save|saved)$", n)}
     assert launched == takes_stream
+
+
+@pytest.mark.parametrize("s,stride,code", [
+    (1, (1 << 25) + 8, 0), (1, 1 << 37, 0), (1, (1 << 37) + 1, -2), (2, 1 << 25, 0), (2, (1 << 25) + 1, -2),
+    (0, (1 << 25) + 8, 0),
+])
+def test_strides_of_single_tokens(s, stride, code):
+    """One token of each sequence may stand as far from the next's as a long projection is."""
+    for which in ("x_stride", "g_stride", "z_stride"):
+        d = M.RecDesc(b=3, s=s, w=16, valid_len=s, dtype=_lib.BF16, gate=1, has_z=1, **{which: stride})
+        assert M.moments_rec_validate(d) == code, which

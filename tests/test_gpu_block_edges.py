@@ -64,3 +64,28 @@ def test_lengths_of_the_mixer_changed_before_the_backward_are_noticed():
     lens.fill_(3)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("w", [64, 33])
+def test_the_last_tokens_of_long_projections(dtype, w):
+    """One token of each sequence, more than 2^25 elements from the next one's: a step, a whole sequence
+    of one token and its gradients, the same bits as of dense tokens."""
+    wide = torch.zeros(3, 5, 7_000_000, dtype=dtype, device=DEV)
+    assert wide.stride(0) > 2 ** 25
+    t = make_rec(3, 1, w, M.GATE_UNIT, dtype, seed=w)
+    far = {}
+    for i, k in enumerate(("x", "g", "z")):
+        far[k] = wide[:, -1:, i * w:(i + 1) * w]
+        far[k].copy_(t[k])
+    got, want = run_all({**t, **far}, M.GATE_UNIT), run_all(t, M.GATE_UNIT)
+    for k in want:
+        assert same(got[k], want[k]), k
+    pool = torch.randn(5, w, device=DEV)
+    slots = torch.tensor([4, 0, 2], dtype=torch.int32, device=DEV)
+    ys, states = [], []
+    for a in (far, t):
+        states.append(pool.clone())
+        d = M.rec_desc(a["x"], a["g"], a["z"], M.GATE_UNIT)
+        ys.append(M.moments_rec_step(d, a["x"], a["g"], a["z"], states[-1], slots))
+    assert same(*ys) and same(*states)
