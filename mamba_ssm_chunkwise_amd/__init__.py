@@ -920,8 +920,8 @@ class GradDesc:
     """Gradients and where their clipped values go; keeps the tensors. See grad_desc."""
 
     def __init__(self, grads, out):
-        self.grads, self.out = list(grads), list(grads if out is None else out)
-        self.in_place = out is None
+        self.grads, self.in_place = list(grads), out is None
+        self.out = list(self.grads if out is None else out)
         if len(self.out) != len(self.grads):
             raise ValueError(f"out holds {len(self.out)} tensors, grads {len(self.grads)}")
         self.device = None

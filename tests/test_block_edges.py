@@ -60,3 +60,14 @@ def test_strides_of_single_tokens(s, stride, code):
     for which in ("x_stride", "g_stride", "z_stride"):
         d = M.RecDesc(b=3, s=s, w=16, valid_len=s, dtype=_lib.BF16, gate=1, has_z=1, **{which: stride})
         assert M.moments_rec_validate(d) == code, which
+
+
+def test_gradients_from_an_iterator():
+    """As a program writes them: the gradients of the parameters that have one."""
+    layer = torch.nn.Linear(3, 4)
+    layer(torch.ones(2, 3)).sum().backward()
+    d = M.grad_desc(p.grad for p in layer.parameters() if p.grad is not None)
+    assert d.count == 2 and d.in_place and [id(t) for t in d.out] == [id(p.grad) for p in layer.parameters()]
+    out = [torch.empty(4, 3), torch.empty(4)]
+    d = M.grad_desc((p.grad for p in layer.parameters()), out=iter(out))
+    assert d.count == 2 and not d.in_place and d.out[0] is out[0] and d.out[1] is out[1]
