@@ -954,6 +954,10 @@ def grad_desc(grads, out=None) -> GradDesc:
     d = GradDesc(grads, out)
     rc = _lib.load().moments_grad_validate(d.spans, d.count)
     if rc == _lib.EINVAL:
+        for name, tensors in (("grads", d.grads), ("out", d.out)):
+            for i, t in enumerate(tensors):
+                if t.data_ptr() % t.element_size():
+                    raise ValueError(f"{name}[{i}] starts at {t.data_ptr():#x}, between two elements")
         raise ValueError("two of the tensors overlap (a gradient listed twice?)")
     _lib.check(rc)
     d.workspace_bytes = _size(_lib.load().moments_grad_workspace_size(d.spans, d.count))

@@ -71,3 +71,16 @@ def test_gradients_from_an_iterator():
     out = [torch.empty(4, 3), torch.empty(4)]
     d = M.grad_desc((p.grad for p in layer.parameters()), out=iter(out))
     assert d.count == 2 and not d.in_place and d.out[0] is out[0] and d.out[1] is out[1]
+
+
+def test_a_misaligned_gradient_is_not_called_an_overlap():
+    raw = bytearray(64)
+    odd = torch.frombuffer(raw, dtype=torch.float32, count=4, offset=2)
+    g = torch.zeros(4)
+    assert odd.data_ptr() % 4 == 2
+    with pytest.raises(ValueError, match=r"grads\[1\] starts"):
+        M.grad_desc([g, odd])
+    with pytest.raises(ValueError, match=r"out\[0\] starts"):
+        M.grad_desc([g], out=[odd])
+    with pytest.raises(ValueError, match="overlap"):
+        M.grad_desc([g, g])
