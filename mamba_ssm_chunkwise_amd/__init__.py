@@ -949,8 +949,10 @@ class GradDesc:
 def grad_desc(grads, out=None) -> GradDesc:
     """Descriptor of many gradients (contiguous float32 or bfloat16 tensors on one device),
     for moments_grad_norm and moments_grad_clip; it keeps the tensors, which may be refilled
-    between calls but not given other memory. ``out``: tensors like them that take the
-    clipped values (None: in place). Raises if a tensor that is written overlaps another."""
+    between calls but not given other memory. It is of these tensors, not of the parameters:
+    where a step gives the parameters new ones (``zero_grad()`` does, unless
+    ``set_to_none=False``), each step makes its descriptor. ``out``: tensors like them that take
+    the clipped values (None: in place). Raises if a tensor that is written overlaps another."""
     d = GradDesc(grads, out)
     rc = _lib.load().moments_grad_validate(d.spans, d.count)
     if rc == _lib.EINVAL:
