@@ -430,7 +430,8 @@ int moments_ln_bwd(const moments_ln_desc* desc, const void* x, const float* weig
  * A span is n values of either dtype from any element on; `out` NULL (or p) writes in place. The
  * array of spans is the host's and is read during the call only; the norm is one float32 on the
  * device, so that a program may join it with other ranks' before it clips (a sum of squares). A norm that is
- * not finite leaves the values as they are (out of place: copies them). Squares are summed in double, in a
+ * not finite, or negative, leaves the values as they are (out of place: copies them); so does one that
+ * leaves the range of float32, where a caller may want zeros instead. Squares are summed in double, in a
  * fixed order. max_norm is a finite or infinite number from 0 on.
  *
  * moments_grad_validate checks the spans, also that no span's output overlaps another span or output

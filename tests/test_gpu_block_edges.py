@@ -4,6 +4,8 @@ import torch
 
 import mamba_ssm_chunkwise_amd as M
 from bounds_util import same
+from test_gpu_grad import both as clip_both, make as make_grads
+from test_gpu_ln import both as ln_both, make as make_ln
 from test_gpu_rec import make as make_rec, run_all
 from test_gpu_recurrent import _example
 
@@ -89,3 +91,35 @@ def test_the_last_tokens_of_long_projections(dtype, w):
         d = M.rec_desc(a["x"], a["g"], a["z"], M.GATE_UNIT)
         ys.append(M.moments_rec_step(d, a["x"], a["g"], a["z"], states[-1], slots))
     assert same(*ys) and same(*states)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("res", [True, False])
+@pytest.mark.parametrize("w", [8200, 16384])
+def test_several_wide_rows_to_a_workgroup(dtype, res, w):
+    """Rows above 8192 columns, whose gradients' sums stand in LDS from row to row."""
+    ln_both(make_ln(601, w, dtype, res=res, seed=w))
+
+
+@pytest.mark.parametrize("n,w", [(40_003, 256), (140_001, 40)])
+def test_more_narrow_rows_than_the_forward_takes_at_once(n, w):
+    ln_both(make_ln(n, w, BF16, res=w == 40, seed=w))
+    ln_both(make_ln(n, w, F32, res=w != 40, seed=w))
+
+
+@pytest.mark.parametrize("max_norm", [0.5, 1e9])
+def test_more_pieces_than_workgroups(max_norm):
+    """Gradients of more than 2048 pieces of 32 KB in a launch: later rounds of the workgroups, over tensors'
+    borders, values outside 16-byte words among them."""
+    sizes = [12_000_000, 4099, 9_000_001, 3, 5_000_003, 70_001]
+    assert sum(n * 4 // 32768 for n in sizes[::2][:2]) > 2048
+    clip_both(make_grads(sizes, dtypes=(F32, BF16), offset=3), max_norm)
+    g = make_grads(sizes, dtypes=(F32, F32, F32, F32, BF16, BF16), seed=2, offset=1)
+    clip_both(g, max_norm, out=[torch.empty(t.numel() + 2, dtype=t.dtype, device=DEV)[2:] for t in g])
+
+
+def test_a_negative_norm_leaves_the_gradients():
+    g = make_grads([100, 5000])
+    copy = [t.clone() for t in g]
+    M.moments_grad_clip(M.grad_desc(g), torch.full((), -2.0, device=DEV), 0.5)
+    assert all(same(a, b) for a, b in zip(g, copy))
