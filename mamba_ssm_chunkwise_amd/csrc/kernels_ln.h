@@ -13,10 +13,13 @@
 // The gradients make the statistics again, with their own two sums in that same reduction, so
 // nothing is kept from the forward.
 //
-// Bound by memory: 65536 x 4096 bf16 with a residual, forward 597 us (3.2 GB, 5.4 TB/s), gradients
-// 821 us (4.3 GB, 5.2 TB/s) and 8 us for the sums over rows. A row has 8 to 64 threads of eight
+// Bound by memory: 65536 x 4096 bf16 with a residual, forward 602 us (3.2 GB, 5.3 TB/s), gradients
+// 822 us (4.3 GB, 5.2 TB/s) and 8 us for the sums over rows. A row has 8 to 64 threads of eight
 // elements up to w = 512 (several rows to a wave: 1e6 x 100 bf16, forward and gradients 667 us, a
-// wave to a row 1215), then 16 elements. Streamed loads or stores: forward 655 and 670 us.
+// wave to a row 1215), then 16 elements. Streamed loads or stores: forward 655 and 670 us. Threads
+// being powers of two, widths just past one leave up to half of them idle (20000 x 8200 bf16,
+// forward and gradients 1136 us, 807 at the copy rate), rows below 64 columns more (4e6 x 8, one
+// thread of eight: 620 us, 157 at the copy rate).
 #pragma once
 
 #include "common.h"
@@ -233,9 +236,13 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_fwd(LnGeo g, const T
 }
 
 // part: a row of w sums for each workgroup, of d_weight, then of d_bias (NULL: neither is wanted).
+// A thread adds its rows' values one after the other in float32, n / 768 of them at w = 4096, n / 24576
+// up to w = 64: the sums are off by at most that many times 2^-24 of the values' magnitudes together;
+// what the workgroups leave is added in double.
 // TS: of the normed rows (float where a residual was added). With E = 32 elements a thread's 2 E
 // sums stand in LDS (ln_wide_lds bytes) and the weights are loaded for each row: 16384 x 16384 bf16
-// with residual 947 us at 1024 threads of 16 elements, whose 128 registers do not hold them.
+// with residual 947 us at 1024 threads of 16 elements, whose 128 registers do not hold them. It
+// still spills 28 to 42 registers (116 to 172 bytes of scratch a lane).
 template <int NT, int E> constexpr size_t ln_wide_lds = E == 32 ? (size_t)2 * E * NT * 4 : 0;
 template <typename T, typename TS, int NT, int E>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_ln_bwd(LnGeo g, const TS* __restrict__ x,

@@ -14,11 +14,13 @@
 // is gone. In a run's map that is a sign bit on P, which no product of decays has by itself, so a
 // product that only underflows is told apart from it.
 //
-// Bound by memory: 8 x 8192 x 4096 bf16 with z, forward 407 us (2.15 GB, 5.3 TB/s; a copy reaches
-// 4.9), gradients 731 us (3.76 GB, 5.1 TB/s), vector pipes 55 and 50 % busy. Where chain groups are
-// too few for the card the sequence is cut into segments, whose maps take a second pass over x and
-// g: 60000 tokens of 4096 channels, 230 us beside the walk's 408. Workgroups that take tiles one by
-// one and hand states on through memory instead were slower (553 us and a launch that clears).
+// Bound by memory: 8 x 8192 x 4096 bf16 with z, forward 425 us (405 to 441; 2.15 GB, 5.1 TB/s; a
+// copy reaches 4.9), gradients 738 us (717 to 784; 3.76 GB, 5.1 TB/s), vector pipes 57 and 52 % busy.
+// Where chain groups are too few for the card the sequence is cut into segments, whose maps take a
+// second pass over x and g, but for the last segment's: 60000 tokens of 4096 channels, 248 us (213 to
+// 271; 0.87 GB, 3.5 TB/s, on 224 of 256 CUs, vector pipes 64 % busy) beside the walk's 430 (2.0 GB,
+// 4.7 TB/s). Workgroups that take tiles one by one and hand states on through memory instead were
+// slower (553 us and a launch that clears).
 #pragma once
 
 #include <type_traits>
@@ -31,7 +33,7 @@ constexpr int REC_W = 16;              // waves of a workgroup of the forward wa
 template <typename T> constexpr int REC_R = 16 / sizeof(T);   // tokens of a lane there
 constexpr int REC_WB = 8;              // waves of a workgroup of the gradients' walk
 constexpr int REC_RB = 8;              // tokens of a lane there
-constexpr int REC_TILE = REC_W * REC_R<__bf16>;   // segments are whole multiples of any tile
+constexpr int REC_TILE = REC_W * REC_R<__bf16>;   // segments are whole multiples of any tile (fp32's are 64 tokens)
 constexpr int REC_SAVE = REC_WB * REC_RB;   // tokens between saved states: a tile of the gradients' walk
 constexpr int REC_SW = 16;             // waves of a workgroup that makes a segment's map
 constexpr int REC_SR = 8;              // its lanes' tokens in flight
@@ -97,7 +99,9 @@ template <typename T, int V> __device__ __forceinline__ rvec<T, V> rec_bld(RecBu
 // Stores are streamed past the caches' other lines: 8 x 8192 x 4096 bf16, forward 448 us without that,
 // 407 with it, gradients 743 and 731; with a kernel that reads y at once behind it 616 and 604 us, of
 // 8 x 1024 x 4096 82 and 79. (Loads likewise slow down where x and g are read twice; single 16-bit
-// stores, 8 x 8192 x 4095 gradients, 1198 us without and 1750 with it, so those go without.)
+// stores, 8 x 8192 x 4095 gradients, 1198 us without and 1750 with it, so those go without.) These two
+// widths are what was measured: rows of 4- and 8-byte stores that are not whole 128-byte lines (8 x
+// 8192 x 4094, 1269 us for the gradients) are streamed too, and have not been timed otherwise.
 constexpr int kRecStream = 2;   // the instruction's nt bit
 template <typename T, int V> __device__ __forceinline__ void rec_bst(RecBuf r, unsigned off, const float (&f)[V]) {
   typedef unsigned u2 __attribute__((ext_vector_type(2)));

@@ -59,7 +59,9 @@ int make_rec_plan(const moments_rec_desc* d, RecPlan* P, bool bases) {
   // (a second round of workgroups costs as much as the first: 8 x 8192 x 2050 bf16, 136 groups, one
   // segment 982 us for forward and gradients, two 1514), of a tile or more, from four tiles on
   // (600 x 512: a tile each 54 us, two 69, one segment 75; 2 x 300 x 4096, three tiles: one segment
-  // 47 us, three 53).
+  // 47 us, three 53). From 129 to 255 groups that is one segment, and the CUs past the groups have no
+  // work; of these only 136 groups were measured. A ragged batch has the same number for each sequence,
+  // so the longest one's segments take longest.
   const int64_t n = tiles < 4 ? 1 : std::max<int64_t>(1, std::min(kCUs / std::max<int64_t>(items, 1), tiles));
   const int64_t per = std::max<int64_t>((tiles + n - 1) / n, 1);
   g.nseg = (int)std::max<int64_t>((tiles + per - 1) / per, 1);
